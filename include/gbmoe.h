@@ -432,6 +432,158 @@ int32_t moe_forward_num_launches_ex(const gbmoe_config_t* cfg, int32_t num_token
 gbmoe_status_t moe_selftest_bounded_wait(void* workspace, int32_t timeout_us,
                                          gbmoe_stream_t stream);
 
+/*
+ * ---- The decoder block around the layer: norm, paged cache, attention.
+ *
+ * moe_rms_norm: root-mean-square norm of each row with the residual's addition, written as
+ * bf16, as the FP8 layer's quantized input, or both:
+ *   h = x + residual (fp32; h = x without one), residual_out = bf16(h)
+ *   y = h / sqrt(mean(h^2) + eps) * weight (fp32), y_out = bf16(y)
+ *   s = max(max |y|, 1e-10) / 448 over each 128 columns, q = e4m3fn(y / s) (one fp32 division
+ *   each, round to nearest even, saturating; from the fp32 y, not from its bf16 rounding)
+ *   x             [T, H] bf16, row t at x + t * x_stride (elements)
+ *   residual      [T, H] bf16, row stride residual_stride; or NULL
+ *   weight        [H] bf16
+ *   y             [T, H] bf16 (out) or NULL
+ *   residual_out  [T, H] bf16 (out) or NULL; needs a residual; may be x's or residual's own
+ *                 contiguous memory
+ *   q, scale      [T, H] e4m3fn bytes and [H / 128, T] fp32, group-major as in
+ *                 moe_quant_fp8_per_token_group (out); both or neither
+ * At least one of y and q. H a multiple of 8 (of 128 with q), at most 32768 (else UNSUPPORTED);
+ * strides multiples of 8 and >= H; bf16 pointers and q 16-byte aligned; eps >= 0. A row with a
+ * NaN or an infinity gives NaN codes and values there. T = 0 is a no-op.
+ */
+typedef struct {
+  const void* x;
+  int64_t x_stride;
+  const void* residual;
+  int64_t residual_stride;
+  const void* weight;
+  float eps;
+  void* y;
+  void* residual_out;
+  uint8_t* q;
+  float* scale;
+} gbmoe_rms_norm_args_t;
+gbmoe_status_t moe_rms_norm(int32_t num_tokens, int32_t hidden_size,
+                            const gbmoe_rms_norm_args_t* args, gbmoe_stream_t stream);
+
+typedef enum { GBMOE_CACHE_BF16 = 0, GBMOE_CACHE_E4M3 = 1 } gbmoe_cache_type_t;
+
+/*
+ * Attention configuration of one layer.
+ *  num_q_heads, num_kv_heads  query head h reads kv head h / (num_q_heads / num_kv_heads);
+ *                             num_q_heads a multiple of num_kv_heads, at most 1024
+ *  head_dim                   64 or 128 (else UNSUPPORTED)
+ *  page_size                  tokens per page, a power of two from 8 to 1024 (else UNSUPPORTED)
+ *  cache_type                 gbmoe_cache_type_t; E4M3: k = code * k_scale, v = code * v_scale
+ *  causal                     !=0: a token attends no later position than its own
+ *  window                     > 0: only the last `window` positions up to its own; 0 = all
+ *  softmax_scale              multiplies q . k
+ *  k_scale, v_scale           1 with a bf16 cache
+ */
+typedef struct {
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t cache_type;
+  int32_t causal;
+  int32_t window;
+  float softmax_scale;
+  float k_scale;
+  float v_scale;
+} gbmoe_attn_config_t;
+
+/*
+ * The paged cache and the sequences of one call.
+ *  k_cache, v_cache  [num_pages, page_size, num_kv_heads, head_dim]: element (page, row, head, d)
+ *                    at page * page_stride + row * token_stride + head * head_stride + d, the
+ *                    same strides (elements, multiples of 16 bytes) for both; 16-byte aligned
+ *  block_table       [num_seqs, block_table_stride] int32: entry i of a sequence is the page of
+ *                    its positions [i * page_size, (i + 1) * page_size). Entries past its length
+ *                    (and, for attention, wholly outside every window) are never read.
+ *  cu_seqlens_q      [num_seqs + 1] int32, ascending: sequence s has the packed new tokens
+ *                    [cu[s], cu[s + 1]); none is allowed
+ *  kv_lens           [num_seqs] int32: positions of each sequence, its new tokens (the last
+ *                    n = cu[s + 1] - cu[s] of them) among them; 0 is allowed
+ * num_seqs 1..8192. The three arrays are device memory, read by the kernels: a captured graph
+ * replays with their current contents. A page id outside the cache, cu_seqlens_q outside the
+ * batch, a length outside the block table or a position outside cos_sin sets
+ * GBMOE_ERR_DEVICE_CHECK in the device status; nothing outside the buffers is touched, and
+ * the sequences concerned have unspecified outputs.
+ */
+typedef struct {
+  void* k_cache;
+  void* v_cache;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t num_pages;
+  int32_t num_seqs;
+  int32_t block_table_stride;
+  const int32_t* block_table;
+  const int32_t* cu_seqlens_q;
+  const int32_t* kv_lens;
+} gbmoe_paged_kv_t;
+
+/*
+ * moe_kv_append: rotary embedding of the new tokens' q and k, and the write of their k and v
+ * into the cache. The token at index i of sequence s sits at position p = kv_lens[s] - n + i.
+ * The first `rotary_dim` columns of every q and k head turn pairwise,
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * pair i being columns (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved != 0; all in
+ * fp32, rounded once (E4M3: code = e4m3fn(value / scale), saturating at +-448).
+ *   q, k, v     [T, heads, head_dim] bf16, token strides q_stride, k_stride, v_stride (elements,
+ *               multiples of 8; heads contiguous), so that one packed projection serves
+ *   cos_sin     [max_position, rotary_dim] fp32: rotary_dim / 2 cosines, then as many sines; or
+ *               NULL with rotary_dim 0 (no rotation)
+ *   q_out       [T, num_q_heads, head_dim] bf16 contiguous (out); may be q itself
+ *   workspace   256 bytes, 256-byte aligned: the status word; or NULL (unreported)
+ * rotary_dim a multiple of 16, at most head_dim. A token of no sequence is left out. T = 0 is a
+ * no-op. Sequences must not share the pages that a call writes.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const float* cos_sin;
+  int32_t max_position;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  void* q_out;
+  void* workspace;
+} gbmoe_kv_append_args_t;
+gbmoe_status_t moe_kv_append(const gbmoe_attn_config_t* cfg, int32_t num_tokens,
+                             const gbmoe_paged_kv_t* kv, const gbmoe_kv_append_args_t* args,
+                             gbmoe_stream_t stream);
+
+/*
+ * moe_paged_attention: softmax attention of every sequence's new tokens over its pages, in one
+ * call for single tokens, chunks after a context and whole prompts (kv_lens = n) alike.
+ * Token i of sequence s at position p = kv_lens[s] - n + i attends the keys j with
+ *   0 <= j < kv_lens[s], j <= p if causal, j > p - window if window > 0;
+ *   out = sum_j softmax_j(softmax_scale q . k_j) v_j, lse = log sum_j exp(softmax_scale q . k_j).
+ * A token without keys has out = 0 and lse = -inf; a row of `out` in no sequence is unspecified.
+ * Scores, the softmax's maximum and sum, and the output's sums are fp32; the weights are
+ * rounded to 16 bits for their product with v. What pages hold past a sequence's length, or
+ * outside every window of the call, is ignored whatever it is; v of the positions inside must be
+ * finite even where a mask hides them from some of the tokens.
+ *   q    [T, num_q_heads, head_dim] bf16, token stride q_stride (elements, a multiple of 8)
+ *   out  [T, num_q_heads, head_dim] bf16 contiguous (out)
+ *   lse  [T, num_q_heads] fp32 (out) or NULL
+ * Workspace: moe_paged_attention_workspace_size(cfg) bytes (0: bad configuration), 256-byte
+ * aligned, its first 256 bytes zeroed once. T = 0 is a no-op.
+ */
+size_t moe_paged_attention_workspace_size(const gbmoe_attn_config_t* cfg);
+gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int32_t num_tokens,
+                                   const gbmoe_paged_kv_t* kv, const void* q, int64_t q_stride,
+                                   void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, gbmoe_stream_t stream);
+
 /* Library version, (major << 16) | minor. */
 int32_t gbmoe_version(void);
 

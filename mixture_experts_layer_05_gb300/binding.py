@@ -21,6 +21,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_CHECK,
     0, -1, -2, -3, -4, -5, -6
 SCORE = {"softmax": 0, "sigmoid": 1}
 QUANT = {None: 0, "none": 0, "fp8": 1, "fp8_block128": 1, "nvfp4": 2}
+CACHE = {"bf16": 0, "fp8": 1, "e4m3": 1}
 NUM_STAGE_EVENTS = 5
 
 # every entry point declared in include/gbmoe.h
@@ -31,7 +32,9 @@ EXPORTS = ("moe_topk", "moe_align_block_size_workspace_size", "moe_align_block_s
            "moe_forward_num_launches", "moe_forward_num_launches_ex",
            "moe_selftest_bounded_wait", "moe_forward_ex",
            "moe_router_logits", "moe_quant_fp8_per_token_group", "moe_quant_nvfp4",
-           "moe_nvfp4_prepared_bytes", "moe_nvfp4_prepare_weight", "gbmoe_version")
+           "moe_nvfp4_prepared_bytes", "moe_nvfp4_prepare_weight", "moe_rms_norm",
+           "moe_kv_append", "moe_paged_attention_workspace_size", "moe_paged_attention",
+           "gbmoe_version")
 
 
 class GbmoeError(RuntimeError):
@@ -79,6 +82,44 @@ class WorkspaceLayout(ctypes.Structure):
         "num_tokens_post_padded", "act", "act_scale", "total", "act_shared")]
 
 
+class RmsNormArgs(ctypes.Structure):
+    """gbmoe_rms_norm_args_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("y", ctypes.c_void_p),
+                ("residual_out", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
+class AttnConfig(ctypes.Structure):
+    """gbmoe_attn_config_t."""
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("cache_type", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class PagedKv(ctypes.Structure):
+    """gbmoe_paged_kv_t."""
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("block_table_stride", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("cu_seqlens_q", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    """gbmoe_kv_append_args_t."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("cos_sin", ctypes.c_void_p),
+                ("max_position", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("q_out", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p)]
+
+
 def make_config(num_experts, top_k, hidden_size, intermediate_size, renormalize=True,
                 use_grouped_topk=False, num_expert_group=0, topk_group=0,
                 scoring_func="softmax", routed_scaling_factor=1.0, activation=0,
@@ -101,6 +142,17 @@ def config_from_workload(w, **variants) -> Config:
                        w.renormalize, w.use_grouped_topk, w.num_expert_group, w.topk_group,
                        w.scoring_func, w.routed_scaling_factor,
                        shared_intermediate_size=w.shared_intermediate_size, **variants)
+
+
+def make_attn_config(num_q_heads, num_kv_heads, head_dim, page_size, cache_dtype="bf16",
+                     causal=True, window=0, softmax_scale=None, k_scale=1.0,
+                     v_scale=1.0) -> AttnConfig:
+    """cache_dtype: "bf16" or "fp8" (e4m3 codes, k = code * k_scale, v = code * v_scale);
+    window 0: no sliding window; softmax_scale None: head_dim ** -0.5."""
+    return AttnConfig(int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size),
+                      CACHE.get(cache_dtype, cache_dtype), int(bool(causal)), int(window),
+                      float(head_dim ** -0.5 if softmax_scale is None else softmax_scale),
+                      float(k_scale), float(v_scale))
 
 
 _lib = None
@@ -137,6 +189,12 @@ def load() -> ctypes.CDLL:
         "moe_nvfp4_prepared_bytes": (SZ, [I32, I32]),
         "moe_nvfp4_prepare_weight": (I32, [I32, I32, P, P, P, P]),
         "moe_selftest_bounded_wait": (I32, [P, I32, P]),
+        "moe_rms_norm": (I32, [I32, I32, ctypes.POINTER(RmsNormArgs), P]),
+        "moe_kv_append": (I32, [ctypes.POINTER(AttnConfig), I32, ctypes.POINTER(PagedKv),
+                                ctypes.POINTER(KvAppendArgs), P]),
+        "moe_paged_attention_workspace_size": (SZ, [ctypes.POINTER(AttnConfig)]),
+        "moe_paged_attention": (I32, [ctypes.POINTER(AttnConfig), I32, ctypes.POINTER(PagedKv),
+                                      P, ctypes.c_int64, P, P, P, SZ, P]),
         "gbmoe_version": (I32, []),
     }
     for name, (res, args) in sig.items():
@@ -410,6 +468,156 @@ def moe_get_device_status(workspace, stream=None) -> int:
     _check("moe_get_device_status",
            load().moe_get_device_status(_p(workspace), ctypes.byref(v), _stream(stream)))
     return v.value
+
+
+def _rows(t, dtype, name, cols):
+    """A [T, cols] (or [T, heads, dim]) tensor whose rows are contiguous; its row stride."""
+    if t is None:
+        return 0
+    inner = (1,) if t.dim() == 2 else (t.shape[2], 1) if t.dim() == 3 else None
+    if (inner is None or not t.is_cuda or t.dtype != dtype
+            or t.numel() != t.shape[0] * cols or t.stride()[1:] != inner):
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor of {cols} contiguous columns a row")
+    return t.stride(0) if t.shape[0] > 1 else cols
+
+
+def moe_rms_norm(x, weight, eps=1e-6, residual=None, out="bf16", y=None, residual_out=None,
+                 q=None, scale=None, stream=None):
+    """RMS norm of bf16 rows x [T, H] (+ residual) by weight [H]; out: "bf16" (y), "fp8" (q,
+    scale: e4m3 codes and group-major fp32 scales [H / 128, T], the FP8 layer's input format)
+    or "both". Rows of x and residual may be strided. Returns (y, residual_out, q, scale), None
+    for what was not asked for (residual_out: without a residual)."""
+    if out not in ("bf16", "fp8", "both"):
+        raise ValueError(f"out must be bf16, fp8 or both, not {out!r}")
+    T, H = x.shape
+    xs = _rows(x, torch.bfloat16, "x", H)
+    rs = _rows(residual, torch.bfloat16, "residual", H)
+    if weight.numel() != H or (residual is not None and residual.shape[0] != T):
+        raise ValueError("weight must have H columns, residual the rows of x")
+    if out == "fp8":
+        y = None
+    elif y is None:
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+    if residual is None:
+        residual_out = None
+    elif residual_out is None:
+        residual_out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+    if out == "bf16":
+        q = scale = None
+    else:
+        if q is None:
+            q = torch.empty(T, H, dtype=torch.float8_e4m3fn, device=x.device)
+        if scale is None:
+            scale = torch.empty(H // 128, T, dtype=torch.float32, device=x.device)
+        _fp8_bytes(q, "q")
+        _need(scale, torch.float32, "scale")
+        if q.numel() != T * H or scale.numel() != H // 128 * T:
+            raise ValueError("q must be [T, H] and scale [H / 128, T]")
+    for t, n in ((weight, "weight"), (y, "y"), (residual_out, "residual_out")):
+        _need(t, torch.bfloat16, n)
+    for t, n in ((y, "y"), (residual_out, "residual_out")):
+        if t is not None and t.numel() != T * H:
+            raise ValueError(f"{n} must be [T, H]")
+    ptr = lambda t: None if t is None else t.data_ptr()
+    a = RmsNormArgs(ptr(x), xs, ptr(residual), rs, ptr(weight), float(eps), ptr(y),
+                    ptr(residual_out), ptr(q), ptr(scale))
+    _check("moe_rms_norm", load().moe_rms_norm(T, H, ctypes.byref(a), _stream(stream)))
+    return y, residual_out, q, scale
+
+
+class PagedAttention:
+    """One layer's attention over a paged cache, and the append that fills it.
+
+    The caches are [num_pages, page_size, num_kv_heads, head_dim] tensors (bf16, or
+    float8_e4m3fn / uint8 codes) of equal strides, any order of pages, rows and heads;
+    block_table [S, max_pages], cu_seqlens_q [S + 1] and kv_lens [S] int32 device tensors (see
+    gbmoe_paged_kv_t). The workspace is the layer's own: calls on different streams must be
+    ordered, or use one object each.
+    """
+
+    def __init__(self, cfg: AttnConfig, device="cuda"):
+        self.cfg = cfg
+        n = load().moe_paged_attention_workspace_size(ctypes.byref(cfg))
+        if n == 0:
+            raise GbmoeError("moe_paged_attention_workspace_size", ERR_INVALID_ARG)
+        self.workspace = alloc_workspace(n, device)
+        self._dtypes = ((torch.bfloat16,) if cfg.cache_type == CACHE["bf16"]
+                        else (torch.float8_e4m3fn, torch.uint8))
+
+    def _paged(self, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens) -> PagedKv:
+        c = self.cfg
+        shape = (c.page_size, c.num_kv_heads, c.head_dim)
+        strides = k_cache.stride()
+        if (not k_cache.is_cuda or not v_cache.is_cuda or k_cache.dtype not in self._dtypes
+                or v_cache.dtype != k_cache.dtype or k_cache.dim() != 4
+                or tuple(k_cache.shape[1:]) != shape or v_cache.shape != k_cache.shape
+                or strides != v_cache.stride() or strides[3] != 1):
+            raise ValueError("k_cache and v_cache must be CUDA tensors [num_pages, page_size, "
+                             "num_kv_heads, head_dim] of the configured type and equal strides, "
+                             "contiguous in head_dim")
+        S = kv_lens.shape[0]
+        for t, n in ((block_table, "block_table"), (cu_seqlens_q, "cu_seqlens_q"),
+                     (kv_lens, "kv_lens")):
+            _need(t, torch.int32, n)
+        if block_table.dim() != 2 or block_table.shape[0] != S or cu_seqlens_q.shape != (S + 1,):
+            raise ValueError("block_table must be [S, max_pages], cu_seqlens_q [S + 1], kv_lens [S]")
+        # the stride of a dimension of one element is never used: any valid number
+        ps, ts, hs = (strides[i] if k_cache.shape[i] > 1 else c.head_dim for i in range(3))
+        return PagedKv(k_cache.data_ptr(), v_cache.data_ptr(), ps, ts, hs, k_cache.shape[0], S,
+                       block_table.shape[1], block_table.data_ptr(), cu_seqlens_q.data_ptr(),
+                       kv_lens.data_ptr())
+
+    def append(self, q, k, v, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, cos_sin=None,
+               interleaved=False, q_out=None, stream=None):
+        """Rotates the new tokens' q and k [T, heads, head_dim] (rows may be strided, as slices
+        of one packed projection), writes k and v into the cache, and returns the rotated q."""
+        c = self.cfg
+        kv = self._paged(k_cache, v_cache, block_table, cu_seqlens_q, kv_lens)
+        T = q.shape[0]
+        strides = [_rows(t, torch.bfloat16, n, h * c.head_dim) for t, n, h in
+                   ((q, "q", c.num_q_heads), (k, "k", c.num_kv_heads), (v, "v", c.num_kv_heads))]
+        if k.shape[0] != T or v.shape[0] != T:
+            raise ValueError("q, k and v must have the same number of tokens")
+        if q_out is None:
+            q_out = torch.empty(T, c.num_q_heads, c.head_dim, dtype=torch.bfloat16,
+                                device=q.device)
+        _need(q_out, torch.bfloat16, "q_out")
+        _need(cos_sin, torch.float32, "cos_sin")
+        if q_out.numel() != T * c.num_q_heads * c.head_dim:
+            raise ValueError("q_out must be [T, num_q_heads, head_dim]")
+        pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+        a = KvAppendArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
+                         None if cos_sin is None else cos_sin.data_ptr(), pos, rot,
+                         int(bool(interleaved)), q_out.data_ptr(), self.workspace.data_ptr())
+        _check("moe_kv_append", load().moe_kv_append(ctypes.byref(c), T, ctypes.byref(kv),
+                                                     ctypes.byref(a), _stream(stream)))
+        return q_out
+
+    def __call__(self, q, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, out=None,
+                 lse=None, stream=None):
+        """out [T, num_q_heads, head_dim] bf16 of the new tokens' q; with lse (True, or a fp32
+        [T, num_q_heads] tensor) also the log-sum-exp of each row's scores: (out, lse)."""
+        c = self.cfg
+        kv = self._paged(k_cache, v_cache, block_table, cu_seqlens_q, kv_lens)
+        T = q.shape[0]
+        qs = _rows(q, torch.bfloat16, "q", c.num_q_heads * c.head_dim)
+        if out is None:
+            out = torch.empty(T, c.num_q_heads, c.head_dim, dtype=torch.bfloat16, device=q.device)
+        _need(out, torch.bfloat16, "out")
+        if lse is True:
+            lse = torch.empty(T, c.num_q_heads, dtype=torch.float32, device=q.device)
+        _need(lse, torch.float32, "lse")
+        if out.numel() != T * c.num_q_heads * c.head_dim or (
+                lse is not None and lse.numel() != T * c.num_q_heads):
+            raise ValueError("out must be [T, num_q_heads, head_dim], lse [T, num_q_heads]")
+        ws = self.workspace
+        _check("moe_paged_attention", load().moe_paged_attention(
+            ctypes.byref(c), T, ctypes.byref(kv), q.data_ptr(), qs, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+        return out if lse is None else (out, lse)
+
+    def device_status(self) -> int:
+        return moe_get_device_status(self.workspace)
 
 
 class FusedMoE:

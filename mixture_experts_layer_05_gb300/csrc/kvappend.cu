@@ -1,0 +1,142 @@
+// Rotary embedding of a batch's new tokens and the write of their k and v into the paged cache.
+//
+// The token at index i of its sequence sits at position p = kv_len - n + i; its k and v go to
+// row p % page_size of page block_table[seq][p / page_size]. The first R columns of each q and
+// k head turn by the angle of p, pair by pair, (a, b) -> (a cos - b sin, b cos + a sin), in
+// fp32 from an fp32 table; q is rounded once to bf16, k and v once to the cache's type (e4m3:
+// from x / scale, saturating at 448).
+//
+// Bound by HBM. One CTA per token; a thread handles two vectors of eight columns at a time,
+// the two halves of eight pairs (half-split pairs) or sixteen neighbouring columns.
+#include "block.cuh"
+#include "fp8.cuh"
+#include "kernels.h"
+
+namespace gbmoe {
+namespace {
+
+constexpr int kAppendThreads = 192;
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_bf16x2(w[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint4 u;
+  u.x = pack_bf16x2(v[0], v[1]);
+  u.y = pack_bf16x2(v[2], v[3]);
+  u.z = pack_bf16x2(v[4], v[5]);
+  u.w = pack_bf16x2(v[6], v[7]);
+  *reinterpret_cast<uint4*>(p) = u;
+}
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&v)[8], float scale) {
+  uint2 c;
+  c.x = e4m3x4(v[0], v[1], v[2], v[3], scale);
+  c.y = e4m3x4(v[4], v[5], v[6], v[7], scale);
+  *reinterpret_cast<uint2*>(p) = c;
+}
+__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvAppendArgs a) {
+  const int t = blockIdx.x, lane = threadIdx.x & 31;
+  const int s = find_seq_warp(a.b, t, lane);  // every warp finds it: no barrier
+  if (s < 0) return;                          // a token of no sequence (padding)
+  const SeqInfo q = seq_info(a.b, s);
+  const int pos = q.L - q.n + (t - q.q0);
+  if (t - q.q0 >= q.n || pos < 0 || (a.cos_sin && pos >= a.max_pos)) {
+    if (threadIdx.x == 0) record_status(a.b.status, GBMOE_ERR_DEVICE_CHECK);
+    return;
+  }
+  const int page = __ldg(a.b.table + (size_t)s * a.b.table_stride + (pos >> a.b.page_shift));
+  const bool page_ok = (unsigned)page < (unsigned)a.b.num_pages;
+  if (!page_ok && threadIdx.x == 0) record_status(a.b.status, GBMOE_ERR_DEVICE_CHECK);
+  const size_t row = (size_t)page * a.c.page_stride +
+                     (size_t)(pos & ((1 << a.b.page_shift) - 1)) * a.c.token_stride;
+  const int per_head = a.D / 16;
+  const int items = (a.hq + 2 * a.hkv) * per_head;
+  const int R = a.rotary;
+  const float* cs = a.cos_sin ? a.cos_sin + (size_t)pos * R : nullptr;
+  for (int it = threadIdx.x; it < items; it += blockDim.x) {
+    int h = it / per_head;
+    const int p = it % per_head;
+    const int kind = h < a.hq ? 0 : (h < a.hq + a.hkv ? 1 : 2);  // q, k, v
+    h -= kind == 0 ? 0 : (kind == 1 ? a.hq : a.hq + a.hkv);
+    const bool turn = kind < 2 && p < R / 16;
+    // columns of the two vectors
+    const bool split = kind < 2 && !a.interleaved && p < R / 16;
+    const int c0 = split ? 8 * p : 16 * p;
+    const int c1 = split ? 8 * p + R / 2 : 16 * p + 8;
+    const __nv_bfloat16* src =
+        kind == 0 ? static_cast<const __nv_bfloat16*>(a.q) + (size_t)t * a.q_stride
+        : kind == 1 ? static_cast<const __nv_bfloat16*>(a.k) + (size_t)t * a.k_stride
+                    : static_cast<const __nv_bfloat16*>(a.v) + (size_t)t * a.v_stride;
+    src += (size_t)h * a.D;
+    float x[8], y[8];
+    load8(src + c0, x);
+    load8(src + c1, y);
+    if (turn) {
+      float c[8], z[8];
+      load8f(cs + 8 * p, c);
+      load8f(cs + R / 2 + 8 * p, z);
+      if (split) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float u = x[i] * c[i] - y[i] * z[i];
+          y[i] = y[i] * c[i] + x[i] * z[i];
+          x[i] = u;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u = x[2 * i] * c[i] - x[2 * i + 1] * z[i];
+          x[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * z[i];
+          x[2 * i] = u;
+          const float w = y[2 * i] * c[4 + i] - y[2 * i + 1] * z[4 + i];
+          y[2 * i + 1] = y[2 * i + 1] * c[4 + i] + y[2 * i] * z[4 + i];
+          y[2 * i] = w;
+        }
+      }
+    }
+    if (kind == 0) {
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.q_out) + ((size_t)t * a.hq + h) * a.D;
+      store8(dst + c0, x);
+      store8(dst + c1, y);
+    } else if (page_ok) {
+      const size_t at = row + (size_t)h * a.c.head_stride;
+      if (FP8) {
+        uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.c.k : a.c.v) + at;
+        const float sc = kind == 1 ? a.k_scale : a.v_scale;
+        store8_e4m3(dst + c0, x, sc);
+        store8_e4m3(dst + c1, y, sc);
+      } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(kind == 1 ? a.c.k : a.c.v) + at;
+        store8(dst + c0, x);
+        store8(dst + c1, y);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
+  if (a.fp8)
+    launch_kernel(kv_append_kernel<true>, dim3(a.b.T), dim3(kAppendThreads), 0, stream, a);
+  else
+    launch_kernel(kv_append_kernel<false>, dim3(a.b.T), dim3(kAppendThreads), 0, stream, a);
+  return cudaGetLastError();
+}
+
+}  // namespace gbmoe

@@ -1,0 +1,216 @@
+"""The decoder-block operators on the host: argument refusals of the C ABI and the binding, and
+the index rules of the paged batch (csrc/paged_checks.h, compiled for the host)."""
+import ctypes
+import itertools
+import os
+import subprocess
+
+import pytest
+import torch
+
+from mixture_experts_layer_05_gb300 import binding
+from mixture_experts_layer_05_gb300 import build as build_mod
+
+P = ctypes.c_void_p
+OK, BAD, UNSUP, WS = (binding.OK, binding.ERR_INVALID_ARG, binding.ERR_UNSUPPORTED,
+                      binding.ERR_WORKSPACE)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_mod.build()
+    return binding.load()
+
+
+def _norm(lib, T=4, H=256, x=256, xs=None, res=0, rs=0, w=256, eps=1e-6, y=256, ro=0, q=0, s=0):
+    a = binding.RmsNormArgs(x or None, H if xs is None else xs, res or None, rs, w or None, eps,
+                            y or None, ro or None, q or None, s or None)
+    return lib.moe_rms_norm(T, H, ctypes.byref(a), None)
+
+
+def test_rms_norm_refusals(lib):
+    assert lib.moe_rms_norm(0, 256, None, None) == OK                  # empty batch
+    assert lib.moe_rms_norm(4, 256, None, None) == BAD
+    for kw in (dict(T=-1), dict(H=0), dict(x=0), dict(w=0), dict(y=0), dict(q=256), dict(s=256),
+               dict(ro=256), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")),
+               dict(x=264), dict(w=264), dict(y=264), dict(q=264, s=256), dict(q=256, s=258),
+               dict(xs=128), dict(xs=260), dict(res=256, rs=128), dict(res=256, rs=260),
+               dict(res=264, rs=256), dict(res=256, rs=256, ro=264)):
+        assert _norm(lib, **kw) == BAD, kw
+    for kw in (dict(H=100), dict(H=264, q=256, s=256), dict(H=32776)):
+        assert _norm(lib, **kw) == UNSUP, kw
+
+
+def _cfg(**kw):
+    d = dict(num_q_heads=8, num_kv_heads=2, head_dim=64, page_size=16)
+    d.update(kw)
+    return binding.make_attn_config(**d)
+
+
+def _kv(**kw):
+    d = dict(k_cache=256, v_cache=256, page_stride=2048, token_stride=128, head_stride=64,
+             num_pages=4, num_seqs=2, block_table_stride=3, block_table=256, cu_seqlens_q=256,
+             kv_lens=256)
+    d.update(kw)
+    return binding.PagedKv(**d)
+
+
+BAD_CONFIGS = (dict(num_q_heads=0), dict(num_kv_heads=0), dict(num_q_heads=9),
+               dict(num_q_heads=2048), dict(head_dim=0, softmax_scale=1.0), dict(page_size=0),
+               dict(window=-1), dict(cache_dtype=7), dict(softmax_scale=0.0),
+               dict(softmax_scale=float("nan")), dict(softmax_scale=float("inf")),
+               dict(k_scale=0.5), dict(v_scale=2.0), dict(cache_dtype="fp8", k_scale=0.0),
+               dict(cache_dtype="fp8", v_scale=float("inf")))
+UNSUP_CONFIGS = (dict(head_dim=96), dict(head_dim=256), dict(page_size=4), dict(page_size=24),
+                 dict(page_size=2048))
+BAD_KV = (dict(k_cache=None), dict(v_cache=None), dict(block_table=None), dict(cu_seqlens_q=None),
+          dict(kv_lens=None), dict(num_pages=0), dict(num_seqs=0), dict(block_table_stride=0),
+          dict(page_stride=0), dict(token_stride=-64), dict(head_stride=0), dict(k_cache=264),
+          dict(v_cache=264), dict(page_stride=2052), dict(token_stride=132), dict(head_stride=68),
+          dict(block_table=258), dict(cu_seqlens_q=258), dict(kv_lens=258))
+
+
+def _attn(lib, cfg=None, T=4, kv=None, q=256, qs=512, out=256, lse=0, ws=256, nbytes=1 << 40):
+    cfg, kv = cfg or _cfg(), kv or _kv()
+    return lib.moe_paged_attention(ctypes.byref(cfg), T, ctypes.byref(kv), P(q or None), qs,
+                                   P(out or None), P(lse or None), P(ws or None), nbytes, None)
+
+
+def test_paged_attention_refusals(lib):
+    assert lib.moe_paged_attention(None, 4, None, None, 0, None, None, None, 0, None) == BAD
+    assert _attn(lib, T=0) == OK
+    for kw in BAD_CONFIGS:
+        assert _attn(lib, cfg=_cfg(**kw)) == BAD, kw
+        assert lib.moe_paged_attention_workspace_size(ctypes.byref(_cfg(**kw))) == 0, kw
+    for kw in UNSUP_CONFIGS:
+        assert _attn(lib, cfg=_cfg(**kw)) == UNSUP, kw
+        assert lib.moe_paged_attention_workspace_size(ctypes.byref(_cfg(**kw))) == 0, kw
+    for kw in BAD_KV:
+        assert _attn(lib, kv=_kv(**kw)) == BAD, kw
+    assert _attn(lib, kv=_kv(num_seqs=8193)) == UNSUP
+    for kw in (dict(T=-1), dict(q=0), dict(out=0), dict(qs=504), dict(qs=516), dict(q=264),
+               dict(out=264), dict(lse=258)):
+        assert _attn(lib, **kw) == BAD, kw
+    need = lib.moe_paged_attention_workspace_size(ctypes.byref(_cfg()))
+    assert need >= 256
+    for kw in (dict(ws=0), dict(ws=128), dict(nbytes=need - 1)):
+        assert _attn(lib, **kw) == WS, kw
+
+
+def _append(lib, cfg=None, T=4, kv=None, **kw):
+    cfg, kv = cfg or _cfg(), kv or _kv()
+    d = dict(q=256, k=256, v=256, q_stride=768, k_stride=768, v_stride=768, cos_sin=256,
+             max_position=64, rotary_dim=64, interleaved=0, q_out=256, workspace=256)
+    d.update(kw)
+    return lib.moe_kv_append(ctypes.byref(cfg), T, ctypes.byref(kv),
+                             ctypes.byref(binding.KvAppendArgs(**d)), None)
+
+
+def test_kv_append_refusals(lib):
+    assert lib.moe_kv_append(None, 4, None, None, None) == BAD
+    assert _append(lib, T=0) == OK
+    for kw in BAD_CONFIGS:
+        assert _append(lib, cfg=_cfg(**kw)) == BAD, kw
+    for kw in UNSUP_CONFIGS:
+        assert _append(lib, cfg=_cfg(**kw)) == UNSUP, kw
+    for kw in BAD_KV:
+        assert _append(lib, kv=_kv(**kw)) == BAD, kw
+    for kw in (dict(T=-1), dict(q=None), dict(k=None), dict(v=None), dict(q_out=None),
+               dict(q_stride=504), dict(q_stride=516), dict(k_stride=120), dict(k_stride=132),
+               dict(v_stride=120), dict(v_stride=132), dict(q=264), dict(k=264), dict(v=264),
+               dict(q_out=264), dict(cos_sin=264), dict(workspace=128), dict(rotary_dim=80),
+               dict(rotary_dim=8), dict(rotary_dim=-16), dict(rotary_dim=0), dict(cos_sin=None),
+               dict(max_position=0)):
+        assert _append(lib, **kw) == BAD, kw
+
+
+def test_binding_refuses_host_tensors(lib):
+    x = torch.zeros(2, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        binding.moe_rms_norm(x, x[0])
+    with pytest.raises(ValueError):
+        binding.moe_rms_norm(x, x[0], out="int8")
+    with pytest.raises(binding.GbmoeError):
+        binding.PagedAttention(_cfg(head_dim=96), device="cpu")
+    op = binding.PagedAttention(_cfg(), device="cpu")
+    c = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        op(torch.zeros(2, 8, 64, dtype=torch.bfloat16), c, c, i[None], i[:2], i[:1])
+
+
+CHECKS = r"""
+#include <cstdio>
+#include "paged_checks.h"
+using namespace gbmoe;
+int main() {
+  int q0, q1, L, T, n, i, causal, window, id, pages;
+  long long cap;
+  char kind;
+  while (scanf(" %c", &kind) == 1) {
+    bool bad = false;
+    if (kind == 's') {
+      if (scanf("%d %d %d %d %lld", &q0, &q1, &L, &T, &cap) != 5) return 1;
+      const SeqInfo r = checked_seq(q0, q1, L, T, cap, &bad);
+      printf("%d %d %d %d\n", r.q0, r.n, r.L, bad);
+    } else if (kind == 'k') {
+      if (scanf("%d %d %d %d %d", &L, &n, &i, &causal, &window) != 5) return 1;
+      const KeyRange r = key_range(SeqInfo{0, n, L}, i, causal != 0, window);
+      printf("%d %d\n", r.lo, r.hi);
+    } else {
+      if (scanf("%d %d", &id, &pages) != 2) return 1;
+      printf("%d", checked_page(id, pages, &bad));
+      printf(" %d\n", bad);
+    }
+  }
+  return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def checks(tmp_path_factory):
+    d = tmp_path_factory.mktemp("checks")
+    (d / "checks.cpp").write_text(CHECKS)
+    subprocess.run(["g++", "-std=c++17", "-I", build_mod.CSRC, str(d / "checks.cpp"), "-o",
+                    str(d / "checks")], check=True)
+
+    def ask(lines):
+        out = subprocess.run([str(d / "checks")], input="\n".join(lines), text=True,
+                             capture_output=True, check=True).stdout
+        return [tuple(int(x) for x in l.split()) for l in out.splitlines()]
+    return ask
+
+
+def test_sequences_stay_in_their_buffers(checks):
+    """Whatever the arrays hold, tokens lie in the batch and keys in the block table."""
+    vals = (-(2 ** 31), -1, 0, 1, 5, 7, 8, 2 ** 30, 2 ** 31 - 1)
+    asks = [(q0, q1, L, 7, cap) for q0, q1, L in itertools.product(vals, vals, vals)
+            for cap in (8, 2 ** 30, 2 ** 41)]
+    got = checks(["s " + " ".join(map(str, a)) for a in asks])
+    for (q0, q1, L, T, cap), (r0, n, rL, bad) in zip(asks, got):
+        assert 0 <= r0 and 0 <= n and r0 + n <= T
+        assert 0 <= rL <= min(cap, 2 ** 30)
+        good = 0 <= q0 <= q1 <= T and 0 <= L <= min(cap, 2 ** 30)
+        assert bad == (not good)
+        if good:
+            assert (r0, n, rL) == (q0, q1 - q0, L)
+
+
+def test_key_ranges_match_the_definition(checks):
+    asks = [(L, n, i, causal, w) for L in (0, 1, 2, 5, 9) for n in (1, 3, 9) for i in range(n)
+            for causal in (0, 1) for w in (0, 1, 2, 7)]
+    got = checks(["k " + " ".join(map(str, a)) for a in asks])
+    for (L, n, i, causal, w), (lo, hi) in zip(asks, got):
+        pos = L - n + i
+        want = [j for j in range(L) if (not causal or j <= pos) and (not w or j > pos - w)]
+        assert list(range(lo, hi)) == want
+
+
+def test_pages_stay_in_the_cache(checks):
+    asks = [(i, p) for i in (-(2 ** 31), -1, 0, 3, 4, 5, 2 ** 31 - 1) for p in (1, 4, 2 ** 31 - 1)]
+    got = checks([f"p {i} {p}" for i, p in asks])
+    for (i, p), (page, bad) in zip(asks, got):
+        assert 0 <= page < p and bad == (not 0 <= i < p)
+        if not bad:
+            assert page == i

@@ -1,0 +1,332 @@
+"""The decoder-block operators on the GPU against their 64-bit references: RMS norm with its
+8-bit output, the cache append with rotary embedding, and paged attention. Every tolerance
+counts the roundings of the operator (tests/block_cases.py)."""
+import math
+
+import pytest
+import torch
+
+from mixture_experts_layer_05_gb300 import binding
+from tests.block_cases import (BF16, E4M3_SUB, FP8_HALF, FP32, Paged, attention_reference,
+                               norm_reference, rotate_reference)
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _rand(g, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g) * std).to(torch.bfloat16)
+
+
+# ------------------------------------------------------------------------------ norm
+@pytest.mark.parametrize("T,H", [(1, 8), (1, 128), (3, 136), (2, 256), (5, 384), (7, 1000),
+                                 (4, 5120), (33, 7168), (300, 4096), (2, 8320), (3, 32768)])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("out", ["bf16", "fp8", "both"])
+def test_rms_norm(cuda_lib, T, H, residual, out):
+    if out != "bf16" and H % 128:
+        pytest.skip("8-bit groups are 128 columns")
+    g = torch.Generator().manual_seed(T * 1000 + H)
+    x, w = _rand(g, T, H), (1 + _rand(g, H, std=0.2)).to(torch.bfloat16)
+    r = _rand(g, T, H, std=3.0) if residual else None
+    if T > 1:
+        x[1] = 0                                   # a row of zeros
+        if residual:
+            r[1] = 0
+    h, y = norm_reference(x, r, w, 1e-6)
+    got = binding.moe_rms_norm(x.to(DEV), w.to(DEV), 1e-6, out=out,
+                               residual=None if r is None else r.to(DEV))
+    gy, gr, gq, gs = (None if t is None else t.cpu() for t in got)
+    # fp32 sum of H squares: at most 32 terms a thread in sequence, two trees of five, each
+    # off by FP32; half of it reaches y; the root, the division and two products add FP32 each
+    d = (0.5 * (32 + 10 + 2) + 6) * FP32
+    assert (gy is None) == (out == "fp8") and (gr is None) == (not residual)
+    if gy is not None:
+        assert ((gy.double() - y).abs() <= (BF16 * (1 + d) + d) * y.abs()).all()
+    if gr is not None:
+        assert ((gr.double() - h).abs() <= (BF16 + 2 * FP32) * h.abs()).all()
+    if gq is not None:
+        s = (y.view(T, -1, 128).abs().amax(-1).clamp_min(1e-10) / 448).t()
+        assert ((gs.double() - s).abs() <= (d + 2 * FP32) * s).all()
+        deq = gq.view(torch.float8_e4m3fn).double() * gs.double().t().repeat_interleave(128, 1)
+        step = s.t().repeat_interleave(128, 1)
+        assert ((deq - y).abs() <= (FP8_HALF + 4 * d) * y.abs() + E4M3_SUB * (1 + d) * step).all()
+
+
+def test_rms_norm_strided_rows_and_aliases(cuda_lib):
+    g = torch.Generator().manual_seed(5)
+    big, res = _rand(g, 9, 1024).to(DEV), _rand(g, 9, 1536).to(DEV)
+    w = _rand(g, 512).to(DEV)
+    x, r = big[:, 256:768], res[:, 1024:]
+    a = binding.moe_rms_norm(x, w, residual=r, out="both")
+    b = binding.moe_rms_norm(x.contiguous(), w, residual=r.contiguous(), out="both")
+    for u, v in zip(a, b):
+        assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+    rc = r.contiguous()
+    y, ro, _, _ = binding.moe_rms_norm(x, w, residual=rc, residual_out=rc)     # in place
+    assert ro is rc and torch.equal(rc, a[1]) and torch.equal(y, a[0])
+
+
+def test_rms_norm_non_finite_rows(cuda_lib):
+    x = torch.ones(4, 256, dtype=torch.bfloat16)
+    x[1, 7], x[2, 200], x[3, 3] = math.nan, math.inf, -math.inf
+    y, _, q, _ = binding.moe_rms_norm(x.to(DEV), x[0].to(DEV), out="both")
+    y, q = y.cpu().float(), q.cpu().float()
+    assert torch.isfinite(y[0]).all() and torch.isfinite(q[0]).all()
+    assert y[1].isnan().all() and q[1].isnan().all()
+    for row, c in ((2, 200), (3, 3)):              # inf * (1 / sqrt(inf)) = NaN, 1 * 0 = 0
+        assert y[row, c].isnan() and q[row, c].isnan()
+        assert (y[row, :c] == 0).all() and (y[row, c + 1:] == 0).all()
+
+
+def test_norm_output_feeds_the_fp8_layer_format(cuda_lib):
+    """q and scale have the layout of moe_quant_fp8_per_token_group: on rows whose y is exact in
+    bf16 (powers of two), both give the same bytes."""
+    g = torch.Generator().manual_seed(3)
+    x = torch.where(torch.rand(6, 512, generator=g) < 0.5, 1.0, -1.0).to(torch.bfloat16)
+    w = (2.0 ** torch.randint(-6, 6, (512,), generator=g)).to(torch.bfloat16).to(DEV)
+    y, _, q, s = binding.moe_rms_norm(x.to(DEV), w, 0.0, out="both")
+    q2, s2 = binding.moe_quant_fp8_per_token_group(y)
+    assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+
+
+# ------------------------------------------------------------------------------ append
+def _tables(max_pos, R):
+    inv = 10000.0 ** (-torch.arange(0, R, 2, dtype=torch.float64) / R)
+    ang = torch.arange(max_pos, dtype=torch.float64)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], 1).float()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("hq,hkv,d,page,R,inter", [
+    (8, 2, 64, 16, 64, False), (8, 2, 64, 8, 32, True), (7, 1, 128, 64, 128, False),
+    (4, 4, 128, 32, 16, True), (32, 8, 128, 1024, 0, False)])
+def test_kv_append(cuda_lib, cache, hq, hkv, d, page, R, inter):
+    seqs = [(1, 1), (1, 40), (0, 9), (17, 17), (5, 130), (33, 64)]
+    ks, vs = (0.03, 0.01) if cache == "fp8" else (1.0, 1.0)
+    p = Paged(seqs, hkv, d, page, cache, seed=hq + d, k_scale=ks, v_scale=vs)
+    qkv = _rand(p.gen, p.T, hq + 2 * hkv, d)
+    cs = _tables(130, R) if R else None
+    cfg = binding.make_attn_config(hq, hkv, d, page, cache_dtype=cache, k_scale=ks, v_scale=vs)
+    op = binding.PagedAttention(cfg)
+    kc, vc = p.shaped(p.k).to(DEV), p.shaped(p.v).to(DEV)
+    x = qkv.to(DEV)
+    q = op.append(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], kc, vc, p.table.to(DEV),
+                  p.cu.to(DEV), p.kv_lens.to(DEV), cos_sin=None if cs is None else cs.to(DEV),
+                  interleaved=inter)
+    assert op.device_status() == binding.OK
+    got = {"k": kc.cpu().view(p.k.shape), "v": vc.cpu().view(p.v.shape)}
+    written = torch.zeros(p.num_pages * page, dtype=torch.bool)
+    for s, (n, L) in enumerate(seqs):
+        t = slice(int(p.cu[s]), int(p.cu[s + 1]))
+        rows = p.rows[s][L - n:]
+        written[rows] = True
+        want = {"q": qkv[t, :hq], "k": qkv[t, hq:hq + hkv], "v": qkv[t, hq + hkv:]}
+        for name, raw in want.items():
+            if R and name != "v":
+                ref, size = rotate_reference(raw, cs[L - n:L, :R // 2], cs[L - n:L, R // 2:], inter)
+            else:
+                ref, size = raw.double(), torch.zeros(raw.shape, dtype=torch.float64)
+            fp = 2 * FP32 * size                   # two products and a sum in fp32
+            if name == "q" or cache == "bf16":
+                have = q.cpu()[t].double() if name == "q" else got[name][rows].double()
+                assert ((have - ref).abs() <= BF16 * ref.abs() + 2 * fp).all()
+            else:
+                sc = ks if name == "k" else vs
+                have = got[name][rows].view(torch.float8_e4m3fn).double() * sc
+                top = ref.clamp(-448 * sc, 448 * sc)
+                assert ((have - top).abs() <= (FP8_HALF + 2 * FP32) * top.abs()
+                        + E4M3_SUB * sc + 2 * fp).all()
+    for name, before in (("k", p.k), ("v", p.v)):  # nothing else changed
+        assert torch.equal(got[name][~written].view(torch.uint8), before[~written].view(torch.uint8))
+
+
+def test_kv_append_saturates_and_works_in_place(cuda_lib):
+    p = Paged([(4, 4)], 1, 64, 8, "fp8", k_scale=1.0, v_scale=1.0)
+    q = torch.full((4, 2, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    k = torch.full((4, 1, 64), 1e4, dtype=torch.bfloat16, device=DEV)
+    op = binding.PagedAttention(binding.make_attn_config(2, 1, 64, 8, cache_dtype="fp8"))
+    kc, vc = p.shaped(p.k).to(DEV), p.shaped(p.v).to(DEV)
+    cs = _tables(4, 64).to(DEV)
+    want = op.append(q, k, -k, kc, vc, p.table.to(DEV), p.cu.to(DEV), p.kv_lens.to(DEV),
+                     cos_sin=cs)
+    got = op.append(q, k, -k, kc, vc, p.table.to(DEV), p.cu.to(DEV), p.kv_lens.to(DEV),
+                    cos_sin=cs, q_out=q)
+    assert got is q and torch.equal(got, want)
+    v = vc.cpu().view(p.v.shape)[p.rows[0]].view(torch.float8_e4m3fn).float()
+    assert (v == -448).all()
+
+
+# ------------------------------------------------------------------------------ attention
+def _run(p, q, hq, causal=True, window=0, lse=True, layout="rows", stream=None, scale=None):
+    cfg = binding.make_attn_config(hq, p.hkv, p.d, p.page, cache_dtype=p.cache, causal=causal,
+                                   window=window, k_scale=p.k_scale, v_scale=p.v_scale,
+                                   softmax_scale=scale)
+    op = binding.PagedAttention(cfg)
+    k, v = p.shaped(p.k).to(DEV), p.shaped(p.v).to(DEV)
+    if layout == "heads":                          # [pages, heads, rows, d] in memory
+        k, v = (c.transpose(1, 2).contiguous().transpose(1, 2) for c in (k, v))
+    elif layout == "pair":                         # k and v pages next to each other
+        both = torch.stack([k, v], 1)
+        k, v = both[:, 0], both[:, 1]
+    r = op(q, k, v, p.table.to(DEV), p.cu.to(DEV), p.kv_lens.to(DEV), lse=lse, stream=stream)
+    torch.cuda.synchronize()
+    assert op.device_status() == binding.OK
+    return r
+
+
+def _check(p, q, hq, causal=True, window=0, layout="rows", scale=None):
+    out, lse = _run(p, q.to(DEV), hq, causal, window, layout=layout, scale=scale)
+    ref, rl, bound, lb = attention_reference(p, q, causal, window, scale)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    empty = rl == -math.inf
+    assert (lse[empty] == -math.inf).all() and (out[empty] == 0).all()
+    assert torch.isfinite(out).all()
+    assert ((lse - rl).abs()[~empty] <= lb[~empty]).all()
+    worst = ((out - ref).abs() / bound.clamp_min(1e-30)).max()
+    assert worst <= 1.0, float(worst)
+
+
+STEP = [(1, 1), (1, 2), (1, 15), (1, 16), (1, 17), (1, 127), (1, 128), (1, 129), (1, 700),
+        (0, 33), (1, 0), (1, 1025)]
+MIXED = [(1, 1), (3, 3), (1, 300), (17, 17), (0, 5), (130, 130), (5, 4), (64, 400), (2, 0),
+         (257, 300), (1, 128), (31, 129)]
+HEADS = [(8, 2, 64), (4, 4, 128), (7, 1, 128), (32, 8, 128), (20, 1, 64)]
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+@pytest.mark.parametrize("cache,page", [("bf16", 16), ("bf16", 128), ("fp8", 8), ("fp8", 64)])
+@pytest.mark.parametrize("seqs", [STEP, MIXED], ids=["step", "mixed"])
+def test_paged_attention(cuda_lib, hq, hkv, d, cache, page, seqs):
+    ks, vs = (0.02, 0.5) if cache == "fp8" else (1.0, 1.0)
+    p = Paged(seqs, hkv, d, page, cache, seed=hq * d + page, k_scale=ks, v_scale=vs)
+    _check(p, _rand(p.gen, p.T, hq, d, std=1.5), hq)
+
+
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 1), (True, 16), (True, 129),
+                                           (True, 1000), (False, 50)])
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("seqs", [STEP, MIXED], ids=["step", "mixed"])
+def test_paged_attention_masks(cuda_lib, causal, window, cache, seqs):
+    p = Paged(seqs, 2, 64, 16, cache, seed=window)
+    _check(p, _rand(p.gen, p.T, 8, 64), 8, causal, window)
+
+
+@pytest.mark.parametrize("layout", ["rows", "heads", "pair"])
+@pytest.mark.parametrize("seqs", [STEP, MIXED], ids=["step", "mixed"])
+def test_paged_attention_layouts(cuda_lib, layout, seqs):
+    p = Paged(seqs, 2, 128, 32, seed=9)
+    qkv = _rand(p.gen, p.T, 6 + 2 + 2, 128).to(DEV)
+    q = qkv[:, 2:8]                                # rows strided
+    out, lse = _run(p, q, 6, layout=layout)
+    want, wl = _run(p, q.contiguous(), 6)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    _check(p, q.cpu(), 6, layout=layout)
+
+
+def test_paged_attention_peaked_and_growing_scores(cuda_lib):
+    """Scores whose maximum moves far from tile to tile, and one key that takes all weight."""
+    p = Paged([(1, 900), (40, 700), (200, 513)], 1, 128, 16, seed=4)
+    for r in p.rows:                               # k grows along the sequence
+        x = p.k[r].float() * torch.linspace(0.05, 6.0, len(r))[:, None, None]
+        p.k[r] = x.to(torch.bfloat16)
+    q = _rand(p.gen, p.T, 8, 128, std=2.0)
+    _check(p, q, 8)
+    q[:, 3] = 0                                    # equal weights
+    _check(p, q, 8, scale=0.7)
+
+
+def test_paged_attention_long_context(cuda_lib):
+    p = Paged([(1, 40001), (3, 9000), (1, 17)], 2, 128, 64, seed=8)
+    _check(p, _rand(p.gen, p.T, 8, 128), 8)
+    p = Paged([(70, 20011)], 1, 64, 16, "fp8", seed=8, k_scale=0.02, v_scale=0.02)
+    _check(p, _rand(p.gen, p.T, 4, 64), 4)
+
+
+def test_paged_attention_offsets_past_32_bits(cuda_lib):
+    """Pages beyond 2^31 elements of the cache."""
+    p = Paged([(1, 200), (150, 333)], 8, 128, 128, seed=2)
+    per = p.page * p.hkv * p.d
+    far = 2 ** 31 // per + 1000
+    big = [torch.empty(far + p.num_pages, p.page, p.hkv, p.d, dtype=torch.bfloat16, device=DEV)
+           for _ in range(2)]
+    for b, c in zip(big, (p.k, p.v)):
+        b[far:] = p.shaped(c).to(DEV)
+    q = _rand(p.gen, p.T, 8, 128)
+    cfg = binding.make_attn_config(8, 8, 128, 128)
+    op = binding.PagedAttention(cfg)
+    table = torch.where(p.table < p.num_pages, p.table + far, p.table).to(DEV)
+    out = op(q.to(DEV), *big, table, p.cu.to(DEV), p.kv_lens.to(DEV))
+    want, _ = _run(p, q.to(DEV), 8)
+    assert op.device_status() == binding.OK and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("seqs", [STEP, MIXED], ids=["step", "mixed"])
+def test_paged_attention_repeats_and_streams(cuda_lib, seqs):
+    """The same bits every time, on another stream too, and from a captured graph that replays
+    with changed lengths."""
+    p = Paged(seqs, 2, 128, 16, seed=6)
+    q = _rand(p.gen, p.T, 8, 128).to(DEV)
+    want, wl = _run(p, q, 8)
+    for _ in range(3):
+        out, lse = _run(p, q, 8)
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, _ = _run(p, q, 8, stream=s)
+    assert torch.equal(out, want)
+    op = binding.PagedAttention(binding.make_attn_config(8, 2, 128, 16))
+    args = (p.shaped(p.k).to(DEV), p.shaped(p.v).to(DEV), p.table.to(DEV), p.cu.to(DEV))
+    lens = p.kv_lens.to(DEV)
+    out = torch.empty_like(want)
+    with torch.cuda.stream(s):
+        op(q, *args, lens, out=out, stream=s)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            op(q, *args, lens, out=out)
+        out.zero_()
+        g.replay()
+        s.synchronize()
+        assert torch.equal(out, want)
+        short = [(n, max(n, L - 3) if L > n else L) for n, L in seqs]
+        lens.copy_(torch.tensor([L for _, L in short], dtype=torch.int32))
+        g.replay()
+        s.synchronize()
+    p.seqs, p.kv_lens = short, lens.cpu()
+    p.rows = [r[:L] for r, (_, L) in zip(p.rows, short)]
+    again, _ = _run(p, q, 8)
+    assert torch.equal(out, again)
+
+
+def test_bad_pages_and_lengths_are_reported(cuda_lib):
+    """Page ids, lengths and offsets outside their buffers: the status word says so, the other
+    sequences keep their results."""
+    seqs = [(1, 40), (20, 50), (1, 33), (2, 20)]
+    p = Paged(seqs, 1, 64, 16, seed=1)
+    q = _rand(p.gen, p.T, 4, 64).to(DEV)
+    want, _ = _run(p, q, 4)
+    op = binding.PagedAttention(binding.make_attn_config(4, 1, 64, 16))
+    k, v = p.shaped(p.k).to(DEV), p.shaped(p.v).to(DEV)
+    for what in ("page", "length", "negative"):
+        table, lens = p.table.clone(), p.kv_lens.clone()
+        if what == "page":
+            table[1, 2], table[2, 0] = p.num_pages, -5
+        elif what == "length":
+            lens[1] = 16 * table.shape[1] + 1
+            table[1] = table[0, 0]
+        else:
+            lens[1] = -4
+        out = op(q, k, v, table.to(DEV), p.cu.to(DEV), lens.to(DEV))
+        assert op.device_status() == binding.ERR_DEVICE_CHECK, what
+        assert op.device_status() == binding.OK
+        assert torch.equal(out[:1], want[:1])
+        assert torch.equal(out[-2:], want[-2:])
+    x = torch.zeros(p.T, 1, 64, dtype=torch.bfloat16, device=DEV)
+    table = p.table.clone()
+    table[3, 1] = p.num_pages
+    op.append(q, x, x, k, v, table.to(DEV), p.cu.to(DEV), p.kv_lens.to(DEV))
+    assert op.device_status() == binding.ERR_DEVICE_CHECK
+    op.append(q, x, x, k, v, p.table.to(DEV), p.cu.to(DEV), p.kv_lens.to(DEV),
+              cos_sin=_tables(10, 64).to(DEV))     # positions past the angle table
+    assert op.device_status() == binding.ERR_DEVICE_CHECK
