@@ -18,7 +18,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgbmoe.so")
 SOURCES = ["api.cu", "topk.cu", "align.cu", "gemm.cu", "gemm_tn.cu", "gemm_fp8.cu", "fp8.cu", "gemm_fp4.cu", "fp4.cu",
            "combine.cu",
-           "align_static.cu", "block_api.cu", "norm.cu", "kvappend.cu", "attn.cu"]
+           "align_static.cu", "block_api.cu", "norm.cu", "kvappend.cu", "attn.cu",
+           "attn_decode.cu", "attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,195 @@
+// Device side of paged attention's work split (attn_plan.h): every CTA finds its range of the
+// line of tiles, walks its pieces, and leaves the pieces of cut units in the workspace; a
+// second kernel joins those. Shared by the two attention kernels.
+#pragma once
+
+#include "attn_plan.h"
+#include "block.cuh"
+#include "tc.cuh"
+
+namespace gbmoe {
+
+constexpr int kAttnMaxCtas = 160;  // workspace bound; the kernels run one CTA per SM
+constexpr int kAttnTK = 128;       // keys per tile
+constexpr int kAttnMaxBR = 256;    // rows per unit of the widest kernel
+
+// What a CTA's cut units look like, for the joining kernel: the unit that it begins and leaves
+// to the next CTA (starts), whether its first piece is of a unit begun before it (mid), and
+// whether that unit ends there.
+struct AttnRec {
+  int starts, mid, ends;
+  int s, head, rb, pad[2];
+};
+
+// The workspace after the status region: records, then per CTA two piece slots (2c: a unit begun
+// by an earlier CTA; 2c + 1: a unit left to the next) of (m, l) pairs and fp32 output rows.
+struct AttnScratch {
+  AttnRec* rec;
+  float2* ml;   // [slot][BR]
+  float* o;     // [slot][BR][D]
+};
+__host__ __device__ inline AttnScratch attn_scratch(void* base, int BR) {
+  AttnScratch s;
+  char* p = static_cast<char*>(base);
+  s.rec = reinterpret_cast<AttnRec*>(p);
+  p += kAttnMaxCtas * sizeof(AttnRec);
+  s.ml = reinterpret_cast<float2*>(p);
+  p += (size_t)kAttnMaxCtas * 2 * BR * sizeof(float2);
+  s.o = reinterpret_cast<float*>(p);
+  return s;
+}
+
+namespace {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// This CTA's cursor; every thread of the block calls it. line: shared memory for S + 1 prefix
+// sums, wsum: 32 more.
+__device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnShape& sh,
+                                                long long* line, long long* wsum) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (b.S + nt - 1) / nt;
+  const int s0 = min(tid * per, b.S), s1 = min(s0 + per, b.S);
+  long long sum = 0;
+  for (int s = s0; s < s1; ++s) {
+    sum += seq_tiles(sh, seq_info(b, s)) * sh.hkv;
+    line[s + 1] = sum;
+  }
+  long long inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  if (tid == 0) line[0] = 0;
+  __syncthreads();
+  long long base = inc - sum;
+  for (int w = 0; w < warp; ++w) base += wsum[w];
+  for (int s = s0; s < s1; ++s) line[s + 1] += base;
+  __syncthreads();
+  const long long W = line[b.S];
+  const long long a = range_at(W, blockIdx.x, gridDim.x);
+  const long long e = range_at(W, blockIdx.x + 1, gridDim.x);
+  AttnCursor c;
+  c.s = c.head = c.rb = c.off = 0;
+  c.left = 0;
+  if (e > a) {
+    int lo = 0, hi = b.S;  // the sequence with line[s] <= a < line[s + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (line[mid] <= a) lo = mid;
+      else hi = mid;
+    }
+    c = cursor_in_seq(sh, seq_info(b, lo), lo, a - line[lo], e - a);
+  }
+  return c;
+}
+
+// The next piece of the cursor's range (c.left > 0); sequences without rows are passed over.
+__device__ __forceinline__ AttnPiece next_piece(const PagedBatch& b, const AttnShape& sh,
+                                                AttnCursor& c) {
+  SeqInfo q = seq_info(b, c.s);
+  while (q.n == 0 && c.s + 1 < b.S) q = seq_info(b, ++c.s);
+  return take_piece(sh, q, c);
+}
+
+// 4-D tile load (column, row of the page, head, page).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Box of a cache tile: up to 128 columns' bytes x box rows of one page and head.
+bool make_cache_map(CUtensorMap* m, const void* ptr, const AttnArgs& a) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const int es = a.fp8 ? 1 : 2;
+  const uint64_t ps = 1ull << a.b.page_shift;
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, ps, (cuuint64_t)a.hkv, (cuuint64_t)a.b.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)a.c.token_stride * es,
+                                 (cuuint64_t)a.c.head_stride * es,
+                                 (cuuint64_t)a.c.page_stride * es};
+  const cuuint32_t inner = a.D * es < 128 ? a.D : 128 / es;
+  const cuuint32_t box[4] = {inner, (cuuint32_t)(ps < kAttnTK ? ps : kAttnTK), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, a.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             inner * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Joins the pieces of the units that CTA boundaries cut. Block (c, y): rows [16 y, 16 y + 16) of
+// the unit that CTA c began and did not finish. out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i
+// over its pieces in order, M = max m_i: 16 threads a row, so a piece's rows are read whole.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh, int ctas) {
+  constexpr int C = D / 16;  // columns per thread
+  pdl_wait();
+  const AttnScratch sc = attn_scratch(a.scratch, sh.BR);
+  const int c0 = blockIdx.x;
+  const AttnRec rec = sc.rec[c0];
+  if (!rec.starts) return;
+  const SeqInfo q = seq_info(a.b, rec.s);
+  const int row = blockIdx.y * 16 + threadIdx.x / 16, col = threadIdx.x % 16 * C;
+  const int r = rec.rb * sh.BR + row;
+  if (r >= q.n * sh.G) return;
+  float M = sc.ml[(size_t)(2 * c0 + 1) * sh.BR + row].x;
+  int c1 = c0;  // the last CTA with a piece (CTAs between them may have had no tile)
+  while (c1 + 1 < ctas) {
+    const AttnRec r1 = sc.rec[++c1];
+    if (r1.mid) M = fmaxf(M, sc.ml[(size_t)(2 * c1) * sh.BR + row].x);
+    if (r1.ends) break;
+  }
+  const float Ms = M == -INFINITY ? 0.f : M;
+  float l = 0.f, o[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    if (c > c0 && !sc.rec[c].mid) continue;
+    const size_t at = (size_t)(c == c0 ? 2 * c + 1 : 2 * c) * sh.BR + row;
+    const float2 ml = sc.ml[at];
+    const float w = ex2(ml.x - Ms);
+    l = fmaf(w, ml.y, l);
+    const float4* src = reinterpret_cast<const float4*>(sc.o + at * D + col);
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) {
+      const float4 v = src[i];
+      o[4 * i] = fmaf(w, v.x, o[4 * i]);
+      o[4 * i + 1] = fmaf(w, v.y, o[4 * i + 1]);
+      o[4 * i + 2] = fmaf(w, v.z, o[4 * i + 2]);
+      o[4 * i + 3] = fmaf(w, v.w, o[4 * i + 3]);
+    }
+  }
+  const size_t orow = (size_t)(q.q0 + r / sh.G) * a.hq + rec.head * sh.G + r % sh.G;
+  const float inv = l == 0.f ? 0.f : a.v_scale / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + col);
+#pragma unroll
+  for (int i = 0; i < C / 2; ++i) dst[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+  if (a.lse && col == 0)
+    a.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
+cudaError_t launch_attn_join(const AttnArgs& a, const AttnShape& sh, int ctas,
+                             cudaStream_t stream) {
+  const dim3 grid(ctas, sh.BR / 16);
+  if (a.D == 64) launch_kernel(attn_join_kernel<64>, grid, dim3(256), 0, stream, a, sh, ctas);
+  else launch_kernel(attn_join_kernel<128>, grid, dim3(256), 0, stream, a, sh, ctas);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace gbmoe

@@ -1,0 +1,127 @@
+// How paged attention is cut into work, free of CUDA so that it also compiles for the host.
+//
+// The rows of one (sequence, kv head) are its new tokens times the G query heads that share
+// the head, row = token * G + head; a unit is a block of BR of them, which walks the tiles of
+// TK keys that any of its tokens attends (at least one tile, so that rows without keys get
+// their zeros). The tiles of all units, in (sequence, kv head, row block) order, form one line
+// that is cut into equal ranges, one per CTA: however ragged the lengths are, every CTA reads
+// the same number of tiles. A unit that a cut crosses is computed in pieces, each leaving its
+// running maximum, sum and unnormalised output in the workspace, joined in order afterwards.
+#pragma once
+
+#include "paged_checks.h"
+
+namespace gbmoe {
+
+struct AttnShape {
+  int G, hkv;      // query heads per kv head, kv heads
+  int BR, TK;      // rows per unit, keys per tile
+  bool causal;
+  int window;
+};
+
+struct UnitKeys {
+  int i0, i1;      // first and last token of the unit
+  int lo, hi;      // keys that any of them attends: [lo, hi), hi <= lo when none
+  int t0, tiles;   // tiles t0 .. t0 + tiles - 1, tile t holding the keys [t * TK, (t + 1) * TK)
+};
+
+GBMOE_HD int unit_blocks(const AttnShape& a, int n) { return (n * a.G + a.BR - 1) / a.BR; }
+
+GBMOE_HD UnitKeys unit_keys(const AttnShape& a, const SeqInfo& q, int rb) {
+  UnitKeys u;
+  const int r0 = rb * a.BR;
+  int r1 = r0 + a.BR;
+  if (r1 > q.n * a.G) r1 = q.n * a.G;
+  u.i0 = r0 / a.G;
+  u.i1 = (r1 - 1) / a.G;
+  u.lo = key_range(q, u.i0, a.causal, a.window).lo;
+  u.hi = key_range(q, u.i1, a.causal, a.window).hi;
+  if (u.hi <= u.lo) {
+    u.hi = u.lo = 0;
+    u.t0 = 0;
+    u.tiles = 1;
+  } else {
+    u.t0 = u.lo / a.TK;
+    u.tiles = (u.hi + a.TK - 1) / a.TK - u.t0;
+  }
+  return u;
+}
+
+// Tiles of one kv head of a sequence.
+GBMOE_HD long long seq_tiles(const AttnShape& a, const SeqInfo& q) {
+  const int blocks = unit_blocks(a, q.n);
+  long long t = 0;
+  for (int rb = 0; rb < blocks; ++rb) t += unit_keys(a, q, rb).tiles;
+  return t;
+}
+
+// A place on the line of tiles.
+struct AttnCursor {
+  int s, head, rb, off;    // sequence, kv head, row block, tiles of the unit that are behind
+  long long left;          // tiles of this CTA's range that lie ahead
+};
+
+// The cursor `rem` tiles into sequence s (rem < hkv * tiles of one head).
+GBMOE_HD AttnCursor cursor_in_seq(const AttnShape& a, const SeqInfo& q, int s, long long rem,
+                                  long long left) {
+  AttnCursor c;
+  const long long per = seq_tiles(a, q);
+  c.s = s;
+  c.head = (int)(rem / per);
+  rem -= c.head * per;
+  c.rb = 0;
+  for (;;) {
+    const int t = unit_keys(a, q, c.rb).tiles;
+    if (rem < t) break;
+    rem -= t;
+    ++c.rb;
+  }
+  c.off = (int)rem;
+  c.left = left;
+  return c;
+}
+
+// The part of a unit that one CTA computes.
+struct AttnPiece {
+  int s, head, rb;
+  SeqInfo q;
+  UnitKeys u;
+  int ta, tb;              // tiles [ta, tb) of the unit, counted from u.t0
+  GBMOE_HD bool first() const { return ta == 0; }
+  GBMOE_HD bool last() const { return tb == u.tiles; }
+  GBMOE_HD bool whole() const { return first() && last(); }
+};
+
+// The piece of the sequence q = sequence c.s at the cursor, which moves past it (c.s may then
+// be a sequence without rows: the caller skips those).
+GBMOE_HD AttnPiece take_piece(const AttnShape& a, const SeqInfo& q, AttnCursor& c) {
+  AttnPiece p;
+  p.s = c.s;
+  p.head = c.head;
+  p.rb = c.rb;
+  p.q = q;
+  p.u = unit_keys(a, q, c.rb);
+  p.ta = c.off;
+  p.tb = p.u.tiles - c.off > c.left ? c.off + (int)c.left : p.u.tiles;
+  c.left -= p.tb - p.ta;
+  c.off = p.tb;
+  if (p.tb == p.u.tiles) {
+    c.off = 0;
+    if (++c.rb == unit_blocks(a, q.n)) {
+      c.rb = 0;
+      if (++c.head == a.hkv) {
+        c.head = 0;
+        ++c.s;
+      }
+    }
+  }
+  return p;
+}
+
+// CTA c of g takes the tiles [range_at(c), range_at(c + 1)) of W.
+GBMOE_HD long long range_at(long long W, int c, int g) {
+  return W / g * c + W % g * c / g;
+}
+
+}  // namespace gbmoe

@@ -167,6 +167,7 @@ GBMOE_API gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int
   if (s != GBMOE_OK) return s;
   if (num_tokens < 0 || num_tokens > kMaxRows) return GBMOE_ERR_INVALID_ARG;
   if (num_tokens == 0) return GBMOE_OK;
+  if ((int64_t)num_tokens * cfg->num_q_heads > (1 << 30)) return GBMOE_ERR_UNSUPPORTED;
   s = check_paged(*cfg, kv);
   if (s != GBMOE_OK) return s;
   if (!q || !out || q_stride < (int64_t)cfg->num_q_heads * cfg->head_dim || q_stride % 8 ||

@@ -3,6 +3,7 @@ the index rules of the paged batch (csrc/paged_checks.h, compiled for the host).
 import ctypes
 import itertools
 import os
+import random
 import subprocess
 
 import pytest
@@ -88,6 +89,7 @@ def test_paged_attention_refusals(lib):
     for kw in BAD_KV:
         assert _attn(lib, kv=_kv(**kw)) == BAD, kw
     assert _attn(lib, kv=_kv(num_seqs=8193)) == UNSUP
+    assert _attn(lib, cfg=_cfg(num_q_heads=1024), T=1 << 21, qs=65536) == UNSUP
     for kw in (dict(T=-1), dict(q=0), dict(out=0), dict(qs=504), dict(qs=516), dict(q=264),
                dict(out=264), dict(lse=258)):
         assert _attn(lib, **kw) == BAD, kw
@@ -214,3 +216,99 @@ def test_pages_stay_in_the_cache(checks):
         assert 0 <= page < p and bad == (not 0 <= i < p)
         if not bad:
             assert page == i
+
+
+PLAN = r"""
+#include <cstdio>
+#include <vector>
+#include "attn_plan.h"
+using namespace gbmoe;
+int main() {
+  AttnShape a;
+  int causal, g, S;
+  while (scanf("%d %d %d %d %d %d %d %d", &a.G, &a.hkv, &a.BR, &a.TK, &causal, &a.window, &g,
+               &S) == 8) {
+    a.causal = causal != 0;
+    std::vector<SeqInfo> q(S);
+    std::vector<long long> line(S + 1, 0);
+    for (int s = 0, q0 = 0; s < S; ++s) {
+      if (scanf("%d %d", &q[s].n, &q[s].L) != 2) return 1;
+      q[s].q0 = q0;
+      q0 += q[s].n;
+      line[s + 1] = line[s] + seq_tiles(a, q[s]) * a.hkv;
+    }
+    for (int c = 0; c < g; ++c) {
+      const long long at = range_at(line[S], c, g), end = range_at(line[S], c + 1, g);
+      if (end <= at) continue;
+      int s = 0;
+      while (line[s + 1] <= at) ++s;
+      AttnCursor cur = cursor_in_seq(a, q[s], s, at - line[s], end - at);
+      while (cur.left > 0) {
+        while (q[cur.s].n == 0) ++cur.s;
+        const AttnPiece p = take_piece(a, q[cur.s], cur);
+        printf("%d %d %d %d %d %d %d %d ", c, p.s, p.head, p.rb, p.ta, p.tb, p.u.t0, p.u.tiles);
+      }
+    }
+    printf("\n");
+  }
+  return 0;
+}
+"""
+
+
+def test_attention_work_is_cut_whole(tmp_path):
+    """Every tile that a unit's tokens attend is computed once, the pieces of a unit follow each
+    other over neighbouring CTAs, no CTA has more than one tile over its share, and a CTA begins
+    at most one unit that it leaves and ends at most one that it did not begin."""
+    (tmp_path / "plan.cpp").write_text(PLAN)
+    subprocess.run(["g++", "-std=c++17", "-I", build_mod.CSRC, str(tmp_path / "plan.cpp"), "-o",
+                    str(tmp_path / "plan")], check=True)
+    rng = random.Random(7)
+    cases = []
+    for _ in range(300):
+        S = rng.choice([1, 1, 2, 5, 12])
+        seqs = []
+        for _ in range(S):
+            n = rng.choice([0, 1, 1, 2, 17, 64, 130, 300])
+            seqs.append((n, max(0, rng.choice([n, n + 1, n - 2, n + 127, n + 128, n + 5000, 0]))))
+        if not any(n for n, _ in seqs):
+            seqs[0] = (1, 3)
+        cases.append((rng.choice([1, 3, 4, 8]), rng.choice([1, 2, 8]), rng.choice([16, 256]), 128,
+                      int(rng.random() < 0.8), rng.choice([0, 0, 1, 100, 1000]),
+                      rng.choice([1, 7, 148, 152]), S, seqs))
+    text = "\n".join(" ".join(map(str, c[:8])) + " " + " ".join(f"{n} {L}" for n, L in c[8])
+                     for c in cases)
+    out = subprocess.run([str(tmp_path / "plan")], input=text, text=True, capture_output=True,
+                         check=True).stdout.splitlines()
+    assert len(out) == len(cases)
+    for (G, hkv, BR, TK, causal, window, g, S, seqs), line in zip(cases, out):
+        v = [int(x) for x in line.split()]
+        pieces = [tuple(v[i:i + 8]) for i in range(0, len(v), 8)]
+        units = {}
+        for s, (n, L) in enumerate(seqs):
+            for head in range(hkv):
+                for rb in range(-(-n * G // BR)):
+                    toks = range(rb * BR // G, (min(n * G, (rb + 1) * BR) - 1) // G + 1)
+                    keys = set()
+                    for i in (toks[0], toks[-1]):
+                        pos = L - n + i
+                        lo = max(0, pos - window + 1) if window else 0
+                        hi = min(L, pos + 1) if causal else L
+                        keys.add((lo, hi))
+                    lo, hi = min(k[0] for k in keys), max(k[1] for k in keys)
+                    units[s, head, rb] = (lo // TK, -(-hi // TK)) if hi > lo else (0, 1)
+        at, per, order = {}, {}, list(units)
+        total = sum(b - a for a, b in units.values())
+        where = 0
+        for c, s, head, rb, ta, tb, t0, tiles in pieces:
+            u = (s, head, rb)
+            assert units[u] == (t0, t0 + tiles)
+            assert ta == at.get(u, 0) and ta < tb <= tiles
+            at[u] = tb
+            while order[where] != u:               # the line's order
+                where += 1
+            per.setdefault(c, []).append((ta > 0, tb < tiles, tb - ta))
+        assert all(at[u] == b - a for u, (a, b) in units.items())
+        for c, ps in per.items():
+            assert abs(sum(p[2] for p in ps) - total / g) < 1 + 1e-9
+            assert not any(p[0] for p in ps[1:]) and not any(p[1] for p in ps[:-1])
