@@ -90,12 +90,17 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
   return c;
 }
 
-// The next piece of the cursor's range (c.left > 0); sequences without rows are passed over.
-__device__ __forceinline__ AttnPiece next_piece(const PagedBatch& b, const AttnShape& sh,
-                                                AttnCursor& c) {
-  SeqInfo q = seq_info(b, c.s);
-  while (q.n == 0 && c.s + 1 < b.S) q = seq_info(b, ++c.s);
-  return take_piece(sh, q, c);
+// The next piece of the cursor's range, false when none is left; sequences without rows and
+// units of which the range holds only the extra cost are passed over.
+__device__ __forceinline__ bool next_piece(const PagedBatch& b, const AttnShape& sh,
+                                           AttnCursor& c, AttnPiece& p) {
+  while (c.left > 0) {
+    SeqInfo q = seq_info(b, c.s);
+    while (q.n == 0 && c.s + 1 < b.S) q = seq_info(b, ++c.s);
+    p = take_piece(sh, q, c);
+    if (p.ta < p.tb) return true;
+  }
+  return false;
 }
 
 // 4-D tile load (column, row of the page, head, page).

@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     uint32_t slot = 0, phase = 0, issued = 0;
     bool ok = true;
     while (ok && cur.left > 0) {
-      const AttnPiece p = next_piece(a.b, sh, cur);
+      AttnPiece p;
+      if (!next_piece(a.b, sh, cur, p)) break;
       // this lane's box of tile t: whether it holds any key of the unit, and its page
       auto live_at = [&](int t) {
         const int j = (p.u.t0 + t) * kAttnTK + pl * box_rows;
@@ -217,7 +218,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     };
     auto swz = [](uint32_t off) { return off ^ ((off >> 3) & T::kSwz); };
     while (cur.left > 0) {
-      const AttnPiece p = next_piece(a.b, sh, cur);
+      AttnPiece p;
+      if (!next_piece(a.b, sh, cur, p)) break;
       const int rows = min(kDecBR, p.q.n * sh.G - p.rb * kDecBR);
       // this lane's two rows: their query vectors as mma fragments, and their keys
       uint32_t qf[D / 16][4];
@@ -499,6 +501,7 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   sh.hkv = a.hkv;
   sh.BR = kDecBR;
   sh.TK = kAttnTK;
+  sh.extra = 0;
   sh.causal = a.causal;
   sh.window = a.window;
   const int ctas = num_sms() < kAttnMaxCtas ? num_sms() : kAttnMaxCtas;

@@ -16,6 +16,7 @@ namespace gbmoe {
 struct AttnShape {
   int G, hkv;      // query heads per kv head, kv heads
   int BR, TK;      // rows per unit, keys per tile
+  int extra;       // cost of a unit beyond its tiles, in tiles
   bool causal;
   int window;
 };
@@ -48,21 +49,21 @@ GBMOE_HD UnitKeys unit_keys(const AttnShape& a, const SeqInfo& q, int rb) {
   return u;
 }
 
-// Tiles of one kv head of a sequence.
+// Length on the line of one kv head of a sequence.
 GBMOE_HD long long seq_tiles(const AttnShape& a, const SeqInfo& q) {
   const int blocks = unit_blocks(a, q.n);
   long long t = 0;
-  for (int rb = 0; rb < blocks; ++rb) t += unit_keys(a, q, rb).tiles;
+  for (int rb = 0; rb < blocks; ++rb) t += unit_keys(a, q, rb).tiles + a.extra;
   return t;
 }
 
 // A place on the line of tiles.
 struct AttnCursor {
-  int s, head, rb, off;    // sequence, kv head, row block, tiles of the unit that are behind
-  long long left;          // tiles of this CTA's range that lie ahead
+  int s, head, rb, off;    // sequence, kv head, row block, length of the unit that is behind
+  long long left;          // length of this CTA's range that lies ahead
 };
 
-// The cursor `rem` tiles into sequence s (rem < hkv * tiles of one head).
+// The cursor `rem` into sequence s (rem < hkv * the length of one head).
 GBMOE_HD AttnCursor cursor_in_seq(const AttnShape& a, const SeqInfo& q, int s, long long rem,
                                   long long left) {
   AttnCursor c;
@@ -72,7 +73,7 @@ GBMOE_HD AttnCursor cursor_in_seq(const AttnShape& a, const SeqInfo& q, int s, l
   rem -= c.head * per;
   c.rb = 0;
   for (;;) {
-    const int t = unit_keys(a, q, c.rb).tiles;
+    const int t = unit_keys(a, q, c.rb).tiles + a.extra;
     if (rem < t) break;
     rem -= t;
     ++c.rb;
@@ -94,7 +95,8 @@ struct AttnPiece {
 };
 
 // The piece of the sequence q = sequence c.s at the cursor, which moves past it (c.s may then
-// be a sequence without rows: the caller skips those).
+// be a sequence without rows: the caller skips those). ta == tb: the range ends in the unit's
+// extra cost and holds none of its tiles.
 GBMOE_HD AttnPiece take_piece(const AttnShape& a, const SeqInfo& q, AttnCursor& c) {
   AttnPiece p;
   p.s = c.s;
@@ -102,11 +104,13 @@ GBMOE_HD AttnPiece take_piece(const AttnShape& a, const SeqInfo& q, AttnCursor& 
   p.rb = c.rb;
   p.q = q;
   p.u = unit_keys(a, q, c.rb);
-  p.ta = c.off;
-  p.tb = p.u.tiles - c.off > c.left ? c.off + (int)c.left : p.u.tiles;
-  c.left -= p.tb - p.ta;
-  c.off = p.tb;
-  if (p.tb == p.u.tiles) {
+  const int len = p.u.tiles + a.extra;
+  const int end = len - c.off > c.left ? c.off + (int)c.left : len;
+  p.ta = c.off > a.extra ? c.off - a.extra : 0;
+  p.tb = end > a.extra ? end - a.extra : 0;
+  c.left -= end - c.off;
+  c.off = end;
+  if (end == len) {
     c.off = 0;
     if (++c.rb == unit_blocks(a, q.n)) {
       c.rb = 0;
@@ -119,7 +123,7 @@ GBMOE_HD AttnPiece take_piece(const AttnShape& a, const SeqInfo& q, AttnCursor& 
   return p;
 }
 
-// CTA c of g takes the tiles [range_at(c), range_at(c + 1)) of W.
+// CTA c of g takes the range [range_at(c), range_at(c + 1)) of a line of length W.
 GBMOE_HD long long range_at(long long W, int c, int g) {
   return W / g * c + W % g * c / g;
 }

@@ -10,15 +10,18 @@
 //                goes back to tensor memory as 16-bit pairs over S's own columns
 //   O += P V     tcgen05.mma with A = P in tensor memory and V as it lies in the pages (keys
 //                down, columns across: the MN-major operand form), 128 x D fp32
-// m is kept until a row's maximum has grown by more than 2^8 (the weights stay below 256, and
-// their sum in fp32 loses nothing): O is rescaled in tensor memory only then.
+// m is the maximum of the row's first tile and is kept until a tile's maximum lies far above it
+// (kSlack: weights of 2^60 in bf16 and fp32 lose nothing against weights of 1): only then is O
+// rescaled in tensor memory, and no tile waits for its own maximum.
 //
 //   warps 0-3, 4-7   softmax of half 0 / 1; they also bring the unit's Q into shared memory (the
 //                    next piece's while the last product runs) and write the piece's result
-//   warp 8           MMA issue (one thread)
-//   warp 9           tile copies: TMA, one box per page and 128 bytes of the head; page ids one
-//                    tile ahead
-//   warps 10, 11     e4m3 cache only: codes to f16 (exact) into the operand tiles
+//   warp 8           MMA issue (one elected thread)
+//   warp 9           the schedule, as a ring of piece descriptors ahead of the other roles, and
+//                    the tile copies: TMA, one box per page and 128 bytes of the head; page ids
+//                    two tiles ahead, the next piece's Q into L2
+//   warp 10          bf16 cache: zeroes what a V tile holds outside the unit's keys
+//   warps 10, 11     e4m3 cache: codes to f16 (exact) into the operand tiles
 //
 // Tensor memory: S/P of half h at columns 128 h, O of half h at 256 + 128 h. Operand order in
 // the ring: K0, K1, V0, K2, V1, ..., so that the next scores are under way before a tile's
@@ -33,18 +36,21 @@ namespace {
 constexpr int kTcBR = 256;
 constexpr int kTcMmaWarp = 8, kTcCopyWarp = 9, kTcCvtWarp = 10;
 constexpr int kTcCvtWarps = 2;
-constexpr float kTcSlack = 8.f;  // log2 growth of a row's maximum that O tolerates
+constexpr int kTcExtra = 1;      // cost of beginning a unit, in tiles
 
 template <bool FP8, int D>
 struct Tc {
-  static constexpr int kThreads = FP8 ? 32 * (kTcCvtWarp + kTcCvtWarps) : 32 * kTcCvtWarp;
+  static constexpr int kThreads = 32 * (kTcCvtWarp + (FP8 ? kTcCvtWarps : 1));
   static constexpr uint32_t kTile = kAttnTK * D * 2;        // one operand tile (16 bit)
   static constexpr uint32_t kRawTile = kAttnTK * D;         // one tile of codes
   static constexpr int kRaw = FP8 ? 4 : 0;                  // code stages
   static constexpr int kStages = FP8 ? 3 : 5;               // operand stages
   static constexpr uint32_t kQ = 2 * kTile;
+  // log2 of the largest weight before O is rescaled: bf16 has fp32's range, f16 ends at 2^16
+  static constexpr float kSlack = FP8 ? 14.f : 60.f;
   static constexpr uint32_t kRawPitch = D < 128 ? D : 128;  // bytes of a code row
   static constexpr uint32_t kRawSwz = kRawPitch == 128 ? 0x70u : 0x30u;
+  static constexpr int kReaders = 8 + 1 + (FP8 ? kTcCvtWarps : 1);  // warps that read a piece
   static constexpr size_t kSmem = 1024 + kQ + kStages * kTile + kRaw * kRawTile + 1024;
   static_assert(kSmem <= 232448, "shared memory per CTA exceeded");
   static_assert((kAttnMaxSeqs + 1) * 8 <= kQ + kStages * kTile, "the plan lies in Q and the ring");
@@ -119,6 +125,33 @@ __device__ __forceinline__ uint32_t bf16x2_f16(uint32_t w) {
   auto cut = [](float v) { return v > 65504.f ? 65504.f : (v < -65504.f ? -65504.f : v); };
   return pack_f16x2(cut(f.x), cut(f.y));
 }
+__device__ __forceinline__ void stg256(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// Two fp32 values in one 64-bit register, and the packed operations on them.
+__device__ __forceinline__ uint64_t pair_bits(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  return pair_bits(__float_as_uint(x), __float_as_uint(y));
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // Spin (bounded) until a copy in flight has landed, so that the CTA does not exit under it.
 __device__ __noinline__ void land(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
@@ -126,9 +159,33 @@ __device__ __noinline__ void land(uint32_t bar, uint32_t parity) {
     if (globaltimer_ns() - t0 > 10000000ull) return;
 }
 
+// One thread of the converged warp; the compiler knows that there is one, so that operands of
+// the instructions it issues stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 struct TcMaps {
   CUtensorMap k, v;
 };
+
+// A piece as the schedule publishes it.
+struct alignas(16) TcPiece {
+  int nt;              // tiles; 0: no piece is left
+  int j0;              // first key of the first tile
+  int lo, hi;          // keys that any row of the unit attends
+  int in_lo, in_hi;    // keys that every row attends
+  int rows, r0;        // rows of the unit, its first row in the sequence
+  int q0, n, L, head;  // the sequence, the kv head
+  int slot;            // piece slot in the workspace, -1: the whole unit
+  int pad[3];
+};
+static_assert(sizeof(TcPiece) == 64, "read as four 16-byte words");
+constexpr int kTcPieces = 4;
 
 // A ring position.
 struct Ring {
@@ -159,13 +216,17 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
   auto empty = [&](int s) { return bar0 + 8u * (5 + s); };    // ... and read by its MMAs
   auto q_full = [&](int g) { return bar0 + 8u * (10 + g); };
   auto s_full = [&](int g) { return bar0 + 8u * (12 + g); };
-  auto p_full = [&](int g) { return bar0 + 8u * (14 + g); };
+  auto p_full = [&](int g, int h) { return bar0 + 8u * (h ? 32 + g : 14 + g); };  // 64 keys each
   auto pv_done = [&](int g) { return bar0 + 8u * (16 + g); };
   auto raw_full = [&](int s) { return bar0 + 8u * (18 + s); };
   auto raw_empty = [&](int s) { return bar0 + 8u * (22 + s); };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+  auto v_raw = [&](int s) { return bar0 + 8u * (26 + s); };   // stage s: an edge V tile landed
+  auto d_full = [&](int i) { return bar0 + 8u * (34 + i); };  // piece descriptors
+  auto d_empty = [&](int i) { return bar0 + 8u * (38 + i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  long long* wsum = reinterpret_cast<long long*>(bars + 28);  // 32
+  TcPiece* pieces = reinterpret_cast<TcPiece*>(bars + 42);
+  long long* wsum = reinterpret_cast<long long*>(bars + 42 + kTcPieces * 8);  // 32
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = a.b.status;
   pdl_trigger();
@@ -173,6 +234,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     for (int s = 0; s < T::kStages; ++s) {
       mbar_init(full(s), FP8 ? kTcCvtWarps : 1);
       mbar_init(empty(s), 1);
+      mbar_init(v_raw(s), 1);
     }
     for (int s = 0; s < T::kRaw; ++s) {
       mbar_init(raw_full(s), 1);
@@ -181,8 +243,13 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     for (int g = 0; g < 2; ++g) {
       mbar_init(q_full(g), 4);
       mbar_init(s_full(g), 1);
-      mbar_init(p_full(g), 4);
+      mbar_init(p_full(g, 0), 4);
+      mbar_init(p_full(g, 1), 4);
       mbar_init(pv_done(g), 1);
+    }
+    for (int i = 0; i < kTcPieces; ++i) {
+      mbar_init(d_full(i), 1);
+      mbar_init(d_empty(i), T::kReaders);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -203,7 +270,26 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
   auto wait = [&](uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_fast(bar, parity, abort_flag, status)) != 0;
   };
-  auto rows_of = [&](const AttnPiece& p) { return min(kTcBR, p.q.n * sh.G - p.rb * kTcBR); };
+  // the next piece, read by a whole warp (or by one thread for its warp)
+  Ring dq{0, 0};
+  auto read_piece = [&](TcPiece& p) {
+    const int4* src = reinterpret_cast<const int4*>(pieces + dq.slot);
+    const int4 w0 = src[0], w1 = src[1], w2 = src[2], w3 = src[3];
+    p.nt = w0.x; p.j0 = w0.y; p.lo = w0.z; p.hi = w0.w;
+    p.in_lo = w1.x; p.in_hi = w1.y; p.rows = w1.z; p.r0 = w1.w;
+    p.q0 = w2.x; p.n = w2.y; p.L = w2.z; p.head = w2.w;
+    p.slot = w3.x;
+  };
+  auto get_piece = [&](TcPiece& p) {
+    if (!wait(d_full(dq.slot), dq.phase)) return false;
+    read_piece(p);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(d_empty(dq.slot));
+    dq.next(kTcPieces);
+    return p.nt > 0;
+  };
+  // whether the tile at key j holds positions outside the unit's keys
+  auto edge = [](const TcPiece& p, int j) { return j < p.lo || j + kAttnTK > p.hi; };
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
@@ -212,31 +298,8 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     const int row = threadIdx.x & 127;                       // of this half
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 128u * g, to = tmem + lanes + 256u + 128u * g;
-    const uint32_t q_row = q_base + g * T::kTile + row * 128u;
-    // the CTA's record in the workspace, by one thread
-    auto note = [&](const AttnPiece& p) {
-      if (threadIdx.x) return;
-      AttnRec& rec = sc.rec[blockIdx.x];
-      if (p.first() && !p.last()) {
-        rec.s = p.s;
-        rec.head = p.head;
-        rec.rb = p.rb;
-        rec.starts = 1;
-      } else if (!p.first()) {
-        rec.mid = 1;
-        rec.ends = p.last();
-      }
-    };
-    if (threadIdx.x == 0) sc.rec[blockIdx.x].starts = sc.rec[blockIdx.x].mid = sc.rec[blockIdx.x].ends = 0;
-    // the next piece that has rows in this half
-    auto fetch = [&](AttnPiece& p) {
-      while (cur.left > 0) {
-        p = next_piece(a.b, sh, cur);
-        note(p);
-        if (rows_of(p) > 128 * g) return true;
-      }
-      return false;
-    };
+    const uint32_t q_half = q_base + g * T::kTile;
+    constexpr int kLanes = D / 8;  // lanes that a query row takes, 16 bytes each
     // A piece as this thread's row needs it.
     struct Job {
       int nt, j0;          // tiles, first key of the first
@@ -245,37 +308,51 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       int row;             // output row (token * heads + head), or the slot's; -1: no such row
       bool whole;
     } job;
-    // Turns the piece into this thread's job and its query row into shared memory.
-    auto begin = [&](const AttnPiece& p) {
-      const int r = 128 * g + row, rr = p.rb * kTcBR + r;
-      const bool valid = r < rows_of(p);
+    // The next piece that has rows in this half: this thread's job, and its warp's query rows
+    // on their way into registers, D / 8 lanes a row so that a load covers whole rows.
+    auto begin = [&](uint4 (&v)[kLanes]) {
+      TcPiece p;
+      do {
+        if (!get_piece(p)) return false;
+      } while (p.rows <= 128 * g);
+      const int r = 128 * g + row, rr = p.r0 + r;
+      const bool valid = r < p.rows;
       const int tok = rr / sh.G, head = p.head * sh.G + rr % sh.G;
-      const KeyRange k0 = key_range(p.q, p.u.i0, sh.causal, sh.window);
-      const KeyRange k1 = key_range(p.q, p.u.i1, sh.causal, sh.window);
-      const KeyRange kr = key_range(p.q, tok, sh.causal, sh.window);
-      job.nt = p.tb - p.ta;
-      job.j0 = (p.u.t0 + p.ta) * kAttnTK;
+      const KeyRange kr = key_range(SeqInfo{p.q0, p.n, p.L}, tok, sh.causal, sh.window);
+      job.nt = p.nt;
+      job.j0 = p.j0;
       job.lo = kr.lo;
       job.hi = valid ? kr.hi : 0;
-      job.in_lo = max(k0.lo, k1.lo);
-      job.in_hi = min(k0.hi, k1.hi);
-      job.whole = p.whole();
-      job.row = !valid ? -1
-                : job.whole ? (p.q.q0 + tok) * a.hq + head
-                            : (p.first() ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x) * kTcBR + r;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                 (size_t)(p.q.q0 + tok) * a.q_stride + (size_t)head * D;
+      job.in_lo = p.in_lo;
+      job.in_hi = p.in_hi;
+      job.whole = p.slot < 0;
+      job.row = !valid ? -1 : job.whole ? (p.q0 + tok) * a.hq + head : p.slot * kTcBR + r;
+      const unsigned long long src =
+          valid ? reinterpret_cast<unsigned long long>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                       (size_t)(p.q0 + tok) * a.q_stride +
+                                                       (size_t)head * D)
+                : 0ull;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (valid) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+      for (int i = 0; i < kLanes; ++i) {
+        const unsigned long long at =
+            __shfl_sync(0xffffffffu, src, i * (32 / kLanes) + lane / kLanes);
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (at) v[i] = __ldg(reinterpret_cast<const uint4*>(at) + lane % kLanes);
+      }
+      return true;
+    };
+    auto store_q = [&](uint4 (&v)[kLanes]) {
+      const int c = lane % kLanes;
+#pragma unroll
+      for (int i = 0; i < kLanes; ++i) {
         if (FP8) {
-          v.x = bf16x2_f16(v.x);
-          v.y = bf16x2_f16(v.y);
-          v.z = bf16x2_f16(v.z);
-          v.w = bf16x2_f16(v.w);
+          v[i].x = bf16x2_f16(v[i].x);
+          v[i].y = bf16x2_f16(v[i].y);
+          v[i].z = bf16x2_f16(v[i].z);
+          v[i].w = bf16x2_f16(v[i].w);
         }
-        sts128(q_row + (c / 8) * kHalf + (((c & 7) ^ (row & 7)) << 4), v);
+        const int r = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes;
+        sts128(q_half + (c / 8) * kHalf + r * 128u + (((c & 7) ^ (r & 7)) << 4), v[i]);
       }
       fence_async_proxy();
       __syncwarp();
@@ -283,11 +360,12 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     };
     bool have;
     {
-      AttnPiece p;
-      have = fetch(p);
-      if (have) begin(p);
+      uint4 v[kLanes];
+      have = begin(v);
+      if (have) store_q(v);
     }
     uint32_t tc = 0;  // tiles of this half so far
+    const uint64_t sc2 = pair(a.scale_log2, a.scale_log2);
     while (have) {
       float m = -INFINITY, l = 0.f;   // m: the reference of the weights, raw score units
       bool ok = true;
@@ -303,81 +381,122 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_wait_ld(s[i]);
         const int j0 = job.j0 + t * kAttnTK;
-        if (j0 < job.in_lo || j0 + kAttnTK > job.in_hi) {
-          const int lo = job.lo - j0, hi = job.hi - j0;
+        const bool masked = j0 < job.in_lo || j0 + kAttnTK > job.in_hi;
+        auto drop = [&](uint32_t (&x)[32], int i) {  // keys that this row does not attend
+          const int lo = job.lo - j0 - 32 * i, hi = job.hi - j0 - 32 * i;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int c = 0; c < 32; ++c)
+            if (c < lo || c >= hi) x[c] = 0xff800000u;  // -inf
+        };
+        if (masked)
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (32 * i + c < lo || 32 * i + c >= hi) s[i][c] = 0xff800000u;  // -inf
-        }
-        float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-          for (int c = 1; c < 32; ++c) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][c]));
-        }
-        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-        if (t == 0) {
-          m = mn;
-        } else if (__any_sync(0xffffffffu, mn > m && (mn - m) * a.scale_log2 > kTcSlack)) {
-          // O catches up with the new maxima, once the product before this tile's is done
-          if (!wait(pv_done(g), (tc - 1) & 1u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const float f = mn > m ? ex2((m - mn) * a.scale_log2) : 1.f;
-          m = mn;
-          l *= f;
-#pragma unroll 1
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * i, o);
-            tmem_wait_ld(o);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-            tmem_st32(to + 32 * i, o);
-          }
-          tmem_wait_st();
-        }
-        const float off = m == -INFINITY ? 0.f : -m * a.scale_log2;
-        float sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+          for (int i = 0; i < 4; ++i) drop(s[i], i);
+        uint64_t off2, sum[2] = {0ull, 0ull};
+        // weights of 64 keys, two to a word, and their sum
+        auto weigh = [&](const uint32_t (&x)[32], const uint32_t (&y)[32], uint32_t (&w)[32]) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const int k = 2 * c;
-            const float e0 = ex2(fmaf(__uint_as_float(s[2 * h + k / 32][k % 32]), a.scale_log2, off));
-            const float e1 =
-                ex2(fmaf(__uint_as_float(s[2 * h + k / 32][k % 32 + 1]), a.scale_log2, off));
-            sum[0] += e0;
-            sum[1] += e1;
+            const uint32_t u = c < 16 ? x[2 * c % 32] : y[2 * c % 32];
+            const uint32_t v = c < 16 ? x[2 * c % 32 + 1] : y[2 * c % 32 + 1];
+            float e0, e1;
+            unpair(fma2(pair_bits(u, v), sc2, off2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            sum[c & 1] = add2(sum[c & 1], pair(e0, e1));
             w[c] = FP8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
           }
-          tmem_st32(ts + 32 * h, w);
+        };
+        auto set_off = [&]() {
+          const float off = m == -INFINITY ? 0.f : -m * a.scale_log2;
+          off2 = pair(off, off);
+        };
+        auto largest = [&]() {
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mx[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+#pragma unroll
+            for (int c = 2; c < 32; c += 2)
+              mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s[i][c])), __uint_as_float(s[i][c + 1]));
+          }
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
+        uint32_t w[32];
+        if (t == 0) {
+          m = largest();
+          set_off();
+          weigh(s[0], s[1], w);
+        } else {
+          // the weights by the reference so far; the tile's own maximum, off that path, only
+          // tells whether they may grow too large
+          set_off();
+          weigh(s[0], s[1], w);
+          const float mn = largest();
+          if (__any_sync(0xffffffffu, mn > m && (mn - m) * a.scale_log2 > T::kSlack)) {
+            // O catches up with the new maxima, once the product before this tile's is done
+            if (!wait(pv_done(g), (tc - 1) & 1u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float f = mn > m ? ex2((m - mn) * a.scale_log2) : 1.f;
+            m = fmaxf(m, mn);
+            l *= f;
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              tmem_ld32(to + 32 * i, w);
+              tmem_wait_ld(w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
+              tmem_st32(to + 32 * i, w);
+            }
+            tmem_wait_st();
+            // the first 64 scores once more: their registers were given up
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, s[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_wait_ld(s[i]);
+            if (masked)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) drop(s[i], i);
+            set_off();
+            sum[0] = sum[1] = 0ull;
+            weigh(s[0], s[1], w);
+          }
         }
-        l += sum[0] + sum[1];
+        // the product over the first 64 keys may begin before the other weights are there
+        tmem_st32(ts, w);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(g));
+        if (lane == 0) mbar_arrive(p_full(g, 0));
+        weigh(s[2], s[3], w);
+        tmem_st32(ts + 32, w);
+        {
+          float x, y;
+          unpair(add2(sum[0], sum[1]), x, y);
+          l += x + y;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(g, 1));
       }
       if (!ok) break;
       // every score of the piece is out, so Q's place is free: the next piece's comes in while
       // the last product runs
       const Job done = job;
       {
-        AttnPiece p;
-        have = fetch(p);
-        if (have) begin(p);
+        uint4 v[kLanes];
+        have = begin(v);
+        if (have) store_q(v);
       }
       if (!wait(pv_done(g), (tc - 1) & 1u)) break;
       tc_fence_after();
       const float ml = m == -INFINITY ? -INFINITY : m * a.scale_log2;
       if (done.whole) {
+        // 32-byte stores fill whole sectors of the thread's row, where out allows them
+        const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
         const float inv = l == 0.f ? 0.f : a.v_scale / l;
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
                                               (size_t)done.row * D);
@@ -386,16 +505,21 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
           uint32_t o[32];
           tmem_ld32(to + 32 * i, o);
           tmem_wait_ld(o);
-          if (done.row >= 0)
+          if (done.row >= 0) {
+            uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t w[4];
+            for (int k = 0; k < 16; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv,
+                                 __uint_as_float(o[2 * k + 1]) * inv);
+            if (wide) {
+              stg256(dst + 4 * i, &w[0]);
+              stg256(dst + 4 * i + 2, &w[8]);
+            } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * k]) * inv,
-                                   __uint_as_float(o[8 * c + 2 * k + 1]) * inv);
-              dst[4 * i + c] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int c = 0; c < 4; ++c)
+                dst[4 * i + c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
             }
+          }
         }
         if (a.lse && done.row >= 0)
           a.lse[done.row] = l == 0.f ? -INFINITY : (ml + log2f(l)) * 0.6931471805599453f;
@@ -408,93 +532,92 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
           tmem_wait_ld(o);
           if (done.row >= 0)
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              dst[8 * i + c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int c = 0; c < 4; ++c) stg256(dst + 8 * i + 2 * c, &o[8 * c]);
         }
         if (done.row >= 0) sc.ml[done.row] = make_float2(ml, l);
       }
       tc_fence_before();
     }
   } else if (warp == kTcMmaWarp) {
-    // ------------------------------------------------------------ products
-    constexpr uint32_t kIdS = idesc_attn(FP8, kAttnTK, false), kIdO = idesc_attn(FP8, D, true);
-    Ring rg{0, 0};
-    uint32_t qc[2] = {0, 0}, tcnt[2] = {0, 0};
-    bool ok = true;
-    auto take = [&](uint32_t& slot) {  // the next operand tile, filled
-      if (!wait(full(rg.slot), rg.phase)) return false;
-      slot = rg.slot;
-      rg.next(T::kStages);
-      return true;
-    };
-    auto scores = [&](int g, uint32_t slot) {
-      if (lane == 0) {
-        const uint64_t qa = sdesc_sw128(q_base + g * T::kTile);
-        const uint64_t kb = sdesc_sw128(ring + slot * T::kTile);
+    // ------------------------------------------------------------ products (one thread)
+    if (elect_one()) {
+      constexpr uint32_t kIdS = idesc_attn(FP8, kAttnTK, false), kIdO = idesc_attn(FP8, D, true);
+      constexpr uint32_t kStep = T::kTile >> 4;  // descriptor units per stage
+      const uint64_t q0 = sdesc_sw128(q_base), q1 = sdesc_advance(q0, T::kTile);
+      const uint64_t k_ring = sdesc_sw128(ring), v_ring = sdesc_v(ring);
+      Ring rg{0, 0};
+      uint32_t qc0 = 0, qc1 = 0, tc0 = 0, tc1 = 0;  // Qs and tiles of each half so far
+      auto wait1 = [&](uint32_t bar, uint32_t parity) {
+        return wait_fast(bar, parity, abort_flag, status);
+      };
+      auto scores = [&](uint32_t col, uint64_t qa, uint32_t slot, uint32_t bar) {
+        const uint64_t kb = k_ring + slot * kStep;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t at = (k / 4) * kHalf + (k % 4) * 32;
-          mma_bf16(tmem + 128u * g, sdesc_advance(qa, at), sdesc_advance(kb, at), kIdS, k > 0);
+          constexpr uint32_t kH = kHalf >> 4;
+          const uint32_t at = (k / 4) * kH + (k % 4) * 2;
+          mma_bf16(tmem + col, qa + at, kb + at, kIdS, k > 0);
         }
-        mma_commit(s_full(g));
-      }
-      __syncwarp();
-    };
-    while (ok && cur.left > 0) {
-      const AttnPiece p = next_piece(a.b, sh, cur);
-      const int halves = rows_of(p) > 128 ? 2 : 1;
-      uint32_t ks = 0, vs = 0;
-      if (!take(ks)) break;
-      for (int g = 0; g < halves && ok; ++g) {
-        ok = wait(q_full(g), qc[g]++ & 1u);
-        tc_fence_after();
-        if (ok) scores(g, ks);
-      }
-      if (!ok) break;
-      if (lane == 0) mma_commit(empty(ks));
-      for (int t = p.ta; ok && t < p.tb; ++t) {
-        const bool more = t + 1 < p.tb;
-        if ((more && !take(ks)) || !take(vs)) {
-          ok = false;
-          break;
-        }
-        const int j0 = (p.u.t0 + t) * kAttnTK;
-        if (!FP8 && (j0 < p.u.lo || j0 + kAttnTK > p.u.hi)) {
-          // v of positions that no row attends: 0, whatever the page holds (0 * NaN = NaN)
-          const int lo = max(p.u.lo - j0, 0), hi = min(p.u.hi - j0, kAttnTK);
-          for (int i = lane; i < kAttnTK * (D / 8); i += 32) {
-            const int r = i / (D / 8), c = i % (D / 8);
-            if (r < lo || r >= hi)
-              sts128(ring + vs * T::kTile + (c / 8) * kHalf + r * 128 + (c & 7) * 16,
-                     make_uint4(0u, 0u, 0u, 0u));
-          }
-          fence_async_proxy();
-          __syncwarp();
-        }
-        for (int g = 0; g < halves; ++g) {
-          if (!wait(p_full(g), tcnt[g]++ & 1u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t vb = sdesc_v(ring + vs * T::kTile);
+        mma_commit(bar);
+      };
+      // O += P V as the two 64-key halves of P arrive; tile n of the half
+      auto weighted = [&](int g, uint32_t n, uint32_t slot, bool add) {
+        const uint64_t vb = v_ring + slot * kStep;
 #pragma unroll
-            for (int k = 0; k < kAttnTK / 16; ++k)
-              mma_ts(tmem + 256u + 128u * g, tmem + 128u * g + 8u * k,
-                     sdesc_advance(vb, k * 2048), kIdO, t > p.ta || k > 0);
-            mma_commit(pv_done(g));
-          }
-          __syncwarp();
-          if (more) scores(g, ks);
+        for (int h = 0; h < 2; ++h) {
+          if (!wait1(p_full(g, h), n & 1u)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 4 * h; k < 4 * h + 4; ++k)
+            mma_ts(tmem + 256u + 128u * g, tmem + 128u * g + 8u * k, vb + k * (2048 >> 4), kIdO,
+                   add || k > 0);
         }
-        if (ok && lane == 0) {
+        mma_commit(pv_done(g));
+        return true;
+      };
+      for (;;) {
+        if (!wait1(d_full(dq.slot), dq.phase)) break;
+        const int nt = pieces[dq.slot].nt;
+        const bool two = pieces[dq.slot].rows > 128;
+        mbar_arrive(d_empty(dq.slot));
+        dq.next(kTcPieces);
+        if (nt == 0) break;
+        uint32_t ks = rg.slot;
+        if (!wait1(full(ks), rg.phase)) break;
+        rg.next(T::kStages);
+        if (!wait1(q_full(0), qc0++ & 1u)) break;
+        tc_fence_after();
+        scores(0u, q0, ks, s_full(0));
+        if (two) {
+          if (!wait1(q_full(1), qc1++ & 1u)) break;
+          tc_fence_after();
+          scores(128u, q1, ks, s_full(1));
+        }
+        mma_commit(empty(ks));
+        bool ok = true;
+        for (int t = 0; t < nt; ++t) {
+          const bool more = t + 1 < nt;
+          if (more) {
+            ks = rg.slot;
+            if (!(ok = wait1(full(ks), rg.phase))) break;
+            rg.next(T::kStages);
+          }
+          const uint32_t vs = rg.slot;
+          if (!(ok = wait1(full(vs), rg.phase))) break;
+          rg.next(T::kStages);
+          if (!(ok = weighted(0, tc0++, vs, t > 0))) break;
+          if (more) scores(0u, q0, ks, s_full(0));
+          if (two) {
+            if (!(ok = weighted(1, tc1++, vs, t > 0))) break;
+            if (more) scores(128u, q1, ks, s_full(1));
+          }
           mma_commit(empty(vs));
           if (more) mma_commit(empty(ks));
         }
-        __syncwarp();
+        if (!ok) break;
       }
     }
+    __syncwarp();
   } else if (warp == kTcCopyWarp) {
     // ------------------------------------------------------------ tile copies
     constexpr int kParts = FP8 ? 1 : D / 64;
@@ -507,53 +630,129 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     const uint32_t box_bytes = (uint32_t)box_rows * kPitch;
     Ring rg{0, 0};
     uint32_t issued = 0;
-    bool ok = true;
     auto fullb = [&](uint32_t s) { return FP8 ? raw_full(s) : full(s); };
     auto emptyb = [&](uint32_t s) { return FP8 ? raw_empty(s) : empty(s); };
-    while (ok && cur.left > 0) {
-      const AttnPiece p = next_piece(a.b, sh, cur);
+    AttnRec* rec = &attn_scratch(a.scratch, kTcBR).rec[blockIdx.x];
+    if (lane == 0) rec->starts = rec->mid = rec->ends = 0;
+    for (;;) {
+      AttnPiece p;
+      const bool have = next_piece(a.b, sh, cur, p);
+      TcPiece d;
+      d.nt = have ? p.tb - p.ta : 0;
+      if (have) {
+        const KeyRange k0 = key_range(p.q, p.u.i0, sh.causal, sh.window);
+        const KeyRange k1 = key_range(p.q, p.u.i1, sh.causal, sh.window);
+        d.j0 = (p.u.t0 + p.ta) * kAttnTK;
+        d.lo = p.u.lo;
+        d.hi = p.u.hi;
+        d.in_lo = max(k0.lo, k1.lo);
+        d.in_hi = min(k0.hi, k1.hi);
+        d.r0 = p.rb * kTcBR;
+        d.rows = min(kTcBR, p.q.n * sh.G - d.r0);
+        d.q0 = p.q.q0;
+        d.n = p.q.n;
+        d.L = p.q.L;
+        d.head = p.head;
+        d.slot = p.whole() ? -1 : p.first() ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
+        if (lane == 0 && p.first() && !p.last()) {
+          rec->s = p.s;
+          rec->head = p.head;
+          rec->rb = p.rb;
+          rec->starts = 1;
+        } else if (lane == 0 && !p.first()) {
+          rec->mid = 1;
+          rec->ends = p.last();
+        }
+      }
+      if (!wait(d_empty(dq.slot), dq.phase ^ 1u)) break;
+      if (lane == 0) {
+        pieces[dq.slot] = d;
+        mbar_arrive(d_full(dq.slot));
+      }
+      __syncwarp();
+      dq.next(kTcPieces);
+      if (!have) break;
+      // the piece's query rows into L2: one run of its heads per token
+      for (int i = p.u.i0 + lane; i <= p.u.i1; i += 32)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                         static_cast<const __nv_bfloat16*>(a.q) +
+                         (size_t)(p.q.q0 + i) * a.q_stride + (size_t)p.head * sh.G * D),
+                     "r"(sh.G * D * 2)
+                     : "memory");
       auto live_at = [&](int t) {
-        const int j = (p.u.t0 + t) * kAttnTK + pl * box_rows;
-        return t < p.tb && lane < boxes && j < p.u.hi && j + box_rows > p.u.lo;
+        const int j = d.j0 + t * kAttnTK + pl * box_rows;
+        return t < d.nt && lane < boxes && j < d.hi && j + box_rows > d.lo;
       };
       auto page_at = [&](int t) {
-        return live_at(t) ? page_of(a.b, p.s, (p.u.t0 + t) * kAttnTK + pl * box_rows) : 0;
+        return live_at(t) ? page_of(a.b, p.s, d.j0 + t * kAttnTK + pl * box_rows) : 0;
       };
       auto copy = [&](int t, int page, bool v) {
         const bool live = live_at(t);
         const uint32_t bytes = box_bytes * __popc(__ballot_sync(0xffffffffu, live));
         if (!wait(emptyb(rg.slot), rg.phase ^ 1u)) return false;
-        if (lane == 0) mbar_expect_tx(fullb(rg.slot), bytes);
+        // a V tile with positions that no row attends passes through the cleaning warp
+        const int j = d.j0 + t * kAttnTK;
+        const uint32_t bar = !FP8 && v && edge(d, j) ? v_raw(rg.slot) : fullb(rg.slot);
+        if (lane == 0) mbar_expect_tx(bar, bytes);
         __syncwarp();
         if (live)
           tma_load_4d((FP8 ? codes + rg.slot * T::kRawTile : ring + rg.slot * T::kTile) +
                           part * kHalf + pl * box_bytes,
-                      v ? &maps.v : &maps.k, fullb(rg.slot), part * 64,
-                      ((p.u.t0 + t) * kAttnTK + pl * box_rows) & (ps - 1), p.head, page);
+                      v ? &maps.v : &maps.k, bar, part * 64, (j + pl * box_rows) & (ps - 1),
+                      d.head, page);
         ++issued;
         rg.next(kN);
         return true;
       };
-      int page = page_at(p.ta), next = page_at(p.ta + 1);
-      ok = copy(p.ta, page, false);
-      for (int t = p.ta; ok && t < p.tb; ++t) {
+      int page = page_at(0), next = page_at(1);
+      bool ok = copy(0, page, false);
+      for (int t = 0; ok && t < d.nt; ++t) {
         const int after = page_at(t + 2);
-        if (t + 1 < p.tb) ok = copy(t + 1, next, false);
+        if (t + 1 < d.nt) ok = copy(t + 1, next, false);
         if (ok) ok = copy(t, page, true);
         page = next;
         next = after;
       }
+      if (!ok) break;
     }
     if (*abort_flag && lane == 0)  // let what is in flight land before the CTA can exit
       for (uint32_t j = issued > kN ? issued - kN : 0; j < issued; ++j)
         land(fullb(j % kN), (j / kN) & 1u);
     __syncwarp();
-  } else if (FP8 && warp >= kTcCvtWarp) {
+  } else if (!FP8) {
+    // ------------------------------------------------------------ V tiles at the edges
+    // v of positions that no row attends becomes 0, whatever the page holds (0 * NaN = NaN).
+    // Only a unit's first tile (window) and last tile (length) have such positions.
+    uint32_t at = 0, phases = 0;  // ring position of the piece, phase of each stage's v_raw
+    bool ok = true;
+    TcPiece p;
+    while (ok && get_piece(p)) {
+      for (int t = 0; ok && t < p.nt; t += max(1, p.nt - 1)) {
+        const int j0 = p.j0 + t * kAttnTK;
+        if (!edge(p, j0)) continue;
+        // operands in the ring: K0, K1, V0, K2, V1, ..., K(nt-1), V(nt-2), V(nt-1)
+        const uint32_t slot = (at + (t + 1 < p.nt ? 2 * t + 2 : 2 * t + 1)) % T::kStages;
+        if (!(ok = wait(v_raw(slot), (phases >> slot) & 1u))) break;
+        phases ^= 1u << slot;
+        const int lo = max(p.lo - j0, 0), hi = min(p.hi - j0, kAttnTK);
+        for (int i = lane; i < kAttnTK * (D / 8); i += 32) {
+          const int r = i / (D / 8), c = i % (D / 8);
+          if (r < lo || r >= hi)
+            sts128(ring + slot * T::kTile + (c / 8) * kHalf + r * 128 + (c & 7) * 16,
+                   make_uint4(0u, 0u, 0u, 0u));
+        }
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(slot));
+      }
+      at += 2 * p.nt;
+    }
+  } else {
     // ------------------------------------------------------------ codes to f16
     const int row0 = threadIdx.x - 32 * kTcCvtWarp;
     Ring rq{0, 0}, rg{0, 0};
     bool ok = true;
-    auto convert = [&](const AttnPiece& p, int t, bool v) {
+    auto convert = [&](const TcPiece& p, int t, bool v) {
       if (!wait(raw_full(rq.slot), rq.phase) ||
           !wait(empty(rg.slot), rg.phase ^ 1u))
         return false;
@@ -566,8 +765,8 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
           const uint32_t off = row * T::kRawPitch + c * 16;
           w[c] = lds128(src + (off ^ ((off >> 3) & T::kRawSwz)));
         }
-        const int j = (p.u.t0 + t) * kAttnTK + row;
-        if (v && (j < p.u.lo || j >= p.u.hi)) {  // no row attends it: 0, whatever the page holds
+        const int j = p.j0 + t * kAttnTK + row;
+        if (v && (j < p.lo || j >= p.hi)) {  // no row attends it: 0, whatever the page holds
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -593,11 +792,11 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       rg.next(T::kStages);
       return true;
     };
-    while (ok && cur.left > 0) {
-      const AttnPiece p = next_piece(a.b, sh, cur);
-      ok = convert(p, p.ta, false);
-      for (int t = p.ta; ok && t < p.tb; ++t) {
-        if (t + 1 < p.tb) ok = convert(p, t + 1, false);
+    TcPiece p;
+    while (ok && get_piece(p)) {
+      ok = convert(p, 0, false);
+      for (int t = 0; ok && t < p.nt; ++t) {
+        if (t + 1 < p.nt) ok = convert(p, t + 1, false);
         if (ok) ok = convert(p, t, true);
       }
     }
@@ -630,6 +829,7 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   sh.hkv = a.hkv;
   sh.BR = kTcBR;
   sh.TK = kAttnTK;
+  sh.extra = kTcExtra;
   sh.causal = a.causal;
   sh.window = a.window;
   const int ctas = num_sms() < kAttnMaxCtas ? num_sms() : kAttnMaxCtas;

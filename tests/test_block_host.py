@@ -226,8 +226,8 @@ using namespace gbmoe;
 int main() {
   AttnShape a;
   int causal, g, S;
-  while (scanf("%d %d %d %d %d %d %d %d", &a.G, &a.hkv, &a.BR, &a.TK, &causal, &a.window, &g,
-               &S) == 8) {
+  while (scanf("%d %d %d %d %d %d %d %d %d", &a.G, &a.hkv, &a.BR, &a.TK, &a.extra, &causal,
+               &a.window, &g, &S) == 9) {
     a.causal = causal != 0;
     std::vector<SeqInfo> q(S);
     std::vector<long long> line(S + 1, 0);
@@ -246,6 +246,7 @@ int main() {
       while (cur.left > 0) {
         while (q[cur.s].n == 0) ++cur.s;
         const AttnPiece p = take_piece(a, q[cur.s], cur);
+        if (p.ta == p.tb) continue;
         printf("%d %d %d %d %d %d %d %d ", c, p.s, p.head, p.rb, p.ta, p.tb, p.u.t0, p.u.tiles);
       }
     }
@@ -258,7 +259,7 @@ int main() {
 
 def test_attention_work_is_cut_whole(tmp_path):
     """Every tile that a unit's tokens attend is computed once, the pieces of a unit follow each
-    other over neighbouring CTAs, no CTA has more than one tile over its share, and a CTA begins
+    other over neighbouring CTAs, no CTA has more than its share of the cost, and a CTA begins
     at most one unit that it leaves and ends at most one that it did not begin."""
     (tmp_path / "plan.cpp").write_text(PLAN)
     subprocess.run(["g++", "-std=c++17", "-I", build_mod.CSRC, str(tmp_path / "plan.cpp"), "-o",
@@ -274,14 +275,14 @@ def test_attention_work_is_cut_whole(tmp_path):
         if not any(n for n, _ in seqs):
             seqs[0] = (1, 3)
         cases.append((rng.choice([1, 3, 4, 8]), rng.choice([1, 2, 8]), rng.choice([16, 256]), 128,
-                      int(rng.random() < 0.8), rng.choice([0, 0, 1, 100, 1000]),
+                      rng.choice([0, 1, 3]), int(rng.random() < 0.8), rng.choice([0, 0, 1, 100, 1000]),
                       rng.choice([1, 7, 148, 152]), S, seqs))
-    text = "\n".join(" ".join(map(str, c[:8])) + " " + " ".join(f"{n} {L}" for n, L in c[8])
+    text = "\n".join(" ".join(map(str, c[:9])) + " " + " ".join(f"{n} {L}" for n, L in c[9])
                      for c in cases)
     out = subprocess.run([str(tmp_path / "plan")], input=text, text=True, capture_output=True,
                          check=True).stdout.splitlines()
     assert len(out) == len(cases)
-    for (G, hkv, BR, TK, causal, window, g, S, seqs), line in zip(cases, out):
+    for (G, hkv, BR, TK, extra, causal, window, g, S, seqs), line in zip(cases, out):
         v = [int(x) for x in line.split()]
         pieces = [tuple(v[i:i + 8]) for i in range(0, len(v), 8)]
         units = {}
@@ -298,7 +299,7 @@ def test_attention_work_is_cut_whole(tmp_path):
                     lo, hi = min(k[0] for k in keys), max(k[1] for k in keys)
                     units[s, head, rb] = (lo // TK, -(-hi // TK)) if hi > lo else (0, 1)
         at, per, order = {}, {}, list(units)
-        total = sum(b - a for a, b in units.values())
+        total = sum(b - a + extra for a, b in units.values())
         where = 0
         for c, s, head, rb, ta, tb, t0, tiles in pieces:
             u = (s, head, rb)
@@ -310,5 +311,7 @@ def test_attention_work_is_cut_whole(tmp_path):
             per.setdefault(c, []).append((ta > 0, tb < tiles, tb - ta))
         assert all(at[u] == b - a for u, (a, b) in units.items())
         for c, ps in per.items():
-            assert abs(sum(p[2] for p in ps) - total / g) < 1 + 1e-9
+            begun = sum(not p[0] for p in ps)      # their extra cost lies in this range, but
+            share = sum(p[2] for p in ps) + extra * begun      # for a cut through it at an end
+            assert total / g - 1 - extra < share < total / g + 1 + extra
             assert not any(p[0] for p in ps[1:]) and not any(p[1] for p in ps[:-1])
