@@ -36,22 +36,24 @@ namespace {
 constexpr int kTcBR = 256;
 constexpr int kTcMmaWarp = 8, kTcCopyWarp = 9, kTcCvtWarp = 10;
 constexpr int kTcCvtWarps = 2;
-constexpr int kTcExtra = 1;      // cost of beginning a unit, in tiles
+constexpr int kTcExtra = 3;      // cost of beginning a unit, in tiles
 
 template <bool FP8, int D>
 struct Tc {
   static constexpr int kThreads = 32 * (kTcCvtWarp + (FP8 ? kTcCvtWarps : 1));
   static constexpr uint32_t kTile = kAttnTK * D * 2;        // one operand tile (16 bit)
   static constexpr uint32_t kRawTile = kAttnTK * D;         // one tile of codes
-  static constexpr int kRaw = FP8 ? 4 : 0;                  // code stages
-  static constexpr int kStages = FP8 ? 3 : 5;               // operand stages
+  static constexpr int kRaw = FP8 ? 3 : 0;                  // code stages
+  static constexpr int kStages = FP8 ? 3 : 4;               // operand stages
+  static constexpr int kOutCols = 32;                       // columns staged at a time
+  static constexpr uint32_t kOut = 2 * 128 * kOutCols * 2;  // staging of the output rows
   static constexpr uint32_t kQ = 2 * kTile;
   // log2 of the largest weight before O is rescaled: bf16 has fp32's range, f16 ends at 2^16
   static constexpr float kSlack = FP8 ? 14.f : 60.f;
   static constexpr uint32_t kRawPitch = D < 128 ? D : 128;  // bytes of a code row
   static constexpr uint32_t kRawSwz = kRawPitch == 128 ? 0x70u : 0x30u;
   static constexpr int kReaders = 8 + 1 + (FP8 ? kTcCvtWarps : 1);  // warps that read a piece
-  static constexpr size_t kSmem = 1024 + kQ + kStages * kTile + kRaw * kRawTile + 1024;
+  static constexpr size_t kSmem = 1024 + kQ + kStages * kTile + kRaw * kRawTile + kOut + 1024;
   static_assert(kSmem <= 232448, "shared memory per CTA exceeded");
   static_assert((kAttnMaxSeqs + 1) * 8 <= kQ + kStages * kTile, "the plan lies in Q and the ring");
 };
@@ -152,6 +154,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Spin (bounded) until a copy in flight has landed, so that the CTA does not exit under it.
 __device__ __noinline__ void land(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
@@ -209,8 +223,8 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
   const uint32_t base = (raw0 + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw0);
   const uint32_t q_base = base, ring = base + T::kQ, codes = ring + T::kStages * T::kTile;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kQ + T::kStages * T::kTile +
-                                               T::kRaw * T::kRawTile);
+  const uint32_t outs = codes + T::kRaw * T::kRawTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (outs - base) + T::kOut);
   const uint32_t bar0 = smem_addr(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };           // operand stage filled
   auto empty = [&](int s) { return bar0 + 8u * (5 + s); };    // ... and read by its MMAs
@@ -280,12 +294,15 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     p.q0 = w2.x; p.n = w2.y; p.L = w2.z; p.head = w2.w;
     p.slot = w3.x;
   };
-  auto get_piece = [&](TcPiece& p) {
-    if (!wait(d_full(dq.slot), dq.phase)) return false;
-    read_piece(p);
+  auto release_piece = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(d_empty(dq.slot));
     dq.next(kTcPieces);
+  };
+  auto get_piece = [&](TcPiece& p) {
+    if (!wait(d_full(dq.slot), dq.phase)) return false;
+    read_piece(p);
+    release_piece();
     return p.nt > 0;
   };
   // whether the tile at key j holds positions outside the unit's keys
@@ -308,16 +325,48 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       int row;             // output row (token * heads + head), or the slot's; -1: no such row
       bool whole;
     } job;
-    // The next piece that has rows in this half: this thread's job, and its warp's query rows
-    // on their way into registers, D / 8 lanes a row so that a load covers whole rows.
-    auto begin = [&](uint4 (&v)[kLanes]) {
-      TcPiece p;
-      do {
-        if (!get_piece(p)) return false;
-      } while (p.rows <= 128 * g);
+    // Moves to the next piece that has rows in this half: 1, 0 when none is left, or, unless
+    // `block`, 2 when the schedule has not got there (it may be waiting for this very tile's
+    // weights).
+    auto seek = [&](bool block) {
+      for (;;) {
+        if (!block && !__all_sync(0xffffffffu, mbar_test_wait(d_full(dq.slot), dq.phase)))
+          return 2;
+        if (!wait(d_full(dq.slot), dq.phase)) return 0;
+        const TcPiece& p = pieces[dq.slot];
+        if (p.nt == 0) return 0;
+        if (p.rows > 128 * g) return 1;
+        release_piece();
+      }
+    };
+    // Sends the warp's query rows of that piece to shared memory (Q's place must be free), D / 8
+    // lanes a row so that a copy covers whole rows.
+    auto send_q = [&]() {
+      const TcPiece& p = pieces[dq.slot];
+      const int r = 128 * g + row, rr = p.r0 + r;
+      const int tok = rr / sh.G, head = p.head * sh.G + (rr - tok * sh.G);
+      const unsigned long long src =
+          reinterpret_cast<unsigned long long>(a.q) +
+          (r < p.rows ? 2ull * ((size_t)(p.q0 + tok) * a.q_stride + (size_t)head * D) : 0ull);
+      const uint32_t some = __ballot_sync(0xffffffffu, r < p.rows);
+      const int c = lane % kLanes;
+      const uint32_t dst = q_half + (c / 8) * kHalf;
+#pragma unroll 4
+      for (int i = 0; i < kLanes; ++i) {
+        const int l = i * (32 / kLanes) + lane / kLanes, r2 = (warp & 3) * 32 + l;
+        const unsigned long long at = __shfl_sync(0xffffffffu, src, l) + c * 16;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         dst + r2 * 128u + (((c & 7) ^ (r2 & 7)) << 4)),
+                     "l"(at), "r"((some >> l) & 1u ? 16u : 0u)
+                     : "memory");
+      }
+    };
+    // This thread's job in that piece, which is given back to the schedule.
+    auto take_job = [&]() {
+      const TcPiece& p = pieces[dq.slot];
       const int r = 128 * g + row, rr = p.r0 + r;
       const bool valid = r < p.rows;
-      const int tok = rr / sh.G, head = p.head * sh.G + rr % sh.G;
+      const int tok = rr / sh.G, head = p.head * sh.G + (rr - tok * sh.G);
       const KeyRange kr = key_range(SeqInfo{p.q0, p.n, p.L}, tok, sh.causal, sh.window);
       job.nt = p.nt;
       job.j0 = p.j0;
@@ -327,54 +376,50 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       job.in_hi = p.in_hi;
       job.whole = p.slot < 0;
       job.row = !valid ? -1 : job.whole ? (p.q0 + tok) * a.hq + head : p.slot * kTcBR + r;
-      const unsigned long long src =
-          valid ? reinterpret_cast<unsigned long long>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                       (size_t)(p.q0 + tok) * a.q_stride +
-                                                       (size_t)head * D)
-                : 0ull;
-#pragma unroll
-      for (int i = 0; i < kLanes; ++i) {
-        const unsigned long long at =
-            __shfl_sync(0xffffffffu, src, i * (32 / kLanes) + lane / kLanes);
-        v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (at) v[i] = __ldg(reinterpret_cast<const uint4*>(at) + lane % kLanes);
-      }
-      return true;
+      release_piece();
     };
-    auto store_q = [&](uint4 (&v)[kLanes]) {
-      const int c = lane % kLanes;
+    // The query rows have arrived: hand Q to the tensor core.
+    auto finish_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (FP8) {  // bf16 to f16 in place, by the thread that copied it
+        const int c = lane % kLanes;
 #pragma unroll
-      for (int i = 0; i < kLanes; ++i) {
-        if (FP8) {
-          v[i].x = bf16x2_f16(v[i].x);
-          v[i].y = bf16x2_f16(v[i].y);
-          v[i].z = bf16x2_f16(v[i].z);
-          v[i].w = bf16x2_f16(v[i].w);
+        for (int i = 0; i < kLanes; ++i) {
+          const int r2 = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes;
+          const uint32_t at = q_half + (c / 8) * kHalf + r2 * 128u + (((c & 7) ^ (r2 & 7)) << 4);
+          uint4 v = lds128(at);
+          v.x = bf16x2_f16(v.x);
+          v.y = bf16x2_f16(v.y);
+          v.z = bf16x2_f16(v.z);
+          v.w = bf16x2_f16(v.w);
+          sts128(at, v);
         }
-        const int r = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes;
-        sts128(q_half + (c / 8) * kHalf + r * 128u + (((c & 7) ^ (r & 7)) << 4), v[i]);
       }
       fence_async_proxy();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(g));
     };
-    bool have;
-    {
-      uint4 v[kLanes];
-      have = begin(v);
-      if (have) store_q(v);
+    int have = seek(true);
+    if (have) {
+      send_q();
+      finish_q();
     }
     uint32_t tc = 0;  // tiles of this half so far
     const uint64_t sc2 = pair(a.scale_log2, a.scale_log2);
     while (have) {
+      take_job();
       float m = -INFINITY, l = 0.f;   // m: the reference of the weights, raw score units
       bool ok = true;
+      have = 2;
       for (int t = 0; t < job.nt; ++t, ++tc) {
         if (!wait(s_full(g), tc & 1u)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        // the last scores are out, so Q's place is free: the next piece's is on its way while
+        // this tile is weighed
+        if (t + 1 == job.nt && (have = seek(false)) == 1) send_q();
         uint32_t s[4][32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s[i]);
@@ -385,19 +430,23 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         auto drop = [&](uint32_t (&x)[32], int i) {  // keys that this row does not attend
           const int lo = job.lo - j0 - 32 * i, hi = job.hi - j0 - 32 * i;
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c < lo || c >= hi) x[c] = 0xff800000u;  // -inf
+          for (int c = 0; c < 32; ++c) x[c] = c >= hi ? 0xff800000u : x[c];  // -inf
+          if (j0 < job.in_lo)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] = c < lo ? 0xff800000u : x[c];
         };
         if (masked)
 #pragma unroll
           for (int i = 0; i < 4; ++i) drop(s[i], i);
         uint64_t off2, sum[2] = {0ull, 0ull};
-        // weights of 64 keys, two to a word, and their sum
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // weights of 64 keys, two to a word, their sum and the largest score
         auto weigh = [&](const uint32_t (&x)[32], const uint32_t (&y)[32], uint32_t (&w)[32]) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const uint32_t u = c < 16 ? x[2 * c % 32] : y[2 * c % 32];
             const uint32_t v = c < 16 ? x[2 * c % 32 + 1] : y[2 * c % 32 + 1];
+            mx[c & 3] = fmaxf(fmaxf(mx[c & 3], __uint_as_float(u)), __uint_as_float(v));
             float e0, e1;
             unpair(fma2(pair_bits(u, v), sc2, off2), e0, e1);
             e0 = ex2(e0);
@@ -406,64 +455,55 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
             w[c] = FP8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
           }
         };
-        auto set_off = [&]() {
-          const float off = m == -INFINITY ? 0.f : -m * a.scale_log2;
-          off2 = pair(off, off);
-        };
-        auto largest = [&]() {
-          float mx[4];
+        auto largest = [&](int i0) {  // with chunks i0 .. 3
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            mx[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+          for (int i = i0; i < 4; ++i)
 #pragma unroll
-            for (int c = 2; c < 32; c += 2)
-              mx[i] = fmaxf(fmaxf(mx[i], __uint_as_float(s[i][c])), __uint_as_float(s[i][c + 1]));
-          }
+            for (int c = 0; c < 32; c += 2)
+              mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(s[i][c])),
+                                    __uint_as_float(s[i][c + 1]));
           return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         };
         uint32_t w[32];
-        if (t == 0) {
-          m = largest();
-          set_off();
+        // The weights go by the reference so far; the tile's own maximum, off that path, only
+        // tells whether they grow too large. A piece's first tile sets the reference.
+        if (t == 0) m = largest(0);
+        for (;;) {
+          const float off = m == -INFINITY ? 0.f : -m * a.scale_log2;
+          off2 = pair(off, off);
           weigh(s[0], s[1], w);
-        } else {
-          // the weights by the reference so far; the tile's own maximum, off that path, only
-          // tells whether they may grow too large
-          set_off();
-          weigh(s[0], s[1], w);
-          const float mn = largest();
-          if (__any_sync(0xffffffffu, mn > m && (mn - m) * a.scale_log2 > T::kSlack)) {
-            // O catches up with the new maxima, once the product before this tile's is done
-            if (!wait(pv_done(g), (tc - 1) & 1u)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const float f = mn > m ? ex2((m - mn) * a.scale_log2) : 1.f;
-            m = fmaxf(m, mn);
-            l *= f;
-#pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
-              tmem_ld32(to + 32 * i, w);
-              tmem_wait_ld(w);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
-              tmem_st32(to + 32 * i, w);
-            }
-            tmem_wait_st();
-            // the first 64 scores once more: their registers were given up
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, s[i]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_wait_ld(s[i]);
-            if (masked)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) drop(s[i], i);
-            set_off();
-            sum[0] = sum[1] = 0ull;
-            weigh(s[0], s[1], w);
+          const float mn = largest(2);
+          if (!__any_sync(0xffffffffu, mn > m && (mn - m) * a.scale_log2 > T::kSlack)) break;
+          // O catches up with the new maxima, once the product before this tile's is done (t > 0:
+          // the first tile's reference is its maximum)
+          if (!wait(pv_done(g), (tc - 1) & 1u)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+          const float f = mn > m ? ex2((m - mn) * a.scale_log2) : 1.f;
+          m = fmaxf(m, mn);
+          l *= f;
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            tmem_ld32(to + 32 * i, w);
+            tmem_wait_ld(w);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
+            tmem_st32(to + 32 * i, w);
+          }
+          tmem_wait_st();
+          // the first 64 scores once more: their registers were given up
+#pragma unroll
+          for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, s[i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) tmem_wait_ld(s[i]);
+          if (masked)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) drop(s[i], i);
+          sum[0] = sum[1] = 0ull;
         }
+        if (!ok) break;
         // the product over the first 64 keys may begin before the other weights are there
         tmem_st32(ts, w);
         tmem_wait_st();
@@ -483,58 +523,62 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         if (lane == 0) mbar_arrive(p_full(g, 1));
       }
       if (!ok) break;
-      // every score of the piece is out, so Q's place is free: the next piece's comes in while
-      // the last product runs
-      const Job done = job;
-      {
-        uint4 v[kLanes];
-        have = begin(v);
-        if (have) store_q(v);
-      }
+      if (have == 2 && (have = seek(true)) == 1) send_q();
+      if (have) finish_q();
       if (!wait(pv_done(g), (tc - 1) & 1u)) break;
       tc_fence_after();
       const float ml = m == -INFINITY ? -INFINITY : m * a.scale_log2;
-      if (done.whole) {
-        // 32-byte stores fill whole sectors of the thread's row, where out allows them
-        const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+      if (job.whole) {
+        // through shared memory, kOutCols columns at a time, so that a store covers whole
+        // stretches of a row. Rolled: code of a piece's end that is not in the instruction cache
+        // costs more than its execution.
+        constexpr int kPer = T::kOutCols / 8;  // lanes (16 bytes each) a row
+        constexpr uint32_t kPitch = T::kOutCols * 2;
+        static_assert(T::kOutCols == 32, "one tensor memory load a pass");
+        const uint32_t st = outs + warp * (32 * kPitch);
         const float inv = l == 0.f ? 0.f : a.v_scale / l;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
-                                              (size_t)done.row * D);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
+        const int c = lane % kPer;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += T::kOutCols) {
           uint32_t o[32];
-          tmem_ld32(to + 32 * i, o);
+          tmem_ld32(to + c0, o);
           tmem_wait_ld(o);
-          if (done.row >= 0) {
-            uint32_t w[16];
+          __syncwarp();  // the columns before have been read
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv,
-                                 __uint_as_float(o[2 * k + 1]) * inv);
-            if (wide) {
-              stg256(dst + 4 * i, &w[0]);
-              stg256(dst + 4 * i + 2, &w[8]);
-            } else {
+          for (int k = 0; k < kPer; ++k) {
+            uint32_t w[4];
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                dst[4 * i + c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-            }
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * i]) * inv,
+                                 __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
+            sts128(st + lane * kPitch + ((k ^ ((lane >> 1) & (kPer - 1))) << 4),
+                   make_uint4(w[0], w[1], w[2], w[3]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int r = i * (32 / kPer) + lane / kPer;
+            const int orow = __shfl_sync(0xffffffffu, job.row, r);
+            const uint4 v = lds128(st + r * kPitch + ((c ^ ((r >> 1) & (kPer - 1))) << 4));
+            if (orow >= 0)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)orow * D +
+                                        c0 + c * 8) = v;
           }
         }
-        if (a.lse && done.row >= 0)
-          a.lse[done.row] = l == 0.f ? -INFINITY : (ml + log2f(l)) * 0.6931471805599453f;
+        if (a.lse && job.row >= 0)
+          a.lse[job.row] = l == 0.f ? -INFINITY : (ml + log2f(l)) * 0.6931471805599453f;
       } else {
-        uint4* dst = reinterpret_cast<uint4*>(sc.o + (size_t)done.row * D);
-#pragma unroll
+        uint4* dst = reinterpret_cast<uint4*>(sc.o + (size_t)job.row * D);
+#pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           uint32_t o[32];
           tmem_ld32(to + 32 * i, o);
           tmem_wait_ld(o);
-          if (done.row >= 0)
+          if (job.row >= 0)
 #pragma unroll
             for (int c = 0; c < 4; ++c) stg256(dst + 8 * i + 2 * c, &o[8 * c]);
         }
-        if (done.row >= 0) sc.ml[done.row] = make_float2(ml, l);
+        if (job.row >= 0) sc.ml[job.row] = make_float2(ml, l);
       }
       tc_fence_before();
     }
@@ -543,78 +587,75 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     if (elect_one()) {
       constexpr uint32_t kIdS = idesc_attn(FP8, kAttnTK, false), kIdO = idesc_attn(FP8, D, true);
       constexpr uint32_t kStep = T::kTile >> 4;  // descriptor units per stage
-      const uint64_t q0 = sdesc_sw128(q_base), q1 = sdesc_advance(q0, T::kTile);
-      const uint64_t k_ring = sdesc_sw128(ring), v_ring = sdesc_v(ring);
+      const uint64_t q_half = sdesc_sw128(q_base), k_ring = sdesc_sw128(ring),
+                     v_ring = sdesc_v(ring);
       Ring rg{0, 0};
-      uint32_t qc0 = 0, qc1 = 0, tc0 = 0, tc1 = 0;  // Qs and tiles of each half so far
+      uint32_t pieces_of = 0;  // bit g: parity of half g's pieces so far
+      uint32_t tiles_of = 0;   // ... of its tiles
       auto wait1 = [&](uint32_t bar, uint32_t parity) {
         return wait_fast(bar, parity, abort_flag, status);
       };
-      auto scores = [&](uint32_t col, uint64_t qa, uint32_t slot, uint32_t bar) {
-        const uint64_t kb = k_ring + slot * kStep;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          constexpr uint32_t kH = kHalf >> 4;
-          const uint32_t at = (k / 4) * kH + (k % 4) * 2;
-          mma_bf16(tmem + col, qa + at, kb + at, kIdS, k > 0);
-        }
-        mma_commit(bar);
-      };
-      // O += P V as the two 64-key halves of P arrive; tile n of the half
-      auto weighted = [&](int g, uint32_t n, uint32_t slot, bool add) {
-        const uint64_t vb = v_ring + slot * kStep;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!wait1(p_full(g, h), n & 1u)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 4 * h; k < 4 * h + 4; ++k)
-            mma_ts(tmem + 256u + 128u * g, tmem + 128u * g + 8u * k, vb + k * (2048 >> 4), kIdO,
-                   add || k > 0);
-        }
-        mma_commit(pv_done(g));
-        return true;
-      };
-      for (;;) {
+      bool ok = true;
+      while (ok) {
         if (!wait1(d_full(dq.slot), dq.phase)) break;
         const int nt = pieces[dq.slot].nt;
-        const bool two = pieces[dq.slot].rows > 128;
+        const int halves = pieces[dq.slot].rows > 128 ? 2 : 1;
         mbar_arrive(d_empty(dq.slot));
         dq.next(kTcPieces);
         if (nt == 0) break;
-        uint32_t ks = rg.slot;
-        if (!wait1(full(ks), rg.phase)) break;
-        rg.next(T::kStages);
-        if (!wait1(q_full(0), qc0++ & 1u)) break;
-        tc_fence_after();
-        scores(0u, q0, ks, s_full(0));
-        if (two) {
-          if (!wait1(q_full(1), qc1++ & 1u)) break;
-          tc_fence_after();
-          scores(128u, q1, ks, s_full(1));
-        }
-        mma_commit(empty(ks));
-        bool ok = true;
-        for (int t = 0; t < nt; ++t) {
+        // step t: the products of tile t with V, and the scores of tile t + 1
+#pragma unroll 1
+        for (int t = -1; ok && t < nt; ++t) {
           const bool more = t + 1 < nt;
+          uint32_t ks = 0, vs = 0;
           if (more) {
             ks = rg.slot;
             if (!(ok = wait1(full(ks), rg.phase))) break;
             rg.next(T::kStages);
           }
-          const uint32_t vs = rg.slot;
-          if (!(ok = wait1(full(vs), rg.phase))) break;
-          rg.next(T::kStages);
-          if (!(ok = weighted(0, tc0++, vs, t > 0))) break;
-          if (more) scores(0u, q0, ks, s_full(0));
-          if (two) {
-            if (!(ok = weighted(1, tc1++, vs, t > 0))) break;
-            if (more) scores(128u, q1, ks, s_full(1));
+          if (t >= 0) {
+            vs = rg.slot;
+            if (!(ok = wait1(full(vs), rg.phase))) break;
+            rg.next(T::kStages);
           }
-          mma_commit(empty(vs));
+#pragma unroll 1
+          for (int g = 0; g < halves; ++g) {
+            const uint32_t col = tmem + 128u * g;
+            if (t >= 0) {
+              // O += P V as the two 64-key halves of P arrive
+              const uint64_t vb = v_ring + vs * kStep;
+              const uint32_t par = (tiles_of >> g) & 1u;
+              tiles_of ^= 1u << g;
+              if (!(ok = wait1(p_full(g, 0), par))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(col + 256u, col + 8u * k, vb + k * (2048 >> 4), kIdO, t > 0 || k > 0);
+              if (!(ok = wait1(p_full(g, 1), par))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 4; k < 8; ++k)
+                mma_ts(col + 256u, col + 8u * k, vb + k * (2048 >> 4), kIdO, 1u);
+              mma_commit(pv_done(g));
+            } else {
+              if (!(ok = wait1(q_full(g), (pieces_of >> g) & 1u))) break;
+              pieces_of ^= 1u << g;
+              tc_fence_after();
+            }
+            if (more) {
+              const uint64_t qa = q_half + g * kStep, kb = k_ring + ks * kStep;
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t at = (k / 4) * (kHalf >> 4) + (k % 4) * 2;
+                mma_bf16(col, qa + at, kb + at, kIdS, k > 0);
+              }
+              mma_commit(s_full(g));
+            }
+          }
+          if (!ok) break;
+          if (t >= 0) mma_commit(empty(vs));
           if (more) mma_commit(empty(ks));
         }
-        if (!ok) break;
       }
     }
     __syncwarp();
@@ -634,14 +675,20 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     auto emptyb = [&](uint32_t s) { return FP8 ? raw_empty(s) : empty(s); };
     AttnRec* rec = &attn_scratch(a.scratch, kTcBR).rec[blockIdx.x];
     if (lane == 0) rec->starts = rec->mid = rec->ends = 0;
-    for (;;) {
+    TcPiece d, d2;       // the piece being copied, and the one after it
+    int ds = 0, ds2 = 0;  // their sequences
+    // Publishes the next piece (nt = 0: none is left) and sends its query rows to L2: one run of
+    // the group's heads per token.
+    auto publish = [&](TcPiece& d, int& ds) {
       AttnPiece p;
       const bool have = next_piece(a.b, sh, cur, p);
-      TcPiece d;
-      d.nt = have ? p.tb - p.ta : 0;
+      d.nt = d.j0 = d.lo = d.hi = d.in_lo = d.in_hi = d.rows = d.r0 = 0;
+      d.q0 = d.n = d.L = d.head = d.slot = 0;
       if (have) {
         const KeyRange k0 = key_range(p.q, p.u.i0, sh.causal, sh.window);
         const KeyRange k1 = key_range(p.q, p.u.i1, sh.causal, sh.window);
+        ds = p.s;
+        d.nt = p.tb - p.ta;
         d.j0 = (p.u.t0 + p.ta) * kAttnTK;
         d.lo = p.u.lo;
         d.hi = p.u.hi;
@@ -663,28 +710,34 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
           rec->mid = 1;
           rec->ends = p.last();
         }
+        for (int i = p.u.i0 + lane; i <= p.u.i1; i += 32)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                           static_cast<const __nv_bfloat16*>(a.q) +
+                           (size_t)(p.q.q0 + i) * a.q_stride + (size_t)p.head * sh.G * D),
+                       "r"(sh.G * D * 2)
+                       : "memory");
       }
-      if (!wait(d_empty(dq.slot), dq.phase ^ 1u)) break;
+      if (!wait(d_empty(dq.slot), dq.phase ^ 1u)) return false;
       if (lane == 0) {
-        pieces[dq.slot] = d;
+        int4* dst = reinterpret_cast<int4*>(pieces + dq.slot);
+        dst[0] = make_int4(d.nt, d.j0, d.lo, d.hi);
+        dst[1] = make_int4(d.in_lo, d.in_hi, d.rows, d.r0);
+        dst[2] = make_int4(d.q0, d.n, d.L, d.head);
+        dst[3] = make_int4(d.slot, 0, 0, 0);
         mbar_arrive(d_full(dq.slot));
       }
       __syncwarp();
       dq.next(kTcPieces);
-      if (!have) break;
-      // the piece's query rows into L2: one run of its heads per token
-      for (int i = p.u.i0 + lane; i <= p.u.i1; i += 32)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                         static_cast<const __nv_bfloat16*>(a.q) +
-                         (size_t)(p.q.q0 + i) * a.q_stride + (size_t)p.head * sh.G * D),
-                     "r"(sh.G * D * 2)
-                     : "memory");
+      return true;
+    };
+    bool ok = publish(d, ds);
+    for (; ok && d.nt > 0; d = d2, ds = ds2) {
       auto live_at = [&](int t) {
         const int j = d.j0 + t * kAttnTK + pl * box_rows;
         return t < d.nt && lane < boxes && j < d.hi && j + box_rows > d.lo;
       };
       auto page_at = [&](int t) {
-        return live_at(t) ? page_of(a.b, p.s, d.j0 + t * kAttnTK + pl * box_rows) : 0;
+        return live_at(t) ? page_of(a.b, ds, d.j0 + t * kAttnTK + pl * box_rows) : 0;
       };
       auto copy = [&](int t, int page, bool v) {
         const bool live = live_at(t);
@@ -705,15 +758,15 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         return true;
       };
       int page = page_at(0), next = page_at(1);
-      bool ok = copy(0, page, false);
+      ok = copy(0, page, false);
       for (int t = 0; ok && t < d.nt; ++t) {
         const int after = page_at(t + 2);
         if (t + 1 < d.nt) ok = copy(t + 1, next, false);
         if (ok) ok = copy(t, page, true);
         page = next;
         next = after;
+        if (ok && t == 0) ok = publish(d2, ds2);  // one piece ahead, behind the first copies
       }
-      if (!ok) break;
     }
     if (*abort_flag && lane == 0)  // let what is in flight land before the CTA can exit
       for (uint32_t j = issued > kN ? issued - kN : 0; j < issued; ++j)

@@ -243,6 +243,15 @@ def test_paged_attention_long_context(cuda_lib):
     _check(p, _rand(p.gen, p.T, 4, 64), 4)
 
 
+@pytest.mark.parametrize("hq,hkv,d,cache", [(32, 8, 64, "bf16"), (12, 12, 128, "bf16"),
+                                            (28, 4, 128, "fp8")])
+def test_paged_attention_packed_prompts(cuda_lib, hq, hkv, d, cache):
+    """Units of one and of two halves after each other in every order, several to an SM."""
+    p = Paged([(1, 1), (700, 700), (33, 33), (1300, 1300), (5, 900), (100, 100), (1, 2000),
+               (400, 1100), (17, 17), (2, 2)], hkv, d, 16, cache, seed=12)
+    _check(p, _rand(p.gen, p.T, hq, d, std=1.5), hq)
+
+
 def test_paged_attention_offsets_past_32_bits(cuda_lib):
     """Pages beyond 2^31 elements of the cache."""
     p = Paged([(1, 200), (150, 333)], 8, 128, 128, seed=2)
