@@ -19,7 +19,7 @@
 //   warp 8           MMA issue (one elected thread)
 //   warp 9           the schedule, as a ring of piece descriptors ahead of the other roles, and
 //                    the tile copies: TMA, one box per page and 128 bytes of the head; page ids
-//                    two tiles ahead, the next piece's Q into L2
+//                    a tile ahead, the next piece's Q into L2
 //   warp 10          bf16 cache: zeroes what a V tile holds outside the unit's keys
 //   warps 10, 11     e4m3 cache: codes to f16 (exact) into the operand tiles
 //
@@ -608,11 +608,6 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         for (int t = -1; ok && t < nt; ++t) {
           const bool more = t + 1 < nt;
           uint32_t ks = 0, vs = 0;
-          if (more) {
-            ks = rg.slot;
-            if (!(ok = wait1(full(ks), rg.phase))) break;
-            rg.next(T::kStages);
-          }
           if (t >= 0) {
             vs = rg.slot;
             if (!(ok = wait1(full(vs), rg.phase))) break;
@@ -637,12 +632,18 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
               for (int k = 4; k < 8; ++k)
                 mma_ts(col + 256u, col + 8u * k, vb + k * (2048 >> 4), kIdO, 1u);
               mma_commit(pv_done(g));
+              if (g + 1 == halves) mma_commit(empty(vs));
             } else {
               if (!(ok = wait1(q_full(g), (pieces_of >> g) & 1u))) break;
               pieces_of ^= 1u << g;
               tc_fence_after();
             }
             if (more) {
+              if (g == 0) {
+                ks = rg.slot;
+                if (!(ok = wait1(full(ks), rg.phase))) break;
+                rg.next(T::kStages);
+              }
               const uint64_t qa = q_half + g * kStep, kb = k_ring + ks * kStep;
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
@@ -650,11 +651,9 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
                 mma_bf16(col, qa + at, kb + at, kIdS, k > 0);
               }
               mma_commit(s_full(g));
+              if (g + 1 == halves) mma_commit(empty(ks));
             }
           }
-          if (!ok) break;
-          if (t >= 0) mma_commit(empty(vs));
-          if (more) mma_commit(empty(ks));
         }
       }
     }
@@ -757,14 +756,11 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         rg.next(kN);
         return true;
       };
-      int page = page_at(0), next = page_at(1);
-      ok = copy(0, page, false);
+      int page = page_at(0);
       for (int t = 0; ok && t < d.nt; ++t) {
-        const int after = page_at(t + 2);
-        if (t + 1 < d.nt) ok = copy(t + 1, next, false);
-        if (ok) ok = copy(t, page, true);
+        const int next = page_at(t + 1);
+        ok = copy(t, page, false) && copy(t, page, true);
         page = next;
-        next = after;
         if (ok && t == 0) ok = publish(d2, ds2);  // one piece ahead, behind the first copies
       }
     }
@@ -783,8 +779,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       for (int t = 0; ok && t < p.nt; t += max(1, p.nt - 1)) {
         const int j0 = p.j0 + t * kAttnTK;
         if (!edge(p, j0)) continue;
-        // operands in the ring: K0, K1, V0, K2, V1, ..., K(nt-1), V(nt-2), V(nt-1)
-        const uint32_t slot = (at + (t + 1 < p.nt ? 2 * t + 2 : 2 * t + 1)) % T::kStages;
+        const uint32_t slot = (at + 2 * t + 1) % T::kStages;
         if (!(ok = wait(v_raw(slot), (phases >> slot) & 1u))) break;
         phases ^= 1u << slot;
         const int lo = max(p.lo - j0, 0), hi = min(p.hi - j0, kAttnTK);
@@ -847,11 +842,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     };
     TcPiece p;
     while (ok && get_piece(p)) {
-      ok = convert(p, 0, false);
-      for (int t = 0; ok && t < p.nt; ++t) {
-        if (t + 1 < p.nt) ok = convert(p, t + 1, false);
-        if (ok) ok = convert(p, t, true);
-      }
+      for (int t = 0; ok && t < p.nt; ++t) ok = convert(p, t, false) && convert(p, t, true);
     }
   }
   tc_fence_before();
