@@ -10,7 +10,6 @@
 namespace gbmoe {
 
 constexpr int kAttnMaxCtas = 160;  // workspace bound; the kernels run one CTA per SM
-constexpr int kAttnTK = 128;       // keys per tile
 constexpr int kAttnMaxBR = 256;    // rows per unit of the widest kernel
 
 // What a CTA's cut units look like, for the joining kernel: the unit that it begins and leaves
@@ -47,16 +46,41 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+constexpr int kPlanBlocks = 4;  // row blocks that one thread adds up by itself
+
 // This CTA's cursor; every thread of the block calls it. line: shared memory for S + 1 prefix
-// sums, wsum: 32 more.
+// sums, wsum: 32 more. A thread takes a sequence of few row blocks (single tokens), a warp one of
+// many: a prompt of 8191 tokens has 128, and one thread walking them cost 45 us.
 __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnShape& sh,
                                                 long long* line, long long* wsum) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int warps = nt >> 5;
+  for (int s = tid; s < b.S; s += nt) {
+    const SeqInfo q = seq_info(b, s);
+    line[s + 1] = unit_blocks(sh, q.n) <= kPlanBlocks ? seq_length(sh, q) * sh.hkv : -1;
+  }
+  if (tid == 0) line[0] = 0;
+  __syncthreads();
+  for (int s0 = warp * 32; s0 < b.S; s0 += warps * 32) {
+    uint32_t many = __ballot_sync(0xffffffffu, s0 + lane < b.S && line[s0 + lane + 1] < 0);
+    while (many) {
+      const int s = s0 + __ffs(many) - 1;
+      many &= many - 1;
+      const SeqInfo q = seq_info(b, s);
+      long long t = 0;
+      for (int rb = lane; rb < unit_blocks(sh, q.n); rb += 32) t += unit_length(sh, q, rb);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (lane == 0) line[s + 1] = t * sh.hkv;
+    }
+  }
+  __syncthreads();
+  // prefix sums: a run of sequences per thread
   const int per = (b.S + nt - 1) / nt;
   const int s0 = min(tid * per, b.S), s1 = min(s0 + per, b.S);
   long long sum = 0;
   for (int s = s0; s < s1; ++s) {
-    sum += seq_tiles(sh, seq_info(b, s)) * sh.hkv;
+    sum += line[s + 1];
     line[s + 1] = sum;
   }
   long long inc = sum;
@@ -66,7 +90,6 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
     if (lane >= o) inc += v;
   }
   if (lane == 31) wsum[warp] = inc;
-  if (tid == 0) line[0] = 0;
   __syncthreads();
   long long base = inc - sum;
   for (int w = 0; w < warp; ++w) base += wsum[w];
@@ -85,7 +108,39 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
       if (line[mid] <= a) lo = mid;
       else hi = mid;
     }
-    c = cursor_in_seq(sh, seq_info(b, lo), lo, a - line[lo], e - a);
+    const SeqInfo q = seq_info(b, lo);
+    const long long head = (line[lo + 1] - line[lo]) / sh.hkv;  // length of one head
+    long long rem = a - line[lo];
+    c.s = lo;
+    c.left = e - a;
+    while (c.head + 1 < sh.hkv && rem >= head) {
+      rem -= head;
+      ++c.head;
+    }
+    const int blocks = unit_blocks(sh, q.n);
+    if (blocks > kPlanBlocks) {
+      // every warp finds the row block, 32 at a time
+      for (; c.rb < blocks; c.rb += 32) {
+        const int rb = c.rb + lane;
+        long long at = rb < blocks ? unit_length(sh, q, rb) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += v;
+        }
+        const uint32_t behind = __ballot_sync(0xffffffffu, at <= rem);
+        if (behind != 0xffffffffu) {
+          const int k = __popc(behind);  // whole units behind the cursor
+          if (k > 0) rem -= __shfl_sync(0xffffffffu, at, k - 1);
+          c.rb += k;
+          break;
+        }
+        rem -= __shfl_sync(0xffffffffu, at, 31);
+      }
+      c.off = (int)rem;
+    } else {
+      walk_blocks(sh, q, rem, c);
+    }
   }
   return c;
 }
@@ -143,19 +198,19 @@ template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh, int ctas) {
   constexpr int C = D / 16;  // columns per thread
   pdl_wait();
-  const AttnScratch sc = attn_scratch(a.scratch, sh.BR);
+  const AttnScratch sc = attn_scratch(a.scratch, 1 << sh.br_shift);
   const int c0 = blockIdx.x;
   const AttnRec rec = sc.rec[c0];
   if (!rec.starts) return;
   const SeqInfo q = seq_info(a.b, rec.s);
   const int row = blockIdx.y * 16 + threadIdx.x / 16, col = threadIdx.x % 16 * C;
-  const int r = rec.rb * sh.BR + row;
+  const int r = (rec.rb << sh.br_shift) + row;
   if (r >= q.n * sh.G) return;
-  float M = sc.ml[(size_t)(2 * c0 + 1) * sh.BR + row].x;
+  float M = sc.ml[((size_t)(2 * c0 + 1) << sh.br_shift) + row].x;
   int c1 = c0;  // the last CTA with a piece (CTAs between them may have had no tile)
   while (c1 + 1 < ctas) {
     const AttnRec r1 = sc.rec[++c1];
-    if (r1.mid) M = fmaxf(M, sc.ml[(size_t)(2 * c1) * sh.BR + row].x);
+    if (r1.mid) M = fmaxf(M, sc.ml[((size_t)(2 * c1) << sh.br_shift) + row].x);
     if (r1.ends) break;
   }
   const float Ms = M == -INFINITY ? 0.f : M;
@@ -165,7 +220,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh
 #pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
     if (c > c0 && !sc.rec[c].mid) continue;
-    const size_t at = (size_t)(c == c0 ? 2 * c + 1 : 2 * c) * sh.BR + row;
+    const size_t at = ((size_t)(c == c0 ? 2 * c + 1 : 2 * c) << sh.br_shift) + row;
     const float2 ml = sc.ml[at];
     const float w = ex2(ml.x - Ms);
     l = fmaf(w, ml.y, l);
@@ -190,7 +245,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh
 
 cudaError_t launch_attn_join(const AttnArgs& a, const AttnShape& sh, int ctas,
                              cudaStream_t stream) {
-  const dim3 grid(ctas, sh.BR / 16);
+  const dim3 grid(ctas, (1 << sh.br_shift) / 16);
   if (a.D == 64) launch_kernel(attn_join_kernel<64>, grid, dim3(256), 0, stream, a, sh, ctas);
   else launch_kernel(attn_join_kernel<128>, grid, dim3(256), 0, stream, a, sh, ctas);
   return cudaGetLastError();

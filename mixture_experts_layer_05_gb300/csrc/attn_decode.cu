@@ -499,8 +499,8 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   AttnShape sh;
   sh.G = a.hq / a.hkv;
   sh.hkv = a.hkv;
-  sh.BR = kDecBR;
-  sh.TK = kAttnTK;
+  sh.br_shift = 4;
+  static_assert(kDecBR == 1 << 4, "rows per unit");
   sh.extra = 0;
   sh.causal = a.causal;
   sh.window = a.window;

@@ -13,9 +13,11 @@
 
 namespace gbmoe {
 
+constexpr int kAttnTK = 128;  // keys per tile
+
 struct AttnShape {
   int G, hkv;      // query heads per kv head, kv heads
-  int BR, TK;      // rows per unit, keys per tile
+  int br_shift;    // rows per unit: 1 << br_shift
   int extra;       // cost of a unit beyond its tiles, in tiles
   bool causal;
   int window;
@@ -24,15 +26,17 @@ struct AttnShape {
 struct UnitKeys {
   int i0, i1;      // first and last token of the unit
   int lo, hi;      // keys that any of them attends: [lo, hi), hi <= lo when none
-  int t0, tiles;   // tiles t0 .. t0 + tiles - 1, tile t holding the keys [t * TK, (t + 1) * TK)
+  int t0, tiles;   // tiles t0 .. t0 + tiles - 1, tile t holding the keys from t * kAttnTK
 };
 
-GBMOE_HD int unit_blocks(const AttnShape& a, int n) { return (n * a.G + a.BR - 1) / a.BR; }
+GBMOE_HD int unit_blocks(const AttnShape& a, int n) {
+  return (n * a.G + (1 << a.br_shift) - 1) >> a.br_shift;
+}
 
 GBMOE_HD UnitKeys unit_keys(const AttnShape& a, const SeqInfo& q, int rb) {
   UnitKeys u;
-  const int r0 = rb * a.BR;
-  int r1 = r0 + a.BR;
+  const int r0 = rb << a.br_shift;
+  int r1 = r0 + (1 << a.br_shift);
   if (r1 > q.n * a.G) r1 = q.n * a.G;
   u.i0 = r0 / a.G;
   u.i1 = (r1 - 1) / a.G;
@@ -43,17 +47,20 @@ GBMOE_HD UnitKeys unit_keys(const AttnShape& a, const SeqInfo& q, int rb) {
     u.t0 = 0;
     u.tiles = 1;
   } else {
-    u.t0 = u.lo / a.TK;
-    u.tiles = (u.hi + a.TK - 1) / a.TK - u.t0;
+    u.t0 = u.lo / kAttnTK;
+    u.tiles = (u.hi + kAttnTK - 1) / kAttnTK - u.t0;
   }
   return u;
 }
 
-// Length on the line of one kv head of a sequence.
-GBMOE_HD long long seq_tiles(const AttnShape& a, const SeqInfo& q) {
+// Length on the line of a unit, and of one kv head of a sequence.
+GBMOE_HD int unit_length(const AttnShape& a, const SeqInfo& q, int rb) {
+  return unit_keys(a, q, rb).tiles + a.extra;
+}
+GBMOE_HD long long seq_length(const AttnShape& a, const SeqInfo& q) {
   const int blocks = unit_blocks(a, q.n);
   long long t = 0;
-  for (int rb = 0; rb < blocks; ++rb) t += unit_keys(a, q, rb).tiles + a.extra;
+  for (int rb = 0; rb < blocks; ++rb) t += unit_length(a, q, rb);
   return t;
 }
 
@@ -63,24 +70,15 @@ struct AttnCursor {
   long long left;          // length of this CTA's range that lies ahead
 };
 
-// The cursor `rem` into sequence s (rem < hkv * the length of one head).
-GBMOE_HD AttnCursor cursor_in_seq(const AttnShape& a, const SeqInfo& q, int s, long long rem,
-                                  long long left) {
-  AttnCursor c;
-  const long long per = seq_tiles(a, q);
-  c.s = s;
-  c.head = (int)(rem / per);
-  rem -= c.head * per;
-  c.rb = 0;
+// Moves the cursor `rem` further, over row blocks of the sequence q.
+GBMOE_HD void walk_blocks(const AttnShape& a, const SeqInfo& q, long long rem, AttnCursor& c) {
   for (;;) {
-    const int t = unit_keys(a, q, c.rb).tiles + a.extra;
+    const int t = unit_length(a, q, c.rb);
     if (rem < t) break;
     rem -= t;
     ++c.rb;
   }
   c.off = (int)rem;
-  c.left = left;
-  return c;
 }
 
 // The part of a unit that one CTA computes.

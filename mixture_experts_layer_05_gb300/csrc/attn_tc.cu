@@ -871,8 +871,8 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   AttnShape sh;
   sh.G = a.hq / a.hkv;
   sh.hkv = a.hkv;
-  sh.BR = kTcBR;
-  sh.TK = kAttnTK;
+  sh.br_shift = 8;
+  static_assert(kTcBR == 1 << 8, "rows per unit");
   sh.extra = kTcExtra;
   sh.causal = a.causal;
   sh.window = a.window;

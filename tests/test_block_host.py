@@ -226,8 +226,8 @@ using namespace gbmoe;
 int main() {
   AttnShape a;
   int causal, g, S;
-  while (scanf("%d %d %d %d %d %d %d %d %d", &a.G, &a.hkv, &a.BR, &a.TK, &a.extra, &causal,
-               &a.window, &g, &S) == 9) {
+  while (scanf("%d %d %d %d %d %d %d %d", &a.G, &a.hkv, &a.br_shift, &a.extra, &causal,
+               &a.window, &g, &S) == 8) {
     a.causal = causal != 0;
     std::vector<SeqInfo> q(S);
     std::vector<long long> line(S + 1, 0);
@@ -235,14 +235,16 @@ int main() {
       if (scanf("%d %d", &q[s].n, &q[s].L) != 2) return 1;
       q[s].q0 = q0;
       q0 += q[s].n;
-      line[s + 1] = line[s] + seq_tiles(a, q[s]) * a.hkv;
+      line[s + 1] = line[s] + seq_length(a, q[s]) * a.hkv;
     }
     for (int c = 0; c < g; ++c) {
       const long long at = range_at(line[S], c, g), end = range_at(line[S], c + 1, g);
       if (end <= at) continue;
       int s = 0;
       while (line[s + 1] <= at) ++s;
-      AttnCursor cur = cursor_in_seq(a, q[s], s, at - line[s], end - at);
+      const long long head = (line[s + 1] - line[s]) / a.hkv;
+      AttnCursor cur = {s, (int)((at - line[s]) / head), 0, 0, end - at};
+      walk_blocks(a, q[s], (at - line[s]) % head, cur);
       while (cur.left > 0) {
         while (q[cur.s].n == 0) ++cur.s;
         const AttnPiece p = take_piece(a, q[cur.s], cur);
@@ -274,15 +276,16 @@ def test_attention_work_is_cut_whole(tmp_path):
             seqs.append((n, max(0, rng.choice([n, n + 1, n - 2, n + 127, n + 128, n + 5000, 0]))))
         if not any(n for n, _ in seqs):
             seqs[0] = (1, 3)
-        cases.append((rng.choice([1, 3, 4, 8]), rng.choice([1, 2, 8]), rng.choice([16, 256]), 128,
+        cases.append((rng.choice([1, 3, 4, 8]), rng.choice([1, 2, 8]), rng.choice([4, 8]),
                       rng.choice([0, 1, 3]), int(rng.random() < 0.8), rng.choice([0, 0, 1, 100, 1000]),
                       rng.choice([1, 7, 148, 152]), S, seqs))
-    text = "\n".join(" ".join(map(str, c[:9])) + " " + " ".join(f"{n} {L}" for n, L in c[9])
+    text = "\n".join(" ".join(map(str, c[:8])) + " " + " ".join(f"{n} {L}" for n, L in c[8])
                      for c in cases)
     out = subprocess.run([str(tmp_path / "plan")], input=text, text=True, capture_output=True,
                          check=True).stdout.splitlines()
     assert len(out) == len(cases)
-    for (G, hkv, BR, TK, extra, causal, window, g, S, seqs), line in zip(cases, out):
+    for (G, hkv, shift, extra, causal, window, g, S, seqs), line in zip(cases, out):
+        BR, TK = 1 << shift, 128
         v = [int(x) for x in line.split()]
         pieces = [tuple(v[i:i + 8]) for i in range(0, len(v), 8)]
         units = {}
