@@ -576,8 +576,9 @@ gbmoe_status_t moe_kv_append(const gbmoe_attn_config_t* cfg, int32_t num_tokens,
  *   out  [T, num_q_heads, head_dim] bf16 contiguous (out)
  *   lse  [T, num_q_heads] fp32 (out) or NULL
  * Workspace: moe_paged_attention_workspace_size(cfg) bytes (0: bad configuration), 256-byte
- * aligned, its first 256 bytes zeroed once. T = 0 is a no-op; T * num_q_heads at most 2^30
- * (else UNSUPPORTED).
+ * aligned, its first 1024 bytes zeroed once (and again after a GBMOE_ERR_TIMEOUT: beside the
+ * status word they hold counters that every completed call leaves at zero). T = 0 is a no-op;
+ * T * num_q_heads at most 2^30 (else UNSUPPORTED).
  */
 size_t moe_paged_attention_workspace_size(const gbmoe_attn_config_t* cfg);
 gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int32_t num_tokens,

@@ -540,7 +540,8 @@ class PagedAttention:
         n = load().moe_paged_attention_workspace_size(ctypes.byref(cfg))
         if n == 0:
             raise GbmoeError("moe_paged_attention_workspace_size", ERR_INVALID_ARG)
-        self.workspace = alloc_workspace(n, device)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        self.workspace[:1024].zero_()         # status word and counters
         self._dtypes = ((torch.bfloat16,) if cfg.cache_type == CACHE["bf16"]
                         else (torch.float8_e4m3fn, torch.uint8))
 

@@ -9,15 +9,15 @@
 
 namespace gbmoe {
 
-constexpr int kAttnMaxCtas = 160;  // workspace bound; the kernels run one CTA per SM
 constexpr int kAttnMaxBR = 256;    // rows per unit of the widest kernel
 
 // What a CTA's cut units look like, for the joining kernel: the unit that it begins and leaves
 // to the next CTA (starts), whether its first piece is of a unit begun before it (mid), and
 // whether that unit ends there.
 struct AttnRec {
-  int starts, mid, ends;
-  int s, head, rb, pad[2];
+  int starts, rb;
+  int mid, ends;
+  int q0, n, head, pad;  // the begun unit's sequence and kv head
 };
 
 // The workspace after the status region: records, then per CTA two piece slots (2c: a unit begun
@@ -46,13 +46,27 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The line, the CTAs that share it, and the end of this one's range.
+struct AttnSpan {
+  long long W, end;
+  int ctas;
+};
+// The CTA whose range holds the place x of the line.
+__device__ __forceinline__ int cta_of(const AttnSpan& s, long long x) {
+  int c = (int)(x * s.ctas / s.W);
+  while (range_at(s.W, c + 1, s.ctas) <= x) ++c;
+  while (range_at(s.W, c, s.ctas) > x) --c;
+  return c;
+}
+
 constexpr int kPlanBlocks = 4;  // row blocks that one thread adds up by itself
 
 // This CTA's cursor; every thread of the block calls it. line: shared memory for S + 1 prefix
 // sums, wsum: 32 more. A thread takes a sequence of few row blocks (single tokens), a warp one of
 // many: a prompt of 8191 tokens has 128, and one thread walking them cost 45 us.
 __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnShape& sh,
-                                                long long* line, long long* wsum) {
+                                                long long* line, long long* wsum,
+                                                AttnSpan& span) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int warps = nt >> 5;
   for (int s = tid; s < b.S; s += nt) {
@@ -96,8 +110,12 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
   for (int s = s0; s < s1; ++s) line[s + 1] += base;
   __syncthreads();
   const long long W = line[b.S];
-  const long long a = range_at(W, blockIdx.x, gridDim.x);
-  const long long e = range_at(W, blockIdx.x + 1, gridDim.x);
+  span.W = W;
+  span.ctas = W < gridDim.x ? (int)W : (int)gridDim.x;  // every one of these has some of the line
+  const int me = min((int)blockIdx.x, span.ctas);
+  const long long a = range_at(W, me, max(span.ctas, 1));
+  const long long e = me < span.ctas ? range_at(W, me + 1, span.ctas) : a;
+  span.end = e;
   AttnCursor c;
   c.s = c.head = c.rb = c.off = 0;
   c.left = 0;
@@ -184,35 +202,52 @@ bool make_cache_map(CUtensorMap* m, const void* ptr, const AttnArgs& a) {
   const cuuint32_t inner = a.D * es < 128 ? a.D : 128 / es;
   const cuuint32_t box[4] = {inner, (cuuint32_t)(ps < kAttnTK ? ps : kAttnTK), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
+  // L2 fetches no more than a row of the head holds: what follows it belongs to other heads,
+  // whose CTAs are elsewhere in the sequence
+  const int run = a.c.token_stride == a.D ? 256 : a.D * es;
+  const CUtensorMapL2promotion fetch = run >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                       : run >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                    : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   return enc(m, a.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
              const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              inner * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
+             fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Joins the pieces of the units that CTA boundaries cut. Block (c, y): rows [16 y, 16 y + 16) of
+// Joins the pieces of the units that CTA boundaries cut. Block (c, y): rows [32 y, 32 y + 32) of
 // the unit that CTA c began and did not finish. out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i
-// over its pieces in order, M = max m_i: 16 threads a row, so a piece's rows are read whole.
+// over its pieces in order, M = max m_i: 8 threads a row.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh, int ctas) {
-  constexpr int C = D / 16;  // columns per thread
+  constexpr int C = D / 8;  // columns per thread
   pdl_wait();
+  const int lane = threadIdx.x & 31;
   const AttnScratch sc = attn_scratch(a.scratch, 1 << sh.br_shift);
   const int c0 = blockIdx.x;
   const AttnRec rec = sc.rec[c0];
-  if (!rec.starts) return;
-  const SeqInfo q = seq_info(a.b, rec.s);
-  const int row = blockIdx.y * 16 + threadIdx.x / 16, col = threadIdx.x % 16 * C;
-  const int r = (rec.rb << sh.br_shift) + row;
-  if (r >= q.n * sh.G) return;
-  float M = sc.ml[((size_t)(2 * c0 + 1) << sh.br_shift) + row].x;
-  int c1 = c0;  // the last CTA with a piece (CTAs between them may have had no tile)
-  while (c1 + 1 < ctas) {
-    const AttnRec r1 = sc.rec[++c1];
-    if (r1.mid) M = fmaxf(M, sc.ml[((size_t)(2 * c1) << sh.br_shift) + row].x);
-    if (r1.ends) break;
+  // the CTAs after c0: which hold a piece, and where the unit ends
+  int2 r[kAttnMaxCtas / 32];  // (mid, ends)
+#pragma unroll
+  for (int i = 0; i < kAttnMaxCtas / 32; ++i) {
+    const int c = c0 + 1 + 32 * i + lane;
+    r[i] = c < ctas ? *reinterpret_cast<const int2*>(&sc.rec[c].mid) : make_int2(0, 0);
   }
+  if (!rec.starts) return;
+  int c1 = ctas - 1;
+#pragma unroll
+  for (int i = kAttnMaxCtas / 32 - 1; i >= 0; --i) {
+    const uint32_t end = __ballot_sync(0xffffffffu, r[i].x && r[i].y);
+    if (end) c1 = c0 + 32 * i + __ffs(end);
+  }
+  const int row = blockIdx.y * 32 + threadIdx.x / 8, col = threadIdx.x % 8 * C;
+  const int ur = (rec.rb << sh.br_shift) + row;
+  if (ur >= rec.n * sh.G) return;
+  const size_t first = ((size_t)(2 * c0 + 1) << sh.br_shift) + row;
+  float2 ml = sc.ml[first];
+  float M = ml.x;
+#pragma unroll 4
+  for (int c = c0 + 1; c <= c1; ++c)
+    if (sc.rec[c].mid) M = fmaxf(M, sc.ml[((size_t)(2 * c) << sh.br_shift) + row].x);
   const float Ms = M == -INFINITY ? 0.f : M;
   float l = 0.f, o[C];
 #pragma unroll
@@ -220,7 +255,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh
 #pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
     if (c > c0 && !sc.rec[c].mid) continue;
-    const size_t at = ((size_t)(c == c0 ? 2 * c + 1 : 2 * c) << sh.br_shift) + row;
+    const size_t at = c == c0 ? first : ((size_t)(2 * c) << sh.br_shift) + row;
     const float2 ml = sc.ml[at];
     const float w = ex2(ml.x - Ms);
     l = fmaf(w, ml.y, l);
@@ -234,7 +269,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh
       o[4 * i + 3] = fmaf(w, v.w, o[4 * i + 3]);
     }
   }
-  const size_t orow = (size_t)(q.q0 + r / sh.G) * a.hq + rec.head * sh.G + r % sh.G;
+  const size_t orow = (size_t)(rec.q0 + ur / sh.G) * a.hq + rec.head * sh.G + ur % sh.G;
   const float inv = l == 0.f ? 0.f : a.v_scale / l;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + col);
 #pragma unroll
@@ -245,7 +280,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh
 
 cudaError_t launch_attn_join(const AttnArgs& a, const AttnShape& sh, int ctas,
                              cudaStream_t stream) {
-  const dim3 grid(ctas, (1 << sh.br_shift) / 16);
+  const dim3 grid(ctas, (1 << sh.br_shift) / 32);
   if (a.D == 64) launch_kernel(attn_join_kernel<64>, grid, dim3(256), 0, stream, a, sh, ctas);
   else launch_kernel(attn_join_kernel<128>, grid, dim3(256), 0, stream, a, sh, ctas);
   return cudaGetLastError();

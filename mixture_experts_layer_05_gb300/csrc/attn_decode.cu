@@ -1,15 +1,22 @@
-// Paged attention of few query rows per kv head (single tokens, short drafts): units of 16 rows
-// (token, query head of the group), bound by reading K and V once from HBM.
+// Paged attention of few query rows per kv head (single tokens, short drafts): units of 8 or 16
+// rows (token, query head of the group), bound by reading K and V once from HBM.
 //
 // One persistent CTA per SM takes an equal share of all sequences' key tiles (attn_plan.h). Warp
 // 8 streams tiles of 128 keys through a ring of shared-memory stages with TMA, one box per page
 // and 128 bytes of the head, 128-byte swizzled; the page ids of a tile are fetched one tile
-// ahead. Warps 0..7 own 16 keys of every tile each:
-//   S = Q K^T (16 x 16 by mma.m16n8k16, fp32), p = 2^(S - m), O += P V,
-// with a running maximum, sum and O of their own, so that no tile needs a barrier between
-// warps; they are joined through shared memory at the end of a piece. A 16-row product leaves
-// the tensor cores almost idle whatever form it takes, and this one needs neither tensor
-// memory nor a trip of P through shared memory.
+// ahead. Warps 0..7 own 16 keys of every tile each, with a running maximum, sum and O of their
+// own, so that no tile needs a barrier between warps; they are joined through shared memory at
+// the end of a piece. Keys and columns lie on the M side of mma.m16n8k16 and the rows on its N
+// side, which 8 rows fill:
+//   S^T = K Q^T (16 keys x 8 rows, fp32), p = 2^(s - m), O^T += V^T P^T (16 columns x 8 rows).
+// Such a product leaves the tensor cores almost idle whatever form it takes, and this one needs
+// neither tensor memory nor a trip of P through shared memory (movmatrix turns it). With the
+// rows on M instead, half of every product was padding and the e4m3 cache ran at 3.0 TB/s.
+// Where a tile is 16 KB (e4m3, or 64 columns) the warps take two at a time: the chain of product,
+// maximum, weights, product of one takes longer than HBM takes for the tile.
+//
+// A unit that the cut between CTAs crosses is joined by the CTA that finishes last (a counter per
+// unit, returned to zero), in the pieces' order: the result does not depend on who that is.
 //
 // bf16 cache: bf16 products, P rounded to bf16. e4m3 cache: codes become f16 (exact) and the
 // products run in f16 with Q rounded (saturating) and P rounded to f16; the scales of k and v
@@ -23,20 +30,25 @@ namespace {
 
 constexpr int kDecWarps = 8;
 constexpr int kDecThreads = 32 * (kDecWarps + 1);
-constexpr int kDecBR = 16;
-constexpr uint32_t kDecRing = 160 * 1024;
-constexpr uint32_t kDecJoin = 64 * 1024;  // 8 warps x 16 rows x 128 columns fp32
-constexpr size_t kDecSmem = 1024 + kDecRing + kDecJoin + 2048;
-static_assert(kDecSmem <= 232448, "shared memory per CTA exceeded");
 
-template <bool FP8, int D>
+// NT: rows per unit / 8
+template <bool FP8, int D, int NT>
 struct Dec {
+  static constexpr int kBR = 8 * NT;
   static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
   static constexpr int kPitch = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a box row
   static constexpr int kParts = kRowBytes / kPitch;                 // boxes across a row
   static constexpr uint32_t kStage = kAttnTK * kRowBytes;           // one K or V tile
-  static constexpr int kStages = kDecRing / kStage < 10 ? kDecRing / kStage : 10;
+  static constexpr uint32_t kRing = (NT == 1 ? 192 : 160) * 1024;
+  static constexpr int kStages = kRing / kStage < 12 ? kRing / kStage : 12;
   static constexpr uint32_t kSwz = kPitch == 128 ? 0x70u : 0x30u;
+  static constexpr int kAtOnce = kStages >= 8 ? 2 : 1;              // tiles per softmax step
+  static constexpr int kJoinPitch = D + (NT == 1 ? 4 : 0);          // floats (4: no conflicts)
+  static constexpr uint32_t kJoin = kDecWarps * kBR * kJoinPitch * 4;
+  static constexpr uint32_t kTail = NT == 1 ? 1024 : 2048;          // barriers, row sums
+  static constexpr size_t kSmem = 1024 + kRing + kJoin + kTail;
+  static_assert(kSmem <= 232448, "shared memory per CTA exceeded");
+  static_assert((kAttnMaxSeqs + 1) * 8 <= kRing, "the plan lies in the ring");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -75,12 +87,17 @@ template <bool F16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
-// Two e4m3 bytes (low byte first) as an f16 pair (exact).
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-      : "=r"(r)
+// Four e4m3 bytes as two f16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(a), "=r"(b)
       : "r"(w));
+}
+// Transposes an 8x8 matrix of 16-bit values held two to a lane.
+__device__ __forceinline__ uint32_t turn(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
@@ -113,25 +130,25 @@ struct DecMaps {
   CUtensorMap k, v;
 };
 
-template <bool FP8, int D>
+template <bool FP8, int D, int NT>
 __global__ void __launch_bounds__(kDecThreads, 1)
     attn_decode_kernel(const __grid_constant__ DecMaps maps, const __grid_constant__ AttnArgs a,
                        const __grid_constant__ AttnShape sh) {
-  using T = Dec<FP8, D>;
+  using T = Dec<FP8, D, NT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw0 = smem_addr(smem_raw);
   const uint32_t base = (raw0 + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw0);
-  float* join = reinterpret_cast<float*>(smem + kDecRing);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDecRing + kDecJoin);
+  float* join = reinterpret_cast<float*>(smem + T::kRing);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kRing + T::kJoin);
   const uint32_t bar0 = smem_addr(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
-  auto empty = [&](int s) { return bar0 + 8u * (10 + s); };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 20);
-  float2* wml = reinterpret_cast<float2*>(bars + 24);              // [16 rows][8 warps] = 1 KB
-  long long* wsum = reinterpret_cast<long long*>(bars + 24 + 128);  // 32
+  auto empty = [&](int s) { return bar0 + 8u * (12 + s); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 24);
+  float2* wml = reinterpret_cast<float2*>(bars + 26);  // [rows][warps]
+  long long* wsum = reinterpret_cast<long long*>(bars + 26 + T::kBR * kDecWarps);  // 32
+  static_assert((26 + T::kBR * kDecWarps + 32) * 8 <= T::kTail, "tail");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
       mbar_init(full(s), 1);
@@ -143,7 +160,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     tma_prefetch(&maps.v);
   }
   // the line of tiles is laid out in the ring before the first copy lands there
-  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<long long*>(smem), wsum);
+  AttnSpan span;
+  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<long long*>(smem), wsum, span);
   fence_async_proxy();
   __syncthreads();
   int* status = a.b.status;
@@ -204,228 +222,284 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ 16 keys of every tile
-    const AttnScratch sc = attn_scratch(a.scratch, kDecBR);
-    AttnRec rec;
-    rec.starts = rec.mid = rec.ends = rec.s = rec.head = rec.rb = 0;
+    const AttnScratch sc = attn_scratch(a.scratch, T::kBR);
     const int g = lane >> 2, c = lane & 3;
-    uint32_t slot = 0, phase = 0;
+    uint32_t at = 0;  // ring position of the next tile's K
     bool ok = true;
-    auto next_stage = [&]() {
-      if (++slot == T::kStages) {
-        slot = 0;
-        phase ^= 1u;
-      }
-    };
     auto swz = [](uint32_t off) { return off ^ ((off >> 3) & T::kSwz); };
-    while (cur.left > 0) {
+    for (;;) {
+      const long long unit_at = span.end - cur.left - cur.off;  // the unit's place on the line
       AttnPiece p;
       if (!next_piece(a.b, sh, cur, p)) break;
-      const int rows = min(kDecBR, p.q.n * sh.G - p.rb * kDecBR);
-      // this lane's two rows: their query vectors as mma fragments, and their keys
-      uint32_t qf[D / 16][4];
-      KeyRange kr[2];
+      auto write_out = [&](int r, int d, const float4& v, float M, float L) {
+        const int rr = p.rb * T::kBR + r;
+        const size_t orow = (size_t)(p.q.q0 + rr / sh.G) * a.hq + p.head * sh.G + rr % sh.G;
+        const float inv = L == 0.f ? 0.f : a.v_scale / L;  // no key: zeros
+        uint2 w;
+        w.x = pack_bf16x2(v.x * inv, v.y * inv);
+        w.y = pack_bf16x2(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + d) = w;
+        if (a.lse && d == 0)
+          a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      };
+      const int rows = min(T::kBR, p.q.n * sh.G - p.rb * T::kBR);
+      // this lane's query columns of row 8 n + lane / 4, as the B side of the products: two
+      // pairs of each 16 columns
+      uint32_t qf[NT][D / 16][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = g + 8 * h;
-        const bool valid = r < rows;
-        const int rr = p.rb * kDecBR + (valid ? r : 0);
-        const int i = rr / sh.G;
-        kr[h] = key_range(p.q, i, sh.causal, sh.window);
-        if (!valid) kr[h].hi = kr[h].lo = 0;
+      for (int n = 0; n < NT; ++n) {
+        const int r = 8 * n + g, rr = p.rb * T::kBR + (r < rows ? r : 0);
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                   (size_t)(p.q.q0 + i) * a.q_stride +
+                                   (size_t)(p.q.q0 + rr / sh.G) * a.q_stride +
                                    (size_t)(p.head * sh.G + rr % sh.G) * D;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t lo = 0u, hi = 0u;
-          if (valid && FP8) {
+          if (r < rows && FP8) {
             // e4m3 fragments hold columns 4c .. 4c + 3 of each 16: Q's follow that order
             const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + 16 * k + 4 * c));
             const float2 x = unpack_bf16x2(w.x), y = unpack_bf16x2(w.y);
             auto cut = [](float v) { return v > 65504.f ? 65504.f : (v < -65504.f ? -65504.f : v); };
             lo = pack_f16x2(cut(x.x), cut(x.y));
             hi = pack_f16x2(cut(y.x), cut(y.y));
-          } else if (valid) {
+          } else if (r < rows) {
             lo = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * c));
             hi = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * c));
           }
-          qf[k][h] = lo;
-          qf[k][2 + h] = hi;
+          qf[n][k][0] = lo;
+          qf[n][k][1] = hi;
         }
       }
-      // keys that every row of the unit attends need no mask
+      // the keys of this lane's rows 8 n + 2 c + e; those that every row attends need no mask
+      KeyRange kr[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * n + 2 * c + e;
+          kr[n][e] = key_range(p.q, (p.rb * T::kBR + r) / sh.G, sh.causal, sh.window);
+          if (r >= rows) kr[n][e].hi = kr[n][e].lo = 0;
+        }
       const KeyRange k0 = key_range(p.q, p.u.i0, sh.causal, sh.window);
       const KeyRange k1 = key_range(p.q, p.u.i1, sh.causal, sh.window);
-      float o[D / 8][4];
+      float o[NT][D / 16][4];  // (column 16 i + g, row 2 c), (.., row 2 c + 1), (column + 8, ..)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
+      float m[NT][2], l[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+      }
 
-      for (int t = p.ta; t < p.tb; ++t) {
-        const int j0 = (p.u.t0 + t) * kAttnTK + warp * 16;  // this warp's keys
-        const bool some = j0 < p.u.hi && j0 + 16 > p.u.lo;
-        uint32_t pf[4];
-        if (!wait_fast(full(slot), phase, abort_flag, status)) {
-          ok = false;
-          break;
-        }
-        if (some) {
-          const uint32_t st = base + slot * T::kStage;
-          float s[2][4];
+      for (int t = p.ta; ok && t < p.tb; t += T::kAtOnce) {
+        const int count = min(T::kAtOnce, p.tb - t);
+        // tile t + u: K in ring position at + 2 u, V in the next; this warp's keys from j0 + 128 u
+        const int j0 = (p.u.t0 + t) * kAttnTK + warp * 16;
+        auto some = [&](int u) {
+          return u < count && j0 + kAttnTK * u < p.u.hi && j0 + kAttnTK * u + 16 > p.u.lo;
+        };
+        auto slot = [&](uint32_t pos) { return pos % T::kStages; };
+        auto filled = [&](uint32_t pos) {
+          return wait_fast(full(slot(pos)), pos / T::kStages & 1u, abort_flag, status);
+        };
+        auto release = [&](uint32_t pos) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty(slot(pos)));
+        };
+        // S^T: (key g, row 2 c), (key g, row 2 c + 1), (key g + 8, ..)
+        float s[T::kAtOnce][NT][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int u = 0; u < T::kAtOnce; ++u) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-          if (FP8) {
-            // one ldmatrix: keys 0-7 and 8-15 x 32 columns, 16 bytes per 8x8 matrix row
-            const uint32_t row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              uint32_t w[4];
-              ldsm4(st + swz(row * T::kPitch + k * 32 + ((lane >> 3) & 1) * 16), w);
+            for (int j = 0; j < 4; ++j) s[u][n][j] = 0.f;
+          if (u >= count) continue;
+          const uint32_t pos = at + 2 * u;
+          if (!filled(pos)) {
+            ok = false;
+            break;
+          }
+          if (some(u)) {
+            const uint32_t st = base + slot(pos) * T::kStage;
+            const uint32_t row = warp * 16 + (lane & 15);
+            if (FP8) {
+              // keys 0-7 and 8-15 x 32 columns, 16 bytes per row of an 8x8 matrix
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t w[4], f[2][4];
+                ldsm4(st + swz(row * T::kPitch + k * 32 + (lane >> 4) * 16), w);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  mma16816<true>(s[n], qf[2 * k + h], e4m3x2_f16(w[2 * n + h]),
-                                 e4m3x2_f16(w[2 * n + h] >> 16));
-            }
-          } else {
-            const uint32_t row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+                for (int h = 0; h < 2; ++h) {
+                  e4m3x4_f16(w[2 * h], f[h][0], f[h][2]);
+                  e4m3x4_f16(w[2 * h + 1], f[h][1], f[h][3]);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t w[4];
-              const uint32_t col = (k % 4) * 32 + ((lane >> 3) & 1) * 16;
-              ldsm4(st + (k / 4) * (kAttnTK * 128) + swz(row * 128 + col), w);
-              mma16816<false>(s[0], qf[k], w[0], w[1]);
-              mma16816<false>(s[1], qf[k], w[2], w[3]);
+                  for (int n = 0; n < NT; ++n)
+                    mma16816<true>(s[u][n], f[h], qf[n][2 * k + h][0], qf[n][2 * k + h][1]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                uint32_t w[4];
+                const uint32_t col = (k % 4) * 32 + (lane >> 4) * 16;
+                ldsm4(st + (k / 4) * (kAttnTK * 128) + swz(row * 128 + col), w);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  mma16816<false>(s[u][n], w, qf[n][k][0], qf[n][k][1]);
+              }
             }
           }
-          // scores in log2 units; keys that a row does not attend drop out
-          const bool mask = j0 < max(k0.lo, k1.lo) || j0 + 16 > min(k0.hi, k1.hi);
+          release(pos);
+        }
+        if (!ok) break;
+        // scores in log2 units; keys that a row does not attend drop out
+        float mn[NT][2];
+        bool grows = false;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n) {
+          mn[n][0] = m[n][0];
+          mn[n][1] = m[n][1];
+#pragma unroll
+          for (int u = 0; u < T::kAtOnce; ++u) {
+            const int ju = j0 + kAttnTK * u;
+            const bool mask =
+                u >= count || ju < max(k0.lo, k1.lo) || ju + 16 > min(k0.hi, k1.hi);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float v = s[n][e] * a.scale_log2;
+              float v = s[u][n][e] * a.scale_log2;
               if (mask) {
-                const int j = j0 + 8 * n + 2 * c + (e & 1);
-                if (j < kr[e >> 1].lo || j >= kr[e >> 1].hi) v = -INFINITY;
+                const int j = ju + g + 8 * (e >> 1);
+                if (u >= count || j < kr[n][e & 1].lo || j >= kr[n][e & 1].hi) v = -INFINITY;
               }
-              s[n][e] = v;
+              s[u][n][e] = v;
+              mn[n][e & 1] = fmaxf(mn[n][e & 1], v);
             }
-          float mn[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            mn[h] = fmaxf(m[h], x);
           }
-          if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1)
+              mn[n][e] = fmaxf(mn[n][e], __shfl_xor_sync(0xffffffffu, mn[n][e], x));
+            grows |= mn[n][e] > m[n][e];
+          }
+        }
+        if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float f = mn[n][e] > m[n][e] ? ex2(m[n][e] - mn[n][e]) : 1.f;
+              m[n][e] = mn[n][e];
+              l[n][e] *= f;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[n][i][e] *= f;
+                o[n][i][2 + e] *= f;
+              }
+            }
+        }
+        uint32_t pf[T::kAtOnce][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
+          const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+          for (int u = 0; u < T::kAtOnce; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float f = mn[h] > m[h] ? ex2(m[h] - mn[h]) : 1.f;
-              m[h] = mn[h];
-              l[h] *= f;
+              const float x = ex2(s[u][n][2 * h] - m0), y = ex2(s[u][n][2 * h + 1] - m1);
+              l[n][0] += x;
+              l[n][1] += y;
+              pf[u][n][h] = turn(pack16<FP8>(x, y));
+            }
+        }
 #pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                o[i][2 * h] *= f;
-                o[i][2 * h + 1] *= f;
+        for (int u = 0; u < T::kAtOnce; ++u) {
+          if (u >= count) continue;
+          const uint32_t pos = at + 2 * u + 1;
+          if (!filled(pos)) {
+            ok = false;
+            break;
+          }
+          if (some(u)) {
+            const uint32_t st = base + slot(pos) * T::kStage;
+            const int ju = j0 + kAttnTK * u;
+            if (ju < p.u.lo || ju + 16 > p.u.hi) {
+              // v of positions that no row attends: 0, whatever the page holds (0 * NaN = NaN)
+              for (int i = lane; i < 16 * (T::kRowBytes / 16); i += 32) {
+                const int r = i / (T::kRowBytes / 16), x = i % (T::kRowBytes / 16);
+                if (ju + r < p.u.lo || ju + r >= p.u.hi)
+                  sts128(st + (x * 16 / T::kPitch) * (kAttnTK * T::kPitch) +
+                             (warp * 16 + r) * T::kPitch + x * 16 % T::kPitch,
+                         make_uint4(0u, 0u, 0u, 0u));
+              }
+              __syncwarp();
+              fence_async_proxy();  // before the stage's next copy
+            }
+            if (FP8) {
+              // transposed 8x8 matrices of byte pairs: columns 2 g and 2 g + 1 of two keys a word
+              const uint32_t row = warp * 16 + (lane & 15);
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t w[4], f[4];
+                ldsm4t(st + swz(row * T::kPitch + k * 32 + (lane >> 4) * 16), w);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  e4m3x4_f16(__byte_perm(w[2 * h], 0u, 0x3120), f[0], f[1]);
+                  e4m3x4_f16(__byte_perm(w[2 * h + 1], 0u, 0x3120), f[2], f[3]);
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+                    mma16816<true>(o[n][2 * k + h], f, pf[u][n][0], pf[u][n][1]);
+                }
+              }
+            } else {
+              // matrices: keys 0-7 x columns 0-7, keys 0-7 x 8-15, keys 8-15 x 0-7, x 8-15
+              const uint32_t row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                uint32_t w[4];
+                const uint32_t col = (k % 4) * 32 + ((lane >> 3) & 1) * 16;
+                ldsm4t(st + (k / 4) * (kAttnTK * 128) + swz(row * 128 + col), w);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  mma16816<false>(o[n][k], w, pf[u][n][0], pf[u][n][1]);
               }
             }
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float mm = m[h] == -INFINITY ? 0.f : m[h];
-            float e[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = ex2(s[i >> 1][2 * h + (i & 1)] - mm);
-            l[h] += (e[0] + e[1]) + (e[2] + e[3]);
-            pf[h] = pack16<FP8>(e[0], e[1]);
-            pf[2 + h] = pack16<FP8>(e[2], e[3]);
-          }
+          release(pos);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(slot));
-        next_stage();
-        if (!wait_fast(full(slot), phase, abort_flag, status)) {
-          ok = false;
-          break;
-        }
-        if (some) {
-          const uint32_t st = base + slot * T::kStage;
-          if (j0 < p.u.lo || j0 + 16 > p.u.hi) {
-            // v of positions that no row attends: 0, whatever the page holds (0 * NaN = NaN)
-            for (int i = lane; i < 16 * (T::kRowBytes / 16); i += 32) {
-              const int r = i / (T::kRowBytes / 16), x = i % (T::kRowBytes / 16);
-              if (j0 + r < p.u.lo || j0 + r >= p.u.hi)
-                sts128(st + (x * 16 / T::kPitch) * (kAttnTK * T::kPitch) +
-                           (warp * 16 + r) * T::kPitch + x * 16 % T::kPitch,
-                       make_uint4(0u, 0u, 0u, 0u));
-            }
-            __syncwarp();
-            fence_async_proxy();  // before the stage's next copy
-          }
-          const uint32_t row = warp * 16 + (lane & 15);
-          if (FP8) {
-            // transposed 8x8 matrices of byte pairs: columns 2n and 2n + 1 of two keys a word
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              uint32_t w[4];
-              ldsm4t(st + swz(row * T::kPitch + k * 32 + (lane >> 4) * 16), w);
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint32_t sel = e ? 0x0031u : 0x0020u;
-                  mma16816<true>(o[4 * k + 2 * h + e], pf,
-                                 e4m3x2_f16(__byte_perm(w[2 * h], 0u, sel)),
-                                 e4m3x2_f16(__byte_perm(w[2 * h + 1], 0u, sel)));
-                }
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t w[4];
-              const uint32_t col = (k % 4) * 32 + (lane >> 4) * 16;
-              ldsm4t(st + (k / 4) * (kAttnTK * 128) + swz(row * 128 + col), w);
-              mma16816<false>(o[2 * k], pf, w[0], w[1]);
-              mma16816<false>(o[2 * k + 1], pf, w[2], w[3]);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(slot));
-        next_stage();
+        at += 2 * count;
       }
 
       // ---------------------------------------------------------- the piece's result
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        const int r = g + 8 * h;
-        if (c == 0) wml[r * kDecWarps + warp] = make_float2(m[h], l[h]);
-        if (r < rows) {
-          float* dst = join + (warp * kDecBR + r) * D;
-          if (FP8) {
-            // fragments (h2, e): columns 32 k + 16 h2 + 4 c + e and + 2
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              *reinterpret_cast<float4*>(dst + 16 * k + 4 * c) =
-                  make_float4(o[2 * k][2 * h], o[2 * k + 1][2 * h], o[2 * k][2 * h + 1],
-                              o[2 * k + 1][2 * h + 1]);
-          } else {
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              *reinterpret_cast<float2*>(dst + 8 * i + 2 * c) =
-                  make_float2(o[i][2 * h], o[i][2 * h + 1]);
+          for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+          const int r = 8 * n + 2 * c + e;
+          if (g == 0) wml[r * kDecWarps + warp] = make_float2(m[n][e], l[n][e]);
+          if (r < rows) {
+            float* dst = join + (warp * T::kBR + r) * T::kJoinPitch;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              if (FP8) {  // columns 2 g and 2 g + 1 of the 16
+                *reinterpret_cast<float2*>(dst + 16 * i + 2 * g) =
+                    make_float2(o[n][i][e], o[n][i][2 + e]);
+              } else {
+                dst[16 * i + g] = o[n][i][e];
+                dst[16 * i + 8 + g] = o[n][i][2 + e];
+              }
+            }
           }
         }
-      }
       if (consumers_sync(!ok)) break;
       const int slot_out = p.first() ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
       for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kDecWarps) {
@@ -443,7 +517,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
           const float f = ex2(ml[w].x - Ms);
-          const float4 x = *reinterpret_cast<const float4*>(join + (w * kDecBR + r) * D + d);
+          const float4 x = *reinterpret_cast<const float4*>(join + (w * T::kBR + r) * T::kJoinPitch + d);
           L = fmaf(f, ml[w].y, L);
           v.x = fmaf(f, x.x, v.x);
           v.y = fmaf(f, x.y, v.y);
@@ -451,45 +525,66 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           v.w = fmaf(f, x.w, v.w);
         }
         if (p.whole()) {
-          const int rr = p.rb * kDecBR + r;
-          const size_t orow = (size_t)(p.q.q0 + rr / sh.G) * a.hq + p.head * sh.G + rr % sh.G;
-          const float inv = L == 0.f ? 0.f : a.v_scale / L;
-          uint2 w;
-          w.x = pack_bf16x2(v.x * inv, v.y * inv);
-          w.y = pack_bf16x2(v.z * inv, v.w * inv);
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + d) = w;
-          if (a.lse && d == 0)
-            a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          write_out(r, d, v, M, L);
         } else {
-          const size_t at = (size_t)slot_out * kDecBR + r;
-          *reinterpret_cast<float4*>(sc.o + at * D + d) = v;
-          if (d == 0) sc.ml[at] = make_float2(M, L);
+          const size_t row = (size_t)slot_out * T::kBR + r;
+          *reinterpret_cast<float4*>(sc.o + row * D + d) = v;
+          if (d == 0) sc.ml[row] = make_float2(M, L);
         }
       }
-      if (p.first() && !p.last()) {
-        rec.starts = 1;
-        rec.s = p.s;
-        rec.head = p.head;
-        rec.rb = p.rb;
-      } else if (!p.first()) {
-        rec.mid = 1;
-        rec.ends = p.last();
+      if (!p.whole()) {
+        // CTAs c0 .. c1 hold the unit's pieces; the one that finishes last joins them
+        const int c0 = cta_of(span, unit_at), c1 = cta_of(span, unit_at + p.u.tiles - 1);
+        __threadfence();
+        consumers_sync(false);
+        bool last = false;
+        if (threadIdx.x == 0) {
+          last = atomicAdd(a.counters + c0, 1) == c1 - c0;
+          if (last) atomicExch(a.counters + c0, 0);
+          __threadfence();
+        }
+        if (consumers_sync(last)) {
+          for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kDecWarps) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
+            auto row = [&](int c) {
+              return (size_t)(c == c0 ? 2 * c + 1 : 2 * c) * T::kBR + r;
+            };
+            float M = -INFINITY;
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(sc.ml + row(c)).x);
+            const float Ms = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+              const float2 ml = __ldcg(sc.ml + row(c));
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(sc.o + row(c) * D + d));
+              const float f = ex2(ml.x - Ms);
+              L = fmaf(f, ml.y, L);
+              v.x = fmaf(f, x.x, v.x);
+              v.y = fmaf(f, x.y, v.y);
+              v.z = fmaf(f, x.z, v.z);
+              v.w = fmaf(f, x.w, v.w);
+            }
+            write_out(r, d, v, M, L);
+          }
+        }
       }
       consumers_sync(false);  // the join area is free again
     }
-    if (threadIdx.x == 0) sc.rec[blockIdx.x] = rec;
   }
   __syncthreads();
 }
 
-template <bool FP8, int D>
+template <bool FP8, int D, int NT>
 cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
+  using T = Dec<FP8, D, NT>;
   static int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
     const cudaError_t e = cudaFuncSetAttribute(
-        attn_decode_kernel<FP8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDecSmem);
+        attn_decode_kernel<FP8, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::kSmem);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
@@ -499,24 +594,26 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   AttnShape sh;
   sh.G = a.hq / a.hkv;
   sh.hkv = a.hkv;
-  sh.br_shift = 4;
-  static_assert(kDecBR == 1 << 4, "rows per unit");
+  sh.br_shift = NT == 1 ? 3 : 4;
+  static_assert(T::kBR == 1 << (NT == 1 ? 3 : 4), "rows per unit");
   sh.extra = 0;
   sh.causal = a.causal;
   sh.window = a.window;
   const int ctas = num_sms() < kAttnMaxCtas ? num_sms() : kAttnMaxCtas;
-  const cudaError_t e = launch_kernel(attn_decode_kernel<FP8, D>, dim3(ctas), dim3(kDecThreads),
-                                      kDecSmem, stream, maps, a, sh);
-  if (e != cudaSuccess) return e;
-  return launch_attn_join(a, sh, ctas, stream);
+  return launch_kernel(attn_decode_kernel<FP8, D, NT>, dim3(ctas), dim3(kDecThreads), T::kSmem,
+                       stream, maps, a, sh);
+}
+template <int NT>
+cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
+  if (a.fp8)
+    return a.D == 64 ? launch_typed<true, 64, NT>(a, stream) : launch_typed<true, 128, NT>(a, stream);
+  return a.D == 64 ? launch_typed<false, 64, NT>(a, stream) : launch_typed<false, 128, NT>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {
-  if (a.fp8)
-    return a.D == 64 ? launch_typed<true, 64>(a, stream) : launch_typed<true, 128>(a, stream);
-  return a.D == 64 ? launch_typed<false, 64>(a, stream) : launch_typed<false, 128>(a, stream);
+cudaError_t launch_attn_decode(const AttnArgs& a, bool eight, cudaStream_t stream) {
+  return eight ? launch_rows<1>(a, stream) : launch_rows<2>(a, stream);
 }
 
 }  // namespace gbmoe

@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
-  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<long long*>(smem), wsum);
+  AttnSpan span;
+  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<long long*>(smem), wsum, span);
   fence_async_proxy();
   tc_fence_before();
   __syncthreads();
@@ -701,7 +702,8 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         d.head = p.head;
         d.slot = p.whole() ? -1 : p.first() ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
         if (lane == 0 && p.first() && !p.last()) {
-          rec->s = p.s;
+          rec->q0 = p.q.q0;
+          rec->n = p.q.n;
           rec->head = p.head;
           rec->rb = p.rb;
           rec->starts = 1;

@@ -72,10 +72,12 @@ struct AttnArgs {
   int window;
   float scale_log2;      // softmax scale * k_scale * log2(e)
   float v_scale;
-  void* scratch;         // after the status region of the workspace
+  int* counters;         // kAttnMaxCtas, zero between calls
+  void* scratch;
 };
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream);
 size_t attn_scratch_bytes(int D);
 constexpr int kAttnMaxSeqs = 8192;
+constexpr int kAttnMaxCtas = 160;  // workspace bound; the kernels run one CTA per SM
 
 }  // namespace gbmoe

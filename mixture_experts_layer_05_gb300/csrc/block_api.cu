@@ -13,6 +13,9 @@ namespace {
 
 constexpr int kMaxRows = 1 << 22;
 constexpr size_t kStatusBytes = 256;
+// attention: the status region, then the counters of cut units
+constexpr size_t kAttnHeadBytes = 1024;
+static_assert(kStatusBytes + kAttnMaxCtas * sizeof(int) <= kAttnHeadBytes, "counters");
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -155,7 +158,7 @@ GBMOE_API gbmoe_status_t moe_kv_append(const gbmoe_attn_config_t* cfg, int32_t n
 
 GBMOE_API size_t moe_paged_attention_workspace_size(const gbmoe_attn_config_t* cfg) {
   if (check_attn(cfg) != GBMOE_OK) return 0;
-  return kStatusBytes + attn_scratch_bytes(cfg->head_dim);
+  return kAttnHeadBytes + attn_scratch_bytes(cfg->head_dim);
 }
 
 GBMOE_API gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int32_t num_tokens,
@@ -191,7 +194,8 @@ GBMOE_API gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int
   a.window = cfg->window;
   a.scale_log2 = cfg->softmax_scale * cfg->k_scale * 1.4426950408889634f;
   a.v_scale = cfg->v_scale;
-  a.scratch = static_cast<char*>(workspace) + kStatusBytes;
+  a.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + kStatusBytes);
+  a.scratch = static_cast<char*>(workspace) + kAttnHeadBytes;
   PdlChain chain;
   return cuda_status(launch_attn(a, (cudaStream_t)stream));
 }
