@@ -215,65 +215,72 @@ bool make_cache_map(CUtensorMap* m, const void* ptr, const AttnArgs& a) {
 }
 
 // Joins the pieces of the units that CTA boundaries cut. Block (c, y): rows [32 y, 32 y + 32) of
-// the unit that CTA c began and did not finish. out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i
-// over its pieces in order, M = max m_i: 8 threads a row.
+// the unit that CTA c began and did not finish: sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i
+// over its pieces in order, M = max m_i: 8 threads a row, four columns each in turn.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh, int ctas) {
-  constexpr int C = D / 8;  // columns per thread
+  constexpr int C = D / 32;  // vectors of four columns per thread
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const AttnScratch sc = attn_scratch(a.scratch, 1 << sh.br_shift);
   const int c0 = blockIdx.x;
+  const int row = blockIdx.y * 32 + threadIdx.x / 8, col = threadIdx.x % 8 * 4;
+  // everything that does not wait for something else is loaded at once: the record, the records
+  // of the CTAs after c0, and the first two pieces (most units have no more)
   const AttnRec rec = sc.rec[c0];
-  // the CTAs after c0: which hold a piece, and where the unit ends
-  int2 r[kAttnMaxCtas / 32];  // (mid, ends)
+  int2 held[kAttnMaxCtas / 32];  // (mid, ends)
 #pragma unroll
   for (int i = 0; i < kAttnMaxCtas / 32; ++i) {
     const int c = c0 + 1 + 32 * i + lane;
-    r[i] = c < ctas ? *reinterpret_cast<const int2*>(&sc.rec[c].mid) : make_int2(0, 0);
+    held[i] = c < ctas ? *reinterpret_cast<const int2*>(&sc.rec[c].mid) : make_int2(0, 0);
   }
+  const size_t first = ((size_t)(2 * c0 + 1) << sh.br_shift) + row;
+  float2 ml = sc.ml[first];
+  float4 o[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    o[i] = *reinterpret_cast<const float4*>(sc.o + first * D + col + 32 * i);
   if (!rec.starts) return;
   int c1 = ctas - 1;
 #pragma unroll
   for (int i = kAttnMaxCtas / 32 - 1; i >= 0; --i) {
-    const uint32_t end = __ballot_sync(0xffffffffu, r[i].x && r[i].y);
+    const uint32_t end = __ballot_sync(0xffffffffu, held[i].x && held[i].y);
     if (end) c1 = c0 + 32 * i + __ffs(end);
   }
-  const int row = blockIdx.y * 32 + threadIdx.x / 8, col = threadIdx.x % 8 * C;
   const int ur = (rec.rb << sh.br_shift) + row;
-  if (ur >= rec.n * sh.G) return;
-  const size_t first = ((size_t)(2 * c0 + 1) << sh.br_shift) + row;
-  float2 ml = sc.ml[first];
-  float M = ml.x;
-#pragma unroll 4
-  for (int c = c0 + 1; c <= c1; ++c)
-    if (sc.rec[c].mid) M = fmaxf(M, sc.ml[((size_t)(2 * c) << sh.br_shift) + row].x);
-  const float Ms = M == -INFINITY ? 0.f : M;
-  float l = 0.f, o[C];
+  const bool valid = ur < rec.n * sh.G;
+  float M = ml.x, l = ml.y;
+#pragma unroll 2
+  for (int c = c0 + 1; c <= c1; ++c) {
+    if (!sc.rec[c].mid) continue;
+    const size_t at = ((size_t)(2 * c) << sh.br_shift) + row;
+    const float2 next = sc.ml[at];
+    float4 v[C];
 #pragma unroll
-  for (int i = 0; i < C; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    if (c > c0 && !sc.rec[c].mid) continue;
-    const size_t at = c == c0 ? first : ((size_t)(2 * c) << sh.br_shift) + row;
-    const float2 ml = sc.ml[at];
-    const float w = ex2(ml.x - Ms);
-    l = fmaf(w, ml.y, l);
-    const float4* src = reinterpret_cast<const float4*>(sc.o + at * D + col);
+    for (int i = 0; i < C; ++i)
+      v[i] = *reinterpret_cast<const float4*>(sc.o + at * D + col + 32 * i);
+    const float Mn = fmaxf(M, next.x), Ms = Mn == -INFINITY ? 0.f : Mn;
+    const float f = ex2(M - Ms), w = ex2(next.x - Ms);
+    M = Mn;
+    l = l * f + next.y * w;
 #pragma unroll
-    for (int i = 0; i < C / 4; ++i) {
-      const float4 v = src[i];
-      o[4 * i] = fmaf(w, v.x, o[4 * i]);
-      o[4 * i + 1] = fmaf(w, v.y, o[4 * i + 1]);
-      o[4 * i + 2] = fmaf(w, v.z, o[4 * i + 2]);
-      o[4 * i + 3] = fmaf(w, v.w, o[4 * i + 3]);
+    for (int i = 0; i < C; ++i) {
+      o[i].x = o[i].x * f + v[i].x * w;
+      o[i].y = o[i].y * f + v[i].y * w;
+      o[i].z = o[i].z * f + v[i].z * w;
+      o[i].w = o[i].w * f + v[i].w * w;
     }
   }
+  if (!valid) return;
   const size_t orow = (size_t)(rec.q0 + ur / sh.G) * a.hq + rec.head * sh.G + ur % sh.G;
   const float inv = l == 0.f ? 0.f : a.v_scale / l;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + col);
 #pragma unroll
-  for (int i = 0; i < C / 2; ++i) dst[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+  for (int i = 0; i < C; ++i) {
+    uint2 w;
+    w.x = pack_bf16x2(o[i].x * inv, o[i].y * inv);
+    w.y = pack_bf16x2(o[i].z * inv, o[i].w * inv);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + col + 32 * i) = w;
+  }
   if (a.lse && col == 0)
     a.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
