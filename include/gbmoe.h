@@ -439,8 +439,8 @@ gbmoe_status_t moe_selftest_bounded_wait(void* workspace, int32_t timeout_us,
  * bf16, as the FP8 layer's quantized input, or both:
  *   h = x + residual (fp32; h = x without one), residual_out = bf16(h)
  *   y = h / sqrt(mean(h^2) + eps) * weight (fp32), y_out = bf16(y)
- *   s = max(max |y|, 1e-10) / 448 over each 128 columns, q = e4m3fn(y / s) (one fp32 division
- *   each, round to nearest even, saturating; from the fp32 y, not from its bf16 rounding)
+ *   s = max(max |y|, 1e-10) / 448 over each 128 columns, q = e4m3fn(y * (1 / s)) (fp32, round
+ *   to nearest even, saturating; from the fp32 y, not from its bf16 rounding)
  *   x             [T, H] bf16, row t at x + t * x_stride (elements)
  *   residual      [T, H] bf16, row stride residual_stride; or NULL
  *   weight        [H] bf16
@@ -533,7 +533,7 @@ typedef struct {
  * The first `rotary_dim` columns of every q and k head turn pairwise,
  *   (a, b) -> (a cos - b sin, b cos + a sin),
  * pair i being columns (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved != 0; all in
- * fp32, rounded once (E4M3: code = e4m3fn(value / scale), saturating at +-448).
+ * fp32, rounded once (E4M3: code = e4m3fn(value * (1 / scale)), saturating at +-448).
  *   q, k, v     [T, heads, head_dim] bf16, token strides q_stride, k_stride, v_stride (elements,
  *               multiples of 8; heads contiguous), so that one packed projection serves
  *   cos_sin     [max_position, rotary_dim] fp32: rotary_dim / 2 cosines, then as many sines; or

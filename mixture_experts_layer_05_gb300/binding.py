@@ -470,15 +470,33 @@ def moe_get_device_status(workspace, stream=None) -> int:
     return v.value
 
 
-def _rows(t, dtype, name, cols):
-    """A [T, cols] (or [T, heads, dim]) tensor whose rows are contiguous; its row stride."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(t, stream):
+    """The stream argument as an integer; None: the current one of t's device (without the
+    Stream object, whose construction takes longer than a small kernel's launch)."""
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _row_stride(t, name, T, cols):
+    """Row stride of a CUDA bf16 [T, cols] or [T, heads, dim] tensor with contiguous rows."""
+    st = t.stride()
+    if (not t.is_cuda or t.dtype is not torch.bfloat16 or t.shape[0] != T
+            or t.numel() != T * cols or st[-1] != 1 or not 2 <= len(st) <= 3
+            or (len(st) == 3 and st[1] != t.shape[2])):
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor of {T} rows of {cols} contiguous "
+                         "columns")
+    return st[0] if T > 1 else cols
+
+
+def _out(t, name, like, shape, dtype=torch.bfloat16):
+    """t, checked, or a new contiguous tensor."""
     if t is None:
-        return 0
-    inner = (1,) if t.dim() == 2 else (t.shape[2], 1) if t.dim() == 3 else None
-    if (inner is None or not t.is_cuda or t.dtype != dtype
-            or t.numel() != t.shape[0] * cols or t.stride()[1:] != inner):
-        raise ValueError(f"{name} must be a CUDA {dtype} tensor of {cols} contiguous columns a row")
-    return t.stride(0) if t.shape[0] > 1 else cols
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}")
+    return t
 
 
 def moe_rms_norm(x, weight, eps=1e-6, residual=None, out="bf16", y=None, residual_out=None,
@@ -487,41 +505,35 @@ def moe_rms_norm(x, weight, eps=1e-6, residual=None, out="bf16", y=None, residua
     scale: e4m3 codes and group-major fp32 scales [H / 128, T], the FP8 layer's input format)
     or "both". Rows of x and residual may be strided. Returns (y, residual_out, q, scale), None
     for what was not asked for (residual_out: without a residual)."""
-    if out not in ("bf16", "fp8", "both"):
-        raise ValueError(f"out must be bf16, fp8 or both, not {out!r}")
     T, H = x.shape
-    xs = _rows(x, torch.bfloat16, "x", H)
-    rs = _rows(residual, torch.bfloat16, "residual", H)
-    if weight.numel() != H or (residual is not None and residual.shape[0] != T):
-        raise ValueError("weight must have H columns, residual the rows of x")
-    if out == "fp8":
-        y = None
-    elif y is None:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
-    if residual is None:
+    xs, rs, rp = _row_stride(x, "x", T, H), 0, None
+    if not weight.is_cuda or weight.dtype is not torch.bfloat16 or weight.shape != (H,) or (
+            not weight.is_contiguous()):
+        raise ValueError("weight must be a contiguous CUDA bfloat16 tensor of H columns")
+    yp = ro = qp = sp = None
+    if residual is not None:
+        rs, rp = _row_stride(residual, "residual", T, H), residual.data_ptr()
+        residual_out = _out(residual_out, "residual_out", x, (T, H))
+        ro = residual_out.data_ptr()
+    else:
         residual_out = None
-    elif residual_out is None:
-        residual_out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
-    if out == "bf16":
+    if out == "bf16" or out == "both":
+        y = _out(y, "y", x, (T, H))
+        yp = y.data_ptr()
+    else:
+        y = None
+    if out == "fp8" or out == "both":
+        q = _out(q, "q", x, (T, H), torch.float8_e4m3fn)
+        scale = _out(scale, "scale", x, (H // 128, T), torch.float32)
+        qp, sp = q.data_ptr(), scale.data_ptr()
+    elif out == "bf16":
         q = scale = None
     else:
-        if q is None:
-            q = torch.empty(T, H, dtype=torch.float8_e4m3fn, device=x.device)
-        if scale is None:
-            scale = torch.empty(H // 128, T, dtype=torch.float32, device=x.device)
-        _fp8_bytes(q, "q")
-        _need(scale, torch.float32, "scale")
-        if q.numel() != T * H or scale.numel() != H // 128 * T:
-            raise ValueError("q must be [T, H] and scale [H / 128, T]")
-    for t, n in ((weight, "weight"), (y, "y"), (residual_out, "residual_out")):
-        _need(t, torch.bfloat16, n)
-    for t, n in ((y, "y"), (residual_out, "residual_out")):
-        if t is not None and t.numel() != T * H:
-            raise ValueError(f"{n} must be [T, H]")
-    ptr = lambda t: None if t is None else t.data_ptr()
-    a = RmsNormArgs(ptr(x), xs, ptr(residual), rs, ptr(weight), float(eps), ptr(y),
-                    ptr(residual_out), ptr(q), ptr(scale))
-    _check("moe_rms_norm", load().moe_rms_norm(T, H, ctypes.byref(a), _stream(stream)))
+        raise ValueError(f"out must be bf16, fp8 or both, not {out!r}")
+    a = RmsNormArgs(x.data_ptr(), xs, rp, rs, weight.data_ptr(), eps, yp, ro, qp, sp)
+    code = load().moe_rms_norm(T, H, ctypes.byref(a), _stream_of(x, stream))
+    if code:
+        raise GbmoeError("moe_rms_norm", code)
     return y, residual_out, q, scale
 
 
@@ -542,79 +554,79 @@ class PagedAttention:
             raise GbmoeError("moe_paged_attention_workspace_size", ERR_INVALID_ARG)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device)
         self.workspace[:1024].zero_()         # status word and counters
+        self._ws = (self.workspace.data_ptr(), n)
         self._dtypes = ((torch.bfloat16,) if cfg.cache_type == CACHE["bf16"]
                         else (torch.float8_e4m3fn, torch.uint8))
+        self._heads = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
+        self._page = cfg.page_size, cfg.num_kv_heads, cfg.head_dim
 
     def _paged(self, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens) -> PagedKv:
-        c = self.cfg
-        shape = (c.page_size, c.num_kv_heads, c.head_dim)
-        strides = k_cache.stride()
-        if (not k_cache.is_cuda or not v_cache.is_cuda or k_cache.dtype not in self._dtypes
-                or v_cache.dtype != k_cache.dtype or k_cache.dim() != 4
-                or tuple(k_cache.shape[1:]) != shape or v_cache.shape != k_cache.shape
-                or strides != v_cache.stride() or strides[3] != 1):
+        shape, st = k_cache.shape, k_cache.stride()
+        if (shape[1:] != self._page or v_cache.shape != shape or v_cache.stride() != st
+                or st[3] != 1 or k_cache.dtype not in self._dtypes
+                or v_cache.dtype is not k_cache.dtype or not k_cache.is_cuda
+                or not v_cache.is_cuda):
             raise ValueError("k_cache and v_cache must be CUDA tensors [num_pages, page_size, "
                              "num_kv_heads, head_dim] of the configured type and equal strides, "
                              "contiguous in head_dim")
-        S = kv_lens.shape[0]
-        for t, n in ((block_table, "block_table"), (cu_seqlens_q, "cu_seqlens_q"),
-                     (kv_lens, "kv_lens")):
-            _need(t, torch.int32, n)
-        if block_table.dim() != 2 or block_table.shape[0] != S or cu_seqlens_q.shape != (S + 1,):
+        S, = kv_lens.shape
+        rows, cols = block_table.shape
+        if rows != S or cu_seqlens_q.shape != (S + 1,):
             raise ValueError("block_table must be [S, max_pages], cu_seqlens_q [S + 1], kv_lens [S]")
+        for t in (block_table, cu_seqlens_q, kv_lens):
+            if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
+                raise ValueError("block_table, cu_seqlens_q and kv_lens must be contiguous CUDA "
+                                 "int32 tensors")
         # the stride of a dimension of one element is never used: any valid number
-        ps, ts, hs = (strides[i] if k_cache.shape[i] > 1 else c.head_dim for i in range(3))
-        return PagedKv(k_cache.data_ptr(), v_cache.data_ptr(), ps, ts, hs, k_cache.shape[0], S,
-                       block_table.shape[1], block_table.data_ptr(), cu_seqlens_q.data_ptr(),
-                       kv_lens.data_ptr())
+        if 1 in shape:
+            st = [st[i] if shape[i] > 1 else shape[3] for i in range(3)]
+        return PagedKv(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], shape[0], S,
+                       cols, block_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr())
 
     def append(self, q, k, v, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, cos_sin=None,
                interleaved=False, q_out=None, stream=None):
         """Rotates the new tokens' q and k [T, heads, head_dim] (rows may be strided, as slices
         of one packed projection), writes k and v into the cache, and returns the rotated q."""
-        c = self.cfg
+        hq, hkv, d = self._heads
         kv = self._paged(k_cache, v_cache, block_table, cu_seqlens_q, kv_lens)
         T = q.shape[0]
-        strides = [_rows(t, torch.bfloat16, n, h * c.head_dim) for t, n, h in
-                   ((q, "q", c.num_q_heads), (k, "k", c.num_kv_heads), (v, "v", c.num_kv_heads))]
-        if k.shape[0] != T or v.shape[0] != T:
-            raise ValueError("q, k and v must have the same number of tokens")
-        if q_out is None:
-            q_out = torch.empty(T, c.num_q_heads, c.head_dim, dtype=torch.bfloat16,
-                                device=q.device)
-        _need(q_out, torch.bfloat16, "q_out")
-        _need(cos_sin, torch.float32, "cos_sin")
-        if q_out.numel() != T * c.num_q_heads * c.head_dim:
-            raise ValueError("q_out must be [T, num_q_heads, head_dim]")
-        pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-        a = KvAppendArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
-                         None if cos_sin is None else cos_sin.data_ptr(), pos, rot,
-                         int(bool(interleaved)), q_out.data_ptr(), self.workspace.data_ptr())
-        _check("moe_kv_append", load().moe_kv_append(ctypes.byref(c), T, ctypes.byref(kv),
-                                                     ctypes.byref(a), _stream(stream)))
+        qs = _row_stride(q, "q", T, hq * d)
+        ks = _row_stride(k, "k", T, hkv * d)
+        vs = _row_stride(v, "v", T, hkv * d)
+        q_out = _out(q_out, "q_out", q, (T, hq, d))
+        if cos_sin is None:
+            cp, pos, rot = None, 0, 0
+        else:
+            if not cos_sin.is_cuda or cos_sin.dtype is not torch.float32 or (
+                    not cos_sin.is_contiguous()):
+                raise ValueError("cos_sin must be a contiguous CUDA float32 tensor")
+            cp, (pos, rot) = cos_sin.data_ptr(), cos_sin.shape
+        a = KvAppendArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cp, pos, rot,
+                         bool(interleaved), q_out.data_ptr(), self._ws[0])
+        code = load().moe_kv_append(ctypes.byref(self.cfg), T, ctypes.byref(kv), ctypes.byref(a),
+                                    _stream_of(q, stream))
+        if code:
+            raise GbmoeError("moe_kv_append", code)
         return q_out
 
     def __call__(self, q, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, out=None,
                  lse=None, stream=None):
         """out [T, num_q_heads, head_dim] bf16 of the new tokens' q; with lse (True, or a fp32
         [T, num_q_heads] tensor) also the log-sum-exp of each row's scores: (out, lse)."""
-        c = self.cfg
+        hq, _, d = self._heads
         kv = self._paged(k_cache, v_cache, block_table, cu_seqlens_q, kv_lens)
         T = q.shape[0]
-        qs = _rows(q, torch.bfloat16, "q", c.num_q_heads * c.head_dim)
-        if out is None:
-            out = torch.empty(T, c.num_q_heads, c.head_dim, dtype=torch.bfloat16, device=q.device)
-        _need(out, torch.bfloat16, "out")
-        if lse is True:
-            lse = torch.empty(T, c.num_q_heads, dtype=torch.float32, device=q.device)
-        _need(lse, torch.float32, "lse")
-        if out.numel() != T * c.num_q_heads * c.head_dim or (
-                lse is not None and lse.numel() != T * c.num_q_heads):
-            raise ValueError("out must be [T, num_q_heads, head_dim], lse [T, num_q_heads]")
-        ws = self.workspace
-        _check("moe_paged_attention", load().moe_paged_attention(
-            ctypes.byref(c), T, ctypes.byref(kv), q.data_ptr(), qs, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+        qs = _row_stride(q, "q", T, hq * d)
+        out = _out(out, "out", q, (T, hq, d))
+        lp = None
+        if lse is not None:
+            lse = _out(None if lse is True else lse, "lse", q, (T, hq), torch.float32)
+            lp = lse.data_ptr()
+        code = load().moe_paged_attention(ctypes.byref(self.cfg), T, ctypes.byref(kv), q.data_ptr(),
+                                          qs, out.data_ptr(), lp, *self._ws,
+                                          _stream_of(q, stream))
+        if code:
+            raise GbmoeError("moe_paged_attention", code)
         return out if lse is None else (out, lse)
 
     def device_status(self) -> int:

@@ -2,11 +2,25 @@
 // sequence of a packed token.
 #pragma once
 
+#include <cuda_fp8.h>
+
 #include "block.h"
 #include "common.cuh"
 #include "paged_checks.h"
 
 namespace gbmoe {
+
+// Four e4m3 bytes of (a, b, c, d) * inv, a in the lowest byte. A product with the reciprocal of
+// the scale in place of a division each: the quotient is off by at most 1.5 units of fp32's last
+// place, which changes a code only where it lies that near to a border between two; the
+// divisions bound the norm's 8-bit output (76 us for 8192 x 7168 where HBM needs 27).
+__device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, float d, float inv) {
+  const __nv_fp8x2_storage_t lo =
+      __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hi =
+      __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
 
 // Sizes of sequence s, cut to what can be addressed; what was outside is recorded.
 __device__ __forceinline__ SeqInfo seq_info(const PagedBatch& b, int s) {

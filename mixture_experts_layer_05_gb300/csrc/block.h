@@ -36,7 +36,7 @@ struct RmsNormArgs {
   const void* residual;
   long long residual_stride;
   const void* weight;
-  float eps;
+  float eps, inv_h;      // inv_h = 1 / H
   void* y;
   void* residual_out;
   uint8_t* q;
@@ -56,7 +56,7 @@ struct KvAppendArgs {
   void* q_out;
   int hq, hkv, D;
   bool fp8;
-  float k_scale, v_scale;
+  float k_inv, v_inv;    // 1 / scale
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
 

@@ -4,10 +4,14 @@
 // row p % page_size of page block_table[seq][p / page_size]. The first R columns of each q and
 // k head turn by the angle of p, pair by pair, (a, b) -> (a cos - b sin, b cos + a sin), in
 // fp32 from an fp32 table; q is rounded once to bf16, k and v once to the cache's type (e4m3:
-// from x / scale, saturating at 448).
+// from x times the reciprocal of the scale, saturating at 448).
 //
 // Bound by HBM. One CTA per token; a thread handles two vectors of eight columns at a time,
-// the two halves of eight pairs (half-split pairs) or sixteen neighbouring columns.
+// the two halves of eight pairs (half-split pairs) or sixteen neighbouring columns. What counts
+// is how many tokens an SM has in different phases of their lookups and copies: 12 CTAs of 128
+// threads took 26 us for 5,200 tokens of 32 + 2 x 8 heads of 128 into an e4m3 cache (134 MB, 5.1
+// TB/s), eight of 192 27, six 29; several tokens a CTA with their lookups side by side and the
+// next token's loads under way needed registers that left two, 46.
 #include "block.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
@@ -15,7 +19,7 @@
 namespace gbmoe {
 namespace {
 
-constexpr int kAppendThreads = 192;
+constexpr int kAppendThreads = 128;
 
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
@@ -35,10 +39,10 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   u.w = pack_bf16x2(v[6], v[7]);
   *reinterpret_cast<uint4*>(p) = u;
 }
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&v)[8], float scale) {
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&v)[8], float inv) {
   uint2 c;
-  c.x = e4m3x4(v[0], v[1], v[2], v[3], scale);
-  c.y = e4m3x4(v[4], v[5], v[6], v[7], scale);
+  c.x = e4m3x4_scaled(v[0], v[1], v[2], v[3], inv);
+  c.y = e4m3x4_scaled(v[4], v[5], v[6], v[7], inv);
   *reinterpret_cast<uint2*>(p) = c;
 }
 __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
@@ -49,7 +53,7 @@ __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvAppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 12) kv_append_kernel(KvAppendArgs a) {
   const int t = blockIdx.x, lane = threadIdx.x & 31;
   const int s = find_seq_warp(a.b, t, lane);  // every warp finds it: no barrier
   if (s < 0) return;                          // a token of no sequence (padding)
@@ -59,9 +63,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvAppendArgs 
     if (threadIdx.x == 0) record_status(a.b.status, GBMOE_ERR_DEVICE_CHECK);
     return;
   }
-  const int page = __ldg(a.b.table + (size_t)s * a.b.table_stride + (pos >> a.b.page_shift));
-  const bool page_ok = (unsigned)page < (unsigned)a.b.num_pages;
-  if (!page_ok && threadIdx.x == 0) record_status(a.b.status, GBMOE_ERR_DEVICE_CHECK);
+  bool bad = false;
+  const int page =
+      checked_page(__ldg(a.b.table + (size_t)s * a.b.table_stride + (pos >> a.b.page_shift)),
+                   a.b.num_pages, &bad);
+  if (bad && threadIdx.x == 0) record_status(a.b.status, GBMOE_ERR_DEVICE_CHECK);
   const size_t row = (size_t)page * a.c.page_stride +
                      (size_t)(pos & ((1 << a.b.page_shift) - 1)) * a.c.token_stride;
   const int per_head = a.D / 16;
@@ -113,13 +119,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvAppendArgs 
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.q_out) + ((size_t)t * a.hq + h) * a.D;
       store8(dst + c0, x);
       store8(dst + c1, y);
-    } else if (page_ok) {
+    } else if (!bad) {
       const size_t at = row + (size_t)h * a.c.head_stride;
       if (FP8) {
         uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.c.k : a.c.v) + at;
-        const float sc = kind == 1 ? a.k_scale : a.v_scale;
-        store8_e4m3(dst + c0, x, sc);
-        store8_e4m3(dst + c1, y, sc);
+        const float inv = kind == 1 ? a.k_inv : a.v_inv;
+        store8_e4m3(dst + c0, x, inv);
+        store8_e4m3(dst + c1, y, inv);
       } else {
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(kind == 1 ? a.c.k : a.c.v) + at;
         store8(dst + c0, x);

@@ -5,11 +5,18 @@
 //   s = max(max |y over 128 columns|, 1e-10) / 448,  q = e4m3(y / s)
 //
 // All sums and y are fp32; y is rounded once, to bf16 or (from fp32, not from the bf16 y) to
-// e4m3. One CTA per row: the row stays in registers between the sum of squares and the
-// outputs, so each input is read once. Thread i holds the vectors of eight columns i, i +
-// blockDim, ..., so 16 neighbouring threads hold one 128-column group and find its largest
-// magnitude with four shuffles.
-#include "block.h"
+// e4m3. A row stays in registers between the sum of squares and the outputs, so each input is
+// read once. Thread i holds the vectors of eight columns i, i + blockDim, ..., so 16
+// neighbouring threads hold one 128-column group and find its largest magnitude with four
+// shuffles.
+//
+// Bound by HBM. A CTA per row. Up to two rows an SM a thread holds one vector, the shortest
+// chain; beyond that two (half the threads per row, so that more rows are in different phases on
+// an SM). 8192 x 7168 with a residual and both outputs, 530 MB: 79 us (6.7 TB/s, the rate of a
+// plain copy); 88 with one vector per thread, 81 with four, 126 with CTAs that stay and bulk
+// copies of the next rows into shared memory. Dividing each value by its group's scale, in
+// place of multiplying by the reciprocal, cost 30 us of arithmetic.
+#include "block.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -19,8 +26,7 @@ namespace {
 constexpr int kNormMaxThreads = 1024;
 constexpr int kNormMaxVec = 4;  // vectors of eight columns per thread
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -38,72 +44,83 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = u;
 }
 
+// One row's outputs from its h (fp32, this thread's vectors) and the sum of squares.
 template <int VEC>
-__global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(RmsNormArgs a) {
-  __shared__ float red[32];
-  const int t = blockIdx.x;
-  const int nv = a.H / 8;
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + (size_t)t * a.x_stride;
-  const __nv_bfloat16* r =
-      a.residual ? static_cast<const __nv_bfloat16*>(a.residual) + (size_t)t * a.residual_stride
-                 : nullptr;
-  const __nv_bfloat16* wt = static_cast<const __nv_bfloat16*>(a.weight);
-  float h[VEC][8];
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
-    if (v < nv) {
-      load8(x + v * 8, h[i]);
-      if (r) {
-        float u[8];
-        load8(r + v * 8, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] += u[j];
-        if (a.residual_out)
-          store8(static_cast<__nv_bfloat16*>(a.residual_out) + (size_t)t * a.H + v * 8, h[i]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
-    }
-  }
-  ss = warp_sum(ss);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
-  __syncthreads();
-  const int nw = blockDim.x >> 5;
-  ss = warp_sum((int)(threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.f);
-  const float rs = 1.f / sqrtf(ss / (float)a.H + a.eps);
+__device__ __forceinline__ void write_row(const RmsNormArgs& a, int t, int nv, float ss,
+                                          const float (&h)[VEC][8]) {
+  const float rs = rsqrtf(fmaf(ss, a.inv_h, a.eps));
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     float y[8], amax = 0.f;
+    unpack8(v < nv ? __ldg(static_cast<const uint4*>(a.weight) + v) : make_uint4(0u, 0u, 0u, 0u), y);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = 0.f;
-    if (v < nv) {
-      float w[8];
-      load8(wt + v * 8, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        y[j] = h[i][j] * rs * w[j];
-        amax = fmaxf(amax, fabsf(y[j]));
-      }
-      if (a.y) store8(static_cast<__nv_bfloat16*>(a.y) + (size_t)t * a.H + v * 8, y);
+    for (int j = 0; j < 8; ++j) {
+      y[j] *= h[i][j] * rs;
+      amax = fmaxf(amax, fabsf(y[j]));
     }
+    if (a.y && v < nv) store8(static_cast<__nv_bfloat16*>(a.y) + (size_t)t * a.H + v * 8, y);
     if (a.q) {
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (v < nv) {
         const float s = fp8_group_scale(amax);
         uint2 c;
-        c.x = e4m3x4(y[0], y[1], y[2], y[3], s);
-        c.y = e4m3x4(y[4], y[5], y[6], y[7], s);
+        const float inv = __fdiv_rn(1.f, s);
+        c.x = e4m3x4_scaled(y[0], y[1], y[2], y[3], inv);
+        c.y = e4m3x4_scaled(y[4], y[5], y[6], y[7], inv);
         *reinterpret_cast<uint2*>(a.q + (size_t)t * a.H + v * 8) = c;
         if ((threadIdx.x & 15) == 0) a.scale[(size_t)(v / 16) * a.T + t] = s;
       }
     }
   }
+}
+
+// h = x + r of one vector, and its squares added to ss.
+__device__ __forceinline__ void add_vec(const uint4& x, const uint4& r, float (&h)[8], float& ss) {
+  float u[8];
+  unpack8(x, h);
+  unpack8(r, u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    h[j] += u[j];
+    ss = fmaf(h[j], h[j], ss);
+  }
+}
+
+// A row per CTA.
+template <int VEC>
+__global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(RmsNormArgs a) {
+  __shared__ float red[32];
+  const int nv = a.H / 8, t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) +
+                                                  (size_t)t * a.x_stride);
+  const uint4* r = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.residual) +
+                                                  (size_t)t * a.residual_stride);
+  uint4 xv[VEC], rv[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    xv[i] = rv[i] = zero;
+    if (v < nv) {
+      xv[i] = x[v];
+      if (a.residual) rv[i] = r[v];
+    }
+  }
+  float h[VEC][8], ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    add_vec(xv[i], rv[i], h[i], ss);
+    if (a.residual_out && v < nv)
+      store8(static_cast<__nv_bfloat16*>(a.residual_out) + (size_t)t * a.H + v * 8, h[i]);
+  }
+  ss = warp_sum(ss);
+  if (lane == 0) red[warp] = ss;
+  __syncthreads();
+  write_row(a, t, nv, warp_sum(lane < nw ? red[lane] : 0.f), h);
 }
 
 }  // namespace
@@ -112,9 +129,11 @@ int rms_norm_max_hidden() { return kNormMaxThreads * kNormMaxVec * 8; }
 
 cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t stream) {
   const int nv = a.H / 8;
-  const int vec = (nv + kNormMaxThreads - 1) / kNormMaxThreads;
-  int threads = (nv + vec - 1) / vec;
-  threads = (threads + 31) / 32 * 32;
+  // up to two rows an SM: a vector per thread; more: two, when a row has that many
+  const int wide = a.T <= 2 * num_sms() ? kNormMaxThreads : kNormMaxThreads / 2;
+  int vec = (nv + wide - 1) / wide;
+  if (vec > 2) vec = 4;
+  const int threads = ((nv + vec - 1) / vec + 31) / 32 * 32;
   auto go = [&](auto k) { launch_kernel(k, dim3(a.T), dim3(threads), 0, stream, a); };
   if (vec == 1) go(rms_norm_kernel<1>);
   else if (vec == 2) go(rms_norm_kernel<2>);

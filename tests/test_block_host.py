@@ -130,8 +130,6 @@ def test_binding_refuses_host_tensors(lib):
     x = torch.zeros(2, 256, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         binding.moe_rms_norm(x, x[0])
-    with pytest.raises(ValueError):
-        binding.moe_rms_norm(x, x[0], out="int8")
     with pytest.raises(binding.GbmoeError):
         binding.PagedAttention(_cfg(head_dim=96), device="cpu")
     op = binding.PagedAttention(_cfg(), device="cpu")

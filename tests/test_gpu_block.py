@@ -79,6 +79,43 @@ def test_rms_norm_non_finite_rows(cuda_lib):
         assert (y[row, :c] == 0).all() and (y[row, c + 1:] == 0).all()
 
 
+def test_binding_refuses_other_tensors(cuda_lib):
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device=DEV)
+    w = x[0].clone()
+    bad = [dict(out="int8"), dict(residual=x[:3]), dict(residual=x.float()), dict(y=x.float()),
+           dict(y=x.t().contiguous().t()), dict(residual=x, residual_out=x[:3]),
+           dict(out="fp8", q=x), dict(out="fp8", scale=x.float())]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            binding.moe_rms_norm(x, w, **kw)
+    for args in ((x.float(), w), (x, w[:128]), (x, w.float()), (x[:, ::2], w[:128])):
+        with pytest.raises(ValueError):
+            binding.moe_rms_norm(*args)
+    op = binding.PagedAttention(binding.make_attn_config(4, 2, 64, 16))
+    c = torch.zeros(5, 16, 2, 64, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    i = torch.zeros(8, dtype=torch.int32, device=DEV)
+    ok = dict(q=q, k_cache=c, v_cache=c, block_table=i[:6].view(2, 3), cu_seqlens_q=i[:3],
+              kv_lens=i[:2])
+    op(**ok)
+    for kw in (dict(q=q.float()), dict(q=q[:, :3]), dict(q=q.transpose(1, 2)), dict(k_cache=c[:4]),
+               dict(k_cache=c.float()), dict(v_cache=c.permute(0, 2, 1, 3).contiguous()
+                                             .permute(0, 2, 1, 3)),
+               dict(k_cache=c[..., ::2], v_cache=c[..., ::2]), dict(block_table=i[:6].view(3, 2)),
+               dict(block_table=i[:6].view(2, 3).long()), dict(cu_seqlens_q=i[:2]),
+               dict(kv_lens=i[:4:2]), dict(out=q[:1]), dict(lse=i[:8].view(2, 4))):
+        with pytest.raises(ValueError):
+            op(**{**ok, **kw})
+    kv = [ok[k] for k in ("k_cache", "v_cache", "block_table", "cu_seqlens_q", "kv_lens")]
+    for a in ((q, q, q), (q, q[:, :2], q[:1, :2])):
+        with pytest.raises(ValueError):
+            op.append(*a, *kv)
+    with pytest.raises(ValueError):
+        op.append(q, q[:, :2], q[:, :2], *kv, cos_sin=i.view(2, 4))
+    with pytest.raises(binding.GbmoeError):        # rotary_dim not a multiple of 16
+        op.append(q, q[:, :2], q[:, :2], *kv, cos_sin=torch.zeros(9, 8, device=DEV))
+
+
 def test_norm_output_feeds_the_fp8_layer_format(cuda_lib):
     """q and scale have the layout of moe_quant_fp8_per_token_group: on rows whose y is exact in
     bf16 (powers of two), both give the same bytes."""
