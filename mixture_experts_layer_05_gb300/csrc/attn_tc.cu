@@ -234,13 +234,14 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
   auto pv_done = [&](int g) { return bar0 + 8u * (16 + g); };
   auto raw_full = [&](int s) { return bar0 + 8u * (18 + s); };
   auto raw_empty = [&](int s) { return bar0 + 8u * (22 + s); };
+  auto pa_done = [&](int g) { return bar0 + 8u * (42 + g); };  // first 64 keys' product
   auto v_raw = [&](int s) { return bar0 + 8u * (26 + s); };   // stage s: an edge V tile landed
   auto d_full = [&](int i) { return bar0 + 8u * (34 + i); };  // piece descriptors
   auto d_empty = [&](int i) { return bar0 + 8u * (38 + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  TcPiece* pieces = reinterpret_cast<TcPiece*>(bars + 42);
-  long long* wsum = reinterpret_cast<long long*>(bars + 42 + kTcPieces * 8);  // 32
+  TcPiece* pieces = reinterpret_cast<TcPiece*>(bars + 44);
+  long long* wsum = reinterpret_cast<long long*>(bars + 44 + kTcPieces * 8);  // 32
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = a.b.status;
   pdl_trigger();
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       mbar_init(p_full(g, 0), 4);
       mbar_init(p_full(g, 1), 4);
       mbar_init(pv_done(g), 1);
+      mbar_init(pa_done(g), 1);
     }
     for (int i = 0; i < kTcPieces; ++i) {
       mbar_init(d_full(i), 1);
@@ -421,107 +423,113 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         // the last scores are out, so Q's place is free: the next piece's is on its way while
         // this tile is weighed
         if (t + 1 == job.nt && (have = seek(false)) == 1) send_q();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_wait_ld(s[i]);
         const int j0 = job.j0 + t * kAttnTK;
         const bool masked = j0 < job.in_lo || j0 + kAttnTK > job.in_hi;
-        auto drop = [&](uint32_t (&x)[32], int i) {  // keys that this row does not attend
-          const int lo = job.lo - j0 - 32 * i, hi = job.hi - j0 - 32 * i;
+        uint64_t sum[2] = {0ull, 0ull};
+        // The tile in two steps of 64 keys; the product over a step's keys may begin before the
+        // next step's weights are there.
+        uint32_t s[2][32];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = c >= hi ? 0xff800000u : x[c];  // -inf
-          if (j0 < job.in_lo)
+        for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, s[i]);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] = c < lo ? 0xff800000u : x[c];
-        };
-        if (masked)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) drop(s[i], i);
-        uint64_t off2, sum[2] = {0ull, 0ull};
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        // weights of 64 keys, two to a word, their sum and the largest score
-        auto weigh = [&](const uint32_t (&x)[32], const uint32_t (&y)[32], uint32_t (&w)[32]) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const uint32_t u = c < 16 ? x[2 * c % 32] : y[2 * c % 32];
-            const uint32_t v = c < 16 ? x[2 * c % 32 + 1] : y[2 * c % 32 + 1];
-            mx[c & 3] = fmaxf(fmaxf(mx[c & 3], __uint_as_float(u)), __uint_as_float(v));
-            float e0, e1;
-            unpair(fma2(pair_bits(u, v), sc2, off2), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            sum[c & 1] = add2(sum[c & 1], pair(e0, e1));
-            w[c] = FP8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
-          }
-        };
-        auto largest = [&](int i0) {  // with chunks i0 .. 3
-#pragma unroll
-          for (int i = i0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < 32; c += 2)
-              mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(s[i][c])),
-                                    __uint_as_float(s[i][c + 1]));
-          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        };
-        uint32_t w[32];
-        // The weights go by the reference so far; the tile's own maximum, off that path, only
-        // tells whether they grow too large. A piece's first tile sets the reference.
-        if (t == 0) m = largest(0);
-        for (;;) {
-          const float off = m == -INFINITY ? 0.f : -m * a.scale_log2;
-          off2 = pair(off, off);
-          weigh(s[0], s[1], w);
-          const float mn = largest(2);
-          if (!__any_sync(0xffffffffu, mn > m && (mn - m) * a.scale_log2 > T::kSlack)) break;
-          // O catches up with the new maxima, once the product before this tile's is done (t > 0:
-          // the first tile's reference is its maximum)
-          if (!wait(pv_done(g), (tc - 1) & 1u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const float f = mn > m ? ex2((m - mn) * a.scale_log2) : 1.f;
-          m = fmaxf(m, mn);
-          l *= f;
-#pragma unroll 1
-          for (int i = 0; i < D / 32; ++i) {
-            tmem_ld32(to + 32 * i, w);
-            tmem_wait_ld(w);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
-            tmem_st32(to + 32 * i, w);
-          }
-          tmem_wait_st();
-          // the first 64 scores once more: their registers were given up
-#pragma unroll
-          for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, s[i]);
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) tmem_wait_ld(s[i]);
-          if (masked)
+          auto drop = [&]() {  // keys that this row does not attend
+            const int lo = job.lo - j0 - 64 * h, hi = job.hi - j0 - 64 * h;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) drop(s[i], i);
-          sum[0] = sum[1] = 0ull;
+            for (int c = 0; c < 64; ++c) {
+              uint32_t& x = s[c / 32][c % 32];
+              x = c >= hi ? 0xff800000u : x;  // -inf
+            }
+            if (j0 < job.in_lo)
+#pragma unroll
+              for (int c = 0; c < 64; ++c) {
+                uint32_t& x = s[c / 32][c % 32];
+                x = c < lo ? 0xff800000u : x;
+              }
+          };
+          if (masked) drop();
+          // The weights go by the reference so far; the keys' own maximum, off that path, only
+          // tells whether they grow too large. A piece's first keys set the reference.
+          if (t == 0 && h == 0) {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 64; c += 2)
+              mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(s[c / 32][c % 32])),
+                                    __uint_as_float(s[c / 32][c % 32 + 1]));
+            m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          }
+          uint32_t w[32];
+          for (;;) {
+            const float off = m == -INFINITY ? 0.f : -m * a.scale_log2;
+            const uint64_t off2 = pair(off, off);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint64_t part[2] = {0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const uint32_t u = s[c / 16][2 * c % 32], v = s[c / 16][2 * c % 32 + 1];
+              mx[c & 3] = fmaxf(fmaxf(mx[c & 3], __uint_as_float(u)), __uint_as_float(v));
+              float e0, e1;
+              unpair(fma2(pair_bits(u, v), sc2, off2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              part[c & 1] = add2(part[c & 1], pair(e0, e1));
+              w[c] = FP8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+            }
+            const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (!__any_sync(0xffffffffu, mn > m && (mn - m) * a.scale_log2 > T::kSlack)) {
+              sum[0] = add2(sum[0], part[0]);
+              sum[1] = add2(sum[1], part[1]);
+              break;
+            }
+            // O catches up with the new maxima once the product before these keys' is done (a
+            // piece's first keys have none, but their reference is their maximum)
+            if (!(h ? wait(pa_done(g), tc & 1u) : wait(pv_done(g), (tc - 1) & 1u))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float f = mn > m ? ex2((m - mn) * a.scale_log2) : 1.f;
+            m = fmaxf(m, mn);
+            {
+              float x, y, u, v;
+              unpair(sum[0], x, y);
+              unpair(sum[1], u, v);
+              l = (l + ((x + y) + (u + v))) * f;
+              sum[0] = sum[1] = 0ull;
+            }
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              tmem_ld32(to + 32 * i, w);
+              tmem_wait_ld(w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
+              tmem_st32(to + 32 * i, w);
+            }
+            tmem_wait_st();
+            // the scores once more: their registers were given up
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_ld32(ts + 64 * h + 32 * i, s[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_wait_ld(s[i]);
+            if (masked) drop();
+          }
+          if (!ok) break;
+          if (h == 0)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_ld32(ts + 64 + 32 * i, s[i]);
+          tmem_st32(ts + 32 * h, w);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(g, h));
         }
         if (!ok) break;
-        // the product over the first 64 keys may begin before the other weights are there
-        tmem_st32(ts, w);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(g, 0));
-        weigh(s[2], s[3], w);
-        tmem_st32(ts + 32, w);
-        {
-          float x, y;
-          unpair(add2(sum[0], sum[1]), x, y);
-          l += x + y;
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(g, 1));
+        float x, y, u, v;
+        unpair(sum[0], x, y);
+        unpair(sum[1], u, v);
+        l += (x + y) + (u + v);
       }
       if (!ok) break;
       if (have == 2 && (have = seek(true)) == 1) send_q();
@@ -627,6 +635,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_ts(col + 256u, col + 8u * k, vb + k * (2048 >> 4), kIdO, t > 0 || k > 0);
+              mma_commit(pa_done(g));
               if (!(ok = wait1(p_full(g, 1), par))) break;
               tc_fence_after();
 #pragma unroll
