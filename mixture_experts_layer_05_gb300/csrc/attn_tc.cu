@@ -20,6 +20,8 @@
 //   warp 9           the schedule, as a ring of piece descriptors ahead of the other roles, and
 //                    the tile copies: TMA, one box per page and 128 bytes of the head; page ids
 //                    a tile ahead, the next piece's Q into L2
+//   warp 11          bf16 cache: V's copies (a tile in pages of 16 rows takes 16 boxes, which one
+//                    warp issues one after the other)
 //   warp 10          bf16 cache: zeroes what a V tile holds outside the unit's keys
 //   warps 10, 11     e4m3 cache: codes to f16 (exact) into the operand tiles
 //
@@ -34,13 +36,14 @@ namespace gbmoe {
 namespace {
 
 constexpr int kTcBR = 256;
-constexpr int kTcMmaWarp = 8, kTcCopyWarp = 9, kTcCvtWarp = 10;
+constexpr int kTcMmaWarp = 8, kTcCopyWarp = 9, kTcCvtWarp = 10, kTcCopyWarpV = 11;
 constexpr int kTcCvtWarps = 2;
+constexpr int kTcSplitShift = 6;  // pages below 64 rows: K's and V's copies by a warp each
 constexpr int kTcExtra = 3;      // cost of beginning a unit, in tiles
 
 template <bool FP8, int D>
 struct Tc {
-  static constexpr int kThreads = 32 * (kTcCvtWarp + (FP8 ? kTcCvtWarps : 1));
+  static constexpr int kThreads = 32 * 12;                  // three warps a scheduler
   static constexpr uint32_t kTile = kAttnTK * D * 2;        // one operand tile (16 bit)
   static constexpr uint32_t kRawTile = kAttnTK * D;         // one tile of codes
   static constexpr int kRaw = FP8 ? 3 : 0;                  // code stages
@@ -52,7 +55,7 @@ struct Tc {
   static constexpr float kSlack = FP8 ? 14.f : 60.f;
   static constexpr uint32_t kRawPitch = D < 128 ? D : 128;  // bytes of a code row
   static constexpr uint32_t kRawSwz = kRawPitch == 128 ? 0x70u : 0x30u;
-  static constexpr int kReaders = 8 + 1 + (FP8 ? kTcCvtWarps : 1);  // warps that read a piece
+  static constexpr int kReaders = 8 + 1 + 2;  // warps that read a piece: softmax, MMA, 10 and 11
   static constexpr size_t kSmem = 1024 + kQ + kStages * kTile + kRaw * kRawTile + kOut + 1024;
   static_assert(kSmem <= 232448, "shared memory per CTA exceeded");
   static_assert((kAttnMaxSeqs + 1) * 8 <= kQ + kStages * kTile, "the plan lies in Q and the ring");
@@ -196,7 +199,8 @@ struct alignas(16) TcPiece {
   int rows, r0;        // rows of the unit, its first row in the sequence
   int q0, n, L, head;  // the sequence, the kv head
   int slot;            // piece slot in the workspace, -1: the whole unit
-  int pad[3];
+  int seq;             // index of the sequence
+  int pad[2];
 };
 static_assert(sizeof(TcPiece) == 64, "read as four 16-byte words");
 constexpr int kTcPieces = 4;
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     p.nt = w0.x; p.j0 = w0.y; p.lo = w0.z; p.hi = w0.w;
     p.in_lo = w1.x; p.in_hi = w1.y; p.rows = w1.z; p.r0 = w1.w;
     p.q0 = w2.x; p.n = w2.y; p.L = w2.z; p.head = w2.w;
-    p.slot = w3.x;
+    p.slot = w3.x; p.seq = w3.y;
   };
   auto release_piece = [&]() {
     __syncwarp();
@@ -668,35 +672,43 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kTcCopyWarp) {
+  } else if (warp == kTcCopyWarp || (!FP8 && warp == kTcCopyWarpV)) {
     // ------------------------------------------------------------ tile copies
     constexpr int kParts = FP8 ? 1 : D / 64;
     constexpr uint32_t kPitch = FP8 ? T::kRawPitch : 128;
     constexpr uint32_t kN = FP8 ? T::kRaw : T::kStages;
+    const bool split = !FP8 && a.b.page_shift < kTcSplitShift;  // K and V by a warp each
+    const bool take_k = warp == kTcCopyWarp, take_v = split ? !take_k : take_k;
     const int ps = 1 << a.b.page_shift;
     const int box_rows = min(ps, kAttnTK);
     const int boxes = kAttnTK / box_rows * kParts;  // <= 32: pages of at least 8 rows
     const int pl = lane / kParts, part = lane % kParts;
     const uint32_t box_bytes = (uint32_t)box_rows * kPitch;
-    Ring rg{0, 0};
+    static_assert(FP8 || kN % 2 == 0, "K in the even stages, V in the odd ones");
+    Ring rg{take_k ? 0u : 1u, 0};
     uint32_t issued = 0;
     auto fullb = [&](uint32_t s) { return FP8 ? raw_full(s) : full(s); };
     auto emptyb = [&](uint32_t s) { return FP8 ? raw_empty(s) : empty(s); };
     AttnRec* rec = &attn_scratch(a.scratch, kTcBR).rec[blockIdx.x];
-    if (lane == 0) rec->starts = rec->mid = rec->ends = 0;
-    TcPiece d, d2;       // the piece being copied, and the one after it
-    int ds = 0, ds2 = 0;  // their sequences
+    if (take_k && lane == 0) rec->starts = rec->mid = rec->ends = 0;
+    auto drain_pieces = [&]() {  // a warp without work keeps the schedule going
+      TcPiece p;
+      while (get_piece(p)) {
+      }
+      return false;
+    };
+    TcPiece d, d2;  // the piece being copied, and the one after it
     // Publishes the next piece (nt = 0: none is left) and sends its query rows to L2: one run of
     // the group's heads per token.
-    auto publish = [&](TcPiece& d, int& ds) {
+    auto publish = [&](TcPiece& d) {
       AttnPiece p;
       const bool have = next_piece(a.b, sh, cur, p);
       d.nt = d.j0 = d.lo = d.hi = d.in_lo = d.in_hi = d.rows = d.r0 = 0;
-      d.q0 = d.n = d.L = d.head = d.slot = 0;
+      d.q0 = d.n = d.L = d.head = d.slot = d.seq = 0;
       if (have) {
         const KeyRange k0 = key_range(p.q, p.u.i0, sh.causal, sh.window);
         const KeyRange k1 = key_range(p.q, p.u.i1, sh.causal, sh.window);
-        ds = p.s;
+        d.seq = p.s;
         d.nt = p.tb - p.ta;
         d.j0 = (p.u.t0 + p.ta) * kAttnTK;
         d.lo = p.u.lo;
@@ -733,53 +745,58 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         dst[0] = make_int4(d.nt, d.j0, d.lo, d.hi);
         dst[1] = make_int4(d.in_lo, d.in_hi, d.rows, d.r0);
         dst[2] = make_int4(d.q0, d.n, d.L, d.head);
-        dst[3] = make_int4(d.slot, 0, 0, 0);
+        dst[3] = make_int4(d.slot, d.seq, 0, 0);
         mbar_arrive(d_full(dq.slot));
       }
       __syncwarp();
       dq.next(kTcPieces);
       return true;
     };
-    bool ok = publish(d, ds);
-    for (; ok && d.nt > 0; d = d2, ds = ds2) {
+    bool ok = take_k ? publish(d) : split && get_piece(d);
+    if (!take_k && !split) ok = drain_pieces();
+    while (ok && d.nt > 0) {
       auto live_at = [&](int t) {
         const int j = d.j0 + t * kAttnTK + pl * box_rows;
         return t < d.nt && lane < boxes && j < d.hi && j + box_rows > d.lo;
       };
       auto page_at = [&](int t) {
-        return live_at(t) ? page_of(a.b, ds, d.j0 + t * kAttnTK + pl * box_rows) : 0;
+        return live_at(t) ? page_of(a.b, d.seq, d.j0 + t * kAttnTK + pl * box_rows) : 0;
       };
       auto copy = [&](int t, int page, bool v) {
         const bool live = live_at(t);
         const uint32_t bytes = box_bytes * __popc(__ballot_sync(0xffffffffu, live));
-        if (!wait(emptyb(rg.slot), rg.phase ^ 1u)) return false;
+        const uint32_t slot = rg.slot;
+        if (!wait(emptyb(slot), rg.phase ^ 1u)) return false;
         // a V tile with positions that no row attends passes through the cleaning warp
         const int j = d.j0 + t * kAttnTK;
-        const uint32_t bar = !FP8 && v && edge(d, j) ? v_raw(rg.slot) : fullb(rg.slot);
+        const uint32_t bar = !FP8 && v && edge(d, j) ? v_raw(slot) : fullb(slot);
         if (lane == 0) mbar_expect_tx(bar, bytes);
         __syncwarp();
         if (live)
-          tma_load_4d((FP8 ? codes + rg.slot * T::kRawTile : ring + rg.slot * T::kTile) +
-                          part * kHalf + pl * box_bytes,
+          tma_load_4d((FP8 ? codes + slot * T::kRawTile : ring + slot * T::kTile) + part * kHalf +
+                          pl * box_bytes,
                       v ? &maps.v : &maps.k, bar, part * 64, (j + pl * box_rows) & (ps - 1),
                       d.head, page);
         ++issued;
         rg.next(kN);
+        if (split) rg.next(kN);  // the other warp's stage
         return true;
       };
       int page = page_at(0);
       for (int t = 0; ok && t < d.nt; ++t) {
         const int next = page_at(t + 1);
-        ok = copy(t, page, false) && copy(t, page, true);
+        ok = (!take_k || copy(t, page, false)) && (!take_v || copy(t, page, true));
         page = next;
-        if (ok && t == 0) ok = publish(d2, ds2);  // one piece ahead, behind the first copies
+        if (ok && take_k && t == 0) ok = publish(d2);  // one piece ahead, behind the first copies
       }
+      if (take_k) d = d2;
+      else ok = ok && get_piece(d);
     }
     if (*abort_flag && lane == 0)  // let what is in flight land before the CTA can exit
-      for (uint32_t j = issued > kN ? issued - kN : 0; j < issued; ++j)
-        land(fullb(j % kN), (j / kN) & 1u);
+      for (uint32_t i = 0; i < (issued < kN ? issued : kN); ++i)
+        land(fullb((rg.slot + kN - 1 - i) % kN), rg.slot > i ? rg.phase : rg.phase ^ 1u);
     __syncwarp();
-  } else if (!FP8) {
+  } else if (!FP8 && warp == kTcCvtWarp) {
     // ------------------------------------------------------------ V tiles at the edges
     // v of positions that no row attends becomes 0, whatever the page holds (0 * NaN = NaN).
     // Only a unit's first tile (window) and last tile (length) have such positions.
@@ -806,7 +823,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       }
       at += 2 * p.nt;
     }
-  } else {
+  } else if (FP8) {
     // ------------------------------------------------------------ codes to f16
     const int row0 = threadIdx.x - 32 * kTcCvtWarp;
     Ring rq{0, 0}, rg{0, 0};
