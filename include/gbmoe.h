@@ -578,7 +578,8 @@ gbmoe_status_t moe_kv_append(const gbmoe_attn_config_t* cfg, int32_t num_tokens,
  * Workspace: moe_paged_attention_workspace_size(cfg) bytes (0: bad configuration), 256-byte
  * aligned, its first 1024 bytes zeroed once (and again after a GBMOE_ERR_TIMEOUT: beside the
  * status word they hold counters that every completed call leaves at zero). T = 0 is a no-op;
- * T * num_q_heads at most 2^30 (else UNSUPPORTED).
+ * T * num_q_heads at most 2^30, and num_kv_heads * (T * group / 8 + num_seqs) * (positions of a
+ * block table row / 128 + 5) below 2^31 (else UNSUPPORTED).
  */
 size_t moe_paged_attention_workspace_size(const gbmoe_attn_config_t* cfg);
 gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int32_t num_tokens,

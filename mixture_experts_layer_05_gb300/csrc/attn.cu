@@ -11,6 +11,12 @@ size_t attn_scratch_bytes(int D) {
   return kAttnMaxCtas * (sizeof(AttnRec) + 2 * (size_t)kAttnMaxBR * (sizeof(float2) + D * 4));
 }
 
+bool attn_fits(const AttnArgs& a) {
+  const double cap = (double)a.b.table_stride * (1 << a.b.page_shift);
+  // units of 8 rows and the widest unit's extra cost: no launch has a longer line
+  return line_bound(attn_shape(a, 3, 4), a.b.T, a.b.S, cap) < 2147483647.0;
+}
+
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
   // query rows per sequence and kv head, on average (the lengths are on the device); either
   // kernel is right for any

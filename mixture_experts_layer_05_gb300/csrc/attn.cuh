@@ -48,12 +48,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 // The line, the CTAs that share it, and the end of this one's range.
 struct AttnSpan {
-  long long W, end;
-  int ctas;
+  int W, end, ctas;
 };
 // The CTA whose range holds the place x of the line.
-__device__ __forceinline__ int cta_of(const AttnSpan& s, long long x) {
-  int c = (int)(x * s.ctas / s.W);
+__device__ __forceinline__ int cta_of(const AttnSpan& s, int x) {
+  int c = (int)((float)x * s.ctas / s.W);
+  c = min(max(c, 0), s.ctas - 1);
   while (range_at(s.W, c + 1, s.ctas) <= x) ++c;
   while (range_at(s.W, c, s.ctas) > x) --c;
   return c;
@@ -65,8 +65,7 @@ constexpr int kPlanBlocks = 4;  // row blocks that one thread adds up by itself
 // sums, wsum: 32 more. A thread takes a sequence of few row blocks (single tokens), a warp one of
 // many: a prompt of 8191 tokens has 128, and one thread walking them cost 45 us.
 __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnShape& sh,
-                                                long long* line, long long* wsum,
-                                                AttnSpan& span) {
+                                                int* line, int* wsum, AttnSpan& span) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int warps = nt >> 5;
   for (int s = tid; s < b.S; s += nt) {
@@ -75,51 +74,54 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
   }
   if (tid == 0) line[0] = 0;
   __syncthreads();
-  for (int s0 = warp * 32; s0 < b.S; s0 += warps * 32) {
+  // few sequences: every warp looks through all and takes each `warps`-th; many: 32 apiece
+  const bool few = b.S <= 1024;
+  int mine = 0;
+  for (int s0 = few ? 0 : warp * 32; s0 < b.S; s0 += few ? 32 : warps * 32) {
     uint32_t many = __ballot_sync(0xffffffffu, s0 + lane < b.S && line[s0 + lane + 1] < 0);
     while (many) {
       const int s = s0 + __ffs(many) - 1;
       many &= many - 1;
+      if (few && mine++ % warps != warp) continue;
       const SeqInfo q = seq_info(b, s);
-      long long t = 0;
-      for (int rb = lane; rb < unit_blocks(sh, q.n); rb += 32) t += unit_length(sh, q, rb);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (lane == 0) line[s + 1] = t * sh.hkv;
+      const int blocks = unit_blocks(sh, q.n);
+      int t = 0;
+      for (int rb = lane; rb < blocks; rb += 32) t += unit_length(sh, q, rb);
+      t = __reduce_add_sync(0xffffffffu, t);
+      if (lane == 0) line[s + 1] = -2 - t * sh.hkv;  // marked until every warp has looked
     }
   }
   __syncthreads();
   // prefix sums: a run of sequences per thread
   const int per = (b.S + nt - 1) / nt;
   const int s0 = min(tid * per, b.S), s1 = min(s0 + per, b.S);
-  long long sum = 0;
+  int sum = 0;
   for (int s = s0; s < s1; ++s) {
-    sum += line[s + 1];
+    const int v = line[s + 1];
+    sum += v < 0 ? -2 - v : v;
     line[s + 1] = sum;
   }
-  long long inc = sum;
+  int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
   if (lane == 31) wsum[warp] = inc;
   __syncthreads();
-  long long base = inc - sum;
+  int base = inc - sum;
   for (int w = 0; w < warp; ++w) base += wsum[w];
   for (int s = s0; s < s1; ++s) line[s + 1] += base;
   __syncthreads();
-  const long long W = line[b.S];
+  const int W = line[b.S];
   span.W = W;
-  span.ctas = W < gridDim.x ? (int)W : (int)gridDim.x;  // every one of these has some of the line
-  const int me = min((int)blockIdx.x, span.ctas);
-  const long long a = range_at(W, me, max(span.ctas, 1));
-  const long long e = me < span.ctas ? range_at(W, me + 1, span.ctas) : a;
-  span.end = e;
+  span.ctas = min(W, (int)gridDim.x);  // every one of these has some of the line
   AttnCursor c;
-  c.s = c.head = c.rb = c.off = 0;
-  c.left = 0;
-  if (e > a) {
+  c.s = c.head = c.rb = c.off = c.left = 0;
+  span.end = 0;
+  if ((int)blockIdx.x < span.ctas) {
+    const int a = range_at(W, blockIdx.x, span.ctas);
+    span.end = range_at(W, blockIdx.x + 1, span.ctas);
     int lo = 0, hi = b.S;  // the sequence with line[s] <= a < line[s + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -127,23 +129,21 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
       else hi = mid;
     }
     const SeqInfo q = seq_info(b, lo);
-    const long long head = (line[lo + 1] - line[lo]) / sh.hkv;  // length of one head
-    long long rem = a - line[lo];
+    const int head = (line[lo + 1] - line[lo]) / sh.hkv;  // length of one head
+    int rem = a - line[lo];
     c.s = lo;
-    c.left = e - a;
-    while (c.head + 1 < sh.hkv && rem >= head) {
-      rem -= head;
-      ++c.head;
-    }
+    c.left = span.end - a;
+    c.head = rem / head;
+    rem -= c.head * head;
     const int blocks = unit_blocks(sh, q.n);
     if (blocks > kPlanBlocks) {
       // every warp finds the row block, 32 at a time
       for (; c.rb < blocks; c.rb += 32) {
         const int rb = c.rb + lane;
-        long long at = rb < blocks ? unit_length(sh, q, rb) : 0;
+        int at = rb < blocks ? unit_length(sh, q, rb) : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, at, o);
+          const int v = __shfl_up_sync(0xffffffffu, at, o);
           if (lane >= o) at += v;
         }
         const uint32_t behind = __ballot_sync(0xffffffffu, at <= rem);
@@ -155,7 +155,7 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
         }
         rem -= __shfl_sync(0xffffffffu, at, 31);
       }
-      c.off = (int)rem;
+      c.off = rem;
     } else {
       walk_blocks(sh, q, rem, c);
     }
@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh
     }
   }
   if (!valid) return;
-  const size_t orow = (size_t)(rec.q0 + ur / sh.G) * a.hq + rec.head * sh.G + ur % sh.G;
+  const size_t orow = (size_t)(rec.q0 + div_group(sh, ur)) * a.hq + rec.head * sh.G +
+                      (ur - div_group(sh, ur) * sh.G);
   const float inv = l == 0.f ? 0.f : a.v_scale / l;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -283,6 +284,18 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh
   }
   if (a.lse && col == 0)
     a.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
+// Shape of a launch whose units have 1 << br_shift rows.
+AttnShape attn_shape(const AttnArgs& a, int br_shift, int extra) {
+  AttnShape sh;
+  set_group(sh, a.hq / a.hkv);
+  sh.hkv = a.hkv;
+  sh.br_shift = br_shift;
+  sh.extra = extra;
+  sh.causal = a.causal;
+  sh.window = a.window;
+  return sh;
 }
 
 cudaError_t launch_attn_join(const AttnArgs& a, const AttnShape& sh, int ctas,

@@ -48,7 +48,7 @@ struct Dec {
   static constexpr uint32_t kTail = NT == 1 ? 1024 : 2048;          // barriers, row sums
   static constexpr size_t kSmem = 1024 + kRing + kJoin + kTail;
   static_assert(kSmem <= 232448, "shared memory per CTA exceeded");
-  static_assert((kAttnMaxSeqs + 1) * 8 <= kRing, "the plan lies in the ring");
+  static_assert((kAttnMaxSeqs + 1) * 4 <= kRing, "the plan lies in the ring");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   auto empty = [&](int s) { return bar0 + 8u * (12 + s); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 24);
   float2* wml = reinterpret_cast<float2*>(bars + 26);  // [rows][warps]
-  long long* wsum = reinterpret_cast<long long*>(bars + 26 + T::kBR * kDecWarps);  // 32
-  static_assert((26 + T::kBR * kDecWarps + 32) * 8 <= T::kTail, "tail");
+  int* wsum = reinterpret_cast<int*>(bars + 26 + T::kBR * kDecWarps);  // 32
+  static_assert((26 + T::kBR * kDecWarps + 16) * 8 <= T::kTail, "tail");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   // the line of tiles is laid out in the ring before the first copy lands there
   AttnSpan span;
-  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<long long*>(smem), wsum, span);
+  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
   fence_async_proxy();
   __syncthreads();
   int* status = a.b.status;
@@ -228,12 +228,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     bool ok = true;
     auto swz = [](uint32_t off) { return off ^ ((off >> 3) & T::kSwz); };
     for (;;) {
-      const long long unit_at = span.end - cur.left - cur.off;  // the unit's place on the line
+      const int unit_at = span.end - cur.left - cur.off;  // the unit's place on the line
       AttnPiece p;
       if (!next_piece(a.b, sh, cur, p)) break;
       auto write_out = [&](int r, int d, const float4& v, float M, float L) {
-        const int rr = p.rb * T::kBR + r;
-        const size_t orow = (size_t)(p.q.q0 + rr / sh.G) * a.hq + p.head * sh.G + rr % sh.G;
+        const int rr = p.rb * T::kBR + r, tok = div_group(sh, rr);
+        const size_t orow = (size_t)(p.q.q0 + tok) * a.hq + p.head * sh.G + (rr - tok * sh.G);
         const float inv = L == 0.f ? 0.f : a.v_scale / L;  // no key: zeros
         uint2 w;
         w.x = pack_bf16x2(v.x * inv, v.y * inv);
@@ -249,9 +249,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = 8 * n + g, rr = p.rb * T::kBR + (r < rows ? r : 0);
+        const int tok = div_group(sh, rr);
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                   (size_t)(p.q.q0 + rr / sh.G) * a.q_stride +
-                                   (size_t)(p.head * sh.G + rr % sh.G) * D;
+                                   (size_t)(p.q.q0 + tok) * a.q_stride +
+                                   (size_t)(p.head * sh.G + (rr - tok * sh.G)) * D;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t lo = 0u, hi = 0u;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = 8 * n + 2 * c + e;
-          kr[n][e] = key_range(p.q, (p.rb * T::kBR + r) / sh.G, sh.causal, sh.window);
+          kr[n][e] = key_range(p.q, div_group(sh, p.rb * T::kBR + r), sh.causal, sh.window);
           if (r >= rows) kr[n][e].hi = kr[n][e].lo = 0;
         }
       const KeyRange k0 = key_range(p.q, p.u.i0, sh.causal, sh.window);
@@ -591,14 +592,8 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   DecMaps maps;
   if (!make_cache_map(&maps.k, a.c.k, a) || !make_cache_map(&maps.v, a.c.v, a))
     return cudaErrorInvalidValue;
-  AttnShape sh;
-  sh.G = a.hq / a.hkv;
-  sh.hkv = a.hkv;
-  sh.br_shift = NT == 1 ? 3 : 4;
+  const AttnShape sh = attn_shape(a, NT == 1 ? 3 : 4, 0);
   static_assert(T::kBR == 1 << (NT == 1 ? 3 : 4), "rows per unit");
-  sh.extra = 0;
-  sh.causal = a.causal;
-  sh.window = a.window;
   const int ctas = num_sms() < kAttnMaxCtas ? num_sms() : kAttnMaxCtas;
   return launch_kernel(attn_decode_kernel<FP8, D, NT>, dim3(ctas), dim3(kDecThreads), T::kSmem,
                        stream, maps, a, sh);

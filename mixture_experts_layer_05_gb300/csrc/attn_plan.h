@@ -17,11 +17,31 @@ constexpr int kAttnTK = 128;  // keys per tile
 
 struct AttnShape {
   int G, hkv;      // query heads per kv head, kv heads
+  uint32_t g_mul;  // r / G for 0 <= r < 2^31 is the high word of r * g_mul, shifted (G > 1)
+  int g_shift;
   int br_shift;    // rows per unit: 1 << br_shift
   int extra;       // cost of a unit beyond its tiles, in tiles
   bool causal;
   int window;
 };
+
+// g_mul = ceil(2^(31 + s) / G), s = ceil(log2 G): division by an invariant integer (Granlund and
+// Montgomery); a division instruction sequence per use was a good part of a small call.
+inline void set_group(AttnShape& a, int G) {
+  int s = 0;
+  while ((1 << s) < G) ++s;
+  a.G = G;
+  a.g_mul = G > 1 ? (uint32_t)(((1ull << (31 + s)) + G - 1) / G) : 0;
+  a.g_shift = s - 1;
+}
+GBMOE_HD int div_group(const AttnShape& a, int r) {
+  if (a.G == 1) return r;
+#ifdef __CUDA_ARCH__
+  return (int)(__umulhi((uint32_t)r, a.g_mul) >> a.g_shift);
+#else
+  return (int)(((uint64_t)(uint32_t)r * a.g_mul >> 32) >> a.g_shift);
+#endif
+}
 
 struct UnitKeys {
   int i0, i1;      // first and last token of the unit
@@ -38,8 +58,8 @@ GBMOE_HD UnitKeys unit_keys(const AttnShape& a, const SeqInfo& q, int rb) {
   const int r0 = rb << a.br_shift;
   int r1 = r0 + (1 << a.br_shift);
   if (r1 > q.n * a.G) r1 = q.n * a.G;
-  u.i0 = r0 / a.G;
-  u.i1 = (r1 - 1) / a.G;
+  u.i0 = div_group(a, r0);
+  u.i1 = div_group(a, r1 - 1);
   u.lo = key_range(q, u.i0, a.causal, a.window).lo;
   u.hi = key_range(q, u.i1, a.causal, a.window).hi;
   if (u.hi <= u.lo) {
@@ -57,9 +77,9 @@ GBMOE_HD UnitKeys unit_keys(const AttnShape& a, const SeqInfo& q, int rb) {
 GBMOE_HD int unit_length(const AttnShape& a, const SeqInfo& q, int rb) {
   return unit_keys(a, q, rb).tiles + a.extra;
 }
-GBMOE_HD long long seq_length(const AttnShape& a, const SeqInfo& q) {
+GBMOE_HD int seq_length(const AttnShape& a, const SeqInfo& q) {
   const int blocks = unit_blocks(a, q.n);
-  long long t = 0;
+  int t = 0;
   for (int rb = 0; rb < blocks; ++rb) t += unit_length(a, q, rb);
   return t;
 }
@@ -67,18 +87,18 @@ GBMOE_HD long long seq_length(const AttnShape& a, const SeqInfo& q) {
 // A place on the line of tiles.
 struct AttnCursor {
   int s, head, rb, off;    // sequence, kv head, row block, length of the unit that is behind
-  long long left;          // length of this CTA's range that lies ahead
+  int left;                // length of this CTA's range that lies ahead
 };
 
 // Moves the cursor `rem` further, over row blocks of the sequence q.
-GBMOE_HD void walk_blocks(const AttnShape& a, const SeqInfo& q, long long rem, AttnCursor& c) {
+GBMOE_HD void walk_blocks(const AttnShape& a, const SeqInfo& q, int rem, AttnCursor& c) {
   for (;;) {
     const int t = unit_length(a, q, c.rb);
     if (rem < t) break;
     rem -= t;
     ++c.rb;
   }
-  c.off = (int)rem;
+  c.off = rem;
 }
 
 // The part of a unit that one CTA computes.
@@ -103,7 +123,7 @@ GBMOE_HD AttnPiece take_piece(const AttnShape& a, const SeqInfo& q, AttnCursor& 
   p.q = q;
   p.u = unit_keys(a, q, c.rb);
   const int len = p.u.tiles + a.extra;
-  const int end = len - c.off > c.left ? c.off + (int)c.left : len;
+  const int end = len - c.off > c.left ? c.off + c.left : len;
   p.ta = c.off > a.extra ? c.off - a.extra : 0;
   p.tb = end > a.extra ? end - a.extra : 0;
   c.left -= end - c.off;
@@ -122,8 +142,12 @@ GBMOE_HD AttnPiece take_piece(const AttnShape& a, const SeqInfo& q, AttnCursor& 
 }
 
 // CTA c of g takes the range [range_at(c), range_at(c + 1)) of a line of length W.
-GBMOE_HD long long range_at(long long W, int c, int g) {
-  return W / g * c + W % g * c / g;
+GBMOE_HD int range_at(int W, int c, int g) { return W / g * c + W % g * c / g; }
+
+// An upper bound on the length of a line: T tokens in S sequences of at most `cap` keys. Calls
+// whose bound does not fit an int are refused.
+inline double line_bound(const AttnShape& a, double T, double S, double cap) {
+  return a.hkv * (T * a.G / (1 << a.br_shift) + S) * (cap / kAttnTK + 1 + a.extra);
 }
 
 }  // namespace gbmoe

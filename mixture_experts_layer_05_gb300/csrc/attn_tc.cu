@@ -58,7 +58,7 @@ struct Tc {
   static constexpr int kReaders = 8 + 1 + 2;  // warps that read a piece: softmax, MMA, 10 and 11
   static constexpr size_t kSmem = 1024 + kQ + kStages * kTile + kRaw * kRawTile + kOut + 1024;
   static_assert(kSmem <= 232448, "shared memory per CTA exceeded");
-  static_assert((kAttnMaxSeqs + 1) * 8 <= kQ + kStages * kTile, "the plan lies in Q and the ring");
+  static_assert((kAttnMaxSeqs + 1) * 4 <= kQ + kStages * kTile, "the plan lies in Q and the ring");
 };
 
 // Instruction descriptor of kind::f16 (format 1 bf16, 0 f16), fp32 D, M = 128, A K-major; B
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   TcPiece* pieces = reinterpret_cast<TcPiece*>(bars + 44);
-  long long* wsum = reinterpret_cast<long long*>(bars + 44 + kTcPieces * 8);  // 32
+  int* wsum = reinterpret_cast<int*>(bars + 44 + kTcPieces * 8);  // 32
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = a.b.status;
   pdl_trigger();
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     tmem_relinquish();
   }
   AttnSpan span;
-  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<long long*>(smem), wsum, span);
+  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
   fence_async_proxy();
   tc_fence_before();
   __syncthreads();
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     auto send_q = [&]() {
       const TcPiece& p = pieces[dq.slot];
       const int r = 128 * g + row, rr = p.r0 + r;
-      const int tok = rr / sh.G, head = p.head * sh.G + (rr - tok * sh.G);
+      const int tok = div_group(sh, rr), head = p.head * sh.G + (rr - tok * sh.G);
       const unsigned long long src =
           reinterpret_cast<unsigned long long>(a.q) +
           (r < p.rows ? 2ull * ((size_t)(p.q0 + tok) * a.q_stride + (size_t)head * D) : 0ull);
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       const TcPiece& p = pieces[dq.slot];
       const int r = 128 * g + row, rr = p.r0 + r;
       const bool valid = r < p.rows;
-      const int tok = rr / sh.G, head = p.head * sh.G + (rr - tok * sh.G);
+      const int tok = div_group(sh, rr), head = p.head * sh.G + (rr - tok * sh.G);
       const KeyRange kr = key_range(SeqInfo{p.q0, p.n, p.L}, tok, sh.causal, sh.window);
       job.nt = p.nt;
       job.j0 = p.j0;
@@ -896,14 +896,8 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   TcMaps maps;
   if (!make_cache_map(&maps.k, a.c.k, a) || !make_cache_map(&maps.v, a.c.v, a))
     return cudaErrorInvalidValue;
-  AttnShape sh;
-  sh.G = a.hq / a.hkv;
-  sh.hkv = a.hkv;
-  sh.br_shift = 8;
+  const AttnShape sh = attn_shape(a, 8, kTcExtra);
   static_assert(kTcBR == 1 << 8, "rows per unit");
-  sh.extra = kTcExtra;
-  sh.causal = a.causal;
-  sh.window = a.window;
   const int ctas = num_sms() < kAttnMaxCtas ? num_sms() : kAttnMaxCtas;
   const cudaError_t e = launch_kernel(attn_tc_kernel<FP8, D>, dim3(ctas), dim3(T::kThreads),
                                       T::kSmem, stream, maps, a, sh);

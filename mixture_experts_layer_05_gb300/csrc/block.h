@@ -76,6 +76,7 @@ struct AttnArgs {
   void* scratch;
 };
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream);
+bool attn_fits(const AttnArgs& a);  // whether the call's work can be counted
 size_t attn_scratch_bytes(int D);
 constexpr int kAttnMaxSeqs = 8192;
 constexpr int kAttnMaxCtas = 160;  // workspace bound; the kernels run one CTA per SM

@@ -197,6 +197,7 @@ GBMOE_API gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int
   a.v_scale = cfg->v_scale;
   a.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + kStatusBytes);
   a.scratch = static_cast<char*>(workspace) + kAttnHeadBytes;
+  if (!attn_fits(a)) return GBMOE_ERR_UNSUPPORTED;
   PdlChain chain;
   return cuda_status(launch_attn(a, (cudaStream_t)stream));
 }

@@ -90,6 +90,7 @@ def test_paged_attention_refusals(lib):
         assert _attn(lib, kv=_kv(**kw)) == BAD, kw
     assert _attn(lib, kv=_kv(num_seqs=8193)) == UNSUP
     assert _attn(lib, cfg=_cfg(num_q_heads=1024), T=1 << 21, qs=65536) == UNSUP
+    assert _attn(lib, T=1 << 22, kv=_kv(block_table_stride=1 << 22)) == UNSUP
     for kw in (dict(T=-1), dict(q=0), dict(out=0), dict(qs=504), dict(qs=516), dict(q=264),
                dict(out=264), dict(lse=258)):
         assert _attn(lib, **kw) == BAD, kw
@@ -223,12 +224,13 @@ PLAN = r"""
 using namespace gbmoe;
 int main() {
   AttnShape a;
-  int causal, g, S;
-  while (scanf("%d %d %d %d %d %d %d %d", &a.G, &a.hkv, &a.br_shift, &a.extra, &causal,
+  int causal, g, S, G;
+  while (scanf("%d %d %d %d %d %d %d %d", &G, &a.hkv, &a.br_shift, &a.extra, &causal,
                &a.window, &g, &S) == 8) {
     a.causal = causal != 0;
+    set_group(a, G);
     std::vector<SeqInfo> q(S);
-    std::vector<long long> line(S + 1, 0);
+    std::vector<int> line(S + 1, 0);
     for (int s = 0, q0 = 0; s < S; ++s) {
       if (scanf("%d %d", &q[s].n, &q[s].L) != 2) return 1;
       q[s].q0 = q0;
@@ -236,12 +238,12 @@ int main() {
       line[s + 1] = line[s] + seq_length(a, q[s]) * a.hkv;
     }
     for (int c = 0; c < g; ++c) {
-      const long long at = range_at(line[S], c, g), end = range_at(line[S], c + 1, g);
+      const int at = range_at(line[S], c, g), end = range_at(line[S], c + 1, g);
       if (end <= at) continue;
       int s = 0;
       while (line[s + 1] <= at) ++s;
-      const long long head = (line[s + 1] - line[s]) / a.hkv;
-      AttnCursor cur = {s, (int)((at - line[s]) / head), 0, 0, end - at};
+      const int head = (line[s + 1] - line[s]) / a.hkv;
+      AttnCursor cur = {s, (at - line[s]) / head, 0, 0, end - at};
       walk_blocks(a, q[s], (at - line[s]) % head, cur);
       while (cur.left > 0) {
         while (q[cur.s].n == 0) ++cur.s;
@@ -274,7 +276,7 @@ def test_attention_work_is_cut_whole(tmp_path):
             seqs.append((n, max(0, rng.choice([n, n + 1, n - 2, n + 127, n + 128, n + 5000, 0]))))
         if not any(n for n, _ in seqs):
             seqs[0] = (1, 3)
-        cases.append((rng.choice([1, 3, 4, 8]), rng.choice([1, 2, 8]), rng.choice([4, 8]),
+        cases.append((rng.choice([1, 2, 3, 4, 7, 8, 20, 1024]), rng.choice([1, 2, 8]), rng.choice([4, 8]),
                       rng.choice([0, 1, 3]), int(rng.random() < 0.8), rng.choice([0, 0, 1, 100, 1000]),
                       rng.choice([1, 7, 148, 152]), S, seqs))
     text = "\n".join(" ".join(map(str, c[:8])) + " " + " ".join(f"{n} {L}" for n, L in c[8])
@@ -316,3 +318,32 @@ def test_attention_work_is_cut_whole(tmp_path):
             share = sum(p[2] for p in ps) + extra * begun      # for a cut through it at an end
             assert total / g - 1 - extra < share < total / g + 1 + extra
             assert not any(p[0] for p in ps[1:]) and not any(p[1] for p in ps[:-1])
+
+
+DIVIDE = r"""
+#include <cstdio>
+#include "attn_plan.h"
+using namespace gbmoe;
+int main() {
+  long bad = 0;
+  for (int G = 1; G <= 1024; ++G) {
+    AttnShape a;
+    set_group(a, G);
+    for (long r = 0; r < 5000; ++r) bad += div_group(a, (int)r) != r / G;
+    for (long k = 1; k * G < 2147483647L; k = k * 3 + 1)
+      for (long r = k * G - 2; r <= k * G + 2; ++r)
+        if (r >= 0 && r < 2147483647L) bad += div_group(a, (int)r) != r / G;
+    for (long r = 2147483600L; r < 2147483647L; ++r) bad += div_group(a, (int)r) != r / G;
+  }
+  printf("%ld", bad);
+  return 0;
+}
+"""
+
+
+def test_division_by_the_group_is_exact(tmp_path):
+    (tmp_path / "divide.cpp").write_text(DIVIDE)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I", build_mod.CSRC, str(tmp_path / "divide.cpp"),
+                    "-o", str(tmp_path / "divide")], check=True)
+    out = subprocess.run([str(tmp_path / "divide")], capture_output=True, text=True, check=True)
+    assert out.stdout == "0"
