@@ -68,6 +68,7 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
                                                 int* line, int* wsum, AttnSpan& span) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int warps = nt >> 5;
+#pragma unroll 1
   for (int s = tid; s < b.S; s += nt) {
     const SeqInfo q = seq_info(b, s);
     line[s + 1] = unit_blocks(sh, q.n) <= kPlanBlocks ? seq_length(sh, q) * sh.hkv : -1;
@@ -77,8 +78,10 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
   // few sequences: every warp looks through all and takes each `warps`-th; many: 32 apiece
   const bool few = b.S <= 1024;
   int mine = 0;
+#pragma unroll 1
   for (int s0 = few ? 0 : warp * 32; s0 < b.S; s0 += few ? 32 : warps * 32) {
     uint32_t many = __ballot_sync(0xffffffffu, s0 + lane < b.S && line[s0 + lane + 1] < 0);
+#pragma unroll 1
     while (many) {
       const int s = s0 + __ffs(many) - 1;
       many &= many - 1;
@@ -86,6 +89,7 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
       const SeqInfo q = seq_info(b, s);
       const int blocks = unit_blocks(sh, q.n);
       int t = 0;
+#pragma unroll 1
       for (int rb = lane; rb < blocks; rb += 32) t += unit_length(sh, q, rb);
       t = __reduce_add_sync(0xffffffffu, t);
       if (lane == 0) line[s + 1] = -2 - t * sh.hkv;  // marked until every warp has looked
@@ -96,6 +100,7 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
   const int per = (b.S + nt - 1) / nt;
   const int s0 = min(tid * per, b.S), s1 = min(s0 + per, b.S);
   int sum = 0;
+#pragma unroll 1
   for (int s = s0; s < s1; ++s) {
     const int v = line[s + 1];
     sum += v < 0 ? -2 - v : v;
@@ -110,7 +115,9 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
   if (lane == 31) wsum[warp] = inc;
   __syncthreads();
   int base = inc - sum;
+#pragma unroll 1
   for (int w = 0; w < warp; ++w) base += wsum[w];
+#pragma unroll 1
   for (int s = s0; s < s1; ++s) line[s + 1] += base;
   __syncthreads();
   const int W = line[b.S];
@@ -123,6 +130,7 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
     const int a = range_at(W, blockIdx.x, span.ctas);
     span.end = range_at(W, blockIdx.x + 1, span.ctas);
     int lo = 0, hi = b.S;  // the sequence with line[s] <= a < line[s + 1]
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (line[mid] <= a) lo = mid;
@@ -138,6 +146,7 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
     const int blocks = unit_blocks(sh, q.n);
     if (blocks > kPlanBlocks) {
       // every warp finds the row block, 32 at a time
+#pragma unroll 1
       for (; c.rb < blocks; c.rb += 32) {
         const int rb = c.rb + lane;
         int at = rb < blocks ? unit_length(sh, q, rb) : 0;
@@ -167,8 +176,10 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
 // units of which the range holds only the extra cost are passed over.
 __device__ __forceinline__ bool next_piece(const PagedBatch& b, const AttnShape& sh,
                                            AttnCursor& c, AttnPiece& p) {
+#pragma unroll 1
   while (c.left > 0) {
     SeqInfo q = seq_info(b, c.s);
+#pragma unroll 1
     while (q.n == 0 && c.s + 1 < b.S) q = seq_info(b, ++c.s);
     p = take_piece(sh, q, c);
     if (p.ta < p.tb) return true;

@@ -80,6 +80,7 @@ GBMOE_HD int unit_length(const AttnShape& a, const SeqInfo& q, int rb) {
 GBMOE_HD int seq_length(const AttnShape& a, const SeqInfo& q) {
   const int blocks = unit_blocks(a, q.n);
   int t = 0;
+  GBMOE_ROLLED
   for (int rb = 0; rb < blocks; ++rb) t += unit_length(a, q, rb);
   return t;
 }
@@ -92,6 +93,7 @@ struct AttnCursor {
 
 // Moves the cursor `rem` further, over row blocks of the sequence q.
 GBMOE_HD void walk_blocks(const AttnShape& a, const SeqInfo& q, int rem, AttnCursor& c) {
+  GBMOE_ROLLED
   for (;;) {
     const int t = unit_length(a, q, c.rb);
     if (rem < t) break;

@@ -732,6 +732,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
           rec->mid = 1;
           rec->ends = p.last();
         }
+#pragma unroll 1
         for (int i = p.u.i0 + lane; i <= p.u.i1; i += 32)
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                            static_cast<const __nv_bfloat16*>(a.q) +

@@ -7,8 +7,10 @@
 
 #ifdef __CUDACC__
 #define GBMOE_HD __host__ __device__ __forceinline__
+#define GBMOE_ROLLED _Pragma("unroll 1")
 #else
 #define GBMOE_HD inline
+#define GBMOE_ROLLED
 #endif
 
 namespace gbmoe {
