@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       const uint32_t some = __ballot_sync(0xffffffffu, r < p.rows);
       const int c = lane % kLanes;
       const uint32_t dst = q_half + (c / 8) * kHalf;
-#pragma unroll 4
+#pragma unroll 2
       for (int i = 0; i < kLanes; ++i) {
         const int l = i * (32 / kLanes) + lane / kLanes, r2 = (warp & 3) * 32 + l;
         const unsigned long long at = __shfl_sync(0xffffffffu, src, l) + c * 16;
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (FP8) {  // bf16 to f16 in place, by the thread that copied it
         const int c = lane % kLanes;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < kLanes; ++i) {
           const int r2 = (warp & 3) * 32 + i * (32 / kLanes) + lane / kLanes;
           const uint32_t at = q_half + (c / 8) * kHalf + r2 * 128u + (((c & 7) ^ (r2 & 7)) << 4);
@@ -512,12 +512,6 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
               tmem_st32(to + 32 * i, w);
             }
             tmem_wait_st();
-            // the scores once more: their registers were given up
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_ld32(ts + 64 * h + 32 * i, s[i]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_wait_ld(s[i]);
-            if (masked) drop();
           }
           if (!ok) break;
           if (h == 0)
