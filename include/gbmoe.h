@@ -310,6 +310,18 @@ gbmoe_status_t moe_forward_ex(const gbmoe_config_t* cfg, int32_t num_tokens,
                               const gbmoe_forward_args_t* args, gbmoe_stream_t stream);
 
 /*
+ * moe_forward_q: moe_forward_ex of the FP8_BLOCK128 layer whose input is quantized already, as
+ * moe_rms_norm writes it: hidden_q [T, H] e4m3fn bytes (16-byte aligned) and hidden_scale
+ * [H / 128, T] fp32 take the place of the layer's own quantization of hidden_states, which only
+ * the router GEMM still reads (args->hidden_states may be NULL when router_logits is given).
+ * With the outputs of moe_quant_fp8_per_token_group the result is moe_forward_ex's, bit for bit.
+ * UNSUPPORTED for other layers.
+ */
+gbmoe_status_t moe_forward_q(const gbmoe_config_t* cfg, int32_t num_tokens,
+                             const gbmoe_forward_args_t* args, const uint8_t* hidden_q,
+                             const float* hidden_scale, gbmoe_stream_t stream);
+
+/*
  * moe_router_logits: the router GEMM in front of the layer, `MoEGate.forward` on the
  * sglang `models/deepseek_v2.py` page: router_logits [T, E] fp32 = hidden_states
  * [T, H] bf16 @ gate_weight [E, H]^T bf16, fp32 accumulation on the tensor cores.

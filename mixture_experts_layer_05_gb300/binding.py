@@ -33,7 +33,7 @@ EXPORTS = ("moe_topk", "moe_align_block_size_workspace_size", "moe_align_block_s
            "moe_selftest_bounded_wait", "moe_forward_ex",
            "moe_router_logits", "moe_quant_fp8_per_token_group", "moe_quant_nvfp4",
            "moe_nvfp4_prepared_bytes", "moe_nvfp4_prepare_weight", "moe_rms_norm",
-           "moe_kv_append", "moe_paged_attention_workspace_size", "moe_paged_attention",
+           "moe_forward_q", "moe_kv_append", "moe_paged_attention_workspace_size", "moe_paged_attention",
            "gbmoe_version")
 
 
@@ -189,6 +189,7 @@ def load() -> ctypes.CDLL:
         "moe_nvfp4_prepared_bytes": (SZ, [I32, I32]),
         "moe_nvfp4_prepare_weight": (I32, [I32, I32, P, P, P, P]),
         "moe_selftest_bounded_wait": (I32, [P, I32, P]),
+        "moe_forward_q": (I32, [CP, I32, ctypes.POINTER(ForwardArgs), P, P, P]),
         "moe_rms_norm": (I32, [I32, I32, ctypes.POINTER(RmsNormArgs), P]),
         "moe_kv_append": (I32, [ctypes.POINTER(AttnConfig), I32, ctypes.POINTER(PagedKv),
                                 ctypes.POINTER(KvAppendArgs), P]),
@@ -360,11 +361,12 @@ def moe_forward_ex(cfg: Config, hidden_states, router_logits, e_score_correction
                    w13_scale=None, w2_scale=None, shared_w13_scale=None, shared_w2_scale=None,
                    w13_weight_scale_2=None, w2_weight_scale_2=None, shared_weight_scale_2=None,
                    input_scale=0.0, act_scale=0.0, shared_input_scale=0.0,
-                   shared_act_scale=0.0):
+                   shared_act_scale=0.0, hidden_q=None, hidden_scale=None):
     """moe_forward with the optional per-expert biases, stage events, (router_logits None)
     the gate weight whose router GEMM runs first, or quantized experts: (cfg.weight_quant
     fp8) e4m3 weights with their fp32 128 x 128 block scales; (nvfp4) prepared fp4 weights
-    (moe_nvfp4_prepare_weight) with fp32 per-expert scales and the per-tensor scales."""
+    (moe_nvfp4_prepare_weight) with fp32 per-expert scales and the per-tensor scales.
+    hidden_q [T, H] e4m3 and hidden_scale [H / 128, T] (fp8): the input quantized already."""
     _need(hidden_states, torch.bfloat16, "hidden_states")
     _need(router_logits, torch.float32, "router_logits")
     _need(e_score_correction_bias, torch.float32, "e_score_correction_bias")
@@ -406,6 +408,16 @@ def moe_forward_ex(cfg: Config, hidden_states, router_logits, e_score_correction
                     ptr(w13_weight_scale_2), ptr(w2_weight_scale_2),
                     ptr(shared_weight_scale_2), float(input_scale), float(act_scale),
                     float(shared_input_scale), float(shared_act_scale))
+    if hidden_q is not None:
+        _fp8_bytes(hidden_q, "hidden_q")
+        _need(hidden_scale, torch.float32, "hidden_scale")
+        T, H = hidden_states.shape
+        if hidden_scale is None or hidden_q.shape != (T, H) or hidden_scale.shape != (H // 128, T):
+            raise ValueError("hidden_q must be [T, H] and hidden_scale [H / 128, T]")
+        _check("moe_forward_q", load().moe_forward_q(
+            ctypes.byref(cfg), T, ctypes.byref(a), _p(hidden_q), _p(hidden_scale),
+            _stream(stream)))
+        return
     _check("moe_forward_ex", load().moe_forward_ex(ctypes.byref(cfg), hidden_states.shape[0],
                                                    ctypes.byref(a), _stream(stream)))
 
@@ -661,17 +673,20 @@ class FusedMoE:
             self.max_tokens = max_tokens
 
     def __call__(self, hidden_states, router_logits=None, out=None, events=None, stream=None,
-                 gate_weight=None):
-        """Forward from router logits, or (router_logits None) from the gate weight."""
+                 gate_weight=None, hidden_q=None, hidden_scale=None):
+        """Forward from router logits, or (router_logits None) from the gate weight; hidden_q,
+        hidden_scale: the fp8 layer's input as moe_rms_norm quantized it."""
         T = hidden_states.shape[0]
         self.reserve(T)
         if out is None:
             out = torch.empty_like(hidden_states)
-        if gate_weight is not None or router_logits is None or self.cfg.weight_quant:
+        if (gate_weight is not None or router_logits is None or self.cfg.weight_quant
+                or hidden_q is not None):
             moe_forward_ex(self.cfg, hidden_states, router_logits if gate_weight is None else None,
                            self.bias, self.w13, self.w2, self.shared_w13, self.shared_w2, out,
                            self.workspace, w13_bias=self.w13_bias, w2_bias=self.w2_bias,
-                           events=events, stream=stream, gate_weight=gate_weight, **self.scales)
+                           events=events, stream=stream, gate_weight=gate_weight,
+                           hidden_q=hidden_q, hidden_scale=hidden_scale, **self.scales)
         elif self.w13_bias is None and self.w2_bias is None:
             moe_forward(self.cfg, hidden_states, router_logits, self.bias, self.w13, self.w2,
                         self.shared_w13, self.shared_w2, out, self.workspace, events=events,

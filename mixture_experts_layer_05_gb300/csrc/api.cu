@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "block.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -397,9 +398,14 @@ GBMOE_API gbmoe_status_t moe_forward_workspace_layout(const gbmoe_config_t* cfg,
   return GBMOE_OK;
 }
 
-GBMOE_API gbmoe_status_t moe_forward_ex(const gbmoe_config_t* cfg, int32_t num_tokens,
-                                        const gbmoe_forward_args_t* args,
-                                        gbmoe_stream_t stream_) {
+namespace gbmoe {
+namespace {
+
+// moe_forward_ex, and moe_forward_q with the input's codes hidden_q [T, H] and scales
+// hidden_scale [H / 128, T] (else NULL).
+gbmoe_status_t forward_impl(const gbmoe_config_t* cfg, int32_t num_tokens,
+                            const gbmoe_forward_args_t* args, const uint8_t* hidden_q,
+                            const float* hidden_scale, gbmoe_stream_t stream_) {
   if (!args) return GBMOE_ERR_INVALID_ARG;
   const void* hidden_states = args->hidden_states;
   const float* router_logits = args->router_logits;
@@ -426,8 +432,9 @@ GBMOE_API gbmoe_status_t moe_forward_ex(const gbmoe_config_t* cfg, int32_t num_t
   if ((shared_w13 != nullptr) != (Is > 0) || (shared_w2 != nullptr) != (Is > 0))
     return GBMOE_ERR_INVALID_ARG;
   if (num_tokens == 0) return GBMOE_OK;
-  if (!hidden_states || (!router_logits == !gate_weight) || !w13_weight || !w2_weight ||
-      !output || !aligned16(gate_weight))
+  // codes stand in for the hidden states everywhere but in the router GEMM
+  if ((!hidden_states && (!hidden_q || gate_weight)) || (!router_logits == !gate_weight) ||
+      !w13_weight || !w2_weight || !output || !aligned16(gate_weight))
     return GBMOE_ERR_INVALID_ARG;
   if (!aligned16(hidden_states) || !aligned16(w13_weight) || !aligned16(w2_weight) ||
       !aligned16(output) || (Is && (!aligned16(shared_w13) || !aligned16(shared_w2))) ||
@@ -535,8 +542,10 @@ GBMOE_API gbmoe_status_t moe_forward_ex(const gbmoe_config_t* cfg, int32_t num_t
   const float alpha = c.gemm1_alpha == 0.f ? 1.f : c.gemm1_alpha;
   // fp8: the input is quantized once per token while it is gathered (and kept in token
   // order for the shared expert)
-  uint8_t* xq_tok = at<uint8_t>(workspace, L.xq);
-  float* xs_tok = at<float>(workspace, L.xq + L.xs_tok);
+  uint8_t* xq_tok =
+      hidden_q ? const_cast<uint8_t*>(hidden_q) : at<uint8_t>(workspace, L.xq);
+  float* xs_tok =
+      hidden_q ? const_cast<float*>(hidden_scale) : at<float>(workspace, L.xq + L.xs_tok);
   float* xs_perm = at<float>(workspace, L.x_perm + L.xs_perm);
   void* x_tok16 = at<char>(workspace, L.xq);  // nvfp4: f16 token-order rows (shared expert)
   auto gather = [&]() -> cudaError_t {
@@ -544,6 +553,9 @@ GBMOE_API gbmoe_status_t moe_forward_ex(const gbmoe_config_t* cfg, int32_t num_t
       return launch_quant_gather_fp4(hidden_states, H, inv, L.n, k, T, L.max_sorted,
                                      args->input_scale, x_perm, Is ? x_tok16 : nullptr,
                                      args->shared_input_scale, stream);
+    if (fp8 && hidden_q)
+      return launch_gather_fp8(hidden_q, hidden_scale, H, inv, L.n, k, T,
+                               static_cast<uint8_t*>(x_perm), xs_perm, L.max_sorted, stream);
     if (fp8)
       return launch_quant_gather_fp8(hidden_states, H, inv, L.n, k, T,
                                      static_cast<uint8_t*>(x_perm), xs_perm, L.max_sorted,
@@ -1004,6 +1016,26 @@ GBMOE_API gbmoe_status_t moe_forward_ex(const gbmoe_config_t* cfg, int32_t num_t
   GBMOE_TRY(rec(4));
 #undef GBMOE_TRY
   return GBMOE_OK;
+}
+
+}  // namespace
+}  // namespace gbmoe
+
+GBMOE_API gbmoe_status_t moe_forward_ex(const gbmoe_config_t* cfg, int32_t num_tokens,
+                                        const gbmoe_forward_args_t* args, gbmoe_stream_t stream) {
+  return forward_impl(cfg, num_tokens, args, nullptr, nullptr, stream);
+}
+
+GBMOE_API gbmoe_status_t moe_forward_q(const gbmoe_config_t* cfg, int32_t num_tokens,
+                                       const gbmoe_forward_args_t* args, const uint8_t* hidden_q,
+                                       const float* hidden_scale, gbmoe_stream_t stream) {
+  const gbmoe_status_t s = check_layer(cfg);
+  if (s != GBMOE_OK) return s;
+  if (cfg->weight_quant != GBMOE_QUANT_FP8_BLOCK128) return GBMOE_ERR_UNSUPPORTED;
+  if (num_tokens > 0 && (!hidden_q || !hidden_scale || !aligned16(hidden_q) ||
+                         (reinterpret_cast<uintptr_t>(hidden_scale) & 3u)))
+    return GBMOE_ERR_INVALID_ARG;
+  return forward_impl(cfg, num_tokens, args, hidden_q, hidden_scale, stream);
 }
 
 GBMOE_API gbmoe_status_t moe_forward_events(

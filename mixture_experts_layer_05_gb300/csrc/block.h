@@ -46,6 +46,12 @@ struct RmsNormArgs {
 cudaError_t launch_rms_norm(const RmsNormArgs& a, cudaStream_t stream);
 int rms_norm_max_hidden();
 
+// The FP8 layer's gather of rows that are quantized already: codes q [T, H] and scales
+// s [H / 128, T] of token f / k to row inv[f] of x_perm_q and xs_perm (group stride perm_ld).
+cudaError_t launch_gather_fp8(const uint8_t* q, const float* s, int H, const int* inv, int n,
+                              int k, int T, uint8_t* x_perm_q, float* xs_perm, int perm_ld,
+                              cudaStream_t stream);
+
 struct KvAppendArgs {
   PagedBatch b;
   PagedCache c;

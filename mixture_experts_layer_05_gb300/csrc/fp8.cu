@@ -11,6 +11,7 @@
 //
 // Scales are group-major ([group][row]) so that a GEMM epilogue warp reads the scales of
 // its 32 rows in one transaction.
+#include "block.h"
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -77,6 +78,33 @@ __global__ void __launch_bounds__(256)
     if (xq_tok) {
       reinterpret_cast<uint32_t*>(xq_tok + (size_t)t * H + col)[lane] = v.q;
       if (lane == 0) xs_tok[(size_t)g * T + t] = v.s;
+    }
+  }
+}
+
+// The same gather of rows that arrive quantized (moe_rms_norm's 8-bit output): a warp copies a
+// token's group of 128 codes and its scale to each of the token's k rows.
+__global__ void __launch_bounds__(256)
+    gather_fp8_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs, int H,
+                      const int* __restrict__ inv, int k, int T, uint8_t* __restrict__ xp,
+                      float* __restrict__ xs_perm, int perm_ld) {
+  pdl_trigger();  // the next kernel may start its launch now
+  pdl_wait();     // inputs written by the previous kernel are visible
+  const int lane = threadIdx.x & 31;
+  const int groups = H / kFp8Block;
+  const long long items = (long long)T * groups;
+  const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
+  for (long long it = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items;
+       it += warps) {
+    const int t = (int)(it / groups), g = (int)(it % groups);
+    const size_t col = (size_t)g * kFp8Block;
+    const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(xq + (size_t)t * H + col) + lane);
+    const float s = __ldg(xs + (size_t)g * T + t);
+    for (int j = 0; j < k; ++j) {
+      const int p = inv[t * k + j];
+      if (p < 0 || p >= perm_ld) continue;
+      reinterpret_cast<uint32_t*>(xp + (size_t)p * H + col)[lane] = q;
+      if (lane == 0) xs_perm[(size_t)g * perm_ld + p] = s;
     }
   }
 }
@@ -189,6 +217,16 @@ cudaError_t launch_quant_gather_fp8(const void* x, int H, const int* inv, int n,
   launch_kernel(quant_gather_fp8_kernel, dim3(grid_for_warps((long long)T * (H / kFp8Block))),
                 dim3(256), 0, stream, static_cast<const __nv_bfloat16*>(x), H, inv, k, T, perm_ld,
                 x_perm_q, xs_perm, perm_ld, xq_tok, xs_tok);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather_fp8(const uint8_t* q, const float* s, int H, const int* inv, int n,
+                              int k, int T, uint8_t* x_perm_q, float* xs_perm, int perm_ld,
+                              cudaStream_t stream) {
+  if (T <= 0) return cudaSuccess;
+  if (H % kFp8Block || n != T * k) return cudaErrorInvalidValue;
+  launch_kernel(gather_fp8_kernel, dim3(grid_for_warps((long long)T * (H / kFp8Block))),
+                dim3(256), 0, stream, q, s, H, inv, k, T, x_perm_q, xs_perm, perm_ld);
   return cudaGetLastError();
 }
 

@@ -127,6 +127,24 @@ def test_kv_append_refusals(lib):
         assert _append(lib, **kw) == BAD, kw
 
 
+def test_forward_q_refusals(lib):
+    def call(cfg, T=4, q=256, s=256, logits=256):
+        a = binding.ForwardArgs(router_logits=logits or None, w13_weight=256, w2_weight=256,
+                                output=256, workspace=256, workspace_bytes=1 << 40, w13_scale=256,
+                                w2_scale=256, gate_weight=None if logits else 256)
+        return lib.moe_forward_q(ctypes.byref(cfg), T, ctypes.byref(a), P(q or None), P(s or None),
+                                 None)
+    make = lambda quant: binding.make_config(8, 2, 256, 256, weight_quant=quant)  # noqa: E731
+    fp8 = make("fp8")
+    assert lib.moe_forward_q(None, 4, None, None, None, None) == BAD
+    assert call(make(None)) == UNSUP and call(make("nvfp4")) == UNSUP
+    assert call(fp8, T=0, q=0, s=0) == OK
+    for kw in (dict(T=-1), dict(q=0), dict(s=0), dict(q=264), dict(s=258),
+               dict(logits=0)):                  # the router GEMM needs the hidden states
+        assert call(fp8, **kw) == BAD, kw
+    assert lib.moe_forward_q(ctypes.byref(fp8), 4, None, P(256), P(256), None) == BAD
+
+
 def test_binding_refuses_host_tensors(lib):
     x = torch.zeros(2, 256, dtype=torch.bfloat16)
     with pytest.raises(ValueError):

@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from mixture_experts_layer_05_gb300 import binding
+from mixture_experts_layer_05_gb300 import binding, configs, inputs
 from tests.block_cases import (BF16, E4M3_SUB, FP8_HALF, FP32, Paged, attention_reference,
                                norm_reference, rotate_reference)
 
@@ -125,6 +125,37 @@ def test_norm_output_feeds_the_fp8_layer_format(cuda_lib):
     y, _, q, s = binding.moe_rms_norm(x.to(DEV), w, 0.0, out="both")
     q2, s2 = binding.moe_quant_fp8_per_token_group(y)
     assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
+@pytest.mark.parametrize("shared", [0, 128])
+@pytest.mark.parametrize("gate", [False, True])
+def test_fp8_layer_takes_quantized_input(cuda_lib, T, shared, gate):
+    """The layer's own codes and scales, passed in, give its own result bit for bit; then the
+    norm's, whose codes are of the same rows, without the hidden states' bf16 values."""
+    w = configs.shrink(configs.DSV3, num_experts=16, top_k=4, num_expert_group=4, topk_group=2,
+                       hidden_size=512, intermediate_size=256, shared_intermediate_size=shared)
+    q = {k: None if v is None else v.to(DEV) for k, v in inputs.make_fp8_weights(w, 0).items()}
+    layer = binding.FusedMoE(binding.config_from_workload(w, weight_quant="fp8"), q["w13_q"],
+                             q["w2_q"], q["bias"], q["shared_w13_q"], q["shared_w2_q"],
+                             max_tokens=T, w13_scale=q["w13_s"], w2_scale=q["w2_s"],
+                             shared_w13_scale=q["shared_w13_s"], shared_w2_scale=q["shared_w2_s"])
+    g = torch.Generator().manual_seed(T)
+    x = _rand(g, T, 512).to(DEV)
+    how = (dict(gate_weight=_rand(g, 16, 512, std=0.1).to(DEV)) if gate
+           else dict(router_logits=torch.randn(T, 16, generator=g).to(DEV)))
+    want = layer(x, **how)
+    xq, xs = binding.moe_quant_fp8_per_token_group(x)
+    assert torch.equal(layer(x, hidden_q=xq, hidden_scale=xs, **how), want)
+    weight = (1 + _rand(g, 512, std=0.1)).to(torch.bfloat16).to(DEV)
+    y, _, yq, ys = binding.moe_rms_norm(x, weight, out="both")
+    rows = y if gate else torch.full_like(y, math.nan)     # only the router GEMM reads them
+    out = layer(rows, hidden_q=yq, hidden_scale=ys, **how)
+    assert torch.isfinite(out).all() and layer.device_status() == binding.OK
+    with pytest.raises(ValueError):
+        layer(x, hidden_q=xq, **how)
+    with pytest.raises(ValueError):
+        layer(x, hidden_q=xq, hidden_scale=xs.t().contiguous() if T != 4 else xs[:1], **how)
 
 
 # ------------------------------------------------------------------------------ append
