@@ -126,6 +126,20 @@ __device__ __noinline__ void land(uint32_t bar, uint32_t parity) {
     if (globaltimer_ns() - t0 > 10000000ull) return;
 }
 
+constexpr int kJoinAtOnce = 8;  // pieces of a cut unit whose loads are in flight together
+
+// A unit that a cut crosses: its rows (row r0 + r of a kv head of a sequence), and the CTAs that
+// hold its pieces.
+struct CutUnit {
+  int q0, head, r0, rows, c0, c1;
+};
+// What warp 0 lays out for all consumer warps: the next piece (s < 0: none), and the CTA's first
+// unit if it was begun before it and its last if it is left to the next.
+struct DecPlan {
+  AttnPiece next;
+  CutUnit cut[2];
+};
+
 struct DecMaps {
   CUtensorMap k, v;
 };
@@ -147,7 +161,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 24);
   float2* wml = reinterpret_cast<float2*>(bars + 26);  // [rows][warps]
   int* wsum = reinterpret_cast<int*>(bars + 26 + T::kBR * kDecWarps);  // 32
-  static_assert((26 + T::kBR * kDecWarps + 16) * 8 <= T::kTail, "tail");
+  DecPlan* plan = reinterpret_cast<DecPlan*>(bars + 42 + T::kBR * kDecWarps);
+  static_assert((42 + T::kBR * kDecWarps) * 8 + sizeof(DecPlan) <= T::kTail, "tail");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
@@ -227,25 +242,27 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     uint32_t at = 0;  // ring position of the next tile's K
     bool ok = true;
     auto swz = [](uint32_t off) { return off ^ ((off >> 3) & T::kSwz); };
-    for (;;) {
-      const int unit_at = span.end - cur.left - cur.off;  // the unit's place on the line
-      AttnPiece p;
-      if (!next_piece(a.b, sh, cur, p)) break;
-      auto write_out = [&](int r, int d, const float4& v, float M, float L) {
-        const int rr = p.rb * T::kBR + r, tok = div_group(sh, rr);
-        const size_t orow = (size_t)(p.q.q0 + tok) * a.hq + p.head * sh.G + (rr - tok * sh.G);
-        const float inv = L == 0.f ? 0.f : a.v_scale / L;  // no key: zeros
-        uint2 w;
-        w.x = pack_bf16x2(v.x * inv, v.y * inv);
-        w.y = pack_bf16x2(v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + d) = w;
-        if (a.lse && d == 0)
-          a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-      };
-      const int rows = min(T::kBR, p.q.n * sh.G - p.rb * T::kBR);
-      // this lane's query columns of row 8 n + lane / 4, as the B side of the products: two
-      // pairs of each 16 columns
-      uint32_t qf[NT][D / 16][2];
+    // the unit's place on the line, from the cursor behind the piece
+    auto unit_at = [&](const AttnPiece& x) { return span.end - cur.left - x.tb - sh.extra; };
+    auto write_out = [&](int q0, int head, int rr, int d, const float4& v, float M, float L) {
+      const int tok = div_group(sh, rr);
+      const size_t orow = (size_t)(q0 + tok) * a.hq + head * sh.G + (rr - tok * sh.G);
+      const float inv = L == 0.f ? 0.f : a.v_scale / L;  // no key: zeros
+      uint2 w;
+      w.x = pack_bf16x2(v.x * inv, v.y * inv);
+      w.y = pack_bf16x2(v.z * inv, v.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + d) = w;
+      if (a.lse && d == 0)
+        a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    };
+    auto rows_of = [&](const AttnPiece& x) {
+      return min(T::kBR, x.q.n * sh.G - x.rb * T::kBR);
+    };
+    // this lane's query columns of row 8 n + lane / 4, as the B side of the products: two
+    // pairs of each 16 columns
+    uint32_t qf[NT][D / 16][2];
+    auto load_q = [&](const AttnPiece& p) {
+      const int rows = rows_of(p);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = 8 * n + g, rr = p.rb * T::kBR + (r < rows ? r : 0);
@@ -271,6 +288,32 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           qf[n][k][1] = hi;
         }
       }
+    };
+    AttnPiece p;
+    bool have = next_piece(a.b, sh, cur, p);
+    if (have) load_q(p);
+    int cuts = 0;
+    while (have) {
+      const int rows = rows_of(p);
+      if (warp == 0) {
+        // the next piece is known before this one's tiles have arrived
+        const int place = unit_at(p);
+        AttnPiece next;
+        if (!next_piece(a.b, sh, cur, next)) next.s = -1;
+        if (lane == 0) {
+          plan->next = next;
+          if (!p.whole()) {
+            CutUnit& x = plan->cut[cuts];
+            x.q0 = p.q.q0;
+            x.head = p.head;
+            x.r0 = p.rb * T::kBR;
+            x.rows = rows;
+            x.c0 = cta_of(span, place + sh.extra);
+            x.c1 = cta_of(span, place + sh.extra + p.u.tiles - 1);
+          }
+        }
+      }
+      cuts += !p.whole();
       // the keys of this lane's rows 8 n + 2 c + e; those that every row attends need no mask
       KeyRange kr[NT][2];
 #pragma unroll
@@ -501,7 +544,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
           }
         }
-      if (consumers_sync(!ok)) break;
+      if (consumers_sync(!ok)) {
+        cuts = 0;
+        break;
+      }
+      const AttnPiece next = plan->next;
+      have = next.s >= 0;
+      if (have) load_q(next);  // under way while this piece is joined
       const int slot_out = p.first() ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
       for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kDecWarps) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -526,52 +575,70 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           v.w = fmaf(f, x.w, v.w);
         }
         if (p.whole()) {
-          write_out(r, d, v, M, L);
+          write_out(p.q.q0, p.head, p.rb * T::kBR + r, d, v, M, L);
         } else {
           const size_t row = (size_t)slot_out * T::kBR + r;
           *reinterpret_cast<float4*>(sc.o + row * D + d) = v;
           if (d == 0) sc.ml[row] = make_float2(M, L);
         }
       }
-      if (!p.whole()) {
-        // CTAs c0 .. c1 hold the unit's pieces; the one that finishes last joins them
-        const int c0 = cta_of(span, unit_at), c1 = cta_of(span, unit_at + p.u.tiles - 1);
+      p = next;
+      consumers_sync(false);  // the join area is free again
+    }
+    // Cut units are joined by the CTA that finishes last: both are counted here, so that a piece
+    // that ends in the middle of the CTA's range waits for no fence and no atomic.
+    if (cuts) {
+      __threadfence();
+      consumers_sync(false);
+      if ((int)threadIdx.x < cuts) {
+        const CutUnit x = plan->cut[threadIdx.x];
+        const bool last = atomicAdd(a.counters + x.c0, 1) == x.c1 - x.c0;
+        if (last) atomicExch(a.counters + x.c0, 0);
         __threadfence();
-        consumers_sync(false);
-        bool last = false;
-        if (threadIdx.x == 0) {
-          last = atomicAdd(a.counters + c0, 1) == c1 - c0;
-          if (last) atomicExch(a.counters + c0, 0);
-          __threadfence();
-        }
-        if (consumers_sync(last)) {
-          for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kDecWarps) {
-            const int r = i / (D / 4), d = i % (D / 4) * 4;
-            auto row = [&](int c) {
-              return (size_t)(c == c0 ? 2 * c + 1 : 2 * c) * T::kBR + r;
-            };
-            float M = -INFINITY;
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(sc.ml + row(c)).x);
-            const float Ms = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const float2 ml = __ldcg(sc.ml + row(c));
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(sc.o + row(c) * D + d));
-              const float f = ex2(ml.x - Ms);
-              L = fmaf(f, ml.y, L);
-              v.x = fmaf(f, x.x, v.x);
-              v.y = fmaf(f, x.y, v.y);
-              v.z = fmaf(f, x.z, v.z);
-              v.w = fmaf(f, x.w, v.w);
+        wsum[threadIdx.x] = last;
+      }
+      consumers_sync(false);
+      for (int k = 0; k < cuts; ++k) {
+        if (!wsum[k]) continue;
+        const CutUnit x = plan->cut[k];
+        for (int i = threadIdx.x; i < x.rows * (D / 4); i += 32 * kDecWarps) {
+          const int r = i / (D / 4), d = i % (D / 4) * 4;
+          float M = -INFINITY, L = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c = x.c0; c <= x.c1; c += kJoinAtOnce) {
+            float2 ml[kJoinAtOnce];
+            float4 y[kJoinAtOnce];
+#pragma unroll
+            for (int j = 0; j < kJoinAtOnce; ++j) {
+              const int cj = min(c + j, x.c1);
+              const size_t row = (size_t)(cj == x.c0 ? 2 * cj + 1 : 2 * cj) * T::kBR + r;
+              ml[j] = __ldcg(sc.ml + row);
+              y[j] = __ldcg(reinterpret_cast<const float4*>(sc.o + row * D + d));
             }
-            write_out(r, d, v, M, L);
+            float mx = M;
+#pragma unroll
+            for (int j = 0; j < kJoinAtOnce; ++j) {
+              if (c + j > x.c1) ml[j] = make_float2(-INFINITY, 0.f);
+              mx = fmaxf(mx, ml[j].x);
+            }
+            const float ms = mx == -INFINITY ? 0.f : mx;
+            const float f0 = ex2(M - ms);
+            M = mx;
+            L *= f0;
+            v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
+#pragma unroll
+            for (int j = 0; j < kJoinAtOnce; ++j) {
+              const float f = ex2(ml[j].x - ms);
+              L = fmaf(f, ml[j].y, L);
+              v.x = fmaf(f, y[j].x, v.x);
+              v.y = fmaf(f, y[j].y, v.y);
+              v.z = fmaf(f, y[j].z, v.z);
+              v.w = fmaf(f, y[j].w, v.w);
+            }
           }
+          write_out(x.q0, x.head, x.r0 + r, d, v, M, L);
         }
       }
-      consumers_sync(false);  // the join area is free again
     }
   }
   __syncthreads();
