@@ -105,6 +105,9 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
                "r"(v.w)
                : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // Barrier of the consumer warps; whether any of them came with `failed` (the same answer for all,
 // so that they leave together).
 __device__ __forceinline__ bool consumers_sync(bool failed) {
@@ -133,10 +136,11 @@ constexpr int kJoinAtOnce = 8;  // pieces of a cut unit whose loads are in fligh
 struct CutUnit {
   int q0, head, r0, rows, c0, c1;
 };
-// What warp 0 lays out for all consumer warps: the next piece (s < 0: none), and the CTA's first
-// unit if it was begun before it and its last if it is left to the next.
+// What warp 0 lays out for all consumer warps: the next piece (s < 0: none) and the cut units so
+// far, the CTA's first if it was begun before it and its last if it is left to the next.
 struct DecPlan {
   AttnPiece next;
+  int cuts;
   CutUnit cut[2];
 };
 
@@ -240,10 +244,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const AttnScratch sc = attn_scratch(a.scratch, T::kBR);
     const int g = lane >> 2, c = lane & 3;
     uint32_t at = 0;  // ring position of the next tile's K
-    bool ok = true;
     auto swz = [](uint32_t off) { return off ^ ((off >> 3) & T::kSwz); };
-    // the unit's place on the line, from the cursor behind the piece
-    auto unit_at = [&](const AttnPiece& x) { return span.end - cur.left - x.tb - sh.extra; };
     auto write_out = [&](int q0, int head, int rr, int d, const float4& v, float M, float L) {
       const int tok = div_group(sh, rr);
       const size_t orow = (size_t)(q0 + tok) * a.hq + head * sh.G + (rr - tok * sh.G);
@@ -258,31 +259,68 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     auto rows_of = [&](const AttnPiece& x) {
       return min(T::kBR, x.q.n * sh.G - x.rb * T::kBR);
     };
+    // Warp 0 works the next piece out and fetches its queries into the join area, which is idle
+    // while a piece's tiles are worked through: with the ring full of copies in flight a load
+    // takes up to 4 us, and a piece that began by loading its queries cost as much.
+    constexpr uint32_t kQPitch = 2 * D + 16;
+    static_assert(T::kBR * kQPitch <= T::kJoin, "queries");
+    int place = 0;  // of the unit's first tile on the line
+    auto prepare = [&] {
+      AttnPiece next;
+      if (!next_piece(a.b, sh, cur, next)) next.s = -1;
+      if (next.s >= 0) {
+        const uint32_t at = smem_addr(join);
+        const int r0 = next.rb * T::kBR;
+        for (int i = lane; i < rows_of(next) * (D / 8); i += 32) {
+          const int r = i / (D / 8), x = i % (D / 8), tok = div_group(sh, r0 + r);
+          cp_async16(at + r * kQPitch + 16 * x,
+                     static_cast<const __nv_bfloat16*>(a.q) +
+                         (size_t)(next.q.q0 + tok) * a.q_stride +
+                         (size_t)(next.head * sh.G + (r0 + r - tok * sh.G)) * D + 8 * x);
+        }
+      }
+      if (lane == 0) plan->next = next;
+      place = span.end - cur.left - next.tb;
+    };
+    // Lane 0 of warp 0 notes the piece p, whose unit's first tile lies at `place`.
+    auto note = [&](const AttnPiece& p) {
+      if (p.whole()) return;
+      CutUnit& x = plan->cut[plan->cuts++];
+      x.q0 = p.q.q0;
+      x.head = p.head;
+      x.r0 = p.rb * T::kBR;
+      x.rows = rows_of(p);
+      x.c0 = cta_of(span, place);
+      x.c1 = cta_of(span, place + p.u.tiles - 1);
+    };
     // this lane's query columns of row 8 n + lane / 4, as the B side of the products: two
     // pairs of each 16 columns
     uint32_t qf[NT][D / 16][2];
-    auto load_q = [&](const AttnPiece& p) {
+    bool ok = true;
+    // The prepared piece and its queries; p.s < 0 when there is none, ok false after a failure.
+    auto take = [&](AttnPiece& p) {
+      if (warp == 0) asm volatile("cp.async.wait_all;" ::: "memory");
+      if (consumers_sync(!ok)) ok = false;
+      if (!ok) return;
+      p = plan->next;
+      if (p.s < 0) return;
       const int rows = rows_of(p);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int r = 8 * n + g, rr = p.rb * T::kBR + (r < rows ? r : 0);
-        const int tok = div_group(sh, rr);
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                   (size_t)(p.q.q0 + tok) * a.q_stride +
-                                   (size_t)(p.head * sh.G + (rr - tok * sh.G)) * D;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(join) + (8 * n + g) * kQPitch;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t lo = 0u, hi = 0u;
-          if (r < rows && FP8) {
+          if (8 * n + g < rows && FP8) {
             // e4m3 fragments hold columns 4c .. 4c + 3 of each 16: Q's follow that order
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + 16 * k + 4 * c));
+            const uint2 w = *reinterpret_cast<const uint2*>(src + 32 * k + 8 * c);
             const float2 x = unpack_bf16x2(w.x), y = unpack_bf16x2(w.y);
             auto cut = [](float v) { return v > 65504.f ? 65504.f : (v < -65504.f ? -65504.f : v); };
             lo = pack_f16x2(cut(x.x), cut(x.y));
             hi = pack_f16x2(cut(y.x), cut(y.y));
-          } else if (r < rows) {
-            lo = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * c));
-            hi = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * c));
+          } else if (8 * n + g < rows) {
+            lo = *reinterpret_cast<const uint32_t*>(src + 32 * k + 4 * c);
+            hi = *reinterpret_cast<const uint32_t*>(src + 32 * k + 16 + 4 * c);
           }
           qf[n][k][0] = lo;
           qf[n][k][1] = hi;
@@ -290,30 +328,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       }
     };
     AttnPiece p;
-    bool have = next_piece(a.b, sh, cur, p);
-    if (have) load_q(p);
-    int cuts = 0;
-    while (have) {
-      const int rows = rows_of(p);
+    if (threadIdx.x == 0) plan->cuts = 0;
+    if (warp == 0) prepare();
+    take(p);
+    consumers_sync(false);  // the queries are read
+    while (ok && p.s >= 0) {
       if (warp == 0) {
-        // the next piece is known before this one's tiles have arrived
-        const int place = unit_at(p);
-        AttnPiece next;
-        if (!next_piece(a.b, sh, cur, next)) next.s = -1;
-        if (lane == 0) {
-          plan->next = next;
-          if (!p.whole()) {
-            CutUnit& x = plan->cut[cuts];
-            x.q0 = p.q.q0;
-            x.head = p.head;
-            x.r0 = p.rb * T::kBR;
-            x.rows = rows;
-            x.c0 = cta_of(span, place + sh.extra);
-            x.c1 = cta_of(span, place + sh.extra + p.u.tiles - 1);
-          }
-        }
+        if (lane == 0) note(p);
+        prepare();
       }
-      cuts += !p.whole();
+      const int rows = rows_of(p);
       // the keys of this lane's rows 8 n + 2 c + e; those that every row attends need no mask
       KeyRange kr[NT][2];
 #pragma unroll
@@ -522,6 +546,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       }
 
       // ---------------------------------------------------------- the piece's result
+      AttnPiece next;
+      take(next);
+      if (!ok) break;
+      consumers_sync(false);  // the queries are read
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -544,13 +572,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
           }
         }
-      if (consumers_sync(!ok)) {
-        cuts = 0;
-        break;
-      }
-      const AttnPiece next = plan->next;
-      have = next.s >= 0;
-      if (have) load_q(next);  // under way while this piece is joined
+      consumers_sync(false);
       const int slot_out = p.first() ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
       for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kDecWarps) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -587,11 +609,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     // Cut units are joined by the CTA that finishes last: both are counted here, so that a piece
     // that ends in the middle of the CTA's range waits for no fence and no atomic.
+    const int cuts = ok ? plan->cuts : 0;
     if (cuts) {
-      __threadfence();
-      consumers_sync(false);
-      if ((int)threadIdx.x < cuts) {
+      if ((int)threadIdx.x < cuts) {  // all warps' stores lie behind a barrier
         const CutUnit x = plan->cut[threadIdx.x];
+        __threadfence();
         const bool last = atomicAdd(a.counters + x.c0, 1) == x.c1 - x.c0;
         if (last) atomicExch(a.counters + x.c0, 0);
         __threadfence();
@@ -659,9 +681,15 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   DecMaps maps;
   if (!make_cache_map(&maps.k, a.c.k, a) || !make_cache_map(&maps.v, a.c.v, a))
     return cudaErrorInvalidValue;
-  const AttnShape sh = attn_shape(a, NT == 1 ? 3 : 4, 0);
-  static_assert(T::kBR == 1 << (NT == 1 ? 3 : 4), "rows per unit");
   const int ctas = num_sms() < kAttnMaxCtas ? num_sms() : kAttnMaxCtas;
+  // The cost of beginning a unit, in tiles. e4m3 tiles are short: 3 against 0 takes 256 sequences
+  // of about 1000 keys from 157 to 127 us, 5 of 47500 from 49.5 to 48.0. 64 columns: 64 sequences
+  // of 2000 keys 67.4, 63.7, 64.7 us at 0, 1, 2. bf16 rows of 256 bytes: the ring hides it (194.2
+  // against 200.5 us for 64 long sequences), but with fewer units than CTAs, where a CTA of two
+  // pieces ends last (12.4 against 10.9 us for 3 sequences).
+  const int extra = FP8 ? 3 : (long long)a.b.S * a.hkv < ctas ? 2 : D == 64 ? 1 : 0;
+  const AttnShape sh = attn_shape(a, NT == 1 ? 3 : 4, extra);
+  static_assert(T::kBR == 1 << (NT == 1 ? 3 : 4), "rows per unit");
   return launch_kernel(attn_decode_kernel<FP8, D, NT>, dim3(ctas), dim3(kDecThreads), T::kSmem,
                        stream, maps, a, sh);
 }
