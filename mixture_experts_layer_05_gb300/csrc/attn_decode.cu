@@ -387,45 +387,44 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[u][n][j] = 0.f;
-          if (u >= count) continue;
-          const uint32_t pos = at + 2 * u;
-          if (!filled(pos)) {
+          if (u < count && !filled(at + 2 * u)) {
             ok = false;
             break;
           }
-          if (some(u)) {
-            const uint32_t st = base + slot(pos) * T::kStage;
-            const uint32_t row = warp * 16 + (lane & 15);
-            if (FP8) {
-              // keys 0-7 and 8-15 x 32 columns, 16 bytes per row of an 8x8 matrix
-#pragma unroll
-              for (int k = 0; k < D / 32; ++k) {
-                uint32_t w[4], f[2][4];
-                ldsm4(st + swz(row * T::kPitch + k * 32 + (lane >> 4) * 16), w);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  e4m3x4_f16(w[2 * h], f[h][0], f[h][2]);
-                  e4m3x4_f16(w[2 * h + 1], f[h][1], f[h][3]);
-#pragma unroll
-                  for (int n = 0; n < NT; ++n)
-                    mma16816<true>(s[u][n], f[h], qf[n][2 * k + h][0], qf[n][2 * k + h][1]);
-                }
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                uint32_t w[4];
-                const uint32_t col = (k % 4) * 32 + (lane >> 4) * 16;
-                ldsm4(st + (k / 4) * (kAttnTK * 128) + swz(row * 128 + col), w);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                  mma16816<false>(s[u][n], w, qf[n][k][0], qf[n][k][1]);
-              }
-            }
-          }
-          release(pos);
         }
         if (!ok) break;
+        // the tiles' products in turn: each is a chain of sums. A tile that has none of this
+        // warp's keys is worked through as well, whatever its stage holds: its scores drop out
+        const uint32_t row = warp * 16 + (lane & 15);
+#pragma unroll
+        for (int k = 0; k < D / (FP8 ? 32 : 16); ++k)
+#pragma unroll
+          for (int u = 0; u < T::kAtOnce; ++u) {
+            const uint32_t st = base + slot(at + 2 * u) * T::kStage;
+            uint32_t w[4];
+            if (FP8) {
+              // keys 0-7 and 8-15 x 32 columns, 16 bytes per row of an 8x8 matrix
+              uint32_t f[2][4];
+              ldsm4(st + swz(row * T::kPitch + k * 32 + (lane >> 4) * 16), w);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                e4m3x4_f16(w[2 * h], f[h][0], f[h][2]);
+                e4m3x4_f16(w[2 * h + 1], f[h][1], f[h][3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  mma16816<true>(s[u][n], f[h], qf[n][2 * k + h][0], qf[n][2 * k + h][1]);
+              }
+            } else {
+              const uint32_t col = (k % 4) * 32 + (lane >> 4) * 16;
+              ldsm4(st + (k / 4) * (kAttnTK * 128) + swz(row * 128 + col), w);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma16816<false>(s[u][n], w, qf[n][k][0], qf[n][k][1]);
+            }
+          }
+#pragma unroll
+        for (int u = 0; u < T::kAtOnce; ++u)
+          if (u < count) release(at + 2 * u);
         // scores in log2 units; keys that a row does not attend drop out
         float mn[NT][2];
         bool grows = false;
