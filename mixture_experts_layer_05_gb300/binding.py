@@ -8,10 +8,12 @@ fallback of any kind, and loading fails loudly when the library is not built.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
+EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_block.so")
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgbmoe.so")
 
 STATUS = {0: "GBMOE_OK", -1: "GBMOE_ERR_INVALID_ARG", -2: "GBMOE_ERR_UNSUPPORTED",
@@ -482,33 +484,24 @@ def moe_get_device_status(workspace, stream=None) -> int:
     return v.value
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_ext = None
 
 
-def _stream_of(t, stream):
-    """The stream argument as an integer; None: the current one of t's device (without the
-    Stream object, whose construction takes longer than a small kernel's launch)."""
-    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
-
-
-def _row_stride(t, name, T, cols):
-    """Row stride of a CUDA bf16 [T, cols] or [T, heads, dim] tensor with contiguous rows."""
-    st = t.stride()
-    if (not t.is_cuda or t.dtype is not torch.bfloat16 or t.shape[0] != T
-            or t.numel() != T * cols or st[-1] != 1 or not 2 <= len(st) <= 3
-            or (len(st) == 3 and st[1] != t.shape[2])):
-        raise ValueError(f"{name} must be a CUDA bfloat16 tensor of {T} rows of {cols} contiguous "
-                         "columns")
-    return st[0] if T > 1 else cols
-
-
-def _out(t, name, like, shape, dtype=torch.bfloat16):
-    """t, checked, or a new contiguous tensor."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}")
-    return t
+def _block():
+    """The compiled marshalling of the decoder-block entry points, bound to the library."""
+    global _ext
+    if _ext is None:
+        lib = load()
+        if not os.path.exists(EXT_PATH):
+            raise RuntimeError(f"{EXT_PATH} is not built: run mixture_experts_layer_05_gb300.build"
+                               ".build()")
+        spec = importlib.util.spec_from_file_location("_block", EXT_PATH)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                   (lib.moe_rms_norm, lib.moe_kv_append, lib.moe_paged_attention)), GbmoeError)
+        _ext = ext
+    return _ext
 
 
 def moe_rms_norm(x, weight, eps=1e-6, residual=None, out="bf16", y=None, residual_out=None,
@@ -517,36 +510,10 @@ def moe_rms_norm(x, weight, eps=1e-6, residual=None, out="bf16", y=None, residua
     scale: e4m3 codes and group-major fp32 scales [H / 128, T], the FP8 layer's input format)
     or "both". Rows of x and residual may be strided. Returns (y, residual_out, q, scale), None
     for what was not asked for (residual_out: without a residual)."""
-    T, H = x.shape
-    xs, rs, rp = _row_stride(x, "x", T, H), 0, None
-    if not weight.is_cuda or weight.dtype is not torch.bfloat16 or weight.shape != (H,) or (
-            not weight.is_contiguous()):
-        raise ValueError("weight must be a contiguous CUDA bfloat16 tensor of H columns")
-    yp = ro = qp = sp = None
-    if residual is not None:
-        rs, rp = _row_stride(residual, "residual", T, H), residual.data_ptr()
-        residual_out = _out(residual_out, "residual_out", x, (T, H))
-        ro = residual_out.data_ptr()
-    else:
-        residual_out = None
-    if out == "bf16" or out == "both":
-        y = _out(y, "y", x, (T, H))
-        yp = y.data_ptr()
-    else:
-        y = None
-    if out == "fp8" or out == "both":
-        q = _out(q, "q", x, (T, H), torch.float8_e4m3fn)
-        scale = _out(scale, "scale", x, (H // 128, T), torch.float32)
-        qp, sp = q.data_ptr(), scale.data_ptr()
-    elif out == "bf16":
-        q = scale = None
-    else:
+    if out not in ("bf16", "fp8", "both"):
         raise ValueError(f"out must be bf16, fp8 or both, not {out!r}")
-    a = RmsNormArgs(x.data_ptr(), xs, rp, rs, weight.data_ptr(), eps, yp, ro, qp, sp)
-    code = load().moe_rms_norm(T, H, ctypes.byref(a), _stream_of(x, stream))
-    if code:
-        raise GbmoeError("moe_rms_norm", code)
-    return y, residual_out, q, scale
+    return _block().rms_norm(x, weight, eps, residual, out != "fp8", out != "bf16", y,
+                             residual_out, q, scale, stream)
 
 
 class PagedAttention:
@@ -566,80 +533,23 @@ class PagedAttention:
             raise GbmoeError("moe_paged_attention_workspace_size", ERR_INVALID_ARG)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device)
         self.workspace[:1024].zero_()         # status word and counters
-        self._ws = (self.workspace.data_ptr(), n)
-        self._dtypes = ((torch.bfloat16,) if cfg.cache_type == CACHE["bf16"]
-                        else (torch.float8_e4m3fn, torch.uint8))
-        self._heads = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
-        self._page = cfg.page_size, cfg.num_kv_heads, cfg.head_dim
-
-    def _paged(self, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens) -> PagedKv:
-        shape, st = k_cache.shape, k_cache.stride()
-        if (shape[1:] != self._page or v_cache.shape != shape or v_cache.stride() != st
-                or st[3] != 1 or k_cache.dtype not in self._dtypes
-                or v_cache.dtype is not k_cache.dtype or not k_cache.is_cuda
-                or not v_cache.is_cuda):
-            raise ValueError("k_cache and v_cache must be CUDA tensors [num_pages, page_size, "
-                             "num_kv_heads, head_dim] of the configured type and equal strides, "
-                             "contiguous in head_dim")
-        S, = kv_lens.shape
-        rows, cols = block_table.shape
-        if rows != S or cu_seqlens_q.shape != (S + 1,):
-            raise ValueError("block_table must be [S, max_pages], cu_seqlens_q [S + 1], kv_lens [S]")
-        for t in (block_table, cu_seqlens_q, kv_lens):
-            if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
-                raise ValueError("block_table, cu_seqlens_q and kv_lens must be contiguous CUDA "
-                                 "int32 tensors")
-        # the stride of a dimension of one element is never used: any valid number
-        if 1 in shape:
-            st = [st[i] if shape[i] > 1 else shape[3] for i in range(3)]
-        return PagedKv(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], shape[0], S,
-                       cols, block_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr())
+        # addresses of what this object keeps alive
+        self._at = ctypes.addressof(cfg), self.workspace.data_ptr()
+        self._bytes = n
 
     def append(self, q, k, v, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, cos_sin=None,
                interleaved=False, q_out=None, stream=None):
         """Rotates the new tokens' q and k [T, heads, head_dim] (rows may be strided, as slices
         of one packed projection), writes k and v into the cache, and returns the rotated q."""
-        hq, hkv, d = self._heads
-        kv = self._paged(k_cache, v_cache, block_table, cu_seqlens_q, kv_lens)
-        T = q.shape[0]
-        qs = _row_stride(q, "q", T, hq * d)
-        ks = _row_stride(k, "k", T, hkv * d)
-        vs = _row_stride(v, "v", T, hkv * d)
-        q_out = _out(q_out, "q_out", q, (T, hq, d))
-        if cos_sin is None:
-            cp, pos, rot = None, 0, 0
-        else:
-            if not cos_sin.is_cuda or cos_sin.dtype is not torch.float32 or (
-                    not cos_sin.is_contiguous()):
-                raise ValueError("cos_sin must be a contiguous CUDA float32 tensor")
-            cp, (pos, rot) = cos_sin.data_ptr(), cos_sin.shape
-        a = KvAppendArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cp, pos, rot,
-                         bool(interleaved), q_out.data_ptr(), self._ws[0])
-        code = load().moe_kv_append(ctypes.byref(self.cfg), T, ctypes.byref(kv), ctypes.byref(a),
-                                    _stream_of(q, stream))
-        if code:
-            raise GbmoeError("moe_kv_append", code)
-        return q_out
+        return _block().kv_append(*self._at, q, k, v, k_cache, v_cache, block_table, cu_seqlens_q,
+                                  kv_lens, cos_sin, interleaved, q_out, stream)
 
     def __call__(self, q, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, out=None,
                  lse=None, stream=None):
         """out [T, num_q_heads, head_dim] bf16 of the new tokens' q; with lse (True, or a fp32
         [T, num_q_heads] tensor) also the log-sum-exp of each row's scores: (out, lse)."""
-        hq, _, d = self._heads
-        kv = self._paged(k_cache, v_cache, block_table, cu_seqlens_q, kv_lens)
-        T = q.shape[0]
-        qs = _row_stride(q, "q", T, hq * d)
-        out = _out(out, "out", q, (T, hq, d))
-        lp = None
-        if lse is not None:
-            lse = _out(None if lse is True else lse, "lse", q, (T, hq), torch.float32)
-            lp = lse.data_ptr()
-        code = load().moe_paged_attention(ctypes.byref(self.cfg), T, ctypes.byref(kv), q.data_ptr(),
-                                          qs, out.data_ptr(), lp, *self._ws,
-                                          _stream_of(q, stream))
-        if code:
-            raise GbmoeError("moe_paged_attention", code)
-        return out if lse is None else (out, lse)
+        return _block().attention(*self._at, self._bytes, q, k_cache, v_cache, block_table,
+                                  cu_seqlens_q, kv_lens, out, lse, stream)
 
     def device_status(self) -> int:
         return moe_get_device_status(self.workspace)
