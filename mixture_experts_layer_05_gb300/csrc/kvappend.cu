@@ -7,11 +7,12 @@
 // from x times the reciprocal of the scale, saturating at 448).
 //
 // Bound by HBM. One CTA per token; a thread handles two vectors of eight columns at a time,
-// the two halves of eight pairs (half-split pairs) or sixteen neighbouring columns. What counts
-// is how many tokens an SM has in different phases of their lookups and copies: 12 CTAs of 128
-// threads took 26 us for 5,200 tokens of 32 + 2 x 8 heads of 128 into an e4m3 cache (134 MB, 5.1
-// TB/s), eight of 192 27, six 29; several tokens a CTA with their lookups side by side and the
-// next token's loads under way needed registers that left two, 46.
+// the two halves of eight pairs (half-split pairs) or sixteen neighbouring columns, and loads the
+// next two before it stores these; the first are loaded before the token's sequence and page are
+// known. 5,200 tokens of 32 + 2 x 8 heads of 128 into an e4m3 cache (134 MB) take 26.4 us, 5.1
+// TB/s, 32 tokens 3.5 (4.1 when the lookups come first). Six CTAs of 192 threads on an SM: with
+// eight the registers spill (34 us), three of 384 take 33, and several tokens a CTA with their
+// lookups side by side 46.
 #include "block.cuh"
 #include "fp8.cuh"
 #include "kernels.h"
@@ -19,10 +20,9 @@
 namespace gbmoe {
 namespace {
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 192, kAppendCtas = 6;
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -52,9 +52,39 @@ __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// Two vectors of eight columns of one head of a token: columns c0 and c1 of q (kind 0), k or v.
+struct Item {
+  int kind, h, p, c0, c1;
+  bool turn;
+  uint4 a, b;  // as loaded
+};
+__device__ __forceinline__ Item load_item(const KvAppendArgs& a, int t, int it) {
+  Item x;
+  const int per_head = a.D / 16;
+  x.h = it / per_head;
+  x.p = it % per_head;
+  x.kind = x.h < a.hq ? 0 : (x.h < a.hq + a.hkv ? 1 : 2);
+  x.h -= x.kind == 0 ? 0 : (x.kind == 1 ? a.hq : a.hq + a.hkv);
+  x.turn = x.kind < 2 && x.p < a.rotary / 16;
+  const bool split = x.turn && !a.interleaved;
+  x.c0 = split ? 8 * x.p : 16 * x.p;
+  x.c1 = split ? 8 * x.p + a.rotary / 2 : 16 * x.p + 8;
+  const __nv_bfloat16* src =
+      x.kind == 0 ? static_cast<const __nv_bfloat16*>(a.q) + (size_t)t * a.q_stride
+      : x.kind == 1 ? static_cast<const __nv_bfloat16*>(a.k) + (size_t)t * a.k_stride
+                    : static_cast<const __nv_bfloat16*>(a.v) + (size_t)t * a.v_stride;
+  src += (size_t)x.h * a.D;
+  x.a = __ldg(reinterpret_cast<const uint4*>(src + x.c0));
+  x.b = __ldg(reinterpret_cast<const uint4*>(src + x.c1));
+  return x;
+}
+
 template <bool FP8>
-__global__ void __launch_bounds__(kAppendThreads, 12) kv_append_kernel(KvAppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) kv_append_kernel(KvAppendArgs a) {
   const int t = blockIdx.x, lane = threadIdx.x & 31;
+  const int items = (a.hq + 2 * a.hkv) * (a.D / 16);
+  Item next;  // the first vectors are under way while the token's place is looked up
+  if ((int)threadIdx.x < items) next = load_item(a, t, threadIdx.x);
   const int s = find_seq_warp(a.b, t, lane);  // every warp finds it: no barrier
   if (s < 0) return;                          // a token of no sequence (padding)
   const SeqInfo q = seq_info(a.b, s);
@@ -70,28 +100,16 @@ __global__ void __launch_bounds__(kAppendThreads, 12) kv_append_kernel(KvAppendA
   if (bad && threadIdx.x == 0) record_status(a.b.status, GBMOE_ERR_DEVICE_CHECK);
   const size_t row = (size_t)page * a.c.page_stride +
                      (size_t)(pos & ((1 << a.b.page_shift) - 1)) * a.c.token_stride;
-  const int per_head = a.D / 16;
-  const int items = (a.hq + 2 * a.hkv) * per_head;
   const int R = a.rotary;
   const float* cs = a.cos_sin ? a.cos_sin + (size_t)pos * R : nullptr;
   for (int it = threadIdx.x; it < items; it += blockDim.x) {
-    int h = it / per_head;
-    const int p = it % per_head;
-    const int kind = h < a.hq ? 0 : (h < a.hq + a.hkv ? 1 : 2);  // q, k, v
-    h -= kind == 0 ? 0 : (kind == 1 ? a.hq : a.hq + a.hkv);
-    const bool turn = kind < 2 && p < R / 16;
-    // columns of the two vectors
-    const bool split = kind < 2 && !a.interleaved && p < R / 16;
-    const int c0 = split ? 8 * p : 16 * p;
-    const int c1 = split ? 8 * p + R / 2 : 16 * p + 8;
-    const __nv_bfloat16* src =
-        kind == 0 ? static_cast<const __nv_bfloat16*>(a.q) + (size_t)t * a.q_stride
-        : kind == 1 ? static_cast<const __nv_bfloat16*>(a.k) + (size_t)t * a.k_stride
-                    : static_cast<const __nv_bfloat16*>(a.v) + (size_t)t * a.v_stride;
-    src += (size_t)h * a.D;
+    const Item now = next;
+    if (it + (int)blockDim.x < items) next = load_item(a, t, it + blockDim.x);
+    const int kind = now.kind, h = now.h, p = now.p, c0 = now.c0, c1 = now.c1;
+    const bool turn = now.turn, split = turn && !a.interleaved;
     float x[8], y[8];
-    load8(src + c0, x);
-    load8(src + c1, y);
+    unpack8(now.a, x);
+    unpack8(now.b, y);
     if (turn) {
       float c[8], z[8];
       load8f(cs + 8 * p, c);
