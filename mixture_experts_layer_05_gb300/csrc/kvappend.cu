@@ -9,7 +9,7 @@
 // Bound by HBM. One CTA per token; a thread handles two vectors of eight columns at a time,
 // the two halves of eight pairs (half-split pairs) or sixteen neighbouring columns, and loads the
 // next two before it stores these; the first are loaded before the token's sequence and page are
-// known. 5,200 tokens of 32 + 2 x 8 heads of 128 into an e4m3 cache (134 MB) take 26.4 us, 5.1
+// known. 5,867 tokens of 32 + 2 x 8 heads of 128 into an e4m3 cache (134 MB) take 26.4 us, 5.1
 // TB/s, 32 tokens 3.5 (4.1 when the lookups come first). Six CTAs of 192 threads on an SM: with
 // eight the registers spill (34 us), three of 384 take 33, and several tokens a CTA with their
 // lookups side by side 46.
