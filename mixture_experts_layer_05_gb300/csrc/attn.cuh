@@ -59,13 +59,20 @@ __device__ __forceinline__ int cta_of(const AttnSpan& s, int x) {
   return c;
 }
 
+// The cursor with the sizes of its sequence qs at hand: reading them again costs a trip to L2 each
+// time a piece is worked out, and the first piece waits for that.
+struct AttnWalk : AttnCursor {
+  int qs;
+  SeqInfo q;
+};
+
 constexpr int kPlanBlocks = 4;  // row blocks that one thread adds up by itself
 
 // This CTA's cursor; every thread of the block calls it. line: shared memory for S + 1 prefix
 // sums, wsum: 32 more. A thread takes a sequence of few row blocks (single tokens), a warp one of
 // many: a prompt of 8191 tokens has 128, and one thread walking them cost 45 us.
-__device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnShape& sh,
-                                                int* line, int* wsum, AttnSpan& span) {
+__device__ __forceinline__ AttnWalk attn_plan(const PagedBatch& b, const AttnShape& sh,
+                                              int* line, int* wsum, AttnSpan& span) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int warps = nt >> 5;
 #pragma unroll 1
@@ -123,8 +130,9 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
   const int W = line[b.S];
   span.W = W;
   span.ctas = min(W, (int)gridDim.x);  // every one of these has some of the line
-  AttnCursor c;
+  AttnWalk c;
   c.s = c.head = c.rb = c.off = c.left = 0;
+  c.qs = -1;
   span.end = 0;
   if ((int)blockIdx.x < span.ctas) {
     const int a = range_at(W, blockIdx.x, span.ctas);
@@ -139,7 +147,8 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
     const SeqInfo q = seq_info(b, lo);
     const int head = (line[lo + 1] - line[lo]) / sh.hkv;  // length of one head
     int rem = a - line[lo];
-    c.s = lo;
+    c.s = c.qs = lo;
+    c.q = q;
     c.left = span.end - a;
     c.head = rem / head;
     rem -= c.head * head;
@@ -175,13 +184,16 @@ __device__ __forceinline__ AttnCursor attn_plan(const PagedBatch& b, const AttnS
 // The next piece of the cursor's range, false when none is left; sequences without rows and
 // units of which the range holds only the extra cost are passed over.
 __device__ __forceinline__ bool next_piece(const PagedBatch& b, const AttnShape& sh,
-                                           AttnCursor& c, AttnPiece& p) {
+                                           AttnWalk& c, AttnPiece& p) {
 #pragma unroll 1
   while (c.left > 0) {
-    SeqInfo q = seq_info(b, c.s);
 #pragma unroll 1
-    while (q.n == 0 && c.s + 1 < b.S) q = seq_info(b, ++c.s);
-    p = take_piece(sh, q, c);
+    while (c.qs != c.s) {
+      c.qs = c.s;
+      c.q = seq_info(b, c.s);
+      if (c.q.n == 0 && c.s + 1 < b.S) ++c.s;
+    }
+    p = take_piece(sh, c.q, c);
     if (p.ta < p.tb) return true;
   }
   return false;

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   // the line of tiles is laid out in the ring before the first copy lands there
   AttnSpan span;
-  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
+  AttnWalk cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
   fence_async_proxy();
   __syncthreads();
   int* status = a.b.status;

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     tmem_relinquish();
   }
   AttnSpan span;
-  AttnCursor cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
+  AttnWalk cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
   fence_async_proxy();
   tc_fence_before();
   __syncthreads();
@@ -726,6 +726,19 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         d.L = p.q.L;
         d.head = p.head;
         d.slot = p.whole() ? -1 : p.first() ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
+      }
+      if (!wait(d_empty(dq.slot), dq.phase ^ 1u)) return false;
+      if (lane == 0) {
+        int4* dst = reinterpret_cast<int4*>(pieces + dq.slot);
+        dst[0] = make_int4(d.nt, d.j0, d.lo, d.hi);
+        dst[1] = make_int4(d.in_lo, d.in_hi, d.rows, d.r0);
+        dst[2] = make_int4(d.q0, d.n, d.L, d.head);
+        dst[3] = make_int4(d.slot, d.seq, 0, 0);
+        mbar_arrive(d_full(dq.slot));
+      }
+      __syncwarp();
+      dq.next(kTcPieces);
+      if (have) {
         if (lane == 0 && p.first() && !p.last()) {
           rec->q0 = p.q.q0;
           rec->n = p.q.n;
@@ -744,17 +757,6 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
                        "r"(sh.G * D * 2)
                        : "memory");
       }
-      if (!wait(d_empty(dq.slot), dq.phase ^ 1u)) return false;
-      if (lane == 0) {
-        int4* dst = reinterpret_cast<int4*>(pieces + dq.slot);
-        dst[0] = make_int4(d.nt, d.j0, d.lo, d.hi);
-        dst[1] = make_int4(d.in_lo, d.in_hi, d.rows, d.r0);
-        dst[2] = make_int4(d.q0, d.n, d.L, d.head);
-        dst[3] = make_int4(d.slot, d.seq, 0, 0);
-        mbar_arrive(d_full(dq.slot));
-      }
-      __syncwarp();
-      dq.next(kTcPieces);
       return true;
     };
     bool ok = take_k ? publish(d) : split && get_piece(d);
