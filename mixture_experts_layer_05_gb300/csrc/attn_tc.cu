@@ -26,15 +26,16 @@
 //   warp 10          bf16 cache: zeroes what a V tile holds outside the unit's keys
 //   warps 10, 11     e4m3 cache: codes to f16 (exact) into the operand tiles
 //
-// Tensor memory: S/P of half h at columns 128 h, O of half h at 256 + 128 h. Operand order in
+// Tensor memory: S/P of half h at columns 128 h, O of half h at 256 + 128 h; heads of 64: S at
+// 128 h, P at 256 + 64 h, O at 384 + 64 h. Operand order in
 // the ring: K0, V0, K1, V1, ...; the scores of the next tile are issued ahead of a tile's second
 // product. bf16 cache: bf16 products; e4m3: f16 products with Q rounded to f16 (saturating).
 //
 // Bound by the tensor cores: a tile of both halves is 2048 cycles of products (heads of 128), and
 // a long prompt's steady step takes 2550 to 2700; the products alone, without a softmax, 2360.
 // 8191 causal tokens of 32 + 8 heads: 350 us, 1570 TFLOP/s (0.83 of the measured bf16 rate).
-// Heads of 64: 627 us, bound by the exponentials, of which there are as many. e4m3: 391 us, bound
-// by the two warps that turn codes to f16. Beginning a piece costs about 4 us (queries, first
+// Heads of 64: 545 us, bound by the softmax, whose work does not halve with the products (626 with
+// P over the scores, as for 128). e4m3: 393 us, bound by the two warps that turn codes to f16. Beginning a piece costs about 4 us (queries, first
 // scores, drain of the last O), which packed prompts feel: 5955 tokens of 5 sequences 89 us, 865
 // TFLOP/s. Two issuing threads, one per half, took 459 us for the long prompt: the halves' products
 // then alternate on the tensor core and none finishes early.
@@ -58,6 +59,14 @@ struct Tc {
   static constexpr uint32_t kRawTile = kAttnTK * D;         // one tile of codes
   static constexpr int kRaw = FP8 ? 3 : 0;                  // code stages
   static constexpr int kStages = FP8 ? 3 : 4;               // operand stages
+  // Tensor memory columns of a half: its scores, weights and output. With 64 columns of output the
+  // weights have a place of their own and the next tile's scores need not wait for their product.
+  static constexpr bool kApart = D == 64;
+  static __host__ __device__ constexpr uint32_t s_col(int g) { return 128u * g; }
+  static __host__ __device__ constexpr uint32_t p_col(int g) { return kApart ? 256u + 64u * g : 128u * g; }
+  static __host__ __device__ constexpr uint32_t o_col(int g) {
+    return kApart ? 384u + 64u * g : 256u + 128u * g;
+  }
   static constexpr int kOutCols = 32;                       // columns staged at a time
   static constexpr uint32_t kOut = 2 * 128 * kOutCols * 2;  // staging of the output rows
   static constexpr uint32_t kQ = 2 * kTile;
@@ -249,13 +258,14 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
   auto raw_full = [&](int s) { return bar0 + 8u * (18 + s); };
   auto raw_empty = [&](int s) { return bar0 + 8u * (22 + s); };
   auto pa_done = [&](int g) { return bar0 + 8u * (42 + g); };  // first 64 keys' product
+  auto s_read = [&](int g) { return bar0 + 8u * (44 + g); };   // kApart: scores in registers
   auto v_raw = [&](int s) { return bar0 + 8u * (26 + s); };   // stage s: an edge V tile landed
   auto d_full = [&](int i) { return bar0 + 8u * (34 + i); };  // piece descriptors
   auto d_empty = [&](int i) { return bar0 + 8u * (38 + i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  TcPiece* pieces = reinterpret_cast<TcPiece*>(bars + 44);
-  int* wsum = reinterpret_cast<int*>(bars + 44 + kTcPieces * 8);  // 32
+  TcPiece* pieces = reinterpret_cast<TcPiece*>(bars + 46);
+  int* wsum = reinterpret_cast<int*>(bars + 46 + kTcPieces * 8);  // 32
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* status = a.b.status;
   pdl_trigger();
@@ -276,6 +286,7 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
       mbar_init(p_full(g, 1), 4);
       mbar_init(pv_done(g), 1);
       mbar_init(pa_done(g), 1);
+      mbar_init(s_read(g), 4);
     }
     for (int i = 0; i < kTcPieces; ++i) {
       mbar_init(d_full(i), 1);
@@ -331,7 +342,8 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     const int g = warp >> 2;
     const int row = threadIdx.x & 127;                       // of this half
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + 128u * g, to = tmem + lanes + 256u + 128u * g;
+    const uint32_t ts = tmem + lanes + T::s_col(g), tp = tmem + lanes + T::p_col(g),
+                   to = tmem + lanes + T::o_col(g);
     const uint32_t q_half = q_base + g * T::kTile;
     constexpr int kLanes = D / 8;  // lanes that a query row takes, 16 bytes each
     // A piece as this thread's row needs it.
@@ -449,6 +461,11 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) tmem_wait_ld(s[i]);
+          if (T::kApart && h == 1) {  // the next tile's scores may overwrite these
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_read(g));
+          }
           auto drop = [&]() {  // keys that this row does not attend
             const int lo = job.lo - j0 - 64 * h, hi = job.hi - j0 - 64 * h;
 #pragma unroll
@@ -527,7 +544,14 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
           if (h == 0)
 #pragma unroll
             for (int i = 0; i < 2; ++i) tmem_ld32(ts + 64 + 32 * i, s[i]);
-          tmem_st32(ts + 32 * h, w);
+          if (T::kApart && h == 0) {  // P's place is free when the last tile's product is done
+            if (!wait(pv_done(g), (tc - 1) & 1u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          tmem_st32(tp + 32 * h, w);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -620,11 +644,34 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
         mbar_arrive(d_empty(dq.slot));
         dq.next(kTcPieces);
         if (nt == 0) break;
-        // step t: the products of tile t with V, and the scores of tile t + 1
+        // step t: the products of tile t with V, and the scores of tile t + 1 (kApart: the scores
+        // first, as soon as the half's of tile t have been read)
 #pragma unroll 1
         for (int t = -1; ok && t < nt; ++t) {
           const bool more = t + 1 < nt;
           uint32_t ks = 0, vs = 0;
+          auto queries = [&](int g) {
+            if (!wait1(q_full(g), (pieces_of >> g) & 1u)) return false;
+            pieces_of ^= 1u << g;
+            tc_fence_after();
+            return true;
+          };
+          auto scores = [&](int g, uint32_t col) {
+            if (g == 0) {
+              ks = rg.slot;
+              if (!wait1(full(ks), rg.phase)) return false;
+              rg.next(T::kStages);
+            }
+            const uint64_t qa = q_half + g * kStep, kb = k_ring + ks * kStep;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = (k / 4) * (kHalf >> 4) + (k % 4) * 2;
+              mma_bf16(col, qa + at, kb + at, kIdS, k > 0);
+            }
+            mma_commit(s_full(g));
+            if (g + 1 == halves) mma_commit(empty(ks));
+            return true;
+          };
           if (t >= 0) {
             vs = rg.slot;
             if (!(ok = wait1(full(vs), rg.phase))) break;
@@ -632,7 +679,17 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
           }
 #pragma unroll 1
           for (int g = 0; g < halves; ++g) {
-            const uint32_t col = tmem + 128u * g;
+            const uint32_t col = tmem + (T::kApart ? 64u : 128u) * g;
+            constexpr uint32_t kO = T::o_col(0), kP = T::p_col(0);
+            if (T::kApart && more) {
+              if (t < 0) {
+                ok = queries(g);
+              } else {
+                ok = wait1(s_read(g), (tiles_of >> g) & 1u);
+                tc_fence_after();
+              }
+              if (!(ok = ok && scores(g, tmem + T::s_col(g)))) break;
+            }
             if (t >= 0) {
               // O += P V as the two 64-key halves of P arrive
               const uint64_t vb = v_ring + vs * kStep;
@@ -642,35 +699,19 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
               tc_fence_after();
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma_ts(col + 256u, col + 8u * k, vb + k * (2048 >> 4), kIdO, t > 0 || k > 0);
+                mma_ts(col + kO, col + kP + 8u * k, vb + k * (2048 >> 4), kIdO, t > 0 || k > 0);
               mma_commit(pa_done(g));
               if (!(ok = wait1(p_full(g, 1), par))) break;
               tc_fence_after();
 #pragma unroll
               for (int k = 4; k < 8; ++k)
-                mma_ts(col + 256u, col + 8u * k, vb + k * (2048 >> 4), kIdO, 1u);
+                mma_ts(col + kO, col + kP + 8u * k, vb + k * (2048 >> 4), kIdO, 1u);
               mma_commit(pv_done(g));
               if (g + 1 == halves) mma_commit(empty(vs));
-            } else {
-              if (!(ok = wait1(q_full(g), (pieces_of >> g) & 1u))) break;
-              pieces_of ^= 1u << g;
-              tc_fence_after();
+            } else if (!T::kApart && !(ok = queries(g))) {
+              break;
             }
-            if (more) {
-              if (g == 0) {
-                ks = rg.slot;
-                if (!(ok = wait1(full(ks), rg.phase))) break;
-                rg.next(T::kStages);
-              }
-              const uint64_t qa = q_half + g * kStep, kb = k_ring + ks * kStep;
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t at = (k / 4) * (kHalf >> 4) + (k % 4) * 2;
-                mma_bf16(col, qa + at, kb + at, kIdS, k > 0);
-              }
-              mma_commit(s_full(g));
-              if (g + 1 == halves) mma_commit(empty(ks));
-            }
+            if (!T::kApart && more && !(ok = scores(g, col))) break;
           }
         }
       }
