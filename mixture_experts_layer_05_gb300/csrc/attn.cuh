@@ -75,13 +75,15 @@ __device__ __forceinline__ AttnWalk attn_plan(const PagedBatch& b, const AttnSha
                                               int* line, int* wsum, AttnSpan& span) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int warps = nt >> 5;
+  bool falls = false;
 #pragma unroll 1
   for (int s = tid; s < b.S; s += nt) {
     const SeqInfo q = seq_info(b, s);
+    falls |= b.cu[s + 1] < b.cu[s];
     line[s + 1] = unit_blocks(sh, q.n) <= kPlanBlocks ? seq_length(sh, q) * sh.hkv : -1;
   }
   if (tid == 0) line[0] = 0;
-  __syncthreads();
+  falls = __syncthreads_or(falls);
   // few sequences: every warp looks through all and takes each `warps`-th; many: 32 apiece
   const bool few = b.S <= 1024;
   int mine = 0;
@@ -103,6 +105,19 @@ __device__ __forceinline__ AttnWalk attn_plan(const PagedBatch& b, const AttnSha
     }
   }
   __syncthreads();
+  AttnWalk c;
+  c.s = c.head = c.rb = c.off = c.left = 0;
+  c.qs = -1;
+  span.W = span.ctas = span.end = 0;
+  if (falls) {
+    // Bounds that go back (reported already) let sequences share tokens: the length of the line is
+    // then not bounded by the batch's, and one that leaves 32 bits gets no work at all.
+    long long all = 0;
+#pragma unroll 1
+    for (int s = 0; s < b.S; ++s) all += line[s + 1] < 0 ? -2 - line[s + 1] : line[s + 1];
+    if (all > 0x7fffffff) return c;
+    __syncthreads();
+  }
   // prefix sums: a run of sequences per thread
   const int per = (b.S + nt - 1) / nt;
   const int s0 = min(tid * per, b.S), s1 = min(s0 + per, b.S);
@@ -130,10 +145,6 @@ __device__ __forceinline__ AttnWalk attn_plan(const PagedBatch& b, const AttnSha
   const int W = line[b.S];
   span.W = W;
   span.ctas = min(W, (int)gridDim.x);  // every one of these has some of the line
-  AttnWalk c;
-  c.s = c.head = c.rb = c.off = c.left = 0;
-  c.qs = -1;
-  span.end = 0;
   if ((int)blockIdx.x < span.ctas) {
     const int a = range_at(W, blockIdx.x, span.ctas);
     span.end = range_at(W, blockIdx.x + 1, span.ctas);

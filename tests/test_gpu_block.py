@@ -407,3 +407,21 @@ def test_bad_pages_and_lengths_are_reported(cuda_lib):
     op.append(q, x, x, k, v, p.table.to(DEV), p.cu.to(DEV), p.kv_lens.to(DEV),
               cos_sin=_tables(10, 64).to(DEV))     # positions past the angle table
     assert op.device_status() == binding.ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("keys", [100, 1 << 24])
+def test_bounds_that_go_back_end_and_are_reported(cuda_lib, keys):
+    """512 sequences that each claim all 512 tokens; with 2^24 keys each their tiles do not fit 32
+    bits, which the host cannot know, and the call ends without work."""
+    S, T, page, width = 1024, 512, 1024, 1 << 14
+    op = binding.PagedAttention(binding.make_attn_config(4, 1, 64, page))
+    k = torch.zeros(2, page, 1, 64, dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros(S, width, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, T] * (S // 2) + [0], dtype=torch.int32, device=DEV)
+    lens = torch.full((S,), keys, dtype=torch.int32, device=DEV)
+    q = torch.zeros(T, 4, 64, dtype=torch.bfloat16, device=DEV)
+    op(q, k, k, table, cu, lens)
+    assert op.device_status() == binding.ERR_DEVICE_CHECK
+    good = torch.arange(S + 1, dtype=torch.int32).clamp(max=T).to(DEV)
+    out = op(q, k, k, table, good, torch.full_like(lens, 100))
+    assert op.device_status() == binding.OK and (out == 0).all()
