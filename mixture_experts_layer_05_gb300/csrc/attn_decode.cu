@@ -178,11 +178,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     tma_prefetch(&maps.k);
     tma_prefetch(&maps.v);
   }
-  // the line of tiles is laid out in the ring before the first copy lands there
   AttnSpan span;
-  AttnWalk cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
-  fence_async_proxy();
+  AttnWalk cur;
+  const bool quick = quick_plan(a.b, sh);
+  if (!quick) {
+    // the line of tiles is laid out in the ring before the first copy lands there
+    cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
+    fence_async_proxy();
+  }
   __syncthreads();
+  if (quick && (warp == 0 || warp == kDecWarps)) cur = attn_plan_warp(a.b, sh, span);
   int* status = a.b.status;
 
   if (warp == kDecWarps) {

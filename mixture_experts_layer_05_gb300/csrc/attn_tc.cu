@@ -302,11 +302,16 @@ __global__ void __launch_bounds__(Tc<FP8, D>::kThreads, 1)
     tmem_relinquish();
   }
   AttnSpan span;
-  AttnWalk cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
-  fence_async_proxy();
+  AttnWalk cur;
+  const bool quick = quick_plan(a.b, sh);
+  if (!quick) {
+    cur = attn_plan(a.b, sh, reinterpret_cast<int*>(smem), wsum, span);
+    fence_async_proxy();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (quick && warp == kTcCopyWarp) cur = attn_plan_warp(a.b, sh, span);
   const uint32_t tmem = *tmem_slot;
   // a wait whose answer is the whole warp's (tcgen05 and warp barriers follow it)
   auto wait = [&](uint32_t bar, uint32_t parity) {

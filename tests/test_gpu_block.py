@@ -409,11 +409,12 @@ def test_bad_pages_and_lengths_are_reported(cuda_lib):
     assert op.device_status() == binding.ERR_DEVICE_CHECK
 
 
-@pytest.mark.parametrize("keys", [100, 1 << 24])
-def test_bounds_that_go_back_end_and_are_reported(cuda_lib, keys):
-    """512 sequences that each claim all 512 tokens; with 2^24 keys each their tiles do not fit 32
-    bits, which the host cannot know, and the call ends without work."""
-    S, T, page, width = 1024, 512, 1024, 1 << 14
+@pytest.mark.parametrize("S, T, keys", [(1024, 512, 100), (1024, 512, 1 << 24), (32, 128, 100),
+                                        (32, 128, 1 << 29)])
+def test_bounds_that_go_back_end_and_are_reported(cuda_lib, S, T, keys):
+    """Every other sequence claims all tokens; with so many keys each that their tiles do not fit
+    32 bits, which the host cannot know, the call ends without work."""
+    page, width = 1024, max(1, keys // 1024)
     op = binding.PagedAttention(binding.make_attn_config(4, 1, 64, page))
     k = torch.zeros(2, page, 1, 64, dtype=torch.bfloat16, device=DEV)
     table = torch.zeros(S, width, dtype=torch.int32, device=DEV)
