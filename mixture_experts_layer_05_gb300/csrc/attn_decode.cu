@@ -129,7 +129,9 @@ __device__ __noinline__ void land(uint32_t bar, uint32_t parity) {
     if (globaltimer_ns() - t0 > 10000000ull) return;
 }
 
-constexpr int kJoinAtOnce = 8;  // pieces of a cut unit whose loads are in flight together
+// Pieces of a cut unit whose loads are in flight together: one sequence of 200,000 keys and one kv
+// head, cut into 152, takes 34 us with 16 and 38 with 8.
+constexpr int kJoinAtOnce = 16;
 
 // A unit that a cut crosses: its rows (row r0 + r of a kv head of a sequence), and the CTAs that
 // hold its pieces.
