@@ -10,15 +10,23 @@
 
 namespace gbmoe {
 
-// Four e4m3 bytes of (a, b, c, d) * inv, a in the lowest byte. A product with the reciprocal of
-// the scale in place of a division each: the quotient is off by at most 1.5 units of fp32's last
-// place, which changes a code only where it lies that near to a border between two; the
-// divisions bound the norm's 8-bit output (76 us for 8192 x 7168 where HBM needs 27).
-__device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, float d, float inv) {
-  const __nv_fp8x2_storage_t lo =
-      __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
-  const __nv_fp8x2_storage_t hi =
-      __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
+// v / s from inv = 1 / s, for e4m3: the product, corrected by what it leaves of v (Newton's step for
+// the quotient), so that a value near the border of two codes falls where the quotient falls.
+// ANY: v may be far beyond 448 s or infinite; a product that saturates stays as it is.
+template <bool ANY>
+__device__ __forceinline__ float divided(float v, float s, float inv) {
+  const float q = v * inv;
+  return !ANY || fabsf(q) < 1024.f ? fmaf(fmaf(-q, s, v), inv, q) : q;
+}
+// Four e4m3 bytes of (a, b, c, d) / s, a in the lowest byte. Divisions proper bound the norm's
+// 8-bit output (76 us for 8192 x 7168 where HBM needs 27).
+template <bool ANY>
+__device__ __forceinline__ uint32_t e4m3x4_divided(float a, float b, float c, float d, float s,
+                                                   float inv) {
+  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+      make_float2(divided<ANY>(a, s, inv), divided<ANY>(b, s, inv)), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+      make_float2(divided<ANY>(c, s, inv), divided<ANY>(d, s, inv)), __NV_SATFINITE, __NV_E4M3);
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 

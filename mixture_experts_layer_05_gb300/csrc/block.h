@@ -62,6 +62,7 @@ struct KvAppendArgs {
   void* q_out;
   int hq, hkv, D;
   bool fp8;
+  float k_scale, v_scale;
   float k_inv, v_inv;    // 1 / scale
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);

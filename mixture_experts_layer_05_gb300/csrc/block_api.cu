@@ -99,8 +99,8 @@ GBMOE_API gbmoe_status_t moe_rms_norm(int32_t num_tokens, int32_t hidden_size,
   a.residual = args->residual;
   a.residual_stride = args->residual_stride;
   a.weight = args->weight;
-  a.eps = args->eps;
   a.inv_h = 1.f / (float)H;
+  a.eps = args->eps;
   a.y = args->y;
   a.residual_out = args->residual_out;
   a.q = args->q;
@@ -151,6 +151,8 @@ GBMOE_API gbmoe_status_t moe_kv_append(const gbmoe_attn_config_t* cfg, int32_t n
   a.hkv = cfg->num_kv_heads;
   a.D = cfg->head_dim;
   a.fp8 = cfg->cache_type == GBMOE_CACHE_E4M3;
+  a.k_scale = cfg->k_scale;
+  a.v_scale = cfg->v_scale;
   a.k_inv = 1.f / cfg->k_scale;
   a.v_inv = 1.f / cfg->v_scale;
   PdlChain chain;

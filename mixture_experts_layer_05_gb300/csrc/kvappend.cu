@@ -4,7 +4,7 @@
 // row p % page_size of page block_table[seq][p / page_size]. The first R columns of each q and
 // k head turn by the angle of p, pair by pair, (a, b) -> (a cos - b sin, b cos + a sin), in
 // fp32 from an fp32 table; q is rounded once to bf16, k and v once to the cache's type (e4m3:
-// from x times the reciprocal of the scale, saturating at 448).
+// of x / scale, saturating at 448).
 //
 // Bound by HBM. One CTA per token; a thread handles two vectors of eight columns at a time,
 // the two halves of eight pairs (half-split pairs) or sixteen neighbouring columns, and loads the
@@ -39,10 +39,10 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   u.w = pack_bf16x2(v[6], v[7]);
   *reinterpret_cast<uint4*>(p) = u;
 }
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&v)[8], float inv) {
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, const float (&v)[8], float s, float inv) {
   uint2 c;
-  c.x = e4m3x4_scaled(v[0], v[1], v[2], v[3], inv);
-  c.y = e4m3x4_scaled(v[4], v[5], v[6], v[7], inv);
+  c.x = e4m3x4_divided<true>(v[0], v[1], v[2], v[3], s, inv);
+  c.y = e4m3x4_divided<true>(v[4], v[5], v[6], v[7], s, inv);
   *reinterpret_cast<uint2*>(p) = c;
 }
 __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
@@ -141,9 +141,9 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) kv_append_kernel(
       const size_t at = row + (size_t)h * a.c.head_stride;
       if (FP8) {
         uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.c.k : a.c.v) + at;
-        const float inv = kind == 1 ? a.k_inv : a.v_inv;
-        store8_e4m3(dst + c0, x, inv);
-        store8_e4m3(dst + c1, y, inv);
+        const float s = kind == 1 ? a.k_scale : a.v_scale, inv = kind == 1 ? a.k_inv : a.v_inv;
+        store8_e4m3(dst + c0, x, s, inv);
+        store8_e4m3(dst + c1, y, s, inv);
       } else {
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(kind == 1 ? a.c.k : a.c.v) + at;
         store8(dst + c0, x);

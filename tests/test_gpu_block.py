@@ -209,6 +209,22 @@ def test_kv_append(cuda_lib, cache, hq, hkv, d, page, R, inter):
         assert torch.equal(got[name][~written].view(torch.uint8), before[~written].view(torch.uint8))
 
 
+def test_kv_append_of_huge_values(cuda_lib):
+    """Quotients that leave fp32 saturate; NaN stays NaN."""
+    op = binding.PagedAttention(binding.make_attn_config(1, 1, 64, 8, cache_dtype="fp8",
+                                                         k_scale=1e-3, v_scale=2.0))
+    x = torch.zeros(1, 1, 64)
+    x[0, 0, :6] = torch.tensor([3e38, -3e38, math.inf, -math.inf, math.nan, 0.25])
+    x = x.to(torch.bfloat16).to(DEV)
+    i = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    k, v = (torch.zeros(1, 8, 1, 64, device=DEV, dtype=torch.float8_e4m3fn) for _ in range(2))
+    op.append(x, x, x, k, v, i[:1].view(1, 1), i, i[1:])
+    for c, last in ((k, 256.0), (v, 0.125)):       # 250 rounds to 256
+        got = c[0, 0, 0, :6].float().cpu()
+        assert got[:4].tolist() == [448.0, -448.0, 448.0, -448.0]
+        assert got[4].isnan() and got[5] == last
+
+
 def test_kv_append_saturates_and_works_in_place(cuda_lib):
     p = Paged([(4, 4)], 1, 64, 8, "fp8", k_scale=1.0, v_scale=1.0)
     q = torch.full((4, 2, 64), 3.0, dtype=torch.bfloat16, device=DEV)
