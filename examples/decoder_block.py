@@ -133,8 +133,9 @@ def main(argv=None):
     print(f"prompts of {a.prompts} tokens: {timed(a.prompts):.0f} us (first call)")
     steps = [timed([1] * len(a.prompts)) for _ in range(a.steps)]
     print(f"one token each: {sorted(steps)[len(steps) // 2]:.0f} us (median of {a.steps} steps)")
-    print(f"a chunk of 64 for the first, one for the others: "
-          f"{timed([64] + [1] * (len(a.prompts) - 1)):.0f} us")
+    chunk = [64] + [1] * (len(a.prompts) - 1)
+    timed(chunk)                                   # the first loads its kernels
+    print(f"a chunk of 64 for the first, one for the others: {timed(chunk):.0f} us")
 
 
 if __name__ == "__main__":
