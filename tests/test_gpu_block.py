@@ -336,6 +336,19 @@ def test_paged_attention_packed_prompts(cuda_lib, hq, hkv, d, cache):
     _check(p, _rand(p.gen, p.T, hq, d, std=1.5), hq)
 
 
+MANY = {"prompts": [(700, 700), (1, 1)] * 2 + [(1, 9 + 30 * i) for i in range(40)] + [(1300, 1400)],
+        "steps": [(1 + i % 2, 5 + 7 * i % 400) for i in range(99)] + [(60, 200), (0, 4), (1, 0)],
+        "thousand": [(1, 3 + i % 140) for i in range(1100)] + [(300, 310), (1, 2)]}
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("what", list(MANY))
+def test_paged_attention_many_sequences(cuda_lib, what, cache):
+    """More sequences than one warp lays out, some of many row blocks, on either kernel."""
+    p = Paged(MANY[what], 2, 64, 16, cache, seed=len(what))
+    _check(p, _rand(p.gen, p.T, 8, 64), 8)
+
+
 def test_paged_attention_offsets_past_32_bits(cuda_lib):
     """Pages beyond 2^31 elements of the cache."""
     p = Paged([(1, 200), (150, 333)], 8, 128, 128, seed=2)
