@@ -14,7 +14,7 @@ size_t attn_scratch_bytes(int D) {
 bool attn_fits(const AttnArgs& a) {
   const double cap = (double)a.b.table_stride * (1 << a.b.page_shift);
   // units of 8 rows and the widest unit's extra cost: no launch has a longer line
-  return line_bound(attn_shape(a, 3, 6), a.b.T, a.b.S, cap) < 2147483647.0;
+  return line_bound(attn_shape<AttnShapeOf<5, 5>>(a, 3, 15), a.b.T, a.b.S, cap) < 2147483647.0;
 }
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {

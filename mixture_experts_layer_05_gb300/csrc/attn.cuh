@@ -70,7 +70,8 @@ constexpr int kPlanBlocks = 4;  // row blocks that one thread adds up by itself
 
 // The cursor `rem` into sequence s of sizes q, whose length on the line is `len`; a range of `left`
 // lies ahead. Whole warps call it.
-__device__ __forceinline__ void enter(const AttnShape& sh, const SeqInfo& q, int s, int rem,
+template <class Shape>
+__device__ __forceinline__ void enter(const Shape& sh, const SeqInfo& q, int s, int rem,
                                       int len, int left, AttnWalk& c) {
   const int lane = threadIdx.x & 31;
   const int head = len / sh.hkv;  // length of one head
@@ -109,7 +110,8 @@ __device__ __forceinline__ void enter(const AttnShape& sh, const SeqInfo& q, int
 // This CTA's cursor; every thread of the block calls it. line: shared memory for S + 1 prefix
 // sums, wsum: 32 more. A thread takes a sequence of few row blocks (single tokens), a warp one of
 // many: a prompt of 8191 tokens has 128, and one thread walking them cost 45 us.
-__device__ __forceinline__ AttnWalk attn_plan(const PagedBatch& b, const AttnShape& sh,
+template <class Shape>
+__device__ __forceinline__ AttnWalk attn_plan(const PagedBatch& b, const Shape& sh,
                                               int* line, int* wsum, AttnSpan& span) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int warps = nt >> 5;
@@ -182,7 +184,7 @@ __device__ __forceinline__ AttnWalk attn_plan(const PagedBatch& b, const AttnSha
   __syncthreads();
   const int W = line[b.S];
   span.W = W;
-  span.ctas = min(W, (int)gridDim.x);  // every one of these has some of the line
+  span.ctas = line_ctas(sh, W, gridDim.x);  // every one of these has some of the line
   if ((int)blockIdx.x < span.ctas) {
     const int a = range_at(W, blockIdx.x, span.ctas);
     span.end = range_at(W, blockIdx.x + 1, span.ctas);
@@ -204,7 +206,8 @@ __device__ __forceinline__ AttnWalk attn_plan(const PagedBatch& b, const AttnSha
 __device__ __forceinline__ bool quick_plan(const PagedBatch& b, const AttnShape& sh) {
   return b.S <= 32 && (long long)b.T * sh.G <= 1024ll << sh.br_shift;
 }
-__device__ __forceinline__ AttnWalk attn_plan_warp(const PagedBatch& b, const AttnShape& sh,
+template <class Shape>
+__device__ __forceinline__ AttnWalk attn_plan_warp(const PagedBatch& b, const Shape& sh,
                                                    AttnSpan& span) {
   const int lane = threadIdx.x & 31;
   AttnWalk c;
@@ -247,7 +250,7 @@ __device__ __forceinline__ AttnWalk attn_plan_warp(const PagedBatch& b, const At
   }
   const int W = __shfl_sync(0xffffffffu, inc, 31);
   span.W = W;
-  span.ctas = min(W, (int)gridDim.x);
+  span.ctas = line_ctas(sh, W, gridDim.x);
   if ((int)blockIdx.x < span.ctas) {
     const int a = range_at(W, blockIdx.x, span.ctas);
     span.end = range_at(W, blockIdx.x + 1, span.ctas);
@@ -262,7 +265,8 @@ __device__ __forceinline__ AttnWalk attn_plan_warp(const PagedBatch& b, const At
 
 // The next piece of the cursor's range, false when none is left; sequences without rows and
 // units of which the range holds only the extra cost are passed over.
-__device__ __forceinline__ bool next_piece(const PagedBatch& b, const AttnShape& sh,
+template <class Shape>
+__device__ __forceinline__ bool next_piece(const PagedBatch& b, const Shape& sh,
                                            AttnWalk& c, AttnPiece& p) {
 #pragma unroll 1
   while (c.left > 0) {
@@ -389,8 +393,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, AttnShape sh
 }
 
 // Shape of a launch whose units have 1 << br_shift rows.
-AttnShape attn_shape(const AttnArgs& a, int br_shift, int extra) {
-  AttnShape sh;
+template <class Shape = AttnShape>
+Shape attn_shape(const AttnArgs& a, int br_shift, int extra) {
+  Shape sh;
   set_group(sh, a.hq / a.hkv);
   sh.hkv = a.hkv;
   sh.br_shift = br_shift;

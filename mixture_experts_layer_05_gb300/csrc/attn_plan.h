@@ -20,9 +20,18 @@ struct AttnShape {
   uint32_t g_mul;  // r / G for 0 <= r < 2^31 is the high word of r * g_mul, shifted (G > 1)
   int g_shift;
   int br_shift;    // rows per unit: 1 << br_shift
-  int extra;       // cost of a unit beyond its tiles, in tiles
+  int extra;       // cost of a unit beyond its tiles
+  // cost of a tile, in units of up to half the rows and in the others
+  static constexpr int half = 1, full = 1;
   bool causal;
   int window;
+};
+
+// The same with other costs. Functions of the plan take either (a cost of 1 known at compile time
+// spares a division where pieces begin).
+template <int HALF, int FULL>
+struct AttnShapeOf : AttnShape {
+  static constexpr int half = HALF, full = FULL;
 };
 
 // g_mul = ceil(2^(31 + s) / G), s = ceil(log2 G): division by an invariant integer (Granlund and
@@ -47,17 +56,20 @@ struct UnitKeys {
   int i0, i1;      // first and last token of the unit
   int lo, hi;      // keys that any of them attends: [lo, hi), hi <= lo when none
   int t0, tiles;   // tiles t0 .. t0 + tiles - 1, tile t holding the keys from t * kAttnTK
+  int cost;        // of a tile, on the line
 };
 
 GBMOE_HD int unit_blocks(const AttnShape& a, int n) {
   return (n * a.G + (1 << a.br_shift) - 1) >> a.br_shift;
 }
 
-GBMOE_HD UnitKeys unit_keys(const AttnShape& a, const SeqInfo& q, int rb) {
+template <class Shape>
+GBMOE_HD UnitKeys unit_keys(const Shape& a, const SeqInfo& q, int rb) {
   UnitKeys u;
   const int r0 = rb << a.br_shift;
   int r1 = r0 + (1 << a.br_shift);
   if (r1 > q.n * a.G) r1 = q.n * a.G;
+  u.cost = 2 * (r1 - r0) > 1 << a.br_shift ? a.full : a.half;
   u.i0 = div_group(a, r0);
   u.i1 = div_group(a, r1 - 1);
   u.lo = key_range(q, u.i0, a.causal, a.window).lo;
@@ -74,15 +86,34 @@ GBMOE_HD UnitKeys unit_keys(const AttnShape& a, const SeqInfo& q, int rb) {
 }
 
 // Length on the line of a unit, and of one kv head of a sequence.
-GBMOE_HD int unit_length(const AttnShape& a, const SeqInfo& q, int rb) {
-  return unit_keys(a, q, rb).tiles + a.extra;
+template <class Shape>
+GBMOE_HD int unit_length(const Shape& a, const SeqInfo& q, int rb) {
+  const UnitKeys u = unit_keys(a, q, rb);
+  return u.tiles * u.cost + a.extra;
 }
-GBMOE_HD int seq_length(const AttnShape& a, const SeqInfo& q) {
+template <class Shape>
+GBMOE_HD int seq_length(const Shape& a, const SeqInfo& q) {
   const int blocks = unit_blocks(a, q.n);
   int t = 0;
   GBMOE_ROLLED
   for (int rb = 0; rb < blocks; ++rb) t += unit_length(a, q, rb);
   return t;
+}
+
+// The first tile that does not lie before the place `off` of a unit: a cut there ends one piece
+// before it and begins the next with it.
+template <class Shape>
+GBMOE_HD int tile_at(const Shape& a, const UnitKeys& u, int off) {
+  if (off <= a.extra) return 0;
+  return u.cost == 1 ? off - a.extra : (off - a.extra + u.cost - 1) / u.cost;
+}
+
+// CTAs that share a line of length W: each range holds the begin of at least one tile, so that
+// the pieces of a unit lie in neighbouring CTAs.
+template <class Shape>
+GBMOE_HD int line_ctas(const Shape& a, int W, int most) {
+  const int n = (W + a.full - 1) / a.full;
+  return n < most ? n : most;
 }
 
 // A place on the line of tiles.
@@ -92,7 +123,8 @@ struct AttnCursor {
 };
 
 // Moves the cursor `rem` further, over row blocks of the sequence q.
-GBMOE_HD void walk_blocks(const AttnShape& a, const SeqInfo& q, int rem, AttnCursor& c) {
+template <class Shape>
+GBMOE_HD void walk_blocks(const Shape& a, const SeqInfo& q, int rem, AttnCursor& c) {
   GBMOE_ROLLED
   for (;;) {
     const int t = unit_length(a, q, c.rb);
@@ -117,17 +149,18 @@ struct AttnPiece {
 // The piece of the sequence q = sequence c.s at the cursor, which moves past it (c.s may then
 // be a sequence without rows: the caller skips those). ta == tb: the range ends in the unit's
 // extra cost and holds none of its tiles.
-GBMOE_HD AttnPiece take_piece(const AttnShape& a, const SeqInfo& q, AttnCursor& c) {
+template <class Shape>
+GBMOE_HD AttnPiece take_piece(const Shape& a, const SeqInfo& q, AttnCursor& c) {
   AttnPiece p;
   p.s = c.s;
   p.head = c.head;
   p.rb = c.rb;
   p.q = q;
   p.u = unit_keys(a, q, c.rb);
-  const int len = p.u.tiles + a.extra;
+  const int len = p.u.tiles * p.u.cost + a.extra;
   const int end = len - c.off > c.left ? c.off + c.left : len;
-  p.ta = c.off > a.extra ? c.off - a.extra : 0;
-  p.tb = end > a.extra ? end - a.extra : 0;
+  p.ta = tile_at(a, p.u, c.off);
+  p.tb = tile_at(a, p.u, end);
   c.left -= end - c.off;
   c.off = end;
   if (end == len) {
@@ -148,8 +181,9 @@ GBMOE_HD int range_at(int W, int c, int g) { return W / g * c + W % g * c / g; }
 
 // An upper bound on the length of a line: T tokens in S sequences of at most `cap` keys. Calls
 // whose bound does not fit an int are refused.
-inline double line_bound(const AttnShape& a, double T, double S, double cap) {
-  return a.hkv * (T * a.G / (1 << a.br_shift) + S) * (cap / kAttnTK + 1 + a.extra);
+template <class Shape>
+inline double line_bound(const Shape& a, double T, double S, double cap) {
+  return a.hkv * (T * a.G / (1 << a.br_shift) + S) * ((cap / kAttnTK + 1) * a.full + a.extra);
 }
 
 }  // namespace gbmoe

@@ -240,11 +240,14 @@ PLAN = r"""
 #include <vector>
 #include "attn_plan.h"
 using namespace gbmoe;
+struct Shape : AttnShape {
+  int half, full;
+};
 int main() {
-  AttnShape a;
+  Shape a;
   int causal, g, S, G;
-  while (scanf("%d %d %d %d %d %d %d %d", &G, &a.hkv, &a.br_shift, &a.extra, &causal,
-               &a.window, &g, &S) == 8) {
+  while (scanf("%d %d %d %d %d %d %d %d %d %d", &G, &a.hkv, &a.br_shift, &a.extra, &a.half,
+               &a.full, &causal, &a.window, &g, &S) == 10) {
     a.causal = causal != 0;
     set_group(a, G);
     std::vector<SeqInfo> q(S);
@@ -255,6 +258,7 @@ int main() {
       q0 += q[s].n;
       line[s + 1] = line[s] + seq_length(a, q[s]) * a.hkv;
     }
+    g = line_ctas(a, line[S], g);
     for (int c = 0; c < g; ++c) {
       const int at = range_at(line[S], c, g), end = range_at(line[S], c + 1, g);
       if (end <= at) continue;
@@ -295,14 +299,14 @@ def test_attention_work_is_cut_whole(tmp_path):
         if not any(n for n, _ in seqs):
             seqs[0] = (1, 3)
         cases.append((rng.choice([1, 2, 3, 4, 7, 8, 20, 1024]), rng.choice([1, 2, 8]), rng.choice([4, 8]),
-                      rng.choice([0, 1, 3]), int(rng.random() < 0.8), rng.choice([0, 0, 1, 100, 1000]),
+                      rng.choice([0, 1, 3]), *rng.choice([(1, 1), (1, 2), (4, 5)]), int(rng.random() < 0.8), rng.choice([0, 0, 1, 100, 1000]),
                       rng.choice([1, 7, 148, 152]), S, seqs))
-    text = "\n".join(" ".join(map(str, c[:8])) + " " + " ".join(f"{n} {L}" for n, L in c[8])
+    text = "\n".join(" ".join(map(str, c[:10])) + " " + " ".join(f"{n} {L}" for n, L in c[10])
                      for c in cases)
     out = subprocess.run([str(tmp_path / "plan")], input=text, text=True, capture_output=True,
                          check=True).stdout.splitlines()
     assert len(out) == len(cases)
-    for (G, hkv, shift, extra, causal, window, g, S, seqs), line in zip(cases, out):
+    for (G, hkv, shift, extra, half, full, causal, window, g, S, seqs), line in zip(cases, out):
         BR, TK = 1 << shift, 128
         v = [int(x) for x in line.split()]
         pieces = [tuple(v[i:i + 8]) for i in range(0, len(v), 8)]
@@ -320,7 +324,10 @@ def test_attention_work_is_cut_whole(tmp_path):
                     lo, hi = min(k[0] for k in keys), max(k[1] for k in keys)
                     units[s, head, rb] = (lo // TK, -(-hi // TK)) if hi > lo else (0, 1)
         at, per, order = {}, {}, list(units)
-        total = sum(b - a + extra for a, b in units.values())
+        cost = {(s, h, rb): full if 2 * min(BR, seqs[s][0] * G - rb * BR) > BR else half
+                for s, h, rb in units}
+        total = sum((b - a) * cost[u] + extra for u, (a, b) in units.items())
+        g = min(g, -(-total // full))
         where = 0
         for c, s, head, rb, ta, tb, t0, tiles in pieces:
             u = (s, head, rb)
@@ -329,12 +336,16 @@ def test_attention_work_is_cut_whole(tmp_path):
             at[u] = tb
             while order[where] != u:               # the line's order
                 where += 1
-            per.setdefault(c, []).append((ta > 0, tb < tiles, tb - ta))
+            per.setdefault(c, []).append((ta > 0, tb < tiles, (tb - ta) * cost[u]))
         assert all(at[u] == b - a for u, (a, b) in units.items())
+        held = {}                                  # a cut unit's CTAs are neighbours
+        for c, s, head, rb, *_ in pieces:
+            held.setdefault((s, head, rb), []).append(c)
+        assert all(cs == list(range(cs[0], cs[-1] + 1)) for cs in held.values())
         for c, ps in per.items():
             begun = sum(not p[0] for p in ps)      # their extra cost lies in this range, but
             share = sum(p[2] for p in ps) + extra * begun      # for a cut through it at an end
-            assert total / g - 1 - extra < share < total / g + 1 + extra
+            assert total / g - full - extra < share < total / g + full + extra
             assert not any(p[0] for p in ps[1:]) and not any(p[1] for p in ps[:-1])
 
 
