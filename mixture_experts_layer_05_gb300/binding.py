@@ -509,7 +509,8 @@ def moe_rms_norm(x, weight, eps=1e-6, residual=None, out="bf16", y=None, residua
     """RMS norm of bf16 rows x [T, H] (+ residual) by weight [H]; out: "bf16" (y), "fp8" (q,
     scale: e4m3 codes and group-major fp32 scales [H / 128, T], the FP8 layer's input format)
     or "both". Rows of x and residual may be strided. Returns (y, residual_out, q, scale), None
-    for what was not asked for (residual_out: without a residual)."""
+    for what was not asked for (residual_out: without a residual). stream: a torch.cuda.Stream
+    (None: the current one); the inputs must be ready on it, and new outputs belong to it."""
     if out not in ("bf16", "fp8", "both"):
         raise ValueError(f"out must be bf16, fp8 or both, not {out!r}")
     return _block().rms_norm(x, weight, eps, residual, out != "fp8", out != "bf16", y,
@@ -523,7 +524,9 @@ class PagedAttention:
     float8_e4m3fn / uint8 codes) of equal strides, any order of pages, rows and heads;
     block_table [S, max_pages], cu_seqlens_q [S + 1] and kv_lens [S] int32 device tensors (see
     gbmoe_paged_kv_t). The workspace is the layer's own: calls on different streams must be
-    ordered, or use one object each.
+    ordered, or use one object each. stream: a torch.cuda.Stream (None: the current one); the
+    inputs must be ready on it, and new outputs belong to it, as if made under
+    torch.cuda.stream(stream).
     """
 
     def __init__(self, cfg: AttnConfig, device="cuda"):

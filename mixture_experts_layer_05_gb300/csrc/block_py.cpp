@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -44,13 +45,25 @@ void* address(PyObject* o) {
   return p;
 }
 
-// The stream argument, a torch.cuda.Stream; None: the current one of t's device.
-gbmoe_stream_t stream_of(const at::Tensor& t, PyObject* stream) {
-  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-  const Ref number(PyObject_GetAttrString(stream, "cuda_stream"));
-  if (!number.p) throw python_error();
-  return static_cast<gbmoe_stream_t>(address(number.p));
-}
+// The call's stream: the stream argument, a torch.cuda.Stream, or (None) the current one of t's
+// device. New outputs are allocated with it as the current stream: the allocator orders a block's
+// reuse by the stream it was allocated on, and on another one than the kernel's, work still queued
+// there could meet the kernel's writes in the same memory.
+struct CallStream {
+  gbmoe_stream_t handle;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  CallStream(const at::Tensor& t, PyObject* stream) {
+    const auto now = c10::cuda::getCurrentCUDAStream(t.get_device());
+    handle = now.stream();
+    if (stream == Py_None) return;
+    const Ref number(PyObject_GetAttrString(stream, "cuda_stream"));
+    if (!number.p) throw python_error();
+    handle = static_cast<gbmoe_stream_t>(address(number.p));
+    if (handle != now.stream())
+      guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle),
+                                                          t.device().index()));
+  }
+};
 
 // Row stride of a CUDA bf16 [T, cols] or [T, heads, dim] tensor with contiguous rows.
 int64_t row_stride(const at::Tensor& t, const char* name, int64_t T, int64_t cols) {
@@ -132,6 +145,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.weight = w.data_ptr();
   g.eps = (float)PyFloat_AsDouble(a[2]);
   if (PyErr_Occurred()) return nullptr;
+  const CallStream stream(x, a[10]);
   Out y, ro, q, scale;
   if (a[3] != Py_None) {
     const at::Tensor& r = tensor(a[3], "residual");
@@ -154,7 +168,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.residual_out = ro.ptr;
   g.q = static_cast<decltype(g.q)>(q.ptr);
   g.scale = static_cast<float*>(scale.ptr);
-  const int code = rms_norm_fn((int32_t)T, (int32_t)H, &g, stream_of(x, a[10]));
+  const int code = rms_norm_fn((int32_t)T, (int32_t)H, &g, stream.handle);
   if (code) return failed("moe_rms_norm", code);
   Ref r(PyTuple_New(4));
   if (!r.p) return nullptr;
@@ -224,6 +238,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.q_stride = row_stride(q, "q", T, hq * d);
   g.k_stride = row_stride(k, "k", T, hkv * d);
   g.v_stride = row_stride(v, "v", T, hkv * d);
+  const CallStream stream(q, a[13]);
   Out out(a[12], "q_out", q, {T, hq, d}, at::kBFloat16);
   if (a[10] != Py_None) {
     const at::Tensor& cs = tensor(a[10], "cos_sin");
@@ -237,7 +252,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.interleaved = PyObject_IsTrue(a[11]);
   g.q_out = out.ptr;
   g.workspace = address(a[1]);
-  const int code = kv_append_fn(&c, (int32_t)T, &p, &g, stream_of(q, a[13]));
+  const int code = kv_append_fn(&c, (int32_t)T, &p, &g, stream.handle);
   return code ? failed("moe_kv_append", code) : out.obj.take();
   END_HANDLE_TH_ERRORS
 }
@@ -255,6 +270,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(q.dim() > 0, "q must have rows");
   const int64_t T = q.size(0), hq = c.num_q_heads, d = c.head_dim;
   const int64_t stride = row_stride(q, "q", T, hq * d);
+  const CallStream stream(q, a[11]);
   Out out(a[9], "out", q, {T, hq, d}, at::kBFloat16);
   Out lse;
   if (a[10] != Py_None) {
@@ -263,7 +279,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!lse.obj.p) return nullptr;
   }
   const int code = attention_fn(&c, (int32_t)T, &p, q.data_ptr(), stride, out.ptr,
-                                static_cast<float*>(lse.ptr), address(a[1]), bytes, stream_of(q, a[11]));
+                                static_cast<float*>(lse.ptr), address(a[1]), bytes, stream.handle);
   if (code) return failed("moe_paged_attention", code);
   if (a[10] == Py_None) return out.obj.take();
   return PyTuple_Pack(2, out.obj.p, lse.obj.p);

@@ -455,3 +455,44 @@ def test_bounds_that_go_back_end_and_are_reported(cuda_lib, S, T, keys):
     good = torch.arange(S + 1, dtype=torch.int32).clamp(max=T).to(DEV)
     out = op(q, k, k, table, good, torch.full_like(lens, 100))
     assert op.device_status() == binding.OK and (out == 0).all()
+
+
+def _pool_of(t):
+    """The stream that the allocator orders the reuse of t's memory by."""
+    at = t.data_ptr()
+    return [s["stream"] for s in torch.cuda.memory_snapshot()
+            if s["address"] <= at < s["address"] + s["total_size"]]
+
+
+@pytest.mark.parametrize("explicit", [False, True])
+def test_new_outputs_belong_to_the_stream_that_writes_them(cuda_lib, explicit):
+    """An output made by a call on another stream than the current one comes from that stream's
+    memory: a block of the current stream's may still be in use by what is queued there."""
+    g = torch.Generator().manual_seed(21)
+    x, w = _rand(g, 5, 256).to(DEV), _rand(g, 256).to(DEV)
+    p = Paged([(1, 20), (4, 9)], 2, 64, 16, seed=3)
+    qkv = _rand(p.gen, p.T, 8, 64).to(DEV)
+    k, v = p.shaped(p.k).to(DEV), p.shaped(p.v).to(DEV)
+    kv = (k, v, p.table.to(DEV), p.cu.to(DEV), p.kv_lens.to(DEV))
+    op = binding.PagedAttention(binding.make_attn_config(4, 2, 64, 16))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    how = dict(stream=s) if explicit else {}
+    before = torch.cuda.current_stream()
+
+    def calls(how):
+        norm = binding.moe_rms_norm(x, w, residual=x, out="both", **how)
+        q = op.append(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], *kv, **how)
+        return [*norm, q, *op(qkv[:, :4], *kv, lse=True, **how)]
+
+    got = calls(how)
+    torch.cuda.synchronize()
+    want = (s if explicit else before).cuda_stream
+    assert all(_pool_of(t) == [want] for t in got)
+    assert torch.cuda.current_stream() == before
+    for a, b in zip(got, calls({})):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    given = torch.empty(p.T, 4, 64, dtype=torch.bfloat16, device=DEV)
+    assert op(qkv[:, :4], *kv, out=given, **how) is given
+    torch.cuda.synchronize()
+    assert torch.equal(given, got[5])
