@@ -510,7 +510,8 @@ def moe_rms_norm(x, weight, eps=1e-6, residual=None, out="bf16", y=None, residua
     scale: e4m3 codes and group-major fp32 scales [H / 128, T], the FP8 layer's input format)
     or "both". Rows of x and residual may be strided. Returns (y, residual_out, q, scale), None
     for what was not asked for (residual_out: without a residual). stream: a torch.cuda.Stream
-    (None: the current one); the inputs must be ready on it, and new outputs belong to it."""
+    (None: the current one); the inputs must be ready on it, and new outputs belong to it. All
+    tensors are on one device."""
     if out not in ("bf16", "fp8", "both"):
         raise ValueError(f"out must be bf16, fp8 or both, not {out!r}")
     return _block().rms_norm(x, weight, eps, residual, out != "fp8", out != "bf16", y,
@@ -523,10 +524,10 @@ class PagedAttention:
     The caches are [num_pages, page_size, num_kv_heads, head_dim] tensors (bf16, or
     float8_e4m3fn / uint8 codes) of equal strides, any order of pages, rows and heads;
     block_table [S, max_pages], cu_seqlens_q [S + 1] and kv_lens [S] int32 device tensors (see
-    gbmoe_paged_kv_t). The workspace is the layer's own: calls on different streams must be
-    ordered, or use one object each. stream: a torch.cuda.Stream (None: the current one); the
-    inputs must be ready on it, and new outputs belong to it, as if made under
-    torch.cuda.stream(stream).
+    gbmoe_paged_kv_t), all on the workspace's device. The workspace is the layer's own: calls on
+    different streams must be ordered, or use one object each. stream: a torch.cuda.Stream (None:
+    the current one); the inputs must be ready on it, and new outputs belong to it, as if made
+    under torch.cuda.stream(stream).
     """
 
     def __init__(self, cfg: AttnConfig, device="cuda"):
@@ -536,9 +537,7 @@ class PagedAttention:
             raise GbmoeError("moe_paged_attention_workspace_size", ERR_INVALID_ARG)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device)
         self.workspace[:1024].zero_()         # status word and counters
-        # addresses of what this object keeps alive
-        self._at = ctypes.addressof(cfg), self.workspace.data_ptr()
-        self._bytes = n
+        self._at = ctypes.addressof(cfg), self.workspace
 
     def append(self, q, k, v, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, cos_sin=None,
                interleaved=False, q_out=None, stream=None):
@@ -551,7 +550,7 @@ class PagedAttention:
                  lse=None, stream=None):
         """out [T, num_q_heads, head_dim] bf16 of the new tokens' q; with lse (True, or a fp32
         [T, num_q_heads] tensor) also the log-sum-exp of each row's scores: (out, lse)."""
-        return _block().attention(*self._at, self._bytes, q, k_cache, v_cache, block_table,
+        return _block().attention(*self._at, q, k_cache, v_cache, block_table,
                                   cu_seqlens_q, kv_lens, out, lse, stream)
 
     def device_status(self) -> int:

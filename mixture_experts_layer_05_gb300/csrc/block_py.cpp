@@ -49,10 +49,12 @@ void* address(PyObject* o) {
 // device. New outputs are allocated with it as the current stream: the allocator orders a block's
 // reuse by the stream it was allocated on, and on another one than the kernel's, work still queued
 // there could meet the kernel's writes in the same memory.
+// The kernels launch on the current device, so t's is made that one for the call.
 struct CallStream {
+  c10::cuda::CUDAGuard device;
   gbmoe_stream_t handle;
   c10::cuda::OptionalCUDAStreamGuard guard;
-  CallStream(const at::Tensor& t, PyObject* stream) {
+  CallStream(const at::Tensor& t, PyObject* stream) : device(t.device()) {
     const auto now = c10::cuda::getCurrentCUDAStream(t.get_device());
     handle = now.stream();
     if (stream == Py_None) return;
@@ -65,43 +67,71 @@ struct CallStream {
   }
 };
 
-// Row stride of a CUDA bf16 [T, cols] or [T, heads, dim] tensor with contiguous rows.
-int64_t row_stride(const at::Tensor& t, const char* name, int64_t T, int64_t cols) {
+// A kernel reads all its tensors from one device, `like`'s.
+void check_device(const at::Tensor& t, const char* name, const at::Tensor& like) {
+  TORCH_CHECK_VALUE(t.device() == like.device(), name, " is on ", t.device(),
+                    ", the call's other tensors are on ", like.device());
+}
+
+// Row stride of a bf16 [T, cols] or [T, heads, dim] tensor with contiguous rows, on like's CUDA
+// device.
+int64_t row_stride(const at::Tensor& t, const char* name, int64_t T, int64_t cols,
+                   const at::Tensor& like) {
   const int64_t d = t.dim();
   TORCH_CHECK_VALUE((d == 2 || d == 3) && t.is_cuda() && t.scalar_type() == at::kBFloat16 &&
                         t.size(0) == T && t.numel() == T * cols && t.stride(d - 1) == 1 &&
                         (d == 2 || t.stride(1) == t.size(2)),
                     name, " must be a CUDA bfloat16 tensor of ", T, " rows of ", cols,
                     " contiguous columns");
+  check_device(t, name, like);
   return T > 1 ? t.stride(0) : cols;
 }
 
-// The given output, checked, or a new contiguous tensor; a new reference.
-struct Out {
-  Ref obj;
-  void* ptr;
-  static PyObject* get(PyObject* given, const char* name, const at::Tensor& like,
-                       at::IntArrayRef shape, at::ScalarType dtype, void** ptr) {
+// An output: none until it is wanted; then the given tensor, checked, or (None) a new contiguous
+// one, which make() allocates. As all addresses it is taken once every argument has been checked.
+class Out {
+ public:
+  Out() : obj_(Py_NewRef(Py_None)) {}
+  void want(PyObject* given, const char* name, const at::Tensor& like, at::IntArrayRef shape,
+            at::ScalarType dtype) {
     if (given == Py_None) {
-      at::Tensor t = at::empty(shape, like.options().dtype(dtype));
-      *ptr = t.data_ptr();
-      return THPVariable_Wrap(std::move(t));
+      shape_ = shape;
+      dtype_ = dtype;
+      fresh_ = true;
+      return;
     }
     const at::Tensor& t = tensor(given, name);
     TORCH_CHECK_VALUE(t.is_cuda() && t.scalar_type() == dtype && t.is_contiguous() &&
                           t.sizes() == shape,
                       name, " must be a contiguous CUDA ", dtype, " tensor of shape ", shape);
-    *ptr = t.data_ptr();
+    check_device(t, name, like);
     Py_INCREF(given);
-    return given;
+    Py_SETREF(obj_.p, given);
   }
-  Out() : obj(Py_NewRef(Py_None)), ptr(nullptr) {}
-  Out(PyObject* given, const char* name, const at::Tensor& like, at::IntArrayRef shape,
-      at::ScalarType dtype)
-      : obj(nullptr), ptr(nullptr) {
-    obj.p = get(given, name, like, shape, dtype, &ptr);
-    if (!obj.p) throw python_error();
+  void make(const at::Tensor& like) {
+    if (!fresh_) {
+      if (obj_.p != Py_None) ptr_ = THPVariable_Unpack(obj_.p).data_ptr();
+      return;
+    }
+    at::Tensor t = at::empty(shape_, like.options().dtype(dtype_));
+    ptr_ = t.data_ptr();
+    PyObject* o = THPVariable_Wrap(std::move(t));
+    if (!o) throw python_error();
+    Py_SETREF(obj_.p, o);
   }
+  template <class T = void>
+  T* ptr() const {
+    return static_cast<T*>(ptr_);
+  }
+  PyObject* obj() const { return obj_.p; }
+  PyObject* take() { return obj_.take(); }
+
+ private:
+  Ref obj_;
+  void* ptr_ = nullptr;
+  bool fresh_ = false;
+  at::DimVector shape_;
+  at::ScalarType dtype_ = at::kFloat;
 };
 
 PyObject* failed(const char* fn, int code) {
@@ -137,51 +167,47 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(x.dim() == 2, "x must have two dimensions");
   const int64_t T = x.size(0), H = x.size(1);
   gbmoe_rms_norm_args_t g = {};
-  g.x = x.data_ptr();
-  g.x_stride = row_stride(x, "x", T, H);
+  g.x_stride = row_stride(x, "x", T, H, x);
   TORCH_CHECK_VALUE(w.is_cuda() && w.scalar_type() == at::kBFloat16 && w.dim() == 1 &&
                         w.size(0) == H && w.is_contiguous(),
                     "weight must be a contiguous CUDA bfloat16 tensor of H columns");
-  g.weight = w.data_ptr();
+  check_device(w, "weight", x);
   g.eps = (float)PyFloat_AsDouble(a[2]);
   if (PyErr_Occurred()) return nullptr;
-  const CallStream stream(x, a[10]);
   Out y, ro, q, scale;
   if (a[3] != Py_None) {
     const at::Tensor& r = tensor(a[3], "residual");
-    g.residual_stride = row_stride(r, "residual", T, H);
-    g.residual = r.data_ptr();
-    Py_SETREF(ro.obj.p, Out::get(a[7], "residual_out", x, {T, H}, at::kBFloat16, &ro.ptr));
-    if (!ro.obj.p) return nullptr;
+    g.residual_stride = row_stride(r, "residual", T, H, x);
+    ro.want(a[7], "residual_out", x, {T, H}, at::kBFloat16);
   }
-  if (a[4] == Py_True) {
-    Py_SETREF(y.obj.p, Out::get(a[6], "y", x, {T, H}, at::kBFloat16, &y.ptr));
-    if (!y.obj.p) return nullptr;
-  }
+  if (a[4] == Py_True) y.want(a[6], "y", x, {T, H}, at::kBFloat16);
   if (a[5] == Py_True) {
-    Py_SETREF(q.obj.p, Out::get(a[8], "q", x, {T, H}, at::kFloat8_e4m3fn, &q.ptr));
-    if (!q.obj.p) return nullptr;
-    Py_SETREF(scale.obj.p, Out::get(a[9], "scale", x, {H / 128, T}, at::kFloat, &scale.ptr));
-    if (!scale.obj.p) return nullptr;
+    q.want(a[8], "q", x, {T, H}, at::kFloat8_e4m3fn);
+    scale.want(a[9], "scale", x, {H / 128, T}, at::kFloat);
   }
-  g.y = y.ptr;
-  g.residual_out = ro.ptr;
-  g.q = static_cast<decltype(g.q)>(q.ptr);
-  g.scale = static_cast<float*>(scale.ptr);
+  const CallStream stream(x, a[10]);
+  for (Out* o : {&y, &ro, &q, &scale}) o->make(x);
+  g.x = x.data_ptr();
+  if (a[3] != Py_None) g.residual = THPVariable_Unpack(a[3]).data_ptr();
+  g.weight = w.data_ptr();
+  g.y = y.ptr();
+  g.residual_out = ro.ptr();
+  g.q = q.ptr<uint8_t>();
+  g.scale = scale.ptr<float>();
   const int code = rms_norm_fn((int32_t)T, (int32_t)H, &g, stream.handle);
   if (code) return failed("moe_rms_norm", code);
   Ref r(PyTuple_New(4));
   if (!r.p) return nullptr;
-  PyTuple_SET_ITEM(r.p, 0, y.obj.take());
-  PyTuple_SET_ITEM(r.p, 1, ro.obj.take());
-  PyTuple_SET_ITEM(r.p, 2, q.obj.take());
-  PyTuple_SET_ITEM(r.p, 3, scale.obj.take());
+  PyTuple_SET_ITEM(r.p, 0, y.take());
+  PyTuple_SET_ITEM(r.p, 1, ro.take());
+  PyTuple_SET_ITEM(r.p, 2, q.take());
+  PyTuple_SET_ITEM(r.p, 3, scale.take());
   return r.take();
   END_HANDLE_TH_ERRORS
 }
 
-// The paged batch from (k_cache, v_cache, block_table, cu_seqlens_q, kv_lens).
-gbmoe_paged_kv_t paged(const gbmoe_attn_config_t& c, PyObject* const* a) {
+// Checks of (k_cache, v_cache, block_table, cu_seqlens_q, kv_lens), which lie on ws's device.
+void check_paged(const gbmoe_attn_config_t& c, PyObject* const* a, const at::Tensor& ws) {
   const at::Tensor& k = tensor(a[0], "k_cache");
   const at::Tensor& v = tensor(a[1], "v_cache");
   const at::ScalarType t = k.scalar_type();
@@ -202,6 +228,18 @@ gbmoe_paged_kv_t paged(const gbmoe_attn_config_t& c, PyObject* const* a) {
   for (const at::Tensor* x : {&table, &cu, &lens})
     TORCH_CHECK_VALUE(x->scalar_type() == at::kInt && x->is_cuda() && x->is_contiguous(),
                       "block_table, cu_seqlens_q and kv_lens must be contiguous CUDA int32 tensors");
+  check_device(k, "k_cache", ws);
+  check_device(v, "v_cache", ws);
+  check_device(table, "block_table", ws);
+  check_device(cu, "cu_seqlens_q", ws);
+  check_device(lens, "kv_lens", ws);
+}
+
+// The paged batch of the same, checked before.
+gbmoe_paged_kv_t paged(PyObject* const* a) {
+  const at::Tensor &k = THPVariable_Unpack(a[0]), &v = THPVariable_Unpack(a[1]),
+                   &table = THPVariable_Unpack(a[2]), &cu = THPVariable_Unpack(a[3]),
+                   &lens = THPVariable_Unpack(a[4]);
   // the stride of a dimension of one element is never used: any valid number
   auto stride = [&](int d) { return k.size(d) > 1 ? k.stride(d) : k.size(3); };
   gbmoe_paged_kv_t p = {};
@@ -219,70 +257,74 @@ gbmoe_paged_kv_t paged(const gbmoe_attn_config_t& c, PyObject* const* a) {
   return p;
 }
 
-// kv_append(config address, workspace address, q, k, v, k_cache, v_cache, block_table,
+// kv_append(config address, workspace, q, k, v, k_cache, v_cache, block_table,
 //           cu_seqlens_q, kv_lens, cos_sin, interleaved, q_out, stream)
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (!arguments(n, 14)) return nullptr;
   const auto& c = *static_cast<const gbmoe_attn_config_t*>(address(a[0]));
-  const gbmoe_paged_kv_t p = paged(c, a + 5);
+  const at::Tensor& ws = tensor(a[1], "workspace");
+  check_paged(c, a + 5, ws);
   const at::Tensor& q = tensor(a[2], "q");
   const at::Tensor& k = tensor(a[3], "k");
   const at::Tensor& v = tensor(a[4], "v");
   TORCH_CHECK_VALUE(q.dim() > 0, "q must have rows");
   const int64_t T = q.size(0), hq = c.num_q_heads, hkv = c.num_kv_heads, d = c.head_dim;
   gbmoe_kv_append_args_t g = {};
-  g.q = q.data_ptr();
-  g.k = k.data_ptr();
-  g.v = v.data_ptr();
-  g.q_stride = row_stride(q, "q", T, hq * d);
-  g.k_stride = row_stride(k, "k", T, hkv * d);
-  g.v_stride = row_stride(v, "v", T, hkv * d);
-  const CallStream stream(q, a[13]);
-  Out out(a[12], "q_out", q, {T, hq, d}, at::kBFloat16);
+  g.q_stride = row_stride(q, "q", T, hq * d, ws);
+  g.k_stride = row_stride(k, "k", T, hkv * d, ws);
+  g.v_stride = row_stride(v, "v", T, hkv * d, ws);
   if (a[10] != Py_None) {
     const at::Tensor& cs = tensor(a[10], "cos_sin");
     TORCH_CHECK_VALUE(cs.is_cuda() && cs.scalar_type() == at::kFloat && cs.dim() == 2 &&
                           cs.is_contiguous(),
                       "cos_sin must be a contiguous CUDA float32 tensor [max_position, rotary_dim]");
-    g.cos_sin = cs.data_ptr<float>();
+    check_device(cs, "cos_sin", ws);
     g.max_position = (int32_t)cs.size(0);
     g.rotary_dim = (int32_t)cs.size(1);
   }
   g.interleaved = PyObject_IsTrue(a[11]);
-  g.q_out = out.ptr;
-  g.workspace = address(a[1]);
+  Out out;
+  out.want(a[12], "q_out", q, {T, hq, d}, at::kBFloat16);
+  const CallStream stream(q, a[13]);
+  out.make(q);
+  const gbmoe_paged_kv_t p = paged(a + 5);
+  g.q = q.data_ptr();
+  g.k = k.data_ptr();
+  g.v = v.data_ptr();
+  if (a[10] != Py_None) g.cos_sin = THPVariable_Unpack(a[10]).data_ptr<float>();
+  g.q_out = out.ptr();
+  g.workspace = ws.data_ptr();
   const int code = kv_append_fn(&c, (int32_t)T, &p, &g, stream.handle);
-  return code ? failed("moe_kv_append", code) : out.obj.take();
+  return code ? failed("moe_kv_append", code) : out.take();
   END_HANDLE_TH_ERRORS
 }
 
-// attention(config address, workspace address, workspace bytes, q, k_cache, v_cache, block_table,
-//           cu_seqlens_q, kv_lens, out, lse (None, True or a tensor), stream)
+// attention(config address, workspace, q, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, out,
+//           lse (None, True or a tensor), stream)
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!arguments(n, 12)) return nullptr;
+  if (!arguments(n, 11)) return nullptr;
   const auto& c = *static_cast<const gbmoe_attn_config_t*>(address(a[0]));
-  const size_t bytes = PyLong_AsSize_t(a[2]);
-  if (PyErr_Occurred()) return nullptr;
-  const gbmoe_paged_kv_t p = paged(c, a + 4);
-  const at::Tensor& q = tensor(a[3], "q");
+  const at::Tensor& ws = tensor(a[1], "workspace");
+  check_paged(c, a + 3, ws);
+  const at::Tensor& q = tensor(a[2], "q");
   TORCH_CHECK_VALUE(q.dim() > 0, "q must have rows");
   const int64_t T = q.size(0), hq = c.num_q_heads, d = c.head_dim;
-  const int64_t stride = row_stride(q, "q", T, hq * d);
-  const CallStream stream(q, a[11]);
-  Out out(a[9], "out", q, {T, hq, d}, at::kBFloat16);
-  Out lse;
-  if (a[10] != Py_None) {
-    Py_SETREF(lse.obj.p, Out::get(a[10] == Py_True ? Py_None : a[10], "lse", q, {T, hq}, at::kFloat,
-                                  &lse.ptr));
-    if (!lse.obj.p) return nullptr;
-  }
-  const int code = attention_fn(&c, (int32_t)T, &p, q.data_ptr(), stride, out.ptr,
-                                static_cast<float*>(lse.ptr), address(a[1]), bytes, stream.handle);
+  const int64_t stride = row_stride(q, "q", T, hq * d, ws);
+  Out out, lse;
+  out.want(a[8], "out", q, {T, hq, d}, at::kBFloat16);
+  if (a[9] != Py_None)
+    lse.want(a[9] == Py_True ? Py_None : a[9], "lse", q, {T, hq}, at::kFloat);
+  const CallStream stream(q, a[10]);
+  out.make(q);
+  lse.make(q);
+  const gbmoe_paged_kv_t p = paged(a + 3);
+  const int code = attention_fn(&c, (int32_t)T, &p, q.data_ptr(), stride, out.ptr(),
+                                lse.ptr<float>(), ws.data_ptr(), ws.nbytes(), stream.handle);
   if (code) return failed("moe_paged_attention", code);
-  if (a[10] == Py_None) return out.obj.take();
-  return PyTuple_Pack(2, out.obj.p, lse.obj.p);
+  if (a[9] == Py_None) return out.take();
+  return PyTuple_Pack(2, out.obj(), lse.obj());
   END_HANDLE_TH_ERRORS
 }
 

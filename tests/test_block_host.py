@@ -376,3 +376,40 @@ def test_division_by_the_group_is_exact(tmp_path):
                     "-o", str(tmp_path / "divide")], check=True)
     out = subprocess.run([str(tmp_path / "divide")], capture_output=True, text=True, check=True)
     assert out.stdout == "0"
+
+
+def _fake(*shape, dtype=torch.bfloat16, device="cuda:0"):
+    return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def test_binding_refuses_tensors_of_two_devices(lib):
+    """Every tensor of a call is on one device (fake tensors: the checks come before any address
+    is used)."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        norm = dict(x=_fake(4, 256), weight=_fake(256), residual=_fake(4, 256), out="both",
+                    y=_fake(4, 256), residual_out=_fake(4, 256),
+                    q=_fake(4, 256, dtype=torch.float8_e4m3fn),
+                    scale=_fake(2, 4, dtype=torch.float32))
+        for name in norm:
+            if name in ("x", "out"):
+                continue
+            with pytest.raises(ValueError, match=f"{name} is on cuda:1"):
+                binding.moe_rms_norm(**{**norm, name: norm[name].to("cuda:1")})
+        op = binding.PagedAttention(_cfg(), device="cuda:0")
+        i32 = dict(dtype=torch.int32)
+        kv = dict(k_cache=_fake(4, 16, 2, 64), v_cache=_fake(4, 16, 2, 64),
+                  block_table=_fake(1, 3, **i32), cu_seqlens_q=_fake(2, **i32),
+                  kv_lens=_fake(1, **i32))
+        attend = dict(kv, q=_fake(2, 8, 64), out=_fake(2, 8, 64),
+                      lse=_fake(2, 8, dtype=torch.float32))
+        append = dict(kv, q=_fake(2, 8, 64), k=_fake(2, 2, 64), v=_fake(2, 2, 64),
+                      cos_sin=_fake(9, 64, dtype=torch.float32), q_out=_fake(2, 8, 64))
+        for call, good in ((op, attend), (op.append, append)):
+            for name in good:
+                with pytest.raises(ValueError, match=f"{name} is on cuda:1"):
+                    call(**{**good, name: good[name].to("cuda:1")})
+        far = binding.PagedAttention(_cfg(), device="cuda:1")     # its workspace
+        for call, good in ((far, attend), (far.append, append)):
+            with pytest.raises(ValueError, match="is on cuda:0"):
+                call(**good)
