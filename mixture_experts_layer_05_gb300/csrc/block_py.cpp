@@ -284,6 +284,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.rotary_dim = (int32_t)cs.size(1);
   }
   g.interleaved = PyObject_IsTrue(a[11]);
+  if (g.interleaved < 0) return nullptr;
   Out out;
   out.want(a[12], "q_out", q, {T, hq, d}, at::kBFloat16);
   const CallStream stream(q, a[13]);

@@ -413,3 +413,18 @@ def test_binding_refuses_tensors_of_two_devices(lib):
         for call, good in ((far, attend), (far.append, append)):
             with pytest.raises(ValueError, match="is on cuda:0"):
                 call(**good)
+
+
+def test_a_flag_without_a_truth_value_raises(lib):
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    class Unclear:
+        def __bool__(self):
+            raise KeyError("unclear")
+    i32 = dict(dtype=torch.int32)
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        op = binding.PagedAttention(_cfg(), device="cuda:0")
+        with pytest.raises(KeyError, match="unclear"):
+            op.append(_fake(2, 8, 64), _fake(2, 2, 64), _fake(2, 2, 64), _fake(4, 16, 2, 64),
+                      _fake(4, 16, 2, 64), _fake(1, 3, **i32), _fake(2, **i32), _fake(1, **i32),
+                      interleaved=Unclear())
