@@ -67,6 +67,13 @@ struct CallStream {
   }
 };
 
+// A size as the C ABI's 32-bit number.
+int32_t size32(const at::Tensor& t, int d, const char* name) {
+  const int64_t n = t.size(d);
+  TORCH_CHECK_VALUE(n <= INT32_MAX, name, " has ", n, " in dimension ", d, ", more than 32 bits hold");
+  return (int32_t)n;
+}
+
 // A kernel reads all its tensors from one device, `like`'s.
 void check_device(const at::Tensor& t, const char* name, const at::Tensor& like) {
   TORCH_CHECK_VALUE(t.device() == like.device(), name, " is on ", t.device(),
@@ -165,7 +172,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& x = tensor(a[0], "x");
   const at::Tensor& w = tensor(a[1], "weight");
   TORCH_CHECK_VALUE(x.dim() == 2, "x must have two dimensions");
-  const int64_t T = x.size(0), H = x.size(1);
+  const int32_t T = size32(x, 0, "x"), H = size32(x, 1, "x");
   gbmoe_rms_norm_args_t g = {};
   g.x_stride = row_stride(x, "x", T, H, x);
   TORCH_CHECK_VALUE(w.is_cuda() && w.scalar_type() == at::kBFloat16 && w.dim() == 1 &&
@@ -194,7 +201,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.residual_out = ro.ptr();
   g.q = q.ptr<uint8_t>();
   g.scale = scale.ptr<float>();
-  const int code = rms_norm_fn((int32_t)T, (int32_t)H, &g, stream.handle);
+  const int code = rms_norm_fn(T, H, &g, stream.handle);
   if (code) return failed("moe_rms_norm", code);
   Ref r(PyTuple_New(4));
   if (!r.p) return nullptr;
@@ -228,6 +235,9 @@ void check_paged(const gbmoe_attn_config_t& c, PyObject* const* a, const at::Ten
   for (const at::Tensor* x : {&table, &cu, &lens})
     TORCH_CHECK_VALUE(x->scalar_type() == at::kInt && x->is_cuda() && x->is_contiguous(),
                       "block_table, cu_seqlens_q and kv_lens must be contiguous CUDA int32 tensors");
+  size32(k, 0, "k_cache");
+  size32(lens, 0, "kv_lens");
+  size32(table, 1, "block_table");
   check_device(k, "k_cache", ws);
   check_device(v, "v_cache", ws);
   check_device(table, "block_table", ws);
@@ -269,7 +279,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& k = tensor(a[3], "k");
   const at::Tensor& v = tensor(a[4], "v");
   TORCH_CHECK_VALUE(q.dim() > 0, "q must have rows");
-  const int64_t T = q.size(0), hq = c.num_q_heads, hkv = c.num_kv_heads, d = c.head_dim;
+  const int32_t T = size32(q, 0, "q");
+  const int64_t hq = c.num_q_heads, hkv = c.num_kv_heads, d = c.head_dim;
   gbmoe_kv_append_args_t g = {};
   g.q_stride = row_stride(q, "q", T, hq * d, ws);
   g.k_stride = row_stride(k, "k", T, hkv * d, ws);
@@ -280,8 +291,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           cs.is_contiguous(),
                       "cos_sin must be a contiguous CUDA float32 tensor [max_position, rotary_dim]");
     check_device(cs, "cos_sin", ws);
-    g.max_position = (int32_t)cs.size(0);
-    g.rotary_dim = (int32_t)cs.size(1);
+    g.max_position = size32(cs, 0, "cos_sin");
+    g.rotary_dim = size32(cs, 1, "cos_sin");
   }
   g.interleaved = PyObject_IsTrue(a[11]);
   if (g.interleaved < 0) return nullptr;
@@ -296,7 +307,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[10] != Py_None) g.cos_sin = THPVariable_Unpack(a[10]).data_ptr<float>();
   g.q_out = out.ptr();
   g.workspace = ws.data_ptr();
-  const int code = kv_append_fn(&c, (int32_t)T, &p, &g, stream.handle);
+  const int code = kv_append_fn(&c, T, &p, &g, stream.handle);
   return code ? failed("moe_kv_append", code) : out.take();
   END_HANDLE_TH_ERRORS
 }
@@ -311,7 +322,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check_paged(c, a + 3, ws);
   const at::Tensor& q = tensor(a[2], "q");
   TORCH_CHECK_VALUE(q.dim() > 0, "q must have rows");
-  const int64_t T = q.size(0), hq = c.num_q_heads, d = c.head_dim;
+  const int32_t T = size32(q, 0, "q");
+  const int64_t hq = c.num_q_heads, d = c.head_dim;
   const int64_t stride = row_stride(q, "q", T, hq * d, ws);
   Out out, lse;
   out.want(a[8], "out", q, {T, hq, d}, at::kBFloat16);
@@ -321,7 +333,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   out.make(q);
   lse.make(q);
   const gbmoe_paged_kv_t p = paged(a + 3);
-  const int code = attention_fn(&c, (int32_t)T, &p, q.data_ptr(), stride, out.ptr(),
+  const int code = attention_fn(&c, T, &p, q.data_ptr(), stride, out.ptr(),
                                 lse.ptr<float>(), ws.data_ptr(), ws.nbytes(), stream.handle);
   if (code) return failed("moe_paged_attention", code);
   if (a[9] == Py_None) return out.take();

@@ -428,3 +428,32 @@ def test_a_flag_without_a_truth_value_raises(lib):
             op.append(_fake(2, 8, 64), _fake(2, 2, 64), _fake(2, 2, 64), _fake(4, 16, 2, 64),
                       _fake(4, 16, 2, 64), _fake(1, 3, **i32), _fake(2, **i32), _fake(1, **i32),
                       interleaved=Unclear())
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """A size that the C ABI's 32 bits would cut to another one."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    far = 2 ** 32 + 4
+    i32 = dict(dtype=torch.int32)
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        with pytest.raises(ValueError, match="32 bits"):
+            binding.moe_rms_norm(_fake(far, 8), _fake(8))
+        with pytest.raises(ValueError, match="32 bits"):
+            binding.moe_rms_norm(_fake(4, far), _fake(far))
+        op = binding.PagedAttention(_cfg(), device="cuda:0")
+        good = dict(k_cache=_fake(4, 16, 2, 64), v_cache=_fake(4, 16, 2, 64),
+                    block_table=_fake(1, 3, **i32), cu_seqlens_q=_fake(2, **i32),
+                    kv_lens=_fake(1, **i32))
+        caches = dict(k_cache=_fake(far, 16, 2, 64), v_cache=_fake(far, 16, 2, 64))
+        many = dict(block_table=_fake(far, 1, **i32), cu_seqlens_q=_fake(far + 1, **i32),
+                    kv_lens=_fake(far, **i32))
+        for kv, T in ((good, far), ({**good, **caches}, 2), ({**good, **many}, 2),
+                      ({**good, "block_table": _fake(1, far, **i32)}, 2)):
+            with pytest.raises(ValueError, match="32 bits"):
+                op(_fake(T, 8, 64), **kv)
+            with pytest.raises(ValueError, match="32 bits"):
+                op.append(_fake(T, 8, 64), _fake(T, 2, 64), _fake(T, 2, 64), **kv)
+        q, k = _fake(2, 8, 64), _fake(2, 2, 64)
+        for shape in ((far, 16), (1, far)):
+            with pytest.raises(ValueError, match="32 bits"):
+                op.append(q, k, k, **good, cos_sin=_fake(*shape, dtype=torch.float32))
