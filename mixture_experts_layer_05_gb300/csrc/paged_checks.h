@@ -48,7 +48,8 @@ GBMOE_HD KeyRange key_range(const SeqInfo& q, int i, bool causal, int window) {
   const int pos = q.L - q.n + i;
   KeyRange r;
   r.hi = causal && pos + 1 < q.L ? pos + 1 : q.L;
-  r.lo = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
+  // compared before it is subtracted: pos may be below 0, window up to 2^31 - 1
+  r.lo = window > 0 && pos >= window ? pos - window + 1 : 0;
   return r;
 }
 

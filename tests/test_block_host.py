@@ -457,3 +457,16 @@ def test_sizes_past_32_bits_are_refused(lib):
         for shape in ((far, 16), (1, far)):
             with pytest.raises(ValueError, match="32 bits"):
                 op.append(q, k, k, **good, cos_sin=_fake(*shape, dtype=torch.float32))
+
+
+def test_key_ranges_of_the_widest_windows(checks):
+    """Tokens before position 0 (more new tokens than keys) and a window of up to 2^31 - 1: the
+    range does not leave 32 bits on its way."""
+    top = 2 ** 31 - 1
+    asks = [(L, n, i, causal, w) for L, n in ((0, 6), (1, 5), (3, 9), (100, 4000000), (2 ** 30, 1))
+            for i in (0, 1, n // 2, n - 1) for causal in (0, 1) for w in (top, top - 1, 2 ** 30)]
+    got = checks(["k " + " ".join(map(str, a)) for a in asks])
+    for (L, n, i, causal, w), (lo, hi) in zip(asks, got):
+        pos = L - n + i
+        want = max(0, pos - w + 1), min(L, pos + 1) if causal else L
+        assert (lo, hi) == want or (hi <= lo and want[1] <= want[0])

@@ -496,3 +496,12 @@ def test_new_outputs_belong_to_the_stream_that_writes_them(cuda_lib, explicit):
     assert op(qkv[:, :4], *kv, out=given, **how) is given
     torch.cuda.synchronize()
     assert torch.equal(given, got[5])
+
+
+@pytest.mark.parametrize("seqs", [[(3, 1), (1, 30)], [(9, 4), (1, 3), (40, 17)]],
+                         ids=["step", "mixed"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_paged_attention_widest_window(cuda_lib, seqs, causal):
+    """A window of 2^31 - 1 is none, for tokens before position 0 too."""
+    p = Paged(seqs, 2, 64, 16, seed=17)
+    _check(p, _rand(p.gen, p.T, 8, 64), 8, causal, 2 ** 31 - 1)
