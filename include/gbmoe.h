@@ -590,8 +590,10 @@ gbmoe_status_t moe_kv_append(const gbmoe_attn_config_t* cfg, int32_t num_tokens,
  * Workspace: moe_paged_attention_workspace_size(cfg) bytes (0: bad configuration), 256-byte
  * aligned, its first 1024 bytes zeroed once (and again after a GBMOE_ERR_TIMEOUT: beside the
  * status word they hold counters that every completed call leaves at zero). T = 0 is a no-op;
- * T * num_q_heads at most 2^30, and num_kv_heads * (T * group / 8 + num_seqs) * (positions of a
- * block table row / 128 + 5) below 2^31 (else UNSUPPORTED).
+ * T * num_q_heads at most 2^30. The work is counted in 32 bits (else UNSUPPORTED): with P the
+ * positions of a block table row (at most 2^30), one of these below 2^31 is enough,
+ *   num_kv_heads * (T * group / 8 + num_seqs) * (P / 128 + 5), or, when T * group > 16 * num_seqs,
+ *   num_kv_heads * (T * group / 256 + num_seqs) * (P / 128 + 5), five times that with heads of 64.
  */
 size_t moe_paged_attention_workspace_size(const gbmoe_attn_config_t* cfg);
 gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int32_t num_tokens,

@@ -688,17 +688,10 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   if (!make_cache_map(&maps.k, a.c.k, a) || !make_cache_map(&maps.v, a.c.v, a))
     return cudaErrorInvalidValue;
   const int ctas = num_sms() < kAttnMaxCtas ? num_sms() : kAttnMaxCtas;
-  // The cost of beginning a unit, in tiles. e4m3 tiles are short: 3 against 0 takes 256 sequences
-  // of about 1000 keys from 157 to 127 us, 5 of 47500 from 49.5 to 48.0. 64 columns: 64 sequences
-  // of 2000 keys 67.4, 63.7, 64.7 us at 0, 1, 2. bf16 rows of 256 bytes: the ring hides it (194.2
-  // against 200.5 us for 64 long sequences), but with fewer units than CTAs, where a CTA of two
-  // pieces ends last (12.4 against 10.9 us for 3 sequences). 16 rows: twice the work at either end
-  // of a piece and a shorter ring; 0, 2, 4, 6, 9: 131, 122, 119, 121, 125 us for 128 sequences of
-  // 2200 keys, 4 tokens each, in bf16, and 119, 123, 118, 117, 121 in e4m3.
   const bool few = (long long)a.b.S * a.hkv < ctas;
-  const int extra = NT == 2 ? (FP8 ? 6 : 4) : FP8 ? 3 : few ? 2 : D == 64 ? 1 : 0;
-  const AttnShape sh = attn_shape(a, NT == 1 ? 3 : 4, extra);
-  static_assert(T::kBR == 1 << (NT == 1 ? 3 : 4), "rows per unit");
+  constexpr int kShift = NT == 1 ? 3 : 4;
+  const AttnShape sh = attn_shape(a, kShift, unit_cost(kShift, D, FP8, few));
+  static_assert(T::kBR == 1 << kShift, "rows per unit");
   return launch_kernel(attn_decode_kernel<FP8, D, NT>, dim3(ctas), dim3(kDecThreads), T::kSmem,
                        stream, maps, a, sh);
 }

@@ -179,11 +179,54 @@ GBMOE_HD AttnPiece take_piece(const Shape& a, const SeqInfo& q, AttnCursor& c) {
 // CTA c of g takes the range [range_at(c), range_at(c + 1)) of a line of length W.
 GBMOE_HD int range_at(int W, int c, int g) { return W / g * c + W % g * c / g; }
 
-// An upper bound on the length of a line: T tokens in S sequences of at most `cap` keys. Calls
-// whose bound does not fit an int are refused.
-template <class Shape>
-inline double line_bound(const Shape& a, double T, double S, double cap) {
-  return a.hkv * (T * a.G / (1 << a.br_shift) + S) * ((cap / kAttnTK + 1) * a.full + a.extra);
+// The costs of the launches, whose units have 1 << br_shift rows: 8 or 16 (attn_decode.cu, a tile
+// costs 1) or 256 (attn_tc.cu).
+//
+// Heads of 64 on the tensor cores, a tile of a unit of one half and of two: a chunk of 400 tokens
+// among 18 single ones of 3500 keys takes 81, 75, 77, 87 us at 1:1, 4:5, 2:3, 1:2 (bf16), two
+// chunks 102, 100, 104, 118. Heads of 128: two chunks 123 us at 1:1, 130 at 4:5.
+template <int D>
+using AttnTcShape = AttnShapeOf<D == 64 ? 4 : 1, D == 64 ? 5 : 1>;
+constexpr int tile_cost(int br_shift, int D) { return br_shift == 8 && D == 64 ? 5 : 1; }
+// The cost of beginning a unit. Units of 256 rows: three tiles of two halves (2 and 4: up to 3 %
+// slower). Few rows, in tiles: e4m3 tiles are short, 3 against 0 takes 256 sequences
+// of about 1000 keys from 157 to 127 us, 5 of 47500 from 49.5 to 48.0. 64 columns: 64 sequences
+// of 2000 keys 67.4, 63.7, 64.7 us at 0, 1, 2. bf16 rows of 256 bytes: the ring hides it (194.2
+// against 200.5 us for 64 long sequences), but with fewer units than CTAs (`few`), where a CTA of
+// two pieces ends last (12.4 against 10.9 us for 3 sequences). 16 rows: twice the work at either
+// end of a piece and a shorter ring; 0, 2, 4, 6, 9: 131, 122, 119, 121, 125 us for 128 sequences of
+// 2200 keys, 4 tokens each, in bf16, and 119, 123, 118, 117, 121 in e4m3.
+constexpr int unit_cost(int br_shift, int D, bool fp8, bool few) {
+  return br_shift == 8   ? 3 * tile_cost(8, D)
+         : br_shift == 4 ? (fp8 ? 6 : 4)
+         : fp8           ? 3
+         : few           ? 2
+         : D == 64       ? 1
+                         : 0;
+}
+
+// An upper bound on the length of a launch's line: T tokens in S sequences of at most `cap` keys.
+inline double line_bound(int br_shift, int G, int hkv, int D, bool fp8, double T, double S,
+                         double cap) {
+  return hkv * (T * G / (1 << br_shift) + S) *
+         ((cap / kAttnTK + 1) * tile_cost(br_shift, D) + unit_cost(br_shift, D, fp8, true));
+}
+
+// log2 of the rows per unit that a batch runs in, 0 when no line fits an int. By the query rows
+// per sequence and kv head, on average (the lengths are on the device); any launch is right for
+// any batch. 32 sequences of 2200 keys, 8 kv heads of 4 query heads, 1, 4, 6 and 8 tokens each: 52,
+// 61, 125, 132 us in units of 8 and 16 rows, 60, 61, 61, 62 on the tensor cores (units of 256);
+// 5 sequences of 47500 keys and 16 query heads a kv head in e4m3 73 and 88. A line that is too
+// long in the units chosen may still fit in those of 8 rows, whose costs are the lowest (heads of
+// 64, block tables of 500,000 positions and more).
+inline int unit_shift(int G, int hkv, int D, bool fp8, int T, int S, double cap) {
+  const long long rows = (long long)T * G;
+  const int first = rows <= 8ll * S ? 3 : rows <= 16ll * S ? 4 : 8;
+  if (cap > 1 << 30) cap = 1 << 30;  // as checked_seq cuts lengths
+  auto fits = [&](int shift) {
+    return line_bound(shift, G, hkv, D, fp8, T, S, cap) < 2147483640.0;
+  };
+  return fits(first) ? first : fits(3) ? 3 : 0;
 }
 
 }  // namespace gbmoe

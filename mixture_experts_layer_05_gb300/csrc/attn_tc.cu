@@ -51,7 +51,6 @@ constexpr int kTcBR = 256;
 constexpr int kTcMmaWarp = 8, kTcCopyWarp = 9, kTcCvtWarp = 10, kTcCopyWarpV = 11;
 constexpr int kTcCvtWarps = 2;
 constexpr int kTcSplitShift = 6;  // pages below 1 << 6 rows: K's and V's copies by a warp each
-constexpr int kTcExtra = 3;      // cost of beginning a unit, in tiles of two halves (2 and 4: up to 3 % slower)
 
 template <bool FP8, int D>
 struct Tc {
@@ -75,10 +74,8 @@ struct Tc {
   static constexpr float kSlack = FP8 ? 14.f : 60.f;
   static constexpr uint32_t kRawPitch = D < 128 ? D : 128;  // bytes of a code row
   static constexpr uint32_t kRawSwz = kRawPitch == 128 ? 0x70u : 0x30u;
-  // What a tile costs in the split: of units of one half, and of two. Heads of 64, a chunk of 400
-  // tokens among 18 single ones of 3500 keys: 81, 75, 77, 87 us at 1:1, 4:5, 2:3, 1:2 (bf16), two
-  // chunks 102, 100, 104, 118. Heads of 128: two chunks 123 us at 1:1, 130 at 4:5.
-  using Shape = AttnShapeOf<kApart ? 4 : 1, kApart ? 5 : 1>;
+  using Shape = AttnTcShape<D>;
+  static_assert(Shape::full == tile_cost(8, D), "one cost");
   static constexpr int kReaders = 8 + 1 + 2;  // warps that read a piece: softmax, MMA, 10 and 11
   static constexpr size_t kSmem = 1024 + kQ + kStages * kTile + kRaw * kRawTile + kOut + 1024;
   static_assert(kSmem <= 232448, "shared memory per CTA exceeded");
@@ -954,7 +951,7 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   TcMaps maps;
   if (!make_cache_map(&maps.k, a.c.k, a) || !make_cache_map(&maps.v, a.c.v, a))
     return cudaErrorInvalidValue;
-  const auto sh = attn_shape<typename T::Shape>(a, 8, kTcExtra * T::Shape::full);
+  const auto sh = attn_shape<typename T::Shape>(a, 8, unit_cost(8, D, FP8, false));
   static_assert(kTcBR == 1 << 8, "rows per unit");
   const int ctas = num_sms() < kAttnMaxCtas ? num_sms() : kAttnMaxCtas;
   const cudaError_t e = launch_kernel(attn_tc_kernel<FP8, D>, dim3(ctas), dim3(T::kThreads),

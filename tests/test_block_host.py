@@ -470,3 +470,82 @@ def test_key_ranges_of_the_widest_windows(checks):
         pos = L - n + i
         want = max(0, pos - w + 1), min(L, pos + 1) if causal else L
         assert (lo, hi) == want or (hi <= lo and want[1] <= want[0])
+
+
+# heads, new tokens, sequences and positions of a block table row that attention takes
+WIDE_CALLS = ((32, 8, 128, 131072, 1, 131072), (64, 8, 128, 98304, 1, 98304),
+              (32, 8, 128, 16384, 1, 1 << 20), (32, 8, 128, 32768, 64, 1 << 20),
+              (64, 64, 64, 1700, 100, 62900 * 128), (32, 8, 64, 131072, 1, 131072),
+              (32, 8, 128, 1 << 20, 1, 1 << 20), (8, 8, 128, 1, 1, 1 << 40))
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls would run, on addresses of nothing")
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_paged_attention_takes_wide_calls(lib, cache):
+    """Calls below the documented limit get as far as the launch, which fails here."""
+    for hq, hkv, d, T, S, positions in WIDE_CALLS:
+        cfg = _cfg(num_q_heads=hq, num_kv_heads=hkv, head_dim=d, page_size=1024, cache_dtype=cache)
+        kv = _kv(num_seqs=S, block_table_stride=min(positions // 1024, 2 ** 31 - 1),
+                 page_stride=1 << 20)
+        assert _attn(lib, cfg=cfg, T=T, kv=kv, qs=hq * d) == binding.ERR_CUDA, (hq, d, T)
+
+
+UNITS = r"""
+#include <cstdio>
+#include "attn_plan.h"
+using namespace gbmoe;
+int main() {
+  int G, hkv, D, fp8, T, S;
+  double cap;
+  while (scanf("%d %d %d %d %d %d %lf", &G, &hkv, &D, &fp8, &T, &S, &cap) == 7) {
+    const int shift = unit_shift(G, hkv, D, fp8 != 0, T, S, cap);
+    printf("%d %d %d\n", shift, tile_cost(shift, D), unit_cost(shift, D, fp8 != 0, true));
+  }
+  return 0;
+}
+"""
+
+
+def test_units_fit_and_the_documented_limit_holds(tmp_path):
+    """No line of a chosen launch leaves 32 bits at any lengths, and what the header says is enough
+    is enough, on either side of each limit."""
+    (tmp_path / "units.cpp").write_text(UNITS)
+    subprocess.run(["g++", "-std=c++17", "-I", build_mod.CSRC, str(tmp_path / "units.cpp"), "-o",
+                    str(tmp_path / "units")], check=True)
+    rng = random.Random(11)
+    cases = [(hq // hkv, hkv, d, fp8, T, S, P) for hq, hkv, d, T, S, P in WIDE_CALLS
+             for fp8 in (0, 1)]
+    for _ in range(4000):
+        hkv = rng.choice([1, 2, 8, 64, 1024])
+        G = rng.choice([1, 2, 4, 8, 7, 1024 // hkv])
+        G = max(1, min(G, 1024 // hkv))
+        S = min(8192, int(2 ** rng.uniform(0, 13.01)))
+        T = min(1 << 22, (1 << 30) // (G * hkv), max(1, int(S * 2 ** rng.uniform(-2, 12))))
+        rows = T * G / S
+        # at a limit, or anywhere
+        units = hkv * (T * G / rng.choice([8, 256]) + S)
+        P = max(1, 128 * (2 ** 31 / units / rng.choice([1, 5]) + rng.choice([-5, -4, -3.9, -5.1])))
+        if rng.random() < 0.3 or rows > 1e6:
+            P = 2 ** rng.uniform(0, 34)
+        cases.append((G, hkv, rng.choice([64, 128]), rng.randint(0, 1), T, S, P))
+    out = subprocess.run([str(tmp_path / "units")], text=True, capture_output=True, check=True,
+                         input="\n".join(" ".join(map(str, c)) for c in cases)).stdout.split("\n")
+    taken, refused = set(), 0
+    for (G, hkv, d, fp8, T, S, P), line in zip(cases, out):
+        shift, tile, extra = (int(x) for x in line.split())
+        P = min(P, 2 ** 30)
+        few = hkv * (T * G / 8 + S) * (P / 128 + 5)
+        many = hkv * (T * G / 256 + S) * (P / 128 + 5) * (5 if d == 64 else 1)
+        enough = few < 2 ** 31 or (T * G > 16 * S and many < 2 ** 31)
+        assert shift in (3, 4, 8) if enough else shift in (0, 3, 4, 8)
+        refused += shift == 0
+        if not shift:
+            continue
+        taken.add((shift, T * G > 16 * S, d))
+        # rows spread to make the most units: one more than they fill for every sequence
+        units = hkv * (T * G // 2 ** shift + S)
+        assert units * (-(-int(P) // 128) * tile + extra) < 2 ** 31 - 8
+        if T * G <= 8 * S:
+            assert shift == 3
+    assert refused > 100 and {(8, True, 64), (8, True, 128), (3, True, 64), (4, False, 128)} <= taken
+    assert all(int(l.split()[0]) for l in out[:2 * len(WIDE_CALLS)])

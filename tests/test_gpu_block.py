@@ -505,3 +505,33 @@ def test_paged_attention_widest_window(cuda_lib, seqs, causal):
     """A window of 2^31 - 1 is none, for tokens before position 0 too."""
     p = Paged(seqs, 2, 64, 16, seed=17)
     _check(p, _rand(p.gen, p.T, 8, 64), 8, causal, 2 ** 31 - 1)
+
+
+def test_paged_attention_long_prompt(cuda_lib):
+    """One prompt of 131,072 tokens, whose line in units of 8 rows would not fit 32 bits; some of
+    its rows, each against a single token at its place."""
+    N, at = 1 << 17, [0, 300, 65535, 131071]
+    p = Paged([(N, N)], 1, 128, 64, seed=33, spare=0)
+    g = torch.Generator(device=DEV).manual_seed(34)
+    q = torch.randn(N, 32, 128, generator=g, device=DEV, dtype=torch.bfloat16)
+    out, lse = _run(p, q, 32)
+    p.seqs, p.rows = [(1, i + 1) for i in at], [p.rows[0][:i + 1] for i in at]
+    p.cu = torch.arange(len(at) + 1).int()
+    ref, rl, bound, lb = attention_reference(p, q[at].cpu())
+    assert ((out[at].cpu().double() - ref).abs() <= bound).all()
+    assert ((lse[at].cpu().double() - rl).abs() <= lb).all()
+
+
+def test_paged_attention_wide_block_tables(cuda_lib):
+    """Tables far wider than the sequences need: the same bits as with narrow ones. With heads of
+    64, 17 rows a sequence and 8,000,000 positions a table row the units of 256 rows do not fit 32
+    bits, and those of 8 rows run."""
+    p = Paged([(700, 900), (1, 40)], 2, 128, 64, seed=35)
+    q = _rand(p.gen, p.T, 8, 128).to(DEV)
+    want, wl = _run(p, q, 8)
+    p.table = torch.nn.functional.pad(p.table, (0, (1 << 14) - p.table.shape[1]), value=-1)
+    out, lse = _run(p, q, 8)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    p = Paged([(17, 17 + 3 * i) for i in range(100)], 64, 64, 64, seed=36)
+    p.table = torch.nn.functional.pad(p.table, (0, 62900 * 2 - p.table.shape[1]), value=-1)
+    _check(p, _rand(p.gen, p.T, 64, 64), 64)
