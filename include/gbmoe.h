@@ -581,7 +581,8 @@ gbmoe_status_t moe_kv_append(const gbmoe_attn_config_t* cfg, int32_t num_tokens,
  *   out = sum_j softmax_j(softmax_scale q . k_j) v_j, lse = log sum_j exp(softmax_scale q . k_j).
  * A token without keys has out = 0 and lse = -inf; a row of `out` in no sequence is unspecified.
  * Scores, the softmax's maximum and sum, and the output's sums are fp32; the weights are
- * rounded to 16 bits for their product with v. What pages hold past a sequence's length, or
+ * rounded for their product with v: to bf16 with a bf16 cache, to f16 with E4M3, where weights
+ * below 2^-32 of the row's largest are lost (N keys: at most N * 2^-32 of that weight). What pages hold past a sequence's length, or
  * outside every window of the call, is ignored whatever it is; v of the positions inside must be
  * finite even where a mask hides them from some of the tokens.
  *   q    [T, num_q_heads, head_dim] bf16, token stride q_stride (elements, a multiple of 8)

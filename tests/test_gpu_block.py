@@ -535,3 +535,43 @@ def test_paged_attention_wide_block_tables(cuda_lib):
     p = Paged([(17, 17 + 3 * i) for i in range(100)], 64, 64, 64, seed=36)
     p.table = torch.nn.functional.pad(p.table, (0, 62900 * 2 - p.table.shape[1]), value=-1)
     _check(p, _rand(p.gen, p.T, 64, 64), 64)
+
+
+@pytest.mark.parametrize("T", [1, 2, 40], ids=["units8", "units16", "units256"])
+@pytest.mark.parametrize("cache,d", [("fp8", 64), ("fp8", 128), ("bf16", 128)])
+@pytest.mark.parametrize("gap", [17.5, 15.5])
+@pytest.mark.parametrize("place,S", [(0, 1), (70000, 1), (150000, 1), (0, 160)])
+def test_paged_attention_keeps_the_tail_of_a_peaked_row(cuda_lib, T, cache, d, gap, place, S):
+    """One key lies `gap` nats above 150,000 others, whose v is 1: the columns where its own v is 0
+    hold the others' share of the weight, below 1 % of the sum. One sequence, cut over all SMs, or
+    160 on the same pages, most of them whole."""
+    N, page = 150001, 64
+    pages = -(-N // page)
+    dtype = torch.float8_e4m3fn if cache == "fp8" else torch.bfloat16
+    k = torch.zeros(pages * page, 1, d, device=DEV)
+    v = torch.ones(pages * page, 1, d, device=DEV)
+    k[place, 0, 0] = 16.0
+    v[place, 0, :d // 2] = 0
+    k, v = (x.to(dtype).view(pages, page, 1, d) for x in (k, v))
+    cfg = binding.make_attn_config(8, 1, d, page, cache_dtype=cache, causal=False,
+                                   softmax_scale=gap / 16)
+    op = binding.PagedAttention(cfg)
+    q = torch.zeros(S * T, 8, d, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 1
+    i32 = dict(dtype=torch.int32, device=DEV)
+    out = op(q, k, v, torch.arange(pages, **i32).repeat(S, 1), torch.arange(S + 1, **i32) * T,
+             torch.full((S,), N, **i32))
+    assert op.device_status() == binding.OK
+    tail = (N - 1) * math.exp(-cfg.softmax_scale * 16)
+    share = tail / (1 + tail)
+    # every weight of the tail is the same value, rounded the same way: bf16 by 2^-8 of itself; f16
+    # by 2^-11, or below its normal range by 2^-25 where the largest weight is 2^10 (2^7 in units of
+    # 256 rows) or more. The exponent (of at most 26, three roundings) and ex2 leave 2^-18, the fp32
+    # sums at most 2^-13 when a piece has fewer than 1100 keys and there are 152, 2^-10 when it has
+    # all, added 16 at a time. Then the output's rounding.
+    w = BF16 if cache == "bf16" else max(2.0 ** -11, 2.0 ** (-32 if T == 40 else -35) * math.exp(gap))
+    rel = w + (2.0 ** -13 if S == 1 else 2.0 ** -10) + 2.0 ** -18
+    tol = torch.tensor([share * (rel + BF16 * (1 + rel)), 2.0 ** -8 + rel]).to(DEV)
+    got = out.double()
+    assert ((got[..., :d // 2] - share).abs() <= tol[0]).all()
+    assert ((got[..., d // 2:] - 1).abs() <= tol[1]).all()
