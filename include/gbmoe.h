@@ -492,7 +492,7 @@ typedef enum { GBMOE_CACHE_BF16 = 0, GBMOE_CACHE_E4M3 = 1 } gbmoe_cache_type_t;
  *  causal                     !=0: a token attends no later position than its own
  *  window                     > 0: only the last `window` positions up to its own; 0 = all
  *  softmax_scale              multiplies q . k
- *  k_scale, v_scale           1 with a bf16 cache
+ *  k_scale, v_scale           1 with a bf16 cache; their reciprocals are finite
  */
 typedef struct {
   int32_t num_q_heads;

@@ -27,9 +27,10 @@ gbmoe_status_t check_attn(const gbmoe_attn_config_t* c) {
       c->num_q_heads % c->num_kv_heads || c->head_dim < 1 || c->page_size < 1 || c->window < 0 ||
       (c->cache_type != GBMOE_CACHE_BF16 && c->cache_type != GBMOE_CACHE_E4M3))
     return GBMOE_ERR_INVALID_ARG;
-  if (!std::isfinite(c->softmax_scale) || !(c->softmax_scale > 0.f) ||
-      !std::isfinite(c->k_scale) || !(c->k_scale > 0.f) || !std::isfinite(c->v_scale) ||
-      !(c->v_scale > 0.f))
+  // the append multiplies by 1 / scale
+  auto scales = [](float x) { return std::isfinite(x) && x > 0.f && std::isfinite(1.f / x); };
+  if (!std::isfinite(c->softmax_scale) || !(c->softmax_scale > 0.f) || !scales(c->k_scale) ||
+      !scales(c->v_scale))
     return GBMOE_ERR_INVALID_ARG;
   if (c->cache_type == GBMOE_CACHE_BF16 && (c->k_scale != 1.f || c->v_scale != 1.f))
     return GBMOE_ERR_INVALID_ARG;

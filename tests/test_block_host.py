@@ -549,3 +549,13 @@ def test_units_fit_and_the_documented_limit_holds(tmp_path):
             assert shift == 3
     assert refused > 100 and {(8, True, 64), (8, True, 128), (3, True, 64), (4, False, 128)} <= taken
     assert all(int(l.split()[0]) for l in out[:2 * len(WIDE_CALLS)])
+
+
+def test_cache_scales_have_a_finite_reciprocal(lib):
+    """1e-39 is a finite scale whose reciprocal is not: zeros would become NaN codes."""
+    for name in ("k_scale", "v_scale"):
+        cfg = _cfg(cache_dtype="fp8", **{name: 1e-39})
+        assert _append(lib, cfg=cfg) == BAD and _attn(lib, cfg=cfg) == BAD
+        assert lib.moe_paged_attention_workspace_size(ctypes.byref(cfg)) == 0
+        cfg = _cfg(cache_dtype="fp8", **{name: 3e-39})
+        assert lib.moe_paged_attention_workspace_size(ctypes.byref(cfg)) > 0
