@@ -1,6 +1,7 @@
-// Device side of paged attention's work split (attn_plan.h): every CTA finds its range of the
-// line of tiles, walks its pieces, and leaves the pieces of cut units in the workspace; a
-// second kernel joins those. Shared by the two attention kernels.
+// Device side of paged attention's work split (attn_plan.h), shared by the two attention kernels:
+// every CTA finds its range of the line of tiles, walks its pieces, and leaves the pieces of cut
+// units in the workspace. attn_decode.cu joins those itself; after attn_tc.cu's kernel, which
+// also leaves a record per CTA, attn_join_kernel does.
 #pragma once
 
 #include "attn_plan.h"
@@ -11,7 +12,7 @@ namespace gbmoe {
 
 constexpr int kAttnMaxBR = 256;    // rows per unit of the widest kernel
 
-// What a CTA's cut units look like, for the joining kernel: the unit that it begins and leaves
+// What a CTA's cut units look like, for attn_join_kernel: the unit that it begins and leaves
 // to the next CTA (starts), whether its first piece is of a unit begun before it (mid), and
 // whether that unit ends there.
 struct AttnRec {

@@ -704,6 +704,8 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   constexpr int kShift = NT == 1 ? 3 : 4;
   const AttnShape sh = attn_shape(a, kShift, unit_cost(kShift, D, FP8, few));
   static_assert(T::kBR == 1 << kShift, "rows per unit");
+  static_assert(AttnShape::half == 1 && AttnShape::full == 1,
+                "a cut unit's CTAs are counted as neighbours");
   return launch_kernel(attn_decode_kernel<FP8, D, NT>, dim3(ctas), dim3(kDecThreads), T::kSmem,
                        stream, maps, a, sh);
 }

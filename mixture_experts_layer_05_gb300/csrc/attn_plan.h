@@ -108,8 +108,11 @@ GBMOE_HD int tile_at(const Shape& a, const UnitKeys& u, int off) {
   return u.cost == 1 ? off - a.extra : (off - a.extra + u.cost - 1) / u.cost;
 }
 
-// CTAs that share a line of length W: each range holds the begin of at least one tile, so that
-// the pieces of a unit lie in neighbouring CTAs.
+// CTAs that share a line of length W, about a tile's cost each at least. Where a tile costs 1, a
+// range holds a tile, but for ranges within a unit's extra cost, which lies before its tiles: the
+// pieces of a unit are in neighbouring CTAs, one each, as attn_decode.cu counts them. With other
+// costs a range may also fall within a tile and hold nothing, so that a unit's pieces skip a CTA:
+// attn_join_kernel passes over those.
 template <class Shape>
 GBMOE_HD int line_ctas(const Shape& a, int W, int most) {
   const int n = (W + a.full - 1) / a.full;

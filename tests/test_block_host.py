@@ -559,3 +559,88 @@ def test_cache_scales_have_a_finite_reciprocal(lib):
         assert lib.moe_paged_attention_workspace_size(ctypes.byref(cfg)) == 0
         cfg = _cfg(cache_dtype="fp8", **{name: 3e-39})
         assert lib.moe_paged_attention_workspace_size(ctypes.byref(cfg)) > 0
+
+
+# rows per unit (log2), cost of a tile in units of half the rows and in the others, cost of a unit
+LAUNCHED = [(3, 1, 1, e) for e in (0, 1, 2, 3)] + [(4, 1, 1, 4), (4, 1, 1, 6), (8, 1, 1, 3),
+                                                   (8, 4, 5, 15)]
+
+
+def test_cut_units_join_in_the_launched_shapes(tmp_path):
+    """The costs that the kernels are launched with: every tile of a unit is computed once, in
+    order, and what joins a cut unit's pieces finds them all. Where a tile costs 1 they are in
+    neighbouring CTAs; else a CTA between two pieces may have none. Among the cases: ranges within
+    one unit's extra cost."""
+    (tmp_path / "plan.cpp").write_text(PLAN)
+    subprocess.run(["g++", "-std=c++17", "-I", build_mod.CSRC, str(tmp_path / "plan.cpp"), "-o",
+                    str(tmp_path / "plan")], check=True)
+    (tmp_path / "units.cpp").write_text(UNITS)
+    subprocess.run(["g++", "-std=c++17", "-I", build_mod.CSRC, str(tmp_path / "units.cpp"), "-o",
+                    str(tmp_path / "units")], check=True)
+    rng = random.Random(19)
+    cases = []
+    for shape in LAUNCHED:
+        for _ in range(150):
+            S = rng.choice([1, 1, 2, 5, 12, 40])
+            seqs = []
+            for _ in range(S):
+                n = rng.choice([0, 1, 1, 1, 2, 4, 17, 130])
+                seqs.append((n, max(0, rng.choice([n, n + 1, n - 2, n + 128, n + 700, n + 9000]))))
+            if not any(n for n, _ in seqs):
+                seqs[0] = (1, 3)
+            cases.append((shape, rng.choice([1, 2, 4, 7, 16]), rng.choice([1, 2, 8]),
+                          int(rng.random() < 0.8), rng.choice([0, 0, 1, 129, 1000]),
+                          rng.choice([2, 148, 152, 152, 152]), seqs))
+    for _ in range(300):       # units of one half and of two after each other: tiles of 4 and of 5
+        seqs = [(n, n + 128 * rng.randint(0, 40)) for n in rng.choices([100, 200], k=4)]
+        cases.append((LAUNCHED[-1], 1, 1, 0, 0, 152, seqs))
+    text = "\n".join(f"{G} {hkv} {sh} {extra} {half} {full} {causal} {window} {g} {len(seqs)} "
+                     + " ".join(f"{n} {L}" for n, L in seqs)
+                     for (sh, half, full, extra), G, hkv, causal, window, g, seqs in cases)
+    out = subprocess.run([str(tmp_path / "plan")], input=text, text=True, capture_output=True,
+                         check=True).stdout.splitlines()
+    assert len(out) == len(cases)
+    cut, skipped, idle = 0, 0, 0
+    for (shape, G, hkv, causal, window, g, seqs), line in zip(cases, out):
+        sh, half, full, extra = shape
+        v = [int(x) for x in line.split()]
+        pieces = [tuple(v[i:i + 8]) for i in range(0, len(v), 8)]   # c s head rb ta tb t0 tiles
+        units, of = {}, {}
+        for c, s, head, rb, ta, tb, t0, tiles in pieces:
+            units.setdefault((s, head, rb), []).append((c, ta, tb, tiles))
+            of.setdefault(c, []).append(((s, head, rb), ta > 0, tb < tiles))
+        want = {(s, h, rb) for s, (n, _) in enumerate(seqs) for h in range(hkv)
+                for rb in range(-(-n * G // 2 ** sh))}
+        assert set(units) == want
+        idle += max(of) + 1 - len(of)
+        for u, ps in units.items():
+            assert ps[0][1] == 0 and ps[-1][2] == ps[-1][3]
+            assert all(a[2] == b[1] and a[0] < b[0] for a, b in zip(ps, ps[1:]))
+            held = [p[0] for p in ps]
+            gaps = held != list(range(held[0], held[-1] + 1))
+            assert not (gaps and full == 1)
+            cut += len(ps) > 1
+            skipped += gaps
+        for c, ps in of.items():
+            # at most the first piece is of a unit begun before, and the last of one left behind
+            assert not any(p[1] for p in ps[1:]) and not any(p[2] for p in ps[:-1])
+            u, mid, leaves = ps[-1]
+            if not leaves or mid:
+                continue
+            # the joining kernel's rule: up to the first later CTA whose first piece ends a unit
+            # that was begun before it, whatever lies between with such a piece
+            rest, found = [], [c]
+            for d in sorted(x for x in of if x > c):
+                if of[d][0][1]:
+                    found.append(d)
+                    rest.append(of[d][0][0])
+                    if not of[d][0][2]:
+                        break
+            assert found == [p[0] for p in units[u]] and all(x == u for x in rest)
+    assert cut > 1000 and skipped > 0 and idle > 100
+    # these are the costs that the launches take
+    ask = [(1, 1, d, fp8, T, 16, 100.0) for d in (64, 128) for fp8 in (0, 1) for T in (16, 256, 4096)]
+    lines = subprocess.run([str(tmp_path / "units")], text=True, capture_output=True, check=True,
+                           input="\n".join(" ".join(map(str, a)) for a in ask)).stdout.splitlines()
+    shapes = {(sh, full, extra) for sh, _, full, extra in LAUNCHED}
+    assert {tuple(int(x) for x in line.split()) for line in lines} <= shapes
