@@ -575,3 +575,57 @@ def test_paged_attention_keeps_the_tail_of_a_peaked_row(cuda_lib, T, cache, d, g
     got = out.double()
     assert ((got[..., :d // 2] - share).abs() <= tol[0]).all()
     assert ((got[..., d // 2:] - 1).abs() <= tol[1]).all()
+
+
+DRAFTS = {"two": [(2, 2), (2, 127), (2, 128), (2, 129), (2, 700), (2, 1), (2, 0), (2, 1026)],
+          "four": [(4, 4), (4, 131), (4, 128), (4, 129), (4, 1300), (0, 7), (4, 2), (3, 400),
+                   (4, 257)]}
+
+
+@pytest.mark.parametrize("hq,hkv,what", [(16, 2, "two"), (8, 1, "two"), (8, 2, "four")])
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 130), (False, 0)])
+def test_paged_attention_drafts(cuda_lib, hq, hkv, what, cache, causal, window):
+    """Two to four tokens a sequence: units of 16 rows of heads of 128."""
+    seqs = DRAFTS[what]
+    ks, vs = (0.02, 0.5) if cache == "fp8" else (1.0, 1.0)
+    p = Paged(seqs, hkv, 128, 16, cache, seed=hq + window, k_scale=ks, v_scale=vs)
+    assert 8 * len(seqs) < p.T * (hq // hkv) <= 16 * len(seqs)
+    _check(p, _rand(p.gen, p.T, hq, 128, std=1.5), hq, causal, window)
+
+
+@pytest.mark.parametrize("page", [8, 256, 1024])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("seqs", [STEP, DRAFTS["four"], MIXED], ids=["step", "drafts", "mixed"])
+def test_paged_attention_page_sizes(cuda_lib, page, d, cache, seqs):
+    """The smallest pages (32 boxes a tile) and pages of several tiles, in all units."""
+    ks, vs = (0.02, 0.5) if cache == "fp8" else (1.0, 1.0)
+    p = Paged(seqs, 2, d, page, cache, seed=page + d, k_scale=ks, v_scale=vs)
+    _check(p, _rand(p.gen, p.T, 8, d, std=1.5), 8)
+
+
+@pytest.mark.parametrize("H", [128, 1000, 4096, 7168, 16384])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rms_norm_of_many_rows(cuda_lib, H, residual):
+    """More than two rows an SM (two vectors a thread), and one row fewer."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator().manual_seed(H)
+    out = "bf16" if H % 128 else "both"
+    for T in (2 * sms, 2 * sms + 1):
+        x, w = _rand(g, T, H), (1 + _rand(g, H, std=0.2)).to(torch.bfloat16)
+        r = _rand(g, T, H, std=3.0) if residual else None
+        h, y = norm_reference(x, r, w, 1e-6)
+        gy, gr, gq, gs = (None if t is None else t.cpu() for t in binding.moe_rms_norm(
+            x.to(DEV), w.to(DEV), 1e-6, out=out, residual=None if r is None else r.to(DEV)))
+        d = (0.5 * (32 + 10 + 2) + 6) * FP32       # as in test_rms_norm
+        assert ((gy.double() - y).abs() <= (BF16 * (1 + d) + d) * y.abs()).all()
+        if residual:
+            assert ((gr.double() - h).abs() <= (BF16 + 2 * FP32) * h.abs()).all()
+        if gq is not None:
+            s = (y.view(T, -1, 128).abs().amax(-1).clamp_min(1e-10) / 448).t()
+            assert ((gs.double() - s).abs() <= (d + 2 * FP32) * s).all()
+            step = gs.double().t().repeat_interleave(128, 1)
+            deq = gq.view(torch.float8_e4m3fn).double() * step
+            assert ((deq - y).abs() <= (FP8_HALF + 4 * d) * y.abs()
+                    + E4M3_SUB * (1 + d) * step).all()
