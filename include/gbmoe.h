@@ -451,8 +451,10 @@ gbmoe_status_t moe_selftest_bounded_wait(void* workspace, int32_t timeout_us,
  * bf16, as the FP8 layer's quantized input, or both:
  *   h = x + residual (fp32; h = x without one), residual_out = bf16(h)
  *   y = h / sqrt(mean(h^2) + eps) * weight (fp32), y_out = bf16(y)
- *   s = max(max |y|, 1e-10) / 448 over each 128 columns, q = e4m3fn(y * (1 / s)) (fp32, round
- *   to nearest even, saturating; from the fp32 y, not from its bf16 rounding)
+ *   s = max(max |y|, 1e-10) / 448 over each 128 columns, q = e4m3fn(y / s) (round to nearest
+ *   even, saturating; from the fp32 y, not from its bf16 rounding). The fp32 quotient is the
+ *   product with 1 / s, corrected once by what it leaves of y: where y / s lies within an fp32
+ *   rounding of the border between two codes, either may come out.
  *   x             [T, H] bf16, row t at x + t * x_stride (elements)
  *   residual      [T, H] bf16, row stride residual_stride; or NULL
  *   weight        [H] bf16
@@ -545,7 +547,8 @@ typedef struct {
  * The first `rotary_dim` columns of every q and k head turn pairwise,
  *   (a, b) -> (a cos - b sin, b cos + a sin),
  * pair i being columns (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved != 0; all in
- * fp32, rounded once (E4M3: code = e4m3fn(value * (1 / scale)), saturating at +-448).
+ * fp32, rounded once (E4M3: code = e4m3fn(value / scale), saturating at +-448, the quotient
+ * formed as moe_rms_norm's).
  *   q, k, v     [T, heads, head_dim] bf16, token strides q_stride, k_stride, v_stride (elements,
  *               multiples of 8; heads contiguous), so that one packed projection serves
  *   cos_sin     [max_position, rotary_dim] fp32: rotary_dim / 2 cosines, then as many sines; or
@@ -582,7 +585,9 @@ gbmoe_status_t moe_kv_append(const gbmoe_attn_config_t* cfg, int32_t num_tokens,
  * A token without keys has out = 0 and lse = -inf; a row of `out` in no sequence is unspecified.
  * Scores, the softmax's maximum and sum, and the output's sums are fp32; the weights are
  * rounded for their product with v: to bf16 with a bf16 cache, to f16 with E4M3, where weights
- * below 2^-32 of the row's largest are lost (N keys: at most N * 2^-32 of that weight). What pages hold past a sequence's length, or
+ * below 2^-32 of the row's largest are lost (N keys: at most N * 2^-32 of that weight). With E4M3
+ * q is rounded to f16 before its product with k: exact from 2^-14 to 65504 in magnitude, with
+ * fewer bits below, saturating at +-65504 above. What pages hold past a sequence's length, or
  * outside every window of the call, is ignored whatever it is; v of the positions inside must be
  * finite even where a mask hides them from some of the tokens.
  *   q    [T, num_q_heads, head_dim] bf16, token stride q_stride (elements, a multiple of 8)

@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (FP8) mn[n][e] = mn[n][e] > m[n][e] + T::kMost ? lowered(mn[n][e], T::kLift) : m[n][e];
+              if (FP8)
+                mn[n][e] = mn[n][e] > m[n][e] + T::kMost ? lowered(mn[n][e], T::kLift) : m[n][e];
               const float f = mn[n][e] > m[n][e] ? ex2(m[n][e] - mn[n][e]) : 1.f;
               m[n][e] = mn[n][e];
               l[n][e] *= f;

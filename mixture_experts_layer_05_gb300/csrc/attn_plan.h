@@ -192,13 +192,13 @@ template <int D>
 using AttnTcShape = AttnShapeOf<D == 64 ? 4 : 1, D == 64 ? 5 : 1>;
 constexpr int tile_cost(int br_shift, int D) { return br_shift == 8 && D == 64 ? 5 : 1; }
 // The cost of beginning a unit. Units of 256 rows: three tiles of two halves (2 and 4: up to 3 %
-// slower). Few rows, in tiles: e4m3 tiles are short, 3 against 0 takes 256 sequences
-// of about 1000 keys from 157 to 127 us, 5 of 47500 from 49.5 to 48.0. 64 columns: 64 sequences
-// of 2000 keys 67.4, 63.7, 64.7 us at 0, 1, 2. bf16 rows of 256 bytes: the ring hides it (194.2
+// slower). Few rows, in tiles: e4m3 tiles are short, 3 against 0 takes 256 sequences of about 1000
+// keys from 157 to 127 us, 5 of 47500 from 49.5 to 48.0. 64 columns: 64 sequences of 2000 keys and
+// 8 kv heads 67.4, 63.7, 64.7 us at 0, 1, 2. bf16 rows of 256 bytes: the ring hides it (194.2
 // against 200.5 us for 64 long sequences), but with fewer units than CTAs (`few`), where a CTA of
 // two pieces ends last (12.4 against 10.9 us for 3 sequences). 16 rows: twice the work at either
 // end of a piece and a shorter ring; 0, 2, 4, 6, 9: 131, 122, 119, 121, 125 us for 128 sequences of
-// 2200 keys, 4 tokens each, in bf16, and 119, 123, 118, 117, 121 in e4m3.
+// 2200 keys, 16 + 4 heads, 4 tokens each, in bf16, and 119, 123, 118, 117, 121 in e4m3.
 constexpr int unit_cost(int br_shift, int D, bool fp8, bool few) {
   return br_shift == 8   ? 3 * tile_cost(8, D)
          : br_shift == 4 ? (fp8 ? 6 : 4)

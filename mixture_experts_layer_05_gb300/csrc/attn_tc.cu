@@ -36,9 +36,10 @@
 //
 // Bound by the tensor cores: a tile of both halves is 2048 cycles of products (heads of 128), and
 // a long prompt's steady step takes 2550 to 2700; the products alone, without a softmax, 2360.
-// 8191 causal tokens of 32 + 8 heads: 346 us, 1590 TFLOP/s (0.84 of the measured bf16 rate).
-// Heads of 64: 550 us, bound by the softmax, whose work does not halve with the products (626 with
-// P over the scores, as for 128). e4m3: 365 us, bound by the two warps that turn codes to f16.
+// 8191 causal tokens of 32 + 8 heads: 347 us, 1585 TFLOP/s (0.83 of the measured bf16 rate).
+// 64 + 8 heads of 64: 552 us, bound by the softmax, whose work does not halve with the products
+// (626 with P over the scores, as for 128). e4m3 (32 + 8 heads of 128): 364 us, bound by the two
+// warps that turn codes to f16.
 // Beginning a piece costs about 2 us (drain of the last O, first scores), which packed prompts
 // feel: 5955 tokens of 5 sequences 85 us, 896 TFLOP/s. Two issuing threads, one per half, took
 // 459 us for the long prompt: the halves' products then alternate on the tensor core and none

@@ -6,11 +6,14 @@
 // fp32 from an fp32 table; q is rounded once to bf16, k and v once to the cache's type (e4m3:
 // of x / scale, saturating at 448).
 //
-// Bound by HBM. One CTA per token; a thread handles two vectors of eight columns at a time,
+// One CTA per token; a thread handles two vectors of eight columns at a time,
 // the two halves of eight pairs (half-split pairs) or sixteen neighbouring columns, and loads the
 // next two before it stores these; the first are loaded before the token's sequence and page are
-// known. 5,867 tokens of 32 + 2 x 8 heads of 128 into an e4m3 cache (134 MB) take 26.4 us, 5.1
-// TB/s, 32 tokens 3.5 (4.1 when the lookups come first). Six CTAs of 192 threads on an SM: with
+// known. 5,867 tokens of 32 + 2 x 8 heads of 128 into an e4m3 cache (134 MB) take 27.4 us, 4.9
+// TB/s, and 27.4 into a bf16 cache (146 MB); 32 tokens 3.5 (4.1 when the lookups come first). HBM
+// would need 20 of the 27.4 us, and with half of the writes still in L2 it carries 3.3 TB/s at 49 %
+// of the warps active: a CTA's loads of bounds, length, page and angles follow one another, before
+// two rounds of work, in six to seven waves of CTAs. Six CTAs of 192 threads on an SM: with
 // eight the registers spill (34 us), three of 384 take 33, and several tokens a CTA with their
 // lookups side by side 46.
 #include "block.cuh"
