@@ -537,6 +537,10 @@ class PagedAttention:
             raise GbmoeError("moe_paged_attention_workspace_size", ERR_INVALID_ARG)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device)
         self.workspace[:1024].zero_()         # status word and counters
+        # the first call may be on any stream; within a capture the graph orders it
+        if (self.workspace.is_cuda and torch.cuda.is_initialized()
+                and not torch.cuda.is_current_stream_capturing()):
+            torch.cuda.current_stream(self.workspace.device).synchronize()
         self._at = ctypes.addressof(cfg), self.workspace
 
     def append(self, q, k, v, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, cos_sin=None,

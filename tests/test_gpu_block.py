@@ -629,3 +629,27 @@ def test_rms_norm_of_many_rows(cuda_lib, H, residual):
             deq = gq.view(torch.float8_e4m3fn).double() * step
             assert ((deq - y).abs() <= (FP8_HALF + 4 * d) * y.abs()
                     + E4M3_SUB * (1 + d) * step).all()
+
+
+def test_a_new_layer_serves_any_stream(cuda_lib):
+    """The workspace is ready when PagedAttention returns: a first call on a stream that does not
+    wait for the current one, which is busy, counts from zero."""
+    p = Paged([(1, 30000), (1, 12)], 2, 64, 16, seed=41)
+    q = _rand(p.gen, p.T, 8, 64).to(DEV)
+    want, _ = _run(p, q, 8)
+    args = (p.shaped(p.k).to(DEV), p.shaped(p.v).to(DEV), p.table.to(DEV), p.cu.to(DEV),
+            p.kv_lens.to(DEV))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for fill in (0x00, 0x01, 0xFF):
+        junk = torch.full((1 << 26,), fill, dtype=torch.uint8, device=DEV)   # what blocks held before
+        torch.cuda.synchronize()
+        del junk
+        busy = torch.cuda.Event()
+        torch.cuda._sleep(100_000_000)             # some 50 ms
+        busy.record()
+        op = binding.PagedAttention(binding.make_attn_config(8, 2, 64, 16))
+        assert busy.query()                        # the zeros queued behind it are written
+        out = op(q, *args, stream=s)
+        s.synchronize()
+        assert torch.equal(out, want) and op.device_status() == binding.OK
