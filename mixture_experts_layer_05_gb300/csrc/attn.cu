@@ -1,4 +1,4 @@
-// Paged attention: which kernel a batch runs on.
+// Paged attention: launches the kernel of the units that a batch runs in (unit_shift).
 #include "attn.cuh"
 #include "kernels.h"
 
