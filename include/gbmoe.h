@@ -607,6 +607,73 @@ gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int32_t num_t
                                    void* out, float* lse, void* workspace,
                                    size_t workspace_bytes, gbmoe_stream_t stream);
 
+/*
+ * ---- The products around the layer: dense projections and experts' products by themselves.
+ *
+ * moe_linear: a matrix product with its epilogue,
+ *   z = x @ weight^T + bias                                (fp32 sums)
+ *   a = act(z); SILU_MUL: a = silu(z[:, :out_features / 2]) * z[:, out_features / 2:]
+ *   out = bf16(a * row_weight[t] + residual)               (fp32, rounded once)
+ * moe_grouped_linear: the same where row t of run g, offsets[g] <= t < offsets[g + 1], meets
+ * weight[g] and bias[g]: the experts' products over rows that lie sorted by expert already.
+ *   x             [T, in_features] bf16, or e4m3fn bytes with weight_quant FP8_BLOCK128; row t at
+ *                 x + t * x_stride (elements)
+ *   x_scale       FP8_BLOCK128: [in_features / 128, T] fp32, group-major, as moe_rms_norm and
+ *                 moe_quant_fp8_per_token_group write it; else NULL
+ *   weight        [out_features, in_features] (grouped: [num_groups, out_features, in_features])
+ *                 contiguous, of x's type
+ *   weight_scale  FP8_BLOCK128: [ceil(out_features / 128), in_features / 128] fp32 per group
+ *                 (w = q * scale[n / 128][k / 128]); else NULL
+ *   bias          [out_features] bf16 (grouped: [num_groups, out_features]) or NULL
+ *   activation    gbmoe_epilogue_t. SILU_MUL takes the rows of `weight` (and the bias) as gate
+ *                 [0, out_features / 2) and up behind it, as w13 lies, and has out_features / 2
+ *                 output columns
+ *   residual      [T, output columns] bf16, row stride residual_stride; or NULL
+ *   row_weight    [T] fp32 or NULL (1)
+ *   out           [T, output columns] bf16 (out), row stride out_stride; may be the residual's own
+ *                 memory (the same stride), must not overlap anything else that the call reads
+ *   offsets       [num_groups + 1] int32, ascending, device memory that the kernel reads: a captured
+ *                 graph replays with its current contents. Empty runs are allowed; rows before
+ *                 offsets[0] and from offsets[num_groups] on are left as they are.
+ *   workspace     256 bytes, 256-byte aligned: the status word; or NULL (unreported)
+ * in_features: a multiple of 8 (FP8_BLOCK128: of 128). out_features: any; with SILU_MUL a multiple
+ * of 32 (FP8_BLOCK128: of 256). Else UNSUPPORTED, as are NVFP4, more than 1024 groups, more
+ * than 2^31 - 1 rows of all weights together, and calls of 2^31 output tiles (of 128 columns by 16
+ * rows) or more. x 16-byte aligned, x_stride a multiple of 16 bytes; weight 16-byte aligned; the
+ * others aligned to their elements. A run that is negative or outside [0, T] sets
+ * GBMOE_ERR_DEVICE_CHECK and has no rows. A NaN or an infinity in a row of x reaches that row
+ * alone, in a row of weight that column alone (SILU_MUL: its pair's). T = 0 is a no-op.
+ */
+typedef enum {
+  GBMOE_EPI_NONE = 0,
+  GBMOE_EPI_RELU = 1,
+  GBMOE_EPI_SILU = 2,
+  GBMOE_EPI_GELU = 3,       /* z * (1 + erf(z / sqrt 2)) / 2 */
+  GBMOE_EPI_GELU_TANH = 4,  /* z * (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  GBMOE_EPI_SILU_MUL = 5
+} gbmoe_epilogue_t;
+typedef struct {
+  const void* x;
+  int64_t x_stride;
+  const float* x_scale;
+  const void* weight;
+  const float* weight_scale;
+  const void* bias;
+  int32_t activation;
+  int32_t weight_quant;  /* gbmoe_weight_quant_t */
+  const void* residual;
+  int64_t residual_stride;
+  const float* row_weight;
+  void* out;
+  int64_t out_stride;
+  void* workspace;
+} gbmoe_linear_args_t;
+gbmoe_status_t moe_linear(int32_t num_tokens, int32_t in_features, int32_t out_features,
+                          const gbmoe_linear_args_t* args, gbmoe_stream_t stream);
+gbmoe_status_t moe_grouped_linear(int32_t num_tokens, int32_t num_groups, int32_t in_features,
+                                  int32_t out_features, const int32_t* offsets,
+                                  const gbmoe_linear_args_t* args, gbmoe_stream_t stream);
+
 /* Library version, (major << 16) | minor. */
 int32_t gbmoe_version(void);
 

@@ -24,6 +24,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_CHECK,
 SCORE = {"softmax": 0, "sigmoid": 1}
 QUANT = {None: 0, "none": 0, "fp8": 1, "fp8_block128": 1, "nvfp4": 2}
 CACHE = {"bf16": 0, "fp8": 1, "e4m3": 1}
+EPILOGUE = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "silu_mul": 5}
 NUM_STAGE_EVENTS = 5
 
 # every entry point declared in include/gbmoe.h
@@ -36,7 +37,7 @@ EXPORTS = ("moe_topk", "moe_align_block_size_workspace_size", "moe_align_block_s
            "moe_router_logits", "moe_quant_fp8_per_token_group", "moe_quant_nvfp4",
            "moe_nvfp4_prepared_bytes", "moe_nvfp4_prepare_weight", "moe_rms_norm",
            "moe_forward_q", "moe_kv_append", "moe_paged_attention_workspace_size", "moe_paged_attention",
-           "gbmoe_version")
+           "moe_linear", "moe_grouped_linear", "gbmoe_version")
 
 
 class GbmoeError(RuntimeError):
@@ -122,6 +123,17 @@ class KvAppendArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p)]
 
 
+class LinearArgs(ctypes.Structure):
+    """gbmoe_linear_args_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("x_scale", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("weight_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("activation", ctypes.c_int32), ("weight_quant", ctypes.c_int32),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("row_weight", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p)]
+
+
 def make_config(num_experts, top_k, hidden_size, intermediate_size, renormalize=True,
                 use_grouped_topk=False, num_expert_group=0, topk_group=0,
                 scoring_func="softmax", routed_scaling_factor=1.0, activation=0,
@@ -198,6 +210,8 @@ def load() -> ctypes.CDLL:
         "moe_paged_attention_workspace_size": (SZ, [ctypes.POINTER(AttnConfig)]),
         "moe_paged_attention": (I32, [ctypes.POINTER(AttnConfig), I32, ctypes.POINTER(PagedKv),
                                       P, ctypes.c_int64, P, P, P, SZ, P]),
+        "moe_linear": (I32, [I32, I32, I32, ctypes.POINTER(LinearArgs), P]),
+        "moe_grouped_linear": (I32, [I32, I32, I32, I32, P, ctypes.POINTER(LinearArgs), P]),
         "gbmoe_version": (I32, []),
     }
     for name, (res, args) in sig.items():
@@ -499,7 +513,8 @@ def _block():
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
         ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                   (lib.moe_rms_norm, lib.moe_kv_append, lib.moe_paged_attention)), GbmoeError)
+                   (lib.moe_rms_norm, lib.moe_kv_append, lib.moe_paged_attention,
+                    lib.moe_linear, lib.moe_grouped_linear)), GbmoeError)
         _ext = ext
     return _ext
 
@@ -516,6 +531,38 @@ def moe_rms_norm(x, weight, eps=1e-6, residual=None, out="bf16", y=None, residua
         raise ValueError(f"out must be bf16, fp8 or both, not {out!r}")
     return _block().rms_norm(x, weight, eps, residual, out != "fp8", out != "bf16", y,
                              residual_out, q, scale, stream)
+
+
+def _epilogue(activation):
+    if activation not in EPILOGUE:
+        raise ValueError(f"activation must be one of {[k for k in EPILOGUE if k]}, not {activation!r}")
+    return EPILOGUE[activation]
+
+
+def moe_linear(x, weight, bias=None, activation="none", residual=None, row_weight=None,
+               x_scale=None, weight_scale=None, out=None, workspace=None, stream=None):
+    """out [T, N] bf16 = act(x @ weight^T + bias) * row_weight + residual, of bf16 x [T, K] and
+    weight [N, K], or of e4m3 codes with x_scale [K / 128, T] (as moe_rms_norm writes them) and
+    weight_scale [ceil(N / 128), K / 128]. activation: "none", "relu", "silu", "gelu",
+    "gelu_tanh", or "silu_mul" (weight rows gate | up, N / 2 output columns). bias [N] and
+    residual [T, columns] bf16, row_weight [T] fp32. Rows of x, residual and out may be strided;
+    out may be the residual. workspace: see alloc_workspace, for device checks that
+    moe_get_device_status reports. stream: a torch.cuda.Stream (None: the current one); the inputs
+    must be ready on it, and a new output belongs to it. All tensors are on one device."""
+    return _block().linear(x, weight, None, bias, _epilogue(activation), residual, row_weight,
+                           x_scale, weight_scale, out, workspace, stream)
+
+
+def moe_grouped_linear(x, weight, offsets, bias=None, activation="none", residual=None,
+                       row_weight=None, x_scale=None, weight_scale=None, out=None, workspace=None,
+                       stream=None):
+    """moe_linear per run of rows: rows [offsets[g], offsets[g + 1]) of x [T, K] meet weight[g] of
+    [G, N, K] and bias[g] of [G, N]; offsets [G + 1] int32 on the device, ascending. weight_scale
+    [G, ceil(N / 128), K / 128]. Rows of no run are left as they are (of a new out: unspecified)."""
+    if offsets is None:
+        raise ValueError("offsets must be a tensor")
+    return _block().linear(x, weight, offsets, bias, _epilogue(activation), residual, row_weight,
+                           x_scale, weight_scale, out, workspace, stream)
 
 
 class PagedAttention:

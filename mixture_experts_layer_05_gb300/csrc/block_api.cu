@@ -1,10 +1,11 @@
 // C ABI of the decoder-block operators around the layer: host-side checks, then one launch
-// sequence each (norm.cu, kvappend.cu, attn.cu).
+// sequence each (norm.cu, kvappend.cu, attn.cu, linear.cu).
 #include <climits>
 #include <cmath>
 
 #include "block.h"
 #include "kernels.h"
+#include "linear.h"
 
 #define GBMOE_API extern "C" __attribute__((visibility("default")))
 
@@ -71,6 +72,57 @@ PagedBatch batch_of(const gbmoe_attn_config_t& c, const gbmoe_paged_kv_t& kv, in
 
 PagedCache cache_of(const gbmoe_paged_kv_t& kv) {
   return PagedCache{kv.k_cache, kv.v_cache, kv.page_stride, kv.token_stride, kv.head_stride};
+}
+
+// moe_linear (offsets NULL, one group) and moe_grouped_linear.
+gbmoe_status_t linear(int T, int G, int K, int N, const int32_t* offsets, bool grouped,
+                      const gbmoe_linear_args_t* g, gbmoe_stream_t stream) {
+  if (T < 0 || T > kMaxRows || G < 1 || K < 1 || N < 1) return GBMOE_ERR_INVALID_ARG;
+  if (T == 0) return GBMOE_OK;
+  if (!g || !g->x || !g->weight || !g->out || (grouped && !offsets)) return GBMOE_ERR_INVALID_ARG;
+  if (g->activation < GBMOE_EPI_NONE || g->activation > GBMOE_EPI_SILU_MUL ||
+      g->weight_quant < GBMOE_QUANT_NONE || g->weight_quant > GBMOE_QUANT_NVFP4)
+    return GBMOE_ERR_INVALID_ARG;
+  if (g->weight_quant == GBMOE_QUANT_NVFP4) return GBMOE_ERR_UNSUPPORTED;
+  const bool fp8 = g->weight_quant == GBMOE_QUANT_FP8_BLOCK128;
+  const bool gated = g->activation == GBMOE_EPI_SILU_MUL;
+  if (fp8 != (g->x_scale != nullptr) || fp8 != (g->weight_scale != nullptr))
+    return GBMOE_ERR_INVALID_ARG;
+  if (K % (fp8 ? kFp8Block : 8) || (gated && N % (fp8 ? 2 * kFp8Block : 32)) ||
+      G > kLinearMaxGroups || (int64_t)G * N > INT32_MAX)
+    return GBMOE_ERR_UNSUPPORTED;
+  // tiles of 128 columns by 16 rows are the smallest that any kernel counts
+  if (((int64_t)T / 16 + G) * ((N + 127) / 128) > INT32_MAX) return GBMOE_ERR_UNSUPPORTED;
+  const int cols = gated ? N / 2 : N;
+  if (g->x_stride < K || g->x_stride % (fp8 ? 16 : 8) || g->out_stride < cols ||
+      (g->residual && g->residual_stride < cols) || !aligned(g->x, 16) || !aligned(g->weight, 16) ||
+      !aligned(g->x_scale, 4) || !aligned(g->weight_scale, 4) || !aligned(g->bias, 2) ||
+      !aligned(g->residual, 2) || !aligned(g->row_weight, 4) || !aligned(g->out, 2) ||
+      !aligned(offsets, 4) || !aligned(g->workspace, kStatusBytes))
+    return GBMOE_ERR_INVALID_ARG;
+  LinearArgs a;
+  a.x = g->x;
+  a.x_stride = g->x_stride;
+  a.x_scale = g->x_scale;
+  a.weight = g->weight;
+  a.w_scale = g->weight_scale;
+  a.bias = g->bias;
+  a.residual = g->residual;
+  a.residual_stride = g->residual_stride;
+  a.row_weight = g->row_weight;
+  a.out = g->out;
+  a.out_stride = g->out_stride;
+  a.offsets = grouped ? offsets : nullptr;
+  a.T = T;
+  a.G = G;
+  a.K = K;
+  a.N = N;
+  a.cols = cols;
+  a.act = g->activation;
+  a.fp8 = fp8;
+  a.status = static_cast<int*>(g->workspace);
+  PdlChain chain;
+  return cuda_status(launch_linear(a, (cudaStream_t)stream));
 }
 
 }  // namespace
@@ -203,4 +255,17 @@ GBMOE_API gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int
   if (!attn_fits(a)) return GBMOE_ERR_UNSUPPORTED;
   PdlChain chain;
   return cuda_status(launch_attn(a, (cudaStream_t)stream));
+}
+
+GBMOE_API gbmoe_status_t moe_linear(int32_t num_tokens, int32_t in_features, int32_t out_features,
+                                    const gbmoe_linear_args_t* args, gbmoe_stream_t stream) {
+  return linear(num_tokens, 1, in_features, out_features, nullptr, false, args, stream);
+}
+
+GBMOE_API gbmoe_status_t moe_grouped_linear(int32_t num_tokens, int32_t num_groups,
+                                            int32_t in_features, int32_t out_features,
+                                            const int32_t* offsets,
+                                            const gbmoe_linear_args_t* args,
+                                            gbmoe_stream_t stream) {
+  return linear(num_tokens, num_groups, in_features, out_features, offsets, true, args, stream);
 }

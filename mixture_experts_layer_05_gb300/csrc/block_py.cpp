@@ -1,5 +1,6 @@
-// Argument marshalling of moe_rms_norm, moe_kv_append and moe_paged_attention for torch tensors:
-// the checks, the outputs and the argument structs of binding.py's entry points, compiled. A
+// Argument marshalling of moe_rms_norm, moe_kv_append, moe_paged_attention, moe_linear and
+// moe_grouped_linear for torch tensors: the checks, the outputs and the argument structs of
+// binding.py's entry points, compiled. A
 // decode step calls these with a few microseconds of GPU work each, and the same checks through
 // ctypes took 10 to 16 us a call. The library is reached through the addresses that bind() is
 // given, so this module does not depend on where libgbmoe.so lies.
@@ -19,6 +20,8 @@ namespace {
 decltype(&moe_rms_norm) rms_norm_fn;
 decltype(&moe_kv_append) kv_append_fn;
 decltype(&moe_paged_attention) attention_fn;
+decltype(&moe_linear) linear_fn;
+decltype(&moe_grouped_linear) grouped_linear_fn;
 PyObject* error_type;  // GbmoeError(entry point, code)
 
 // A new reference when the object dies; unlike a raw pointer it survives the exceptions below.
@@ -115,6 +118,11 @@ class Out {
     Py_INCREF(given);
     Py_SETREF(obj_.p, given);
   }
+  // The given tensor, which the caller checks (one of strided rows).
+  void rows(PyObject* given) {
+    Py_INCREF(given);
+    Py_SETREF(obj_.p, given);
+  }
   void make(const at::Tensor& like) {
     if (!fresh_) {
       if (obj_.p != Py_None) ptr_ = THPVariable_Unpack(obj_.p).data_ptr();
@@ -152,15 +160,18 @@ bool arguments(Py_ssize_t n, Py_ssize_t want) {
   return false;
 }
 
-// bind(address of moe_rms_norm, of moe_kv_append, of moe_paged_attention, GbmoeError)
+// bind(address of moe_rms_norm, of moe_kv_append, of moe_paged_attention, of moe_linear, of
+// moe_grouped_linear, GbmoeError)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!arguments(n, 4)) return nullptr;
+  if (!arguments(n, 6)) return nullptr;
   rms_norm_fn = reinterpret_cast<decltype(rms_norm_fn)>(address(a[0]));
   kv_append_fn = reinterpret_cast<decltype(kv_append_fn)>(address(a[1]));
   attention_fn = reinterpret_cast<decltype(attention_fn)>(address(a[2]));
-  Py_INCREF(a[3]);
-  Py_XSETREF(error_type, a[3]);
+  linear_fn = reinterpret_cast<decltype(linear_fn)>(address(a[3]));
+  grouped_linear_fn = reinterpret_cast<decltype(grouped_linear_fn)>(address(a[4]));
+  Py_INCREF(a[5]);
+  Py_XSETREF(error_type, a[5]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -341,10 +352,102 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A contiguous CUDA tensor of this type and shape on like's device.
+const at::Tensor& exactly(PyObject* o, const char* name, at::ScalarType dtype, at::IntArrayRef shape,
+                          const at::Tensor& like) {
+  const at::Tensor& t = tensor(o, name);
+  TORCH_CHECK_VALUE(t.is_cuda() && t.scalar_type() == dtype && t.is_contiguous() && t.sizes() == shape,
+                    name, " must be a contiguous CUDA ", dtype, " tensor of shape ", shape);
+  check_device(t, name, like);
+  return t;
+}
+
+// linear(x, weight, offsets or None, bias, activation, residual, row_weight, x_scale, weight_scale,
+//        out, workspace, stream)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!arguments(n, 12)) return nullptr;
+  const bool grouped = a[2] != Py_None;
+  const at::Tensor& x = tensor(a[0], "x");
+  const at::Tensor& w = tensor(a[1], "weight");
+  gbmoe_linear_args_t g = {};
+  const bool fp8 = a[7] != Py_None || a[8] != Py_None;
+  auto typed = [&](const at::Tensor& t) {
+    const at::ScalarType s = t.scalar_type();
+    return fp8 ? s == at::kFloat8_e4m3fn || s == at::kByte : s == at::kBFloat16;
+  };
+  TORCH_CHECK_VALUE(x.dim() == 2 && x.is_cuda() && typed(x) && (x.size(1) < 2 || x.stride(1) == 1),
+                    "x must be a CUDA tensor of rows of contiguous columns, bfloat16, or with scales "
+                    "float8_e4m3fn or uint8");
+  const int32_t T = size32(x, 0, "x"), K = size32(x, 1, "x");
+  TORCH_CHECK_VALUE(w.dim() == (grouped ? 3 : 2) && w.is_cuda() && typed(w) && w.is_contiguous() &&
+                        w.size(-1) == K,
+                    "weight must be a contiguous CUDA tensor of x's kind, ",
+                    grouped ? "[groups, out_features, in_features]" : "[out_features, in_features]");
+  check_device(w, "weight", x);
+  const int32_t N = size32(w, w.dim() - 2, "weight"), G = grouped ? size32(w, 0, "weight") : 1;
+  g.x_stride = T > 1 ? x.stride(0) : (K + 15) / 16 * 16;
+  g.activation = (int32_t)PyLong_AsLong(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  const int64_t cols = g.activation == GBMOE_EPI_SILU_MUL ? N / 2 : N;
+  const at::Tensor* offsets = nullptr;
+  if (grouped) offsets = &exactly(a[2], "offsets", at::kInt, {(int64_t)G + 1}, x);
+  const at::Tensor *bias = nullptr, *residual = nullptr, *row_weight = nullptr, *xs = nullptr,
+                   *ws = nullptr, *workspace = nullptr;
+  if (a[3] != Py_None) {
+    if (grouped) bias = &exactly(a[3], "bias", at::kBFloat16, {G, N}, x);
+    else bias = &exactly(a[3], "bias", at::kBFloat16, {N}, x);
+  }
+  if (a[5] != Py_None) {
+    residual = &tensor(a[5], "residual");
+    g.residual_stride = row_stride(*residual, "residual", T, cols, x);
+  }
+  if (a[6] != Py_None) row_weight = &exactly(a[6], "row_weight", at::kFloat, {T}, x);
+  if (fp8) {
+    g.weight_quant = GBMOE_QUANT_FP8_BLOCK128;
+    xs = &exactly(a[7], "x_scale", at::kFloat, {K / 128, T}, x);
+    const int64_t nb = ((int64_t)N + 127) / 128;
+    if (grouped) ws = &exactly(a[8], "weight_scale", at::kFloat, {G, nb, K / 128}, x);
+    else ws = &exactly(a[8], "weight_scale", at::kFloat, {nb, K / 128}, x);
+  }
+  Out out;
+  if (a[9] != Py_None) {
+    // rows may be strided
+    out.rows(a[9]);
+    g.out_stride = row_stride(tensor(a[9], "out"), "out", T, cols, x);
+  } else {
+    out.want(Py_None, "out", x, {T, cols}, at::kBFloat16);
+    g.out_stride = cols;
+  }
+  if (a[10] != Py_None) {
+    workspace = &tensor(a[10], "workspace");
+    TORCH_CHECK_VALUE(workspace->is_cuda() && workspace->is_contiguous() && workspace->nbytes() >= 256,
+                      "workspace must be a contiguous CUDA tensor of 256 bytes or more");
+    check_device(*workspace, "workspace", x);
+  }
+  const CallStream stream(x, a[11]);
+  out.make(x);
+  auto at = [](const at::Tensor* t) { return t ? t->data_ptr() : nullptr; };
+  g.x = x.data_ptr();
+  g.x_scale = static_cast<const float*>(at(xs));
+  g.weight = w.data_ptr();
+  g.weight_scale = static_cast<const float*>(at(ws));
+  g.bias = at(bias);
+  g.residual = at(residual);
+  g.row_weight = static_cast<const float*>(at(row_weight));
+  g.out = out.ptr();
+  g.workspace = at(workspace);
+  const int code = grouped ? grouped_linear_fn(T, G, K, N, static_cast<const int32_t*>(at(offsets)), &g,
+                                               stream.handle)
+                           : linear_fn(T, K, N, &g, stream.handle);
+  return code ? failed(grouped ? "moe_grouped_linear" : "moe_linear", code) : out.take();
+  END_HANDLE_TH_ERRORS
+}
+
 #define GBMOE_METHOD(f) \
   {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GBMOE_METHOD(bind), GBMOE_METHOD(rms_norm), GBMOE_METHOD(kv_append),
-                         GBMOE_METHOD(attention), {nullptr, nullptr, 0, nullptr}};
+                         GBMOE_METHOD(attention), GBMOE_METHOD(linear), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods};
 
 }  // namespace
