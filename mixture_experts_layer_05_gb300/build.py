@@ -23,7 +23,8 @@ EXT_SOURCE = os.path.join(CSRC, "block_py.cpp")
 SOURCES = ["api.cu", "topk.cu", "align.cu", "gemm.cu", "gemm_tn.cu", "gemm_fp8.cu", "fp8.cu", "gemm_fp4.cu", "fp4.cu",
            "combine.cu",
            "align_static.cu", "block_api.cu", "norm.cu", "kvappend.cu", "attn.cu",
-           "attn_decode.cu", "attn_tc.cu", "linear.cu"]
+           "attn_decode.cu", "attn_tc.cu", "linear.cu",
+           "linear_stream.cu", "linear_pair.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

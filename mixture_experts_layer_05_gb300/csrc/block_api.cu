@@ -92,7 +92,7 @@ gbmoe_status_t linear(int T, int G, int K, int N, const int32_t* offsets, bool g
       G > kLinearMaxGroups || (int64_t)G * N > INT32_MAX)
     return GBMOE_ERR_UNSUPPORTED;
   // tiles of 128 columns by 16 rows are the smallest that any kernel counts
-  if (((int64_t)T / 16 + G) * ((N + 127) / 128) > INT32_MAX) return GBMOE_ERR_UNSUPPORTED;
+  if (((int64_t)T / 16 + G) * ((N + 127) / 128) > (1 << 30)) return GBMOE_ERR_UNSUPPORTED;
   const int cols = gated ? N / 2 : N;
   if (g->x_stride < K || g->x_stride % (fp8 ? 16 : 8) || g->out_stride < cols ||
       (g->residual && g->residual_stride < cols) || !aligned(g->x, 16) || !aligned(g->weight, 16) ||

@@ -1,0 +1,346 @@
+// Shared by the kernels of the dense and grouped products (linear_stream.cu, linear_pair.cu): the
+// line of work units, the weight and scale layout in shared memory, and the epilogue.
+//
+// Both kernels put the weights on the MMA's M side (a TMEM lane is an output feature) and a block
+// of at most `bn` rows of one group on N, so a ragged run costs no more than its rows rounded up to
+// 16. A unit is (group, row block, tile of features); a group's units follow one another, row blocks
+// fastest within sections of `gm` blocks, so that a weight tile is read from HBM once.
+//
+// Both types have K blocks of 128 bytes (64 bf16, 128 e4m3: one swizzle row, one scale block).
+// With SILU_MUL a tile of 128 weight rows holds 16 gate rows, the 16 up rows of the same features,
+// and so on, through a five-dimensional tensor map: lane l < 16 of a warp then has the gate and lane
+// l + 16 the up half of one feature, and a shuffle brings them together.
+#pragma once
+
+#include "linear.h"
+#include "tc.cuh"
+
+namespace gbmoe {
+
+constexpr int kLinWRows = 128;                  // weight rows per CTA and unit
+constexpr uint32_t kLinWBytes = kLinWRows * 128;
+constexpr int kLinScaleSlots = 8;               // e4m3: K blocks of row scales in flight
+constexpr uint32_t kLinSmemMax = 232448;
+
+// One launch: the call, and how it is cut.
+struct LinLaunch {
+  LinearArgs a;
+  int bn;          // rows per block, a multiple of 16
+  int n_tiles;     // feature tiles of the weights of one group
+  int gm;          // row blocks walked together across the feature tiles
+  int k_blocks;
+  int stages;
+  int tab_off;     // byte offsets in shared memory, from the aligned base: group table,
+  int red_off;     // partial sums of a cluster (stream kernel),
+  int scale_off;   // row scales (e4m3),
+  int bar_off;     // barriers
+};
+
+namespace {
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int x, int y, int z, int v, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(v), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                 int x, int y, int z, int v, int w,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(v), "r"(w),
+      "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t bar_cluster, int x, int y, int z, int v,
+                                                 int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "r"(v),
+      "r"(w)
+      : "memory");
+}
+// D[tmem of both CTAs] (+)= A * B^T, e4m3, M = 256.
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// a0 += s0 * v0, a1 += s1 * v1 (two IEEE fmas in one instruction).
+__device__ __forceinline__ void fma2(float& a0, float& a1, float s0, float s1, float v0, float v1) {
+  asm("{\n\t.reg .b64 a, v, s;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 s, {%2, %3};\n\t"
+      "mov.b64 v, {%4, %5};\n\t"
+      "fma.rn.f32x2 a, s, v, a;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(s0), "f"(s1), "f"(v0), "f"(v1));
+}
+
+// ---------------------------------------------------------------- units
+struct LinUnit {
+  int g, nt;     // group, feature tile
+  int m0, n;     // first row, rows
+  bool alone;    // the group's only row block: its weights have no other reader
+};
+
+// The groups of a launch, in shared memory: row blocks before each, first row, rows.
+struct LinGroups {
+  int* before;   // [G + 1]
+  int* first;    // [G]
+  int* rows;     // [G]
+  int G;
+
+  __device__ __forceinline__ LinGroups(int* tab, int groups)
+      : before(tab), first(tab + groups + 1), rows(tab + 2 * groups + 1), G(groups) {}
+
+  // By the whole block; ends with a barrier.
+  __device__ void load(const LinLaunch& L) {
+    const LinearArgs& a = L.a;
+    for (int g = threadIdx.x; g < G; g += blockDim.x) {
+      int lo = 0, hi = a.T;
+      if (a.offsets) {
+        lo = a.offsets[g];
+        hi = a.offsets[g + 1];
+        if (lo < 0 || hi < lo || hi > a.T) {
+          record_status(a.status, GBMOE_ERR_DEVICE_CHECK);
+          lo = hi = 0;
+        }
+      }
+      first[g] = lo;
+      rows[g] = hi - lo;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      int carry = 0;
+      for (int g0 = 0; g0 < G; g0 += 32) {
+        const int g = g0 + lane;
+        int v = g < G ? (rows[g] + L.bn - 1) / L.bn : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += t;
+        }
+        if (g < G) before[g + 1] = carry + v;
+        carry += __shfl_sync(0xffffffffu, v, 31);
+      }
+      if (lane == 0) before[0] = 0;
+    }
+    __syncthreads();
+  }
+
+  __device__ __forceinline__ int units(const LinLaunch& L) const { return before[G] * L.n_tiles; }
+
+  __device__ __forceinline__ LinUnit unit(const LinLaunch& L, int u) const {
+    const int b = u / L.n_tiles;
+    int g = 0, end = G;
+    while (end - g > 1) {
+      const int mid = (g + end) >> 1;
+      if (before[mid] <= b) g = mid;
+      else end = mid;
+    }
+    const int blocks = before[g + 1] - before[g];
+    const int s0 = (b - before[g]) / L.gm * L.gm;  // this section's first block
+    const int sn = min(L.gm, blocks - s0);
+    const int local = u - (before[g] + s0) * L.n_tiles;
+    LinUnit r;
+    r.g = g;
+    r.nt = local / sn;
+    const int at = (s0 + local % sn) * L.bn;
+    r.m0 = first[g] + at;
+    r.n = min(L.bn, rows[g] - at);
+    r.alone = blocks == 1;
+    return r;
+  }
+};
+
+// ---------------------------------------------------------------- scales (e4m3)
+// One warp walks the CTA's K blocks ahead of the epilogue and writes, for each of the unit's rows
+// c, the product of its scale and the weight block's: scale[c], or with GATED [c / 4][gate, up][c % 4],
+// so that the 16 gate and the 16 up lanes of a warp read neighbouring 16 bytes.
+template <bool GATED>
+__device__ __forceinline__ int lin_scale_at(int c, int up) {
+  return GATED ? (c >> 2) * 8 + up * 4 + (c & 3) : c;
+}
+
+template <bool GATED, int COLS>  // COLS: rows per block at most
+struct LinScales {
+  static constexpr int kPer = COLS / 32, kBatch = 4;
+
+  // K blocks [kb0, kb1) of one unit; row: the first weight row of this CTA's tile (with GATED the
+  // gate's). false: a wait ran out.
+  __device__ __forceinline__ static bool unit(const LinLaunch& L, const LinUnit& w, int row, int kb0,
+                                              int kb1, float* ring, int slot_floats, uint32_t full0,
+                                              uint32_t empty0, uint32_t& it, volatile int* abort_flag) {
+    const LinearArgs& a = L.a;
+    const int lane = threadIdx.x & 31;
+    const int wblocks = (a.N + 127) >> 7;
+    const float* ws = a.w_scale + ((long long)w.g * wblocks + min(row >> 7, wblocks - 1)) * L.k_blocks;
+    const float* wu = GATED ? ws + (long long)(a.cols >> 7) * L.k_blocks : ws;
+    const float* xs = a.x_scale + w.m0 + lane;
+    for (int kb = kb0; kb < kb1; kb += kBatch) {
+      float v[kBatch][kPer], g[kBatch], u[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const bool in = kb + i < kb1;
+        g[i] = in ? __ldg(ws + kb + i) : 0.f;
+        u[i] = GATED && in ? __ldg(wu + kb + i) : 0.f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          v[i][j] = in && lane + 32 * j < w.n ? __ldg(xs + (long long)(kb + i) * a.T + 32 * j) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (kb + i >= kb1) break;
+        const int slot = it % kLinScaleSlots;
+        const uint32_t ph = (it / kLinScaleSlots) & 1u;
+        if (!wait_fast(empty0 + 8u * slot, ph ^ 1u, abort_flag, a.status)) return false;
+        float* dst = ring + slot * slot_floats;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int c = lane + 32 * j;
+          if (c < L.bn) {
+            dst[lin_scale_at<GATED>(c, 0)] = v[i][j] * g[i];
+            if (GATED) dst[lin_scale_at<GATED>(c, 1)] = v[i][j] * u[i];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full0 + 8u * slot);
+        ++it;
+      }
+    }
+    return true;
+  }
+};
+
+// acc[i] += scale * block product for 16 columns from column c0 of a K block's TMEM buffer.
+template <bool GATED>
+__device__ __forceinline__ void lin_promote16(float* acc, uint32_t tmem, const float* scales, int c0,
+                                              int up) {
+  uint32_t v[16];
+  tmem_ld16(tmem + c0, v);
+  float4 s[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    s[q] = *reinterpret_cast<const float4*>(scales + lin_scale_at<GATED>(c0 + 4 * q, up));
+  tmem_wait_ld16(v);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    fma2(acc[4 * q], acc[4 * q + 1], s[q].x, s[q].y, __uint_as_float(v[4 * q]),
+         __uint_as_float(v[4 * q + 1]));
+    fma2(acc[4 * q + 2], acc[4 * q + 3], s[q].z, s[q].w, __uint_as_float(v[4 * q + 2]),
+         __uint_as_float(v[4 * q + 3]));
+  }
+}
+
+// ---------------------------------------------------------------- epilogue
+template <int N, class F>
+__device__ __forceinline__ void lin_each(float (&y)[N], F f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) y[i] = f(y[i]);
+}
+
+// What this lane stores of a unit: the column of out, and its biases.
+struct LinLane {
+  int f;            // output column
+  bool in;          // f is one
+  float bias, up_bias;
+
+  // f0: the first output column of the warp's 32 weight rows
+  template <bool GATED>
+  __device__ __forceinline__ static LinLane make(const LinearArgs& a, int g, int f0) {
+    LinLane r;
+    const int lane = threadIdx.x & 31;
+    r.f = f0 + (GATED ? lane & 15 : lane);
+    r.in = r.f < a.cols;
+    r.bias = r.up_bias = 0.f;
+    if (a.bias && r.in) {
+      const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(a.bias) + (long long)g * a.N;
+      r.bias = __bfloat162float(b[r.f]);
+      if (GATED) r.up_bias = __bfloat162float(b[a.cols + r.f]);
+    }
+    return r;
+  }
+};
+
+// 2 COLS (GATED) or COLS values per lane: the sums of the warp's weight rows for rows t0 .. t0 + cnt
+// of x, cnt <= the number of values. With GATED lanes l and l + 16 swap halves: the lower keep the
+// first half of the columns, the upper the second.
+template <bool GATED, int COLS>
+__device__ __forceinline__ void lin_store(const LinearArgs& a, const LinLane& l, int t0, int cnt,
+                                          float (&v)[GATED ? 2 * COLS : COLS]) {
+  float y[COLS];
+  if (GATED) {
+    const bool upper = (threadIdx.x & 16) != 0;
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + COLS], 16);
+      const float gate = (upper ? other : v[i]) + l.bias;
+      const float up = (upper ? v[i + COLS] : other) + l.up_bias;
+      y[i] = gate / (1.f + __expf(-gate)) * up;
+    }
+    if (upper) {
+      t0 += COLS;
+      cnt -= COLS;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) y[i] = v[i] + l.bias;
+    switch (a.act) {
+      case GBMOE_EPI_RELU: lin_each(y, [](float z) { return z < 0.f ? 0.f : z; }); break;
+      case GBMOE_EPI_SILU: lin_each(y, [](float z) { return z / (1.f + __expf(-z)); }); break;
+      case GBMOE_EPI_GELU:
+        lin_each(y, [](float z) { return 0.5f * z * (1.f + erff(z * 0.70710678f)); });
+        break;
+      case GBMOE_EPI_GELU_TANH:
+        lin_each(y, [](float z) {
+          return 0.5f * z * (1.f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
+        });
+        break;
+      default: break;
+    }
+  }
+  if (!l.in) return;
+  if (a.row_weight) {
+#pragma unroll
+    for (int i = 0; i < COLS; ++i)
+      if (i < cnt) y[i] *= __ldg(a.row_weight + t0 + i);
+  }
+  if (a.residual) {
+    const __nv_bfloat16* r =
+        static_cast<const __nv_bfloat16*>(a.residual) + (long long)t0 * a.residual_stride + l.f;
+    __nv_bfloat16 b[COLS];
+#pragma unroll
+    for (int i = 0; i < COLS; ++i)
+      if (i < cnt) b[i] = r[i * a.residual_stride];
+#pragma unroll
+    for (int i = 0; i < COLS; ++i)
+      if (i < cnt) y[i] += __bfloat162float(b[i]);
+  }
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (long long)t0 * a.out_stride + l.f;
+#pragma unroll
+  for (int i = 0; i < COLS; ++i)
+    if (i < cnt) o[i * a.out_stride] = __float2bfloat16_rn(y[i]);
+}
+
+}  // namespace
+
+// Tensor maps of a call: the weights as this CTA tile's 128 rows, x with boxes of x_box rows.
+bool lin_maps(const LinearArgs& a, int x_box, CUtensorMap* w, CUtensorMap* x);
+// Launches; false in *fits when the cut does not fit the kernel.
+cudaError_t launch_linear_stream(LinLaunch L, int cluster, int max_units, cudaStream_t stream);
+cudaError_t launch_linear_pair(LinLaunch L, int max_units, cudaStream_t stream);
+
+}  // namespace gbmoe
