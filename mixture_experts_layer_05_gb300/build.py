@@ -24,7 +24,7 @@ SOURCES = ["api.cu", "topk.cu", "align.cu", "gemm.cu", "gemm_tn.cu", "gemm_fp8.c
            "combine.cu",
            "align_static.cu", "block_api.cu", "norm.cu", "kvappend.cu", "attn.cu",
            "attn_decode.cu", "attn_tc.cu", "linear.cu",
-           "linear_stream.cu", "linear_pair.cu"]
+           "linear_stream.cu", "linear_pair.cu", "linear_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -66,16 +66,6 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap
       "r"(w)
       : "memory");
 }
-// D[tmem of both CTAs] (+)= A * B^T, e4m3, M = 256.
-__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                              uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 // a0 += s0 * v0, a1 += s1 * v1 (two IEEE fmas in one instruction).
 __device__ __forceinline__ void fma2(float& a0, float& a1, float s0, float s1, float v0, float v1) {
   asm("{\n\t.reg .b64 a, v, s;\n\t"
@@ -246,10 +236,29 @@ __device__ __forceinline__ void lin_promote16(float* acc, uint32_t tmem, const f
 }
 
 // ---------------------------------------------------------------- epilogue
+// The quotients by __fdividef: 2 ulp, where the result is rounded to bf16 next. A denominator past
+// 2^126 gives 0, where the true value is below 1e-35.
+__device__ __forceinline__ float lin_silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 template <int N, class F>
 __device__ __forceinline__ void lin_each(float (&y)[N], F f) {
 #pragma unroll
   for (int i = 0; i < N; ++i) y[i] = f(y[i]);
+}
+template <int N>
+__device__ __forceinline__ void lin_activate(float (&y)[N], int act) {
+  switch (act) {
+    case GBMOE_EPI_RELU: lin_each(y, [](float z) { return z < 0.f ? 0.f : z; }); break;
+    case GBMOE_EPI_SILU: lin_each(y, [](float z) { return lin_silu(z); }); break;
+    case GBMOE_EPI_GELU:
+      lin_each(y, [](float z) { return 0.5f * z * (1.f + erff(z * 0.70710678f)); });
+      break;
+    case GBMOE_EPI_GELU_TANH:                      // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+      lin_each(y, [](float z) {
+        return __fdividef(z, 1.f + __expf(-1.5957691f * (z + 0.044715f * z * z * z)));
+      });
+      break;
+    default: break;
+  }
 }
 
 // What this lane stores of a unit: the column of out, and its biases.
@@ -281,53 +290,47 @@ struct LinLane {
 template <bool GATED, int COLS>
 __device__ __forceinline__ void lin_store(const LinearArgs& a, const LinLane& l, int t0, int cnt,
                                           float (&v)[GATED ? 2 * COLS : COLS]) {
-  float y[COLS];
+  float y[COLS], rw[COLS];
+  __nv_bfloat16 res[COLS];
+  const bool upper = GATED && (threadIdx.x & 16) != 0;
+  if (upper) {
+    t0 += COLS;
+    cnt -= COLS;
+  }
+  // all loads first and unconditional (rows past the last repeat it), so that they fly together
+  if (cnt > 0) {
+    if (a.row_weight) {
+#pragma unroll
+      for (int i = 0; i < COLS; ++i) rw[i] = __ldg(a.row_weight + t0 + min(i, cnt - 1));
+    }
+    if (a.residual && l.in) {
+      const __nv_bfloat16* r =
+          static_cast<const __nv_bfloat16*>(a.residual) + (long long)t0 * a.residual_stride + l.f;
+#pragma unroll
+      for (int i = 0; i < COLS; ++i) res[i] = r[min(i, cnt - 1) * a.residual_stride];
+    }
+  }
   if (GATED) {
-    const bool upper = (threadIdx.x & 16) != 0;
 #pragma unroll
     for (int i = 0; i < COLS; ++i) {
       const float other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + COLS], 16);
       const float gate = (upper ? other : v[i]) + l.bias;
       const float up = (upper ? v[i + COLS] : other) + l.up_bias;
-      y[i] = gate / (1.f + __expf(-gate)) * up;
-    }
-    if (upper) {
-      t0 += COLS;
-      cnt -= COLS;
+      y[i] = lin_silu(gate) * up;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < COLS; ++i) y[i] = v[i] + l.bias;
-    switch (a.act) {
-      case GBMOE_EPI_RELU: lin_each(y, [](float z) { return z < 0.f ? 0.f : z; }); break;
-      case GBMOE_EPI_SILU: lin_each(y, [](float z) { return z / (1.f + __expf(-z)); }); break;
-      case GBMOE_EPI_GELU:
-        lin_each(y, [](float z) { return 0.5f * z * (1.f + erff(z * 0.70710678f)); });
-        break;
-      case GBMOE_EPI_GELU_TANH:
-        lin_each(y, [](float z) {
-          return 0.5f * z * (1.f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
-        });
-        break;
-      default: break;
-    }
+    lin_activate(y, a.act);
   }
-  if (!l.in) return;
+  if (!l.in || cnt <= 0) return;
   if (a.row_weight) {
 #pragma unroll
-    for (int i = 0; i < COLS; ++i)
-      if (i < cnt) y[i] *= __ldg(a.row_weight + t0 + i);
+    for (int i = 0; i < COLS; ++i) y[i] *= rw[i];
   }
   if (a.residual) {
-    const __nv_bfloat16* r =
-        static_cast<const __nv_bfloat16*>(a.residual) + (long long)t0 * a.residual_stride + l.f;
-    __nv_bfloat16 b[COLS];
 #pragma unroll
-    for (int i = 0; i < COLS; ++i)
-      if (i < cnt) b[i] = r[i * a.residual_stride];
-#pragma unroll
-    for (int i = 0; i < COLS; ++i)
-      if (i < cnt) y[i] += __bfloat162float(b[i]);
+    for (int i = 0; i < COLS; ++i) y[i] += __bfloat162float(res[i]);
   }
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (long long)t0 * a.out_stride + l.f;
 #pragma unroll
@@ -335,12 +338,87 @@ __device__ __forceinline__ void lin_store(const LinearArgs& a, const LinLane& l,
     if (i < cnt) o[i * a.out_stride] = __float2bfloat16_rn(y[i]);
 }
 
+// 8 consecutive bf16 values as fp32, or the first `cnt` of them; wide: 16-byte aligned.
+__device__ __forceinline__ void lin_load8(const __nv_bfloat16* p, bool wide, int cnt, float (&v)[8]) {
+  if (wide && cnt >= 8) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack_bf16x2(u[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < cnt ? __bfloat162float(p[i]) : 0.f;
+  }
+}
+
+// The N sums of one row t from output column f0 on (GATED: N / 2 gate sums, then their up sums).
+template <bool GATED, int N>
+__device__ __forceinline__ void lin_store_row(const LinearArgs& a, int g, int t, int f0,
+                                              float (&acc)[N]) {
+  const __nv_bfloat16* bias =
+      a.bias ? static_cast<const __nv_bfloat16*>(a.bias) + (long long)g * a.N : nullptr;
+  const __nv_bfloat16* res =
+      a.residual ? static_cast<const __nv_bfloat16*>(a.residual) + t * a.residual_stride : nullptr;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + t * a.out_stride;
+  const float rw = a.row_weight ? __ldg(a.row_weight + t) : 1.f;
+  auto wide = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+#pragma unroll
+  for (int c = 0; c < (GATED ? N / 2 : N); c += 8) {
+    const int f = f0 + c, cnt = a.cols - f;
+    if (cnt <= 0) break;
+    float y[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = acc[c + i];
+    if (bias) {
+      lin_load8(bias + f, wide(bias + f), cnt, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += b[i];
+    }
+    if (GATED) {
+      float up[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) up[i] = acc[(c + i + N / 2) % N];
+      if (bias) {
+        lin_load8(bias + a.cols + f, wide(bias + a.cols + f), cnt, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) up[i] += b[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = lin_silu(y[i]) * up[i];
+    } else {
+      lin_activate(y, a.act);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] *= rw;
+    if (res) {
+      lin_load8(res + f, wide(res + f), cnt, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += b[i];
+    }
+    if (cnt >= 8 && wide(out + f)) {
+      *reinterpret_cast<uint4*>(out + f) =
+          make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                     pack_bf16x2(y[6], y[7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < cnt) out[f + i] = __float2bfloat16_rn(y[i]);
+    }
+  }
+}
+
 }  // namespace
 
 // Tensor maps of a call: the weights as this CTA tile's 128 rows, x with boxes of x_box rows.
 bool lin_maps(const LinearArgs& a, int x_box, CUtensorMap* w, CUtensorMap* x);
-// Launches; false in *fits when the cut does not fit the kernel.
+// The same with the weights as plain rows, in boxes of 128, and x in boxes of x_box.
+bool lin_map_rows(const LinearArgs& a, CUtensorMap* w, CUtensorMap* x, int x_box);
 cudaError_t launch_linear_stream(LinLaunch L, int cluster, int max_units, cudaStream_t stream);
 cudaError_t launch_linear_pair(LinLaunch L, int max_units, cudaStream_t stream);
+cudaError_t launch_linear_fp8(LinLaunch L, int max_units, cudaStream_t stream);
 
 }  // namespace gbmoe

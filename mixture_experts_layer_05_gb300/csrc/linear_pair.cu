@@ -4,13 +4,9 @@
 // rows and half of the block's rows of x, which is 64 bytes of operands per clock and SM at full rate,
 // where an SM by itself would need 96. The block's rows are N, at most 256. Persistent: a cluster
 // walks the units, and two TMEM accumulators let the epilogue of one unit run under the products of
-// the next.
+// the next. (e4m3 operands have a kernel of their own, linear_fp8.cu.)
 //
-// e4m3: the products of each K block of 128 go into one of two TMEM buffers, and 16 epilogue warps
-// promote them to fp32 registers with the block's scales (64 columns a thread) while the next K
-// block's run into the other.
-//
-// Warps: 0 TMA, 1 TMEM and MMA (leader), then 8 (e4m3: 16) epilogue, and (e4m3) one for the scales.
+// Warps: 0 TMA, 1 TMEM and MMA (leader), 2..9 epilogue, two to a TMEM lane quarter.
 #include "linear.cuh"
 
 namespace gbmoe {
@@ -21,19 +17,16 @@ constexpr int kMaxStages = 10;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kStride = 256;                // TMEM columns of an accumulator
 
-constexpr int epi_warps(bool fp8) { return fp8 ? 16 : 8; }
-constexpr int threads_of(bool fp8) { return 64 + 32 * epi_warps(fp8) + (fp8 ? 32 : 0); }
-constexpr int kBars = 2 * kMaxStages + 4 + 2 * kLinScaleSlots;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBars = 2 * kMaxStages + 4;
 
-template <bool FP8, bool GATED>
-__global__ void __launch_bounds__(threads_of(FP8), 1)
+template <bool GATED>
+__global__ void __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_x,
                        const __grid_constant__ LinLaunch L) {
-  constexpr int kEpiWarps = epi_warps(FP8);
-  constexpr int kStepElems = FP8 ? 128 : 64;
   constexpr int kTileCols = GATED ? 64 : 128;      // output columns per CTA and unit
-  constexpr int kRound = FP8 ? 32 : 16;            // the MMA's N
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -41,7 +34,6 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   const LinearArgs& a = L.a;
   const int stages = L.stages;
   const uint32_t x_bytes = (uint32_t)(L.bn / 2) * 128, stage_bytes = kLinWBytes + x_bytes;
-  float* scales = reinterpret_cast<float*>(smem + L.scale_off);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bar_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -50,7 +42,6 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
-  const uint32_t sfull0 = bar0 + 8u * (2 * kMaxStages + 4), sempty0 = sfull0 + 8u * kLinScaleSlots;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
@@ -63,10 +54,6 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
       mbar_init(tempty_bar(b), 2 * kEpiWarps);
-    }
-    for (int s = 0; s < kLinScaleSlots; ++s) {
-      mbar_init(sfull0 + 8u * s, 1);
-      mbar_init(sempty0 + 8u * s, kEpiWarps);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -96,21 +83,21 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       bool ok = true;
       for (int u = first; ok && u < units; u += step) {
         const LinUnit w = groups.unit(L, u);
-        const int half = ((w.n + kRound - 1) / kRound * kRound) / 2;
+        const int half = ((w.n + 15) & ~15) / 2;
         const int x_row = w.m0 + rank * half;
         const int tile = w.nt * 2 + rank;
         for (int kb = 0; kb < L.k_blocks; ++kb) {
-          if (!wait_bounded_cluster(empty_bar(s), ph, abort_flag, a.status)) {
+          if (!wait_fast(empty_bar(s), ph, abort_flag, a.status)) {
             ok = false;
             break;
           }
           if (leader) mbar_expect_tx(full_bar(s), 2 * stage_bytes);  // both CTAs' bytes
           const uint32_t fb = leader_full0 + 8u * s, sw = base + s * stage_bytes;
           if (GATED)
-            tma_load_5d_pair(sw, &tm_w, fb, kb * kStepElems, 0, 0, tile * (kTileCols / 16), w.g);
+            tma_load_5d_pair(sw, &tm_w, fb, kb * kGemmBK, 0, 0, tile * (kTileCols / 16), w.g);
           else
-            tma_load_2d_pair(sw, &tm_w, fb, kb * kStepElems, w.g * a.N + tile * kTileCols);
-          tma_load_2d_pair(sw + kLinWBytes, &tm_x, fb, kb * kStepElems, x_row);
+            tma_load_2d_pair(sw, &tm_w, fb, kb * kGemmBK, w.g * a.N + tile * kTileCols);
+          tma_load_2d_pair(sw + kLinWBytes, &tm_x, fb, kb * kGemmBK, x_row);
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
@@ -127,16 +114,11 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       bool ok = true;
       for (int u = first; ok && u < units; u += step) {
         const LinUnit w = groups.unit(L, u);
-        const int n = (w.n + kRound - 1) / kRound * kRound;
-        const uint32_t idesc = FP8 ? idesc_e4m3(256, n) : idesc_bf16(256, n);
+        const int n = (w.n + 15) & ~15;
+        const uint32_t idesc = idesc_bf16(256, n);
         for (int kb = 0; kb < L.k_blocks; ++kb) {
-          if (FP8 || kb == 0) {
-            if (!wait_bounded_cluster(tempty_bar(buf), tph, abort_flag, a.status)) {
-              ok = false;
-              break;
-            }
-          }
-          if (!wait_bounded_cluster(full_bar(s), ph, abort_flag, a.status)) {
+          if ((kb == 0 && !wait_fast(tempty_bar(buf), tph, abort_flag, a.status)) ||
+              !wait_fast(full_bar(s), ph, abort_flag, a.status)) {
             ok = false;
             break;
           }
@@ -145,19 +127,15 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
           const uint64_t dw = sdesc_sw128(sw), dx = sdesc_sw128(sw + kLinWBytes);
           const uint32_t d = tmem_base + buf * kStride;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t more = (FP8 ? kk != 0 : (kb != 0 || kk != 0)) ? 1u : 0u;
-            if (FP8)
-              mma_e4m3_pair(d, sdesc_advance(dw, kk * 32), sdesc_advance(dx, kk * 32), idesc, more);
-            else
-              mma_bf16_pair(d, sdesc_advance(dw, kk * 32), sdesc_advance(dx, kk * 32), idesc, more);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_pair(d, sdesc_advance(dw, kk * 32), sdesc_advance(dx, kk * 32), idesc,
+                          kb != 0 || kk != 0 ? 1u : 0u);
           mma_commit_pair(empty_bar(s));
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
-          if (FP8 || kb == L.k_blocks - 1) {
+          if (kb == L.k_blocks - 1) {
             mma_commit_pair(tfull_bar(buf));
             buf ^= 1;
             if (buf == 0) tph ^= 1u;
@@ -171,84 +149,29 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     const int quarter = warp & 3;                  // TMEM lanes [32 quarter, + 32)
     const int part = (warp - 2) >> 2;              // which of the quarter's warps
     const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    int buf = 0, slot = 0;
-    uint32_t tph = 0, sph = 0;
-    bool ok = true;
-    for (int u = first; ok && u < units; u += step) {
+    int buf = 0;
+    uint32_t tph = 0;
+    for (int u = first; u < units; u += step) {
       const LinUnit w = groups.unit(L, u);
       const LinLane l = LinLane::make<GATED>(
           a, w.g, (w.nt * 2 + rank) * kTileCols + quarter * (kTileCols / 4));
-      if (FP8) {
-        // four warps share the columns in runs of 16
-        const int run = (((w.n + 15) >> 4) + 3) >> 2;
-        const int c0 = part * run * 16;
-        float acc[64];
-#pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = 0.f;
-        for (int kb = 0; kb < L.k_blocks; ++kb) {
-          if (!wait_fast(sfull0 + 8u * slot, sph, abort_flag, a.status) ||
-              !wait_bounded_cluster(tfull_bar(buf), tph, abort_flag, a.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const float* sc = scales + slot * L.bn * (GATED ? 2 : 1);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c < run && c0 + 16 * c < w.n)
-              lin_promote16<GATED>(acc + 16 * c, lanes + buf * kStride, sc, c0 + 16 * c, lane >> 4);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_cluster(leader_tempty0 + 8u * buf);
-            mbar_arrive(sempty0 + 8u * slot);
-          }
-          buf ^= 1;
-          if (buf == 0) tph ^= 1u;
-          if (++slot == kLinScaleSlots) {
-            slot = 0;
-            sph ^= 1u;
-          }
-        }
-        if (!ok) break;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int at = c0 + 16 * c;
-          if (c < run && at < w.n) {
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = acc[16 * c + i];
-            lin_store<GATED, GATED ? 8 : 16>(a, l, w.m0 + at, w.n - at, v);
-          }
-        }
-      } else {
-        if (!wait_bounded_cluster(tfull_bar(buf), tph, abort_flag, a.status)) break;
-        tc_fence_after();
+      if (!wait_fast(tfull_bar(buf), tph, abort_flag, a.status)) break;
+      tc_fence_after();
 #pragma unroll 1
-        for (int at = part * 32; at < w.n; at += 64) {
-          uint32_t t[32];
-          float v[32];
-          tmem_ld32(lanes + buf * kStride + at, t);
-          tmem_wait_ld(t);
+      for (int at = part * 32; at < w.n; at += 64) {
+        uint32_t t[32];
+        float v[32];
+        tmem_ld32(lanes + buf * kStride + at, t);
+        tmem_wait_ld(t);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(t[i]);
-          lin_store<GATED, GATED ? 16 : 32>(a, l, w.m0 + at, w.n - at, v);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8u * buf);
-        buf ^= 1;
-        if (buf == 0) tph ^= 1u;
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(t[i]);
+        lin_store<GATED, GATED ? 16 : 32>(a, l, w.m0 + at, w.n - at, v);
       }
-    }
-  } else if (FP8) {
-    // ------------------------------------------------------------ scales (both CTAs)
-    uint32_t it = 0;
-    for (int u = first; u < units; u += step) {
-      const LinUnit w = groups.unit(L, u);
-      if (!LinScales<GATED, kMaxBn>::unit(L, w, (w.nt * 2 + rank) * kTileCols, 0, L.k_blocks, scales,
-                                          L.bn * (GATED ? 2 : 1), sfull0, sempty0, it, abort_flag))
-        break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_tempty0 + 8u * buf);
+      buf ^= 1;
+      if (buf == 0) tph ^= 1u;
     }
   }
 
@@ -260,10 +183,10 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   }
 }
 
-template <bool FP8, bool GATED>
+template <bool GATED>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& L, int units,
                    size_t smem, cudaStream_t stream) {
-  auto kernel = linear_pair_kernel<FP8, GATED>;
+  auto kernel = linear_pair_kernel<GATED>;
   static bool ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -276,7 +199,7 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& 
   const int most = num_sms() / 2, clusters = units < most ? units : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(threads_of(FP8));
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -292,27 +215,20 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& 
 
 cudaError_t launch_linear_pair(LinLaunch L, int max_units, cudaStream_t stream) {
   const LinearArgs& a = L.a;
-  const bool gated = a.act == GBMOE_EPI_SILU_MUL;
-  if (L.bn < 32 || L.bn > kMaxBn || L.bn % 32) return cudaErrorInvalidValue;
+  if (a.fp8 || L.bn < 32 || L.bn > kMaxBn || L.bn % 32) return cudaErrorInvalidValue;
   const uint32_t stage = kLinWBytes + L.bn / 2 * 128;
-  const uint32_t scale = a.fp8 ? kLinScaleSlots * L.bn * 4 * (gated ? 2 : 1) : 0;
   const uint32_t tab = (4u * (3 * a.G + 1) + 15) & ~15u, bars = kBars * 8 + 16;
-  const uint32_t rest = scale + tab + bars + 1024;
+  const uint32_t rest = tab + bars + 1024;
   int stages = (int)((kLinSmemMax - rest) / stage);
   if (stages > kMaxStages) stages = kMaxStages;
   L.stages = stages;
-  L.red_off = 0;
-  L.scale_off = stages * stage;
-  L.bar_off = L.scale_off + scale;
+  L.bar_off = stages * stage;
   L.tab_off = L.bar_off + bars;
   CUtensorMap w, x;
   if (!lin_maps(a, L.bn / 2, &w, &x)) return cudaErrorInvalidValue;
   const size_t smem = stages * stage + rest;
-  if (a.fp8)
-    return gated ? launch<true, true>(w, x, L, max_units, smem, stream)
-                 : launch<true, false>(w, x, L, max_units, smem, stream);
-  return gated ? launch<false, true>(w, x, L, max_units, smem, stream)
-               : launch<false, false>(w, x, L, max_units, smem, stream);
+  return a.act == GBMOE_EPI_SILU_MUL ? launch<true>(w, x, L, max_units, smem, stream)
+                                     : launch<false>(w, x, L, max_units, smem, stream);
 }
 
 }  // namespace gbmoe
