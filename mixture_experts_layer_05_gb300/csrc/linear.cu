@@ -15,30 +15,36 @@ bool encode(const LinearArgs& a, CUtensorMap* m, const void* p, int rank, const 
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// rows of `cols` elements, `stride` apart, in boxes of 128 bytes by box_rows
+// `rows` rows of K elements, `stride` elements apart.
 bool map_rows(const LinearArgs& a, CUtensorMap* m, const void* p, cuuint64_t rows, cuuint64_t stride,
-              int box_rows) {
-  const cuuint64_t es = a.fp8 ? 1 : 2;
-  const cuuint64_t dims[2] = {(cuuint64_t)a.K, rows}, strides[1] = {stride * es};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows};
-  return encode(a, m, p, 2, dims, strides, box);
+              int box_rows, int kps) {
+  const cuuint64_t es = a.fp8 ? 1 : 2, inner = 128 / es, K = a.K;
+  const bool whole = kps > 0;
+  const cuuint64_t dims[3] = {whole ? inner : K, rows, whole ? K / inner : 1};
+  const cuuint64_t strides[2] = {stride * es, 128};
+  const cuuint32_t box[3] = {(cuuint32_t)inner, (cuuint32_t)box_rows, (cuuint32_t)(whole ? kps : 1)};
+  return encode(a, m, p, 3, dims, strides, box);
 }
 
 }  // namespace
 
-bool lin_map_rows(const LinearArgs& a, CUtensorMap* w, CUtensorMap* x, int x_box) {
-  return map_rows(a, w, a.weight, (cuuint64_t)a.G * a.N, a.K, kLinWRows) &&
-         map_rows(a, x, a.x, a.T, a.x_stride, x_box);
+bool lin_map_x(const LinearArgs& a, int rows, int kps, CUtensorMap* x) {
+  return map_rows(a, x, a.x, a.T, a.x_stride, rows, kps);
 }
 
-bool lin_maps(const LinearArgs& a, int x_box, CUtensorMap* w, CUtensorMap* x) {
-  if (a.act != GBMOE_EPI_SILU_MUL) return lin_map_rows(a, w, x, x_box);
-  // (k, row of 16, gate or up, block of 16 features, group): 16 gate rows, their 16 up rows, ...
-  const cuuint64_t es = a.fp8 ? 1 : 2, K = a.K, N = a.N, I = N / 2;
-  const cuuint64_t dims[5] = {K, 16, 2, I / 16, (cuuint64_t)a.G};
-  const cuuint64_t strides[4] = {K * es, I * K * es, 16 * K * es, N * K * es};
-  const cuuint32_t box[5] = {(cuuint32_t)(128 / es), 16, 2, 4, 1};
-  return encode(a, w, a.weight, 5, dims, strides, box) && map_rows(a, x, a.x, a.T, a.x_stride, x_box);
+bool lin_map_rows(const LinearArgs& a, int rows, int kps, CUtensorMap* w) {
+  return map_rows(a, w, a.weight, (cuuint64_t)a.G * a.N, a.K, rows, kps);
+}
+
+bool lin_map_tiles(const LinearArgs& a, int rows, int kps, CUtensorMap* w) {
+  if (a.act != GBMOE_EPI_SILU_MUL) return lin_map_rows(a, rows, kps, w);
+  // (k, row of 16, gate or up of each group, block of 16 features, K block)
+  const cuuint64_t es = a.fp8 ? 1 : 2, inner = 128 / es, K = a.K, I = a.N / 2;
+  const bool whole = kps > 0;
+  const cuuint64_t dims[5] = {whole ? inner : K, 16, 2 * (cuuint64_t)a.G, I / 16, whole ? K / inner : 1};
+  const cuuint64_t strides[4] = {K * es, I * K * es, 16 * K * es, 128};
+  const cuuint32_t box[5] = {(cuuint32_t)inner, 16, 2, (cuuint32_t)rows / 32, (cuuint32_t)(whole ? kps : 1)};
+  return encode(a, w, a.weight, 5, dims, strides, box);
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
@@ -49,41 +55,96 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   auto ceil_div = [](long long x, long long y) { return (int)((x + y - 1) / y); };
   const int mean = ceil_div(a.T, a.G);
   const int groups = a.G < a.T ? a.G : a.T;                  // with rows, at most
-  const bool pair = mean > 128;
-  if (pair && a.fp8) {
+  // The kernel. Dense bf16 calls change at 96 rows (K = N = 4096: 64 rows 13.9 us in the stream kernel,
+  // 128 rows 15.4 there and 15.0 in pairs, 256 17.6 and 15.7); e4m3 ones likewise, where more rows cost
+  // the stream kernel's promotion more (K = 7168, N = 4096: 96 rows 18.0 and 30.5, K = N = 4096: 128 rows
+  // 19.0 and 20.8). Groups change earlier, as the largest has a multiple of the mean and is then cut (16
+  // of 2048 to 7168, mean 32: 76.9 and 79.4 evenly, 81.0 and 79.5 unevenly filled, mean 48: 77.8 and 80.3,
+  // 87.0 and 85.1; e4m3, mean 8: 42.6 and 44.1, 43.7 and 43.0, mean 16: 46.8 and 45.5, 60.9 and 46.8).
+  const bool many = mean > (!a.offsets ? 96 : a.fp8 ? 8 : 32);
+  if (many && a.fp8) {
     L.bn = 128;
     L.n_tiles = ceil_div(a.cols, 2 * cols);
     L.gm = 16;
     const long long units = ((long long)ceil_div(a.T, L.bn) + groups - 1) * L.n_tiles;
-    return launch_linear_fp8(L, units > 4096 ? 4096 : (int)units, stream);
+    return launch_linear_fp8(L, units, stream);
   }
-  if (pair) {
-    int bn = ceil_div(mean, ceil_div(mean, 256));
-    bn = (bn + 31) & ~31;
-    L.bn = bn;
+  if (many) {
     L.n_tiles = ceil_div(a.cols, 2 * cols);
     L.gm = 16;
+    L.bn = 256;
+    if (!a.offsets) {
+      // the rows are cut evenly, so that the units come out in few rounds; a K block of a unit takes the
+      // MMAs' 1.1 ns a row, or what the issue of its copies takes
+      long long best = 1ll << 62;
+      for (int blocks = ceil_div(a.T, 256); blocks <= 4 * ceil_div(a.T, 256); ++blocks) {
+        const int bn = (ceil_div(a.T, blocks) + 31) & ~31;
+        if (bn < 64) break;
+        const long long units = (long long)ceil_div(a.T, bn) * L.n_tiles;
+        const int ns = 9 * bn / 8 > 140 + bn / 8 ? 9 * bn / 8 : 140 + bn / 8;
+        const long long cost = ceil_div(units, num_sms() / 2) * (long long)ns;
+        if (cost < best) {
+          best = cost;
+          L.bn = bn;
+        }
+      }
+    }
     const long long units = ((long long)ceil_div(a.T, L.bn) + groups - 1) * L.n_tiles;
-    return launch_linear_pair(L, units > 4096 ? 4096 : (int)units, stream);
+    return launch_linear_pair(L, units, stream);
   }
-  int bn = ceil_div(mean, ceil_div(mean, 128));
+  // Dense: the rows, cut evenly. Groups: room for the larger ones, in steps of 16 up to 64 (mean 16: 73.5
+  // us with 64 against 82.6 with 16; mean 2: 65.9 and 66.3).
+  int bn = a.offsets ? 4 * mean : ceil_div(mean, ceil_div(mean, 128));
   bn = (bn + 15) & ~15;
+  if (a.offsets && bn > 64) bn = 64;
   L.bn = bn;
-  L.n_tiles = ceil_div(a.cols, cols);
   L.gm = 1 << 16;
-  const long long units = ((long long)ceil_div(a.T, L.bn) + groups - 1) * L.n_tiles;
-  // the cluster: as many CTAs a unit as the units leave free
-  int best = 1;
-  double best_cost = 1e30;
+  // The cut: tiles of R weight rows, C CTAs to a tile, in whole rounds. No cut is faster than HBM; a
+  // join of partial sums and the cluster's start take about 3.5 us, and some more for the sums' size.
+  const bool gated = a.act == GBMOE_EPI_SILU_MUL;
+  const int grain = gated ? 32 : 8;                          // rows per step of R
+  const long long blocks = ceil_div(a.T, L.bn) + (a.offsets ? groups - 1 : 0);
+  const int n = bn;
+  const double hbm = (double)groups * a.N * a.K * (a.fp8 ? 1 : 2) / 6700;
+  double best = 1e30;
+  int best_C = 1, best_R = 128;
   for (int C = 1; C <= 8 && C <= L.k_blocks; ++C) {
-    const int room = num_sms() / C;
-    const double cost = ceil_div(units, room) * (ceil_div(L.k_blocks, C) + (C > 1 ? 4 : 2));
-    if (cost < best_cost * 0.999) {
-      best_cost = cost;
-      best = C;
+    const int room = linear_stream_room(a, C);
+    if (room < 1) return cudaErrorInvalidConfiguration;
+    const int kb = ceil_div(L.k_blocks, C);
+    for (int rounds = 1; rounds <= 8; ++rounds) {
+      const long long tiles = (long long)room * rounds / blocks;  // of one group's rows
+      int R = tiles < 1 ? 129 : ceil_div(a.N, tiles);
+      R = ceil_div(R < 8 ? 8 : R, grain) * grain;
+      if (gated && a.fp8 && R == 96) R = 128;      // a tile has one scale block of either kind
+      const bool last = rounds == 8;
+      if (R > 128) {
+        if (!last) continue;
+        R = 128;
+      }
+      const int turns = ceil_div(blocks * ceil_div(a.N, R), room);
+      const double run = (double)turns * lin_unit_ns(a.fp8, R, n, kb);
+      const double cost = (run > hbm ? run : hbm) + (C > 1 ? turns * (3500 + n * R / 20.0) : 0);
+      if (cost < best * 0.98) {
+        best = cost;
+        best_C = C;
+        best_R = R;
+      }
     }
   }
-  return launch_linear_stream(L, best, units > 4096 ? 4096 : (int)units, stream);
+  L.cluster = best_C;
+  if (a.offsets) {                                 // the kernel cuts by the rows that it finds
+    L.rows[0] = 128;
+    L.rows[1] = 64;
+    L.rows[2] = 32;
+    L.choices = 3;
+  } else {
+    L.rows[0] = best_R;
+    L.choices = 1;
+  }
+  const int least = L.rows[L.choices - 1];
+  L.n_tiles = ceil_div(a.cols, gated ? least / 2 : least);
+  return launch_linear_stream(L, blocks * L.n_tiles, stream);
 }
 
 }  // namespace gbmoe

@@ -7,8 +7,8 @@
 // fastest within sections of `gm` blocks, so that a weight tile is read from HBM once.
 //
 // Both types have K blocks of 128 bytes (64 bf16, 128 e4m3: one swizzle row, one scale block).
-// With SILU_MUL a tile of 128 weight rows holds 16 gate rows, the 16 up rows of the same features,
-// and so on, through a five-dimensional tensor map: lane l < 16 of a warp then has the gate and lane
+// With SILU_MUL a tile of weight rows holds 16 gate rows, the 16 up rows of the same features, and
+// so on, through a five-dimensional tensor map: lane l < 16 of a warp then has the gate and lane
 // l + 16 the up half of one feature, and a shuffle brings them together.
 #pragma once
 
@@ -17,9 +17,8 @@
 
 namespace gbmoe {
 
-constexpr int kLinWRows = 128;                  // weight rows per CTA and unit
+constexpr int kLinWRows = 128;                  // weight rows per CTA and MMA
 constexpr uint32_t kLinWBytes = kLinWRows * 128;
-constexpr int kLinScaleSlots = 8;               // e4m3: K blocks of row scales in flight
 constexpr uint32_t kLinSmemMax = 232448;
 
 // One launch: the call, and how it is cut.
@@ -31,10 +30,25 @@ struct LinLaunch {
   int k_blocks;
   int stages;
   int tab_off;     // byte offsets in shared memory, from the aligned base: group table,
-  int red_off;     // partial sums of a cluster (stream kernel),
-  int scale_off;   // row scales (e4m3),
-  int bar_off;     // barriers
+  int bar_off;     // barriers,
+  int red_off;     // (stream kernel) partial sums of a cluster,
+  int scale_off;   // row scales (e4m3)
+  // stream kernel
+  int cluster;     // CTAs that cut a unit's K blocks
+  int rows[3];     // weight rows per tile: the choices (the kernel picks, by its groups), largest first,
+  int choices;     // and how many
+  int kps;         // K blocks per stage
+  int whole;       // K is whole K blocks: a box takes kps of them
 };
+
+// The stream kernel's time for a unit of R weight rows and n rows of x over so many K blocks, in ns, fitted
+// to measurements at K = N = 4096: a CTA takes 128 bytes a ns from L2 and HBM together; a K block's
+// MMAs, whose time goes by their 128 rows, and the operands of its columns take 90 and 1 a row (e4m3: its
+// promotion 90 and 5); a unit's beginning and end 300.
+__host__ __device__ inline int lin_unit_ns(bool fp8, int R, int n, int k_blocks) {
+  const int math = 90 + (fp8 ? 5 * n : n);
+  return k_blocks * (R + n > math ? R + n : math) + 300;
+}
 
 namespace {
 
@@ -44,6 +58,22 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(v), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                 int x, int y, int z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_5d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -56,6 +86,14 @@ __device__ __forceinline__ void tma_load_5d_hint(uint32_t dst, const CUtensorMap
       "l"(policy)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t bar_cluster, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap* map,
                                                  uint32_t bar_cluster, int x, int y, int z, int v,
                                                  int w) {
@@ -65,6 +103,16 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "r"(v),
       "r"(w)
       : "memory");
+}
+// One thread of a converged warp. Unlike a test of the lane it tells the compiler that there is one, so
+// that the descriptors of the TMA and MMA instructions stay in uniform registers (with a test of the lane
+// each TMA took 70 ns to issue, with this one a few).
+__device__ __forceinline__ bool lin_elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 // a0 += s0 * v0, a1 += s1 * v1 (two IEEE fmas in one instruction).
 __device__ __forceinline__ void fma2(float& a0, float& a1, float s0, float s1, float v0, float v1) {
@@ -131,109 +179,35 @@ struct LinGroups {
     __syncthreads();
   }
 
-  __device__ __forceinline__ int units(const LinLaunch& L) const { return before[G] * L.n_tiles; }
+  __device__ __forceinline__ int units(int n_tiles) const { return before[G] * n_tiles; }
 
-  __device__ __forceinline__ LinUnit unit(const LinLaunch& L, int u) const {
-    const int b = u / L.n_tiles;
+  __device__ __forceinline__ LinUnit unit(const LinLaunch& L, int n_tiles, int u) const {
+    const int b = u / n_tiles;
     int g = 0, end = G;
     while (end - g > 1) {
       const int mid = (g + end) >> 1;
       if (before[mid] <= b) g = mid;
       else end = mid;
     }
-    const int blocks = before[g + 1] - before[g];
-    const int s0 = (b - before[g]) / L.gm * L.gm;  // this section's first block
+    return place(L, n_tiles, u, g, before[g], before[g + 1] - before[g], first[g], rows[g]);
+  }
+
+  // Unit u of group g, whose `blocks` row blocks come after `before` others.
+  __device__ __forceinline__ static LinUnit place(const LinLaunch& L, int n_tiles, int u, int g,
+                                                  int before, int blocks, int first, int rows) {
+    const int s0 = (u / n_tiles - before) / L.gm * L.gm;  // this section's first block
     const int sn = min(L.gm, blocks - s0);
-    const int local = u - (before[g] + s0) * L.n_tiles;
+    const int local = u - (before + s0) * n_tiles;
     LinUnit r;
     r.g = g;
     r.nt = local / sn;
     const int at = (s0 + local % sn) * L.bn;
-    r.m0 = first[g] + at;
-    r.n = min(L.bn, rows[g] - at);
+    r.m0 = first + at;
+    r.n = min(L.bn, rows - at);
     r.alone = blocks == 1;
     return r;
   }
 };
-
-// ---------------------------------------------------------------- scales (e4m3)
-// One warp walks the CTA's K blocks ahead of the epilogue and writes, for each of the unit's rows
-// c, the product of its scale and the weight block's: scale[c], or with GATED [c / 4][gate, up][c % 4],
-// so that the 16 gate and the 16 up lanes of a warp read neighbouring 16 bytes.
-template <bool GATED>
-__device__ __forceinline__ int lin_scale_at(int c, int up) {
-  return GATED ? (c >> 2) * 8 + up * 4 + (c & 3) : c;
-}
-
-template <bool GATED, int COLS>  // COLS: rows per block at most
-struct LinScales {
-  static constexpr int kPer = COLS / 32, kBatch = 4;
-
-  // K blocks [kb0, kb1) of one unit; row: the first weight row of this CTA's tile (with GATED the
-  // gate's). false: a wait ran out.
-  __device__ __forceinline__ static bool unit(const LinLaunch& L, const LinUnit& w, int row, int kb0,
-                                              int kb1, float* ring, int slot_floats, uint32_t full0,
-                                              uint32_t empty0, uint32_t& it, volatile int* abort_flag) {
-    const LinearArgs& a = L.a;
-    const int lane = threadIdx.x & 31;
-    const int wblocks = (a.N + 127) >> 7;
-    const float* ws = a.w_scale + ((long long)w.g * wblocks + min(row >> 7, wblocks - 1)) * L.k_blocks;
-    const float* wu = GATED ? ws + (long long)(a.cols >> 7) * L.k_blocks : ws;
-    const float* xs = a.x_scale + w.m0 + lane;
-    for (int kb = kb0; kb < kb1; kb += kBatch) {
-      float v[kBatch][kPer], g[kBatch], u[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const bool in = kb + i < kb1;
-        g[i] = in ? __ldg(ws + kb + i) : 0.f;
-        u[i] = GATED && in ? __ldg(wu + kb + i) : 0.f;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          v[i][j] = in && lane + 32 * j < w.n ? __ldg(xs + (long long)(kb + i) * a.T + 32 * j) : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (kb + i >= kb1) break;
-        const int slot = it % kLinScaleSlots;
-        const uint32_t ph = (it / kLinScaleSlots) & 1u;
-        if (!wait_fast(empty0 + 8u * slot, ph ^ 1u, abort_flag, a.status)) return false;
-        float* dst = ring + slot * slot_floats;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int c = lane + 32 * j;
-          if (c < L.bn) {
-            dst[lin_scale_at<GATED>(c, 0)] = v[i][j] * g[i];
-            if (GATED) dst[lin_scale_at<GATED>(c, 1)] = v[i][j] * u[i];
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full0 + 8u * slot);
-        ++it;
-      }
-    }
-    return true;
-  }
-};
-
-// acc[i] += scale * block product for 16 columns from column c0 of a K block's TMEM buffer.
-template <bool GATED>
-__device__ __forceinline__ void lin_promote16(float* acc, uint32_t tmem, const float* scales, int c0,
-                                              int up) {
-  uint32_t v[16];
-  tmem_ld16(tmem + c0, v);
-  float4 s[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    s[q] = *reinterpret_cast<const float4*>(scales + lin_scale_at<GATED>(c0 + 4 * q, up));
-  tmem_wait_ld16(v);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    fma2(acc[4 * q], acc[4 * q + 1], s[q].x, s[q].y, __uint_as_float(v[4 * q]),
-         __uint_as_float(v[4 * q + 1]));
-    fma2(acc[4 * q + 2], acc[4 * q + 3], s[q].z, s[q].w, __uint_as_float(v[4 * q + 2]),
-         __uint_as_float(v[4 * q + 3]));
-  }
-}
 
 // ---------------------------------------------------------------- epilogue
 // The quotients by __fdividef: 2 ulp, where the result is rounded to bf16 next. A denominator past
@@ -413,12 +387,19 @@ __device__ __forceinline__ void lin_store_row(const LinearArgs& a, int g, int t,
 
 }  // namespace
 
-// Tensor maps of a call: the weights as this CTA tile's 128 rows, x with boxes of x_box rows.
-bool lin_maps(const LinearArgs& a, int x_box, CUtensorMap* w, CUtensorMap* x);
-// The same with the weights as plain rows, in boxes of 128, and x in boxes of x_box.
-bool lin_map_rows(const LinearArgs& a, CUtensorMap* w, CUtensorMap* x, int x_box);
-cudaError_t launch_linear_stream(LinLaunch L, int cluster, int max_units, cudaStream_t stream);
-cudaError_t launch_linear_pair(LinLaunch L, int max_units, cudaStream_t stream);
-cudaError_t launch_linear_fp8(LinLaunch L, int max_units, cudaStream_t stream);
+// Tensor maps of a call: boxes of 128 bytes of so many rows, at (element, row, 0); or with kps > 0, for
+// which K has to be whole K blocks (lin_whole), of kps K blocks at (0, row, K block). x:
+inline bool lin_whole(const LinearArgs& a) { return a.K % (a.fp8 ? 128 : 64) == 0; }
+bool lin_map_x(const LinearArgs& a, int rows, int kps, CUtensorMap* x);
+// the weights as plain rows;
+bool lin_map_rows(const LinearArgs& a, int rows, int kps, CUtensorMap* w);
+// or, with SILU_MUL, in tiles of 16 gate rows, their 16 up rows, and so on: (element, 0, 2 group,
+// block of 16 features, 0), or (0, 0, 2 group, block, K block).
+bool lin_map_tiles(const LinearArgs& a, int rows, int kps, CUtensorMap* w);
+// Clusters of `size` CTAs of the stream kernel that the device holds (0: an error).
+int linear_stream_room(const LinearArgs& a, int size);
+cudaError_t launch_linear_stream(LinLaunch L, long long max_units, cudaStream_t stream);
+cudaError_t launch_linear_pair(LinLaunch L, long long max_units, cudaStream_t stream);
+cudaError_t launch_linear_fp8(LinLaunch L, long long max_units, cudaStream_t stream);
 
 }  // namespace gbmoe

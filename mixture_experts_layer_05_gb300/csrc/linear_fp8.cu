@@ -10,9 +10,10 @@
 // with pairs of CTAs it crosses SMs (measured: 674 us for 8192 rows of 7168 to 4096 columns).
 //
 // Unit: 128 rows of one group by 256 weight rows (SILU_MUL: 128 gate rows and their up rows).
-// Warps: 0 TMA, 1 TMEM and MMA, 2..9 epilogue: the two warps of a TMEM lane quarter take 128 columns
-// each, of which every thread keeps the running sums of its row; the next 8 columns are on their
-// way from TMEM while 8 are added.
+// Warps: 0 TMA, 1 TMEM and MMA, 2..17 epilogue: the four warps of a TMEM lane quarter take 64 columns
+// each, of which every thread keeps the running sums of its row (four warps of an SM's quarter hide
+// the latency of TMEM better than two with 128 columns each); 18 scales: it writes the products
+// of the rows' and the weights' scales of a K block beside the TMEM buffer that they belong to.
 #include "linear.cuh"
 
 namespace gbmoe {
@@ -20,25 +21,12 @@ namespace {
 
 constexpr int kBM = 128, kBN = 256;
 constexpr int kStages = 4;
-constexpr int kEpiWarps = 8;
-constexpr int kCols = 128;                       // accumulator columns of an epilogue thread
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kEpiWarps = 16;
+constexpr int kCols = 64;                        // accumulator columns of an epilogue thread
+constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
 constexpr uint32_t kABytes = kBM * 128, kBBytes = kBN * 128, kStageBytes = kABytes + kBBytes;
 constexpr uint32_t kTmemCols = 512, kStride = 256;
-constexpr int kAhead = 2;                        // K blocks that the scales' loads run ahead
-
-// 32 lanes x 8 consecutive fp32 columns.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait_ld8(uint32_t (&r)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7])::"memory");
-}
+constexpr int kAhead = 4;                        // K blocks that the scales' loads run ahead
 
 template <bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -53,6 +41,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const LinearArgs& a = L.a;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bar_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+  // [buffer][row][columns 0 .. 127, 128 .. 255 of the tile]
+  float2* scales = reinterpret_cast<float2*>(smem + L.scale_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t bar0 = smem_addr(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -60,14 +50,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kStages + 2 + b); };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(tfull_bar(b), 1);
+      mbar_init(tfull_bar(b), 2);                  // the products and the scales
       mbar_init(tempty_bar(b), kEpiWarps);
     }
     *abort_flag = 0;
@@ -84,29 +74,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   groups.load(L);                                  // ends with a barrier of the block
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int units = groups.units(L);
+  const int units = groups.units(L.n_tiles);
   const int KB = L.k_blocks;
+  int* const status = a.status;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    if (lin_elect()) {
       int s = 0;
       uint32_t ph = 1;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const LinUnit w = groups.unit(L, u);
+        const LinUnit w = groups.unit(L, L.n_tiles, u);
         const int row = w.g * a.N + w.nt * kTileCols;
         const int row1 = row + (GATED ? a.cols : 128);
         for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_fast(empty_bar(s), ph, abort_flag, a.status)) {
+          if (!wait_fast(empty_bar(s), ph, abort_flag, status)) {
             ok = false;
             break;
           }
           const uint32_t sa = base + s * kStageBytes;
           mbar_expect_tx(full_bar(s), kStageBytes);
-          tma_load_2d(sa, &tm_x, full_bar(s), kb * 128, w.m0);
-          tma_load_2d(sa + kABytes, &tm_w, full_bar(s), kb * 128, row);
-          tma_load_2d(sa + kABytes + kBBytes / 2, &tm_w, full_bar(s), kb * 128, row1);
+          tma_load_3d(sa, &tm_x, full_bar(s), kb * 128, w.m0, 0);
+          tma_load_3d(sa + kABytes, &tm_w, full_bar(s), kb * 128, row, 0);
+          tma_load_3d(sa + kABytes + kBBytes / 2, &tm_w, full_bar(s), kb * 128, row1, 0);
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
@@ -117,15 +108,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (lin_elect()) {
       constexpr uint32_t idesc = idesc_e4m3(kBM, kBN);
       int s = 0, buf = 0;
       uint32_t ph = 0, tph = 1;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_fast(tempty_bar(buf), tph, abort_flag, a.status) ||
-              !wait_fast(full_bar(s), ph, abort_flag, a.status)) {
+          if (!wait_fast(tempty_bar(buf), tph, abort_flag, status) ||
+              !wait_fast(full_bar(s), ph, abort_flag, status)) {
             ok = false;
             break;
           }
@@ -148,75 +139,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;                  // rows [32 quarter, + 32) of the block
-    const int part = (warp - 2) >> 2;              // which half of the accumulator
-    const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    const int part = (warp - 2) >> 2;              // which columns of the accumulator:
+    // SILU_MUL gate [32 part, + 32) and up [128 + 32 part, + 32), else [64 part, + 64)
+    const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16) + (GATED ? 32 : 64) * part;
     const int r = quarter * 32 + lane;
-    const int wblocks = (a.N + 127) >> 7;
     int buf = 0;
     uint32_t tph = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const LinUnit w = groups.unit(L, u);
-      // this thread's columns: SILU_MUL gate [64 part, + 64) and up [128 + 64 part, + 64), else
-      // [128 part, + 128)
-      const int f0 = w.nt * kTileCols + part * (kTileCols / 2);
-      const float* w0 = a.w_scale + ((long long)w.g * wblocks + min(f0 >> 7, wblocks - 1)) * KB;
-      const float* w1 = GATED ? w0 + (long long)(a.cols >> 7) * KB : w0;
-      const bool in = r < w.n;
-      const float* xs = a.x_scale + w.m0 + (in ? r : 0);
-      float acc[kCols], sx[kAhead], s0[kAhead], s1[kAhead];
+      float acc[kCols];
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-      auto fetch = [&](int kb, int i) {
-        if (kb >= KB) return;
-        sx[i] = __ldg(xs + (long long)kb * a.T);
-        s0[i] = __ldg(w0 + kb);
-        if (GATED) s1[i] = __ldg(w1 + kb);
-      };
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!wait_fast(tfull_bar(buf), tph, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tb = lanes + buf * kStride;
+        const float2 sc = scales[buf * kBM + r];
+        const float s0 = GATED || part < 2 ? sc.x : sc.y;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) fetch(i, i);
+        for (int c = 0; c < kCols / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld16(tb + (GATED && c >= 2 ? 96 + 16 * c : 16 * c), v);
+          const float k = GATED && c >= 2 ? sc.y : s0;
+          tmem_wait_ld16(v);
+#pragma unroll
+          for (int q = 0; q < 16; q += 2)
+            fma2(acc[16 * c + q], acc[16 * c + q + 1], k, k, __uint_as_float(v[q]),
+                 __uint_as_float(v[q + 1]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty_bar(buf));
+        buf ^= 1;
+        if (buf == 0) tph ^= 1u;
+      }
+      if (!ok) break;
+      const LinUnit w = groups.unit(L, L.n_tiles, u);
+      if (r < w.n) lin_store_row<GATED>(a, w.g, w.m0 + r, w.nt * kTileCols + part * (kTileCols / 4), acc);
+    }
+  } else {
+    // ------------------------------------------------------------ scales
+    const int wblocks = (a.N + 127) >> 7;
+    int buf = 0;
+    uint32_t tph = 1;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      const LinUnit w = groups.unit(L, L.n_tiles, u);
+      const int b0 = w.nt * (kTileCols / 128), b1 = GATED ? b0 + (a.cols >> 7) : min(b0 + 1, wblocks - 1);
+      const float* w0 = a.w_scale + ((long long)w.g * wblocks + b0) * KB;
+      const float* w1 = a.w_scale + ((long long)w.g * wblocks + b1) * KB;
+      const float* xs = a.x_scale + w.m0 + lane;
       for (int kb0 = 0; ok && kb0 < KB; kb0 += kAhead) {
+        float x[kAhead][4], s0[kAhead], s1[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          const int kb = kb0 + i;
-          if (kb >= KB) break;
-          const float c0 = sx[i] * s0[i], c1 = GATED ? sx[i] * s1[i] : c0;
-          fetch(kb + kAhead, i);
-          if (!wait_fast(tfull_bar(buf), tph, abort_flag, a.status)) {
+          const bool in = kb0 + i < KB;
+          s0[i] = in ? __ldg(w0 + kb0 + i) : 0.f;
+          s1[i] = in ? __ldg(w1 + kb0 + i) : 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            x[i][q] = in && lane + 32 * q < w.n ? __ldg(xs + (long long)(kb0 + i) * a.T + 32 * q) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (kb0 + i >= KB) break;
+          if (!wait_fast(tempty_bar(buf), tph, abort_flag, status)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t tb = lanes + buf * kStride;
-          auto col = [&](int c) {
-            return GATED ? (c < 8 ? 64 * part + 8 * c : 64 + 64 * part + 8 * c)
-                         : 128 * part + 8 * c;
-          };
-          uint32_t v[2][8];
-          tmem_ld8(tb + col(0), v[0]);
-          tmem_wait_ld8(v[0]);
 #pragma unroll
-          for (int c = 0; c < kCols / 8; ++c) {
-            if (c + 1 < kCols / 8) tmem_ld8(tb + col(c + 1), v[(c + 1) & 1]);
-            const float sc = GATED && c >= 8 ? c1 : c0;
-#pragma unroll
-            for (int q = 0; q < 8; q += 2)
-              fma2(acc[8 * c + q], acc[8 * c + q + 1], sc, sc, __uint_as_float(v[c & 1][q]),
-                   __uint_as_float(v[c & 1][q + 1]));
-            if (c + 1 < kCols / 8) tmem_wait_ld8(v[(c + 1) & 1]);
-          }
-          tc_fence_before();
+          for (int q = 0; q < 4; ++q)
+            scales[buf * kBM + lane + 32 * q] = make_float2(x[i][q] * s0[i], x[i][q] * s1[i]);
           __syncwarp();
-          if (lane == 0) mbar_arrive(tempty_bar(buf));
+          if (lane == 0) mbar_arrive(tfull_bar(buf));
           buf ^= 1;
           if (buf == 0) tph ^= 1u;
         }
       }
-      if (!ok) break;
-      if (in) lin_store_row<GATED>(a, w.g, w.m0 + r, f0, acc);
     }
   }
 
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool GATED>
-cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& L, int units,
+cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& L, long long units,
                    size_t smem, cudaStream_t stream) {
   auto kernel = linear_fp8_kernel<GATED>;
   static bool ready[64];
@@ -241,22 +246,23 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& 
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  const int grid = units < num_sms() ? units : num_sms();
+  const int grid = units < num_sms() ? (int)units : num_sms();
   kernel<<<grid, kThreads, smem, stream>>>(w, x, L);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_linear_fp8(LinLaunch L, int max_units, cudaStream_t stream) {
+cudaError_t launch_linear_fp8(LinLaunch L, long long max_units, cudaStream_t stream) {
   const LinearArgs& a = L.a;
   if (!a.fp8 || L.bn != kBM) return cudaErrorInvalidValue;
   L.stages = kStages;
-  L.bar_off = kStages * kStageBytes;
+  L.scale_off = kStages * kStageBytes;
+  L.bar_off = L.scale_off + 2 * kBM * (int)sizeof(float2);
   const uint32_t bars = (2 * kStages + 4) * 8 + 16;
   L.tab_off = L.bar_off + bars;
   CUtensorMap w, x;
-  if (!lin_map_rows(a, &w, &x, kBM)) return cudaErrorInvalidValue;
+  if (!lin_map_rows(a, 128, 0, &w) || !lin_map_x(a, kBM, 0, &x)) return cudaErrorInvalidValue;
   const size_t smem = L.tab_off + 4 * (3 * a.G + 1) + 1024;
   return a.act == GBMOE_EPI_SILU_MUL ? launch<true>(w, x, L, max_units, smem, stream)
                                      : launch<false>(w, x, L, max_units, smem, stream);

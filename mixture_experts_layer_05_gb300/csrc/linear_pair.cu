@@ -21,11 +21,15 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kBars = 2 * kMaxStages + 4;
 
+// The weights, and x in boxes of bn / 2 and of kFewRows rows.
+constexpr int kFewRows = 32;
+struct Maps {
+  CUtensorMap w, x, x_few;
+};
+
 template <bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
-    linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w,
-                       const __grid_constant__ CUtensorMap tm_x,
-                       const __grid_constant__ LinLaunch L) {
+    linear_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LinLaunch L) {
   constexpr int kTileCols = GATED ? 64 : 128;      // output columns per CTA and unit
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -33,7 +37,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + (base - raw);
   const LinearArgs& a = L.a;
   const int stages = L.stages;
-  const uint32_t x_bytes = (uint32_t)(L.bn / 2) * 128, stage_bytes = kLinWBytes + x_bytes;
+  const uint32_t stage_bytes = kLinWBytes + (uint32_t)(L.bn / 2) * 128;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bar_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -43,7 +47,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
@@ -57,8 +61,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch(&tm_w);
-    tma_prefetch(&tm_x);
+    tma_prefetch(&maps.w);
+    tma_prefetch(&maps.x);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_addr(tmem_slot), kTmemCols);
@@ -72,32 +76,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t leader_full0 = mapa_shared(full_bar(0), 0);
   const uint32_t leader_tempty0 = mapa_shared(tempty_bar(0), 0);
-  const int units = groups.units(L);
+  const int units = groups.units(L.n_tiles);
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // in registers: behind an asm statement that touches memory, the launch's values are loaded again
+  const int KB = L.k_blocks, out_features = a.N, half_bn = L.bn / 2;
+  const bool grouped = a.offsets != nullptr;
+  int* const status = a.status;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    if (lin_elect()) {
       int s = 0;
       uint32_t ph = 1;
       bool ok = true;
       for (int u = first; ok && u < units; u += step) {
-        const LinUnit w = groups.unit(L, u);
+        const LinUnit w = groups.unit(L, L.n_tiles, u);
         const int half = ((w.n + 15) & ~15) / 2;
         const int x_row = w.m0 + rank * half;
-        const int tile = w.nt * 2 + rank;
-        for (int kb = 0; kb < L.k_blocks; ++kb) {
-          if (!wait_fast(empty_bar(s), ph, abort_flag, a.status)) {
+        const int tile = w.nt * 2 + rank, w_row = w.g * out_features + tile * kTileCols;
+        const bool few = grouped && half <= kFewRows && half_bn > kFewRows;
+        const CUtensorMap* tx = few ? &maps.x_few : &maps.x;
+        const int xr = few ? kFewRows : half_bn;
+        const uint32_t bytes = 2u * (kLinWBytes + (uint32_t)xr * 128);   // both CTAs'
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait_fast(empty_bar(s), ph, abort_flag, status)) {
             ok = false;
             break;
           }
-          if (leader) mbar_expect_tx(full_bar(s), 2 * stage_bytes);  // both CTAs' bytes
+          if (leader) mbar_expect_tx(full_bar(s), bytes);
           const uint32_t fb = leader_full0 + 8u * s, sw = base + s * stage_bytes;
           if (GATED)
-            tma_load_5d_pair(sw, &tm_w, fb, kb * kGemmBK, 0, 0, tile * (kTileCols / 16), w.g);
+            tma_load_5d_pair(sw, &maps.w, fb, kb * kGemmBK, 0, 2 * w.g, tile * (kTileCols / 16), 0);
           else
-            tma_load_2d_pair(sw, &tm_w, fb, kb * kGemmBK, w.g * a.N + tile * kTileCols);
-          tma_load_2d_pair(sw + kLinWBytes, &tm_x, fb, kb * kGemmBK, x_row);
+            tma_load_3d_pair(sw, &maps.w, fb, kb * kGemmBK, w_row, 0);
+          tma_load_3d_pair(sw + kLinWBytes, tx, fb, kb * kGemmBK, x_row, 0);
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
@@ -108,17 +120,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader only)
-    if (leader && lane == 0) {
+    if (leader && lin_elect()) {
       int s = 0, buf = 0;
       uint32_t ph = 0, tph = 1;
       bool ok = true;
       for (int u = first; ok && u < units; u += step) {
-        const LinUnit w = groups.unit(L, u);
+        const LinUnit w = groups.unit(L, L.n_tiles, u);
         const int n = (w.n + 15) & ~15;
         const uint32_t idesc = idesc_bf16(256, n);
-        for (int kb = 0; kb < L.k_blocks; ++kb) {
-          if ((kb == 0 && !wait_fast(tempty_bar(buf), tph, abort_flag, a.status)) ||
-              !wait_fast(full_bar(s), ph, abort_flag, a.status)) {
+        for (int kb = 0; kb < KB; ++kb) {
+          if ((kb == 0 && !wait_fast(tempty_bar(buf), tph, abort_flag, status)) ||
+              !wait_fast(full_bar(s), ph, abort_flag, status)) {
             ok = false;
             break;
           }
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s = 0;
             ph ^= 1u;
           }
-          if (kb == L.k_blocks - 1) {
+          if (kb == KB - 1) {
             mma_commit_pair(tfull_bar(buf));
             buf ^= 1;
             if (buf == 0) tph ^= 1u;
@@ -152,10 +164,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int buf = 0;
     uint32_t tph = 0;
     for (int u = first; u < units; u += step) {
-      const LinUnit w = groups.unit(L, u);
+      const LinUnit w = groups.unit(L, L.n_tiles, u);
       const LinLane l = LinLane::make<GATED>(
           a, w.g, (w.nt * 2 + rank) * kTileCols + quarter * (kTileCols / 4));
-      if (!wait_fast(tfull_bar(buf), tph, abort_flag, a.status)) break;
+      if (!wait_fast(tfull_bar(buf), tph, abort_flag, status)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int at = part * 32; at < w.n; at += 64) {
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool GATED>
-cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& L, int units,
+cudaError_t launch(const Maps& maps, const LinLaunch& L, long long units,
                    size_t smem, cudaStream_t stream) {
   auto kernel = linear_pair_kernel<GATED>;
   static bool ready[64];
@@ -196,7 +208,7 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& 
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  const int most = num_sms() / 2, clusters = units < most ? units : most;
+  const int most = num_sms() / 2, clusters = units < most ? (int)units : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
   cfg.blockDim = dim3(kThreads);
@@ -208,12 +220,12 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, w, x, L);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, L);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_pair(LinLaunch L, int max_units, cudaStream_t stream) {
+cudaError_t launch_linear_pair(LinLaunch L, long long max_units, cudaStream_t stream) {
   const LinearArgs& a = L.a;
   if (a.fp8 || L.bn < 32 || L.bn > kMaxBn || L.bn % 32) return cudaErrorInvalidValue;
   const uint32_t stage = kLinWBytes + L.bn / 2 * 128;
@@ -224,11 +236,13 @@ cudaError_t launch_linear_pair(LinLaunch L, int max_units, cudaStream_t stream) 
   L.stages = stages;
   L.bar_off = stages * stage;
   L.tab_off = L.bar_off + bars;
-  CUtensorMap w, x;
-  if (!lin_maps(a, L.bn / 2, &w, &x)) return cudaErrorInvalidValue;
+  Maps maps;
+  if (!lin_map_tiles(a, kLinWRows, 0, &maps.w) || !lin_map_x(a, L.bn / 2, 0, &maps.x) ||
+      (a.offsets && !lin_map_x(a, kFewRows, 0, &maps.x_few)))
+    return cudaErrorInvalidValue;
   const size_t smem = stages * stage + rest;
-  return a.act == GBMOE_EPI_SILU_MUL ? launch<true>(w, x, L, max_units, smem, stream)
-                                     : launch<false>(w, x, L, max_units, smem, stream);
+  return a.act == GBMOE_EPI_SILU_MUL ? launch<true>(maps, L, max_units, smem, stream)
+                                     : launch<false>(maps, L, max_units, smem, stream);
 }
 
 }  // namespace gbmoe

@@ -1,14 +1,21 @@
 // moe_linear / moe_grouped_linear for few rows per group: bound by reading the weights.
 //
-// A cluster of C CTAs takes a unit (128 weight rows by at most bn rows of x) and cuts its K blocks into C
-// ranges, so that even a small layer keeps every SM reading. Each CTA streams its range through a ring
-// of TMA stages into one TMEM accumulator (tcgen05.mma, M = 128, N = the rows rounded up to 16). The C
-// partial sums are joined through distributed shared memory: each CTA sends the columns that CTA d
-// finishes to d, which adds them in the order of the ranges and runs the epilogue, so the result does
-// not depend on timing, and nothing is kept in a workspace between calls.
+// One SM draws about 48 GB/s from HBM through TMA, however deep its ring is (measured with 48 to 152
+// CTAs), so the 6.8 TB/s need every SM, all of them for the same time. So the tile is cut to the SMs
+// rather than to the MMA: a unit is R <= 128 weight rows by at most bn rows of x, where R is such that
+// the units come out in whole rounds; the MMA (tcgen05.mma, M = 128) runs over R rows and over what lies
+// behind them in shared memory, whose TMEM lanes nobody reads. Where the rows of x are many against R,
+// their reading costs more than that of the weights; there a cluster of C CTAs takes a tile of C times
+// the rows and cuts its K blocks into C ranges. The C partial sums are joined through distributed
+// shared memory: each CTA sends the columns that CTA d finishes to d (one bulk copy each), which adds
+// them in the order of the ranges, so that the result does not depend on timing and nothing is kept in
+// a workspace between calls.
 //
-// Warps: 0 TMA, 1 TMEM and MMA, 2..5 epilogue (one TMEM lane quarter each), 6 (e4m3) scales. e4m3
-// products are promoted to fp32 with their scales K block by K block, as the FP8 layer's are.
+// Warps: 0 TMA, 1 TMEM and MMA, 2..9 epilogue (two per TMEM lane quarter, alternating by 16 columns), 10
+// (e4m3) scales. e4m3 products are promoted to fp32 with their scales K block by K block, as the FP8
+// layer's are: each K block of a stage has its own TMEM columns.
+#include <cstdlib>
+
 #include "linear.cuh"
 
 namespace gbmoe {
@@ -16,33 +23,62 @@ namespace {
 
 constexpr int kMaxBn = 128;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 16;
+constexpr int kMaxKps = 8;                       // K blocks per stage
+constexpr int kXMaps = 2;                        // x boxes of bn and of 8 rows
+constexpr int kWMaps = 3;                        // weight boxes of L.rows[i] rows
 constexpr uint32_t kTmemCols = 512;
-constexpr int kEpiWarps = 4;
-constexpr int kBufsMax = 32;                     // K block buffers (e4m3): 512 / 16
+constexpr int kEpiWarps = 8;
+constexpr int kBufsMax = 8;                      // TMEM buffers
+constexpr int kScaleSlots = 4;                   // e4m3: stages of scales in flight
 
 constexpr int threads_of(bool fp8) { return 64 + 32 * kEpiWarps + (fp8 ? 32 : 0); }
-// barriers: full, empty per stage; tfull, tempty per TMEM buffer; red full, red empty; scale full,
-// empty per slot
-constexpr int kBars = 2 * kMaxStages + 2 * kBufsMax + 2 + 2 * kLinScaleSlots;
+// barriers: full, empty per stage; tfull, tempty per TMEM buffer; partial sums received, sent ones
+// consumed; scales full, empty per slot
+constexpr int kBars = 2 * kMaxStages + 2 * kBufsMax + 2 + 2 * kScaleSlots;
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+struct Maps {
+  CUtensorMap w[kWMaps];
+  CUtensorMap x[kXMaps];
+};
+
+// Shared memory to the shared memory of a CTA of the cluster, counted on a barrier there.
+__device__ __forceinline__ void copy_to_cluster(uint32_t dst, uint32_t src, uint32_t bytes,
+                                                uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void epilogue_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// Scales of a slot: for K block j of the stage and row c, the products with the two weight blocks that
+// a tile can meet (gate and up; or the blocks before and behind a border of 128 rows), four rows of
+// one next to four of the other, so that lanes of both kinds read without conflicts.
+__device__ __forceinline__ int scale_at(int bn, int j, int c, int kind) {
+  return j * 2 * bn + (c >> 2) * 8 + kind * 4 + (c & 3);
 }
 
 template <bool FP8, bool GATED>
 __global__ void __launch_bounds__(threads_of(FP8), 1)
-    linear_stream_kernel(const __grid_constant__ CUtensorMap tm_w,
-                         const __grid_constant__ CUtensorMap tm_x,
-                         const __grid_constant__ LinLaunch L, const int C) {
+    linear_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LinLaunch L) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const LinearArgs& a = L.a;
-  const int bn = L.bn, stages = L.stages;
-  const uint32_t stage_bytes = kLinWBytes + (uint32_t)bn * 128;
-  float* red = reinterpret_cast<float*>(smem + L.red_off);
+  const int C = L.cluster, bn = L.bn, stages = L.stages, kps = L.kps;
+  const int w_rows = L.rows[0];                    // the weights' room in a stage, per K block
+  const uint32_t stage_bytes = (uint32_t)kps * (w_rows + bn) * 128;
   float* scales = reinterpret_cast<float*>(smem + L.scale_off);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bar_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
@@ -54,14 +90,56 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + kBufsMax + b); };
   const uint32_t rfull_bar = bar0 + 8u * (2 * kMaxStages + 2 * kBufsMax);
   const uint32_t rempty_bar = rfull_bar + 8u;
-  const uint32_t sfull0 = rempty_bar + 8u, sempty0 = sfull0 + 8u * kLinScaleSlots;
-  // TMEM buffers: two accumulators, or as many K block products as fit
+  auto sfull_bar = [&](int s) { return rempty_bar + 8u + 8u * s; };
+  auto sempty_bar = [&](int s) { return rempty_bar + 8u + 8u * (kScaleSlots + s); };
+  // TMEM: two accumulators, or a stage's K block products side by side
   uint32_t stride = 16;
   while ((int)stride < bn) stride *= 2;
-  const int bufs = FP8 ? (int)(kTmemCols / stride) : 2;
+  const uint32_t buf_cols = FP8 ? stride * kps : stride;
+  const int bufs = FP8 ? min(kBufsMax, (int)(kTmemCols / buf_cols)) : 2;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_ctarank();
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = C > 1 ? (int)cluster_ctarank() : 0;
+  const int first = blockIdx.x / C, step = gridDim.x / C;
+  const int kb0 = (int)((long long)rank * L.k_blocks / C);
+  const int kb1 = (int)((long long)(rank + 1) * L.k_blocks / C);
+  const uint64_t policy = l2_evict_first_policy();
+  // in registers: behind an asm statement that touches memory, the launch's values are loaded again
+  const int out_features = a.N;
+  const bool whole = L.whole != 0, grouped = a.offsets != nullptr;
+  int* const status = a.status;
+
+  // One stage: the K blocks from kb on of a tile of R weight rows (the choice `pick`).
+  auto fill = [&](const LinUnit& w, int R, int pick, int kb, int s) {
+    const int nk = min(kps, kb1 - kb);
+    const bool few = grouped && w.n <= 8;
+    const CUtensorMap* tw = &maps.w[pick];
+    const CUtensorMap* tx = &maps.x[few ? 1 : 0];
+    const int xr = few ? 8 : bn;
+    const uint32_t sw = base + s * stage_bytes, sx = sw + (uint32_t)(kps * w_rows) * 128;
+    const uint32_t fb = full_bar(s);
+    const int nt = w.nt * (GATED ? R / 32 : R), row = w.g * out_features + nt;
+    // a box is always whole: K blocks past the end come as zeros, and those of another CTA's range
+    // are read for nothing
+    mbar_expect_tx(fb, (uint32_t)((whole ? kps : nk) * (R + xr)) * 128u);
+    constexpr int kElems = FP8 ? 128 : 64;
+    const int turns = whole ? 1 : nk;
+    for (int j = 0; j < turns; ++j) {
+      const int x0 = whole ? 0 : (kb + j) * kElems, z = whole ? kb : 0;
+      const uint32_t dst = sw + (uint32_t)(j * R) * 128;
+      // weights that no other unit reads go first from L2
+      if (GATED) {
+        if (w.alone) tma_load_5d_hint(dst, tw, fb, x0, 0, 2 * w.g, nt, z, policy);
+        else tma_load_5d(dst, tw, fb, x0, 0, 2 * w.g, nt, z);
+      } else {
+        if (w.alone) tma_load_3d_hint(dst, tw, fb, x0, row, z, policy);
+        else tma_load_3d(dst, tw, fb, x0, row, z);
+      }
+      tma_load_3d(sx + (uint32_t)(j * xr) * 128, tx, fb, x0, w.m0, z);
+    }
+  };
+
+  int early = 0;                                   // stages filled before the barrier below
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(full_bar(s), 1);
@@ -71,16 +149,27 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       mbar_init(tfull_bar(b), 1);
       mbar_init(tempty_bar(b), kEpiWarps);
     }
-    mbar_init(rfull_bar, kEpiWarps * C);
+    mbar_init(rfull_bar, 1);
     mbar_init(rempty_bar, kEpiWarps * C);
-    for (int s = 0; s < kLinScaleSlots; ++s) {
-      mbar_init(sfull0 + 8u * s, 1);
-      mbar_init(sempty0 + 8u * s, kEpiWarps);
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(sfull_bar(s), 1);
+      mbar_init(sempty_bar(s), kEpiWarps);
     }
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch(&tm_w);
-    tma_prefetch(&tm_x);
+  }
+  if (!a.offsets && warp == 0) {
+    // one group of known rows: the first loads start now
+    const int blocks = (a.T + bn - 1) / bn;
+    if (first < blocks * L.n_tiles) {
+      early = min(stages, (kb1 - kb0 + kps - 1) / kps);
+      __syncwarp();
+      if (lin_elect()) {
+        const LinUnit w = LinGroups::place(L, L.n_tiles, first, 0, 0, blocks, 0, a.T);
+        for (int i = 0; i < early; ++i) fill(w, w_rows, 0, kb0 + i * kps, i);
+      }
+      __syncwarp();
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), kTmemCols);
@@ -89,48 +178,51 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   LinGroups groups(reinterpret_cast<int*>(smem + L.tab_off), a.G);
   groups.load(L);
   tc_fence_before();
-  cluster_sync();
+  if (C > 1) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int units = groups.units(L);
-  const int first = blockIdx.x / C, step = gridDim.x / C;
-  const int kb0 = (int)((long long)rank * L.k_blocks / C);
-  const int kb1 = (int)((long long)(rank + 1) * L.k_blocks / C);
-  constexpr int kTileCols = GATED ? 64 : 128;      // output columns per unit
+
+  // The tile: of the choices, the one with the shortest line of rounds.
+  int R = L.rows[0], pick = 0, n_tiles = L.n_tiles;
+  if (grouped) {
+    long long best = 0;
+    const int xr = (a.T + a.G - 1) / a.G <= 8 ? 8 : bn;
+    for (int i = 0; i < L.choices; ++i) {
+      const int r = L.rows[i], cols = GATED ? r / 2 : r;
+      const int nt = (a.cols + cols - 1) / cols;
+      const long long u = (long long)groups.before[a.G] * nt;
+      if (i > 0 && u > 1 << 30) break;             // units are counted in 32 bits
+      const long long cost = (u + step - 1) / step * lin_unit_ns(FP8, r, xr, kb1 - kb0);
+      if (i == 0 || cost < best) {
+        best = cost;
+        pick = i;
+        R = r;
+        n_tiles = nt;
+      }
+    }
+  }
+  const int units = groups.units(n_tiles);
+  const int tile_cols = GATED ? R / 2 : R;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint64_t policy = l2_evict_first_policy();
-      constexpr int kStepElems = FP8 ? 128 : 64;
-      uint32_t it = 0;
+    if (lin_elect()) {
       int s = 0;
       uint32_t ph = 1;
       bool ok = true;
       for (int u = first; ok && u < units; u += step) {
-        const LinUnit w = groups.unit(L, u);
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          if (!wait_fast(empty_bar(s), ph, abort_flag, a.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sw = base + s * stage_bytes;
-          mbar_expect_tx(full_bar(s), stage_bytes);
-          // weights that no other unit reads go first from L2
-          if (GATED) {
-            const int fb = w.nt * (kTileCols / 16);
-            if (w.alone)
-              tma_load_5d_hint(sw, &tm_w, full_bar(s), kb * kStepElems, 0, 0, fb, w.g, policy);
-            else
-              tma_load_5d(sw, &tm_w, full_bar(s), kb * kStepElems, 0, 0, fb, w.g);
+        const LinUnit w = groups.unit(L, n_tiles, u);
+        for (int kb = kb0; kb < kb1; kb += kps) {
+          if (early > 0) {
+            --early;                               // on its way already
           } else {
-            const int row = w.g * a.N + w.nt * kTileCols;
-            if (w.alone)
-              tma_load_2d_hint(sw, &tm_w, full_bar(s), kb * kStepElems, row, policy);
-            else
-              tma_load_2d(sw, &tm_w, full_bar(s), kb * kStepElems, row);
+            if (!wait_fast(empty_bar(s), ph, abort_flag, status)) {
+              ok = false;
+              break;
+            }
+            fill(w, R, pick, kb, s);
           }
-          tma_load_2d(sw + kLinWBytes, &tm_x, full_bar(s), kb * kStepElems, w.m0);
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
@@ -141,41 +233,45 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (lin_elect()) {
       int s = 0, buf = 0;
       uint32_t ph = 0, tph = 1;
       bool ok = true;
       for (int u = first; ok && u < units; u += step) {
-        const LinUnit w = groups.unit(L, u);
+        const LinUnit w = groups.unit(L, n_tiles, u);
         const int n = (w.n + 15) & ~15;
         const uint32_t idesc = FP8 ? idesc_e4m3(128, n) : idesc_bf16(128, n);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (FP8 || kb == kb0) {
-            if (!wait_fast(tempty_bar(buf), tph, abort_flag, a.status)) {
-              ok = false;
-              break;
-            }
-          }
-          if (!wait_fast(full_bar(s), ph, abort_flag, a.status)) {
+        const uint32_t step_w = (uint32_t)R * 8;   // a K block's weights and rows, in 16-byte units
+        const uint32_t step_x = (uint32_t)(grouped && w.n <= 8 ? 8 : bn) * 8;
+        for (int kb = kb0; kb < kb1; kb += kps) {
+          if (((FP8 || kb == kb0) && !wait_fast(tempty_bar(buf), tph, abort_flag, status)) ||
+              !wait_fast(full_bar(s), ph, abort_flag, status)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sw = base + s * stage_bytes;
-          const uint64_t dw = sdesc_sw128(sw), dx = sdesc_sw128(sw + kLinWBytes);
-          const uint32_t d = tmem_base + buf * stride;
+          uint64_t dw = sdesc_sw128(sw), dx = sdesc_sw128(sw + (uint32_t)(kps * w_rows) * 128);
+          uint32_t d = tmem_base + buf * buf_cols;
+          const int nk = min(kps, kb1 - kb);
+          uint32_t more = FP8 || kb == kb0 ? 0u : 1u;
+          for (int j = 0; j < nk; ++j) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t more = (FP8 ? kk != 0 : (kb != kb0 || kk != 0)) ? 1u : 0u;
-            if (FP8) mma_e4m3(d, sdesc_advance(dw, kk * 32), sdesc_advance(dx, kk * 32), idesc, more);
-            else mma_bf16(d, sdesc_advance(dw, kk * 32), sdesc_advance(dx, kk * 32), idesc, more);
+            for (int kk = 0; kk < 4; ++kk) {
+              if (FP8) mma_e4m3(d, dw + 2 * kk, dx + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+              else mma_bf16(d, dw + 2 * kk, dx + 2 * kk, idesc, kk != 0 ? 1u : more);
+            }
+            more = 1u;
+            dw += step_w;
+            dx += step_x;
+            if (FP8) d += stride;
           }
           mma_commit(empty_bar(s));
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
-          if (FP8 || kb == kb1 - 1) {
+          if (FP8 || kb + kps >= kb1) {
             mma_commit(tfull_bar(buf));
             if (++buf == bufs) {
               buf = 0;
@@ -188,87 +284,140 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     __syncwarp();
   } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const int row = quarter * 32 + lane;
+    constexpr int kChunks = kMaxBn / 32;           // runs of 16 columns of this warp: part, part + 2, ..
+    float* sent = reinterpret_cast<float*>(smem + L.red_off);   // [column][w_rows]
+    float* got = sent + bn * w_rows;                            // [rank][column][w_rows]
+    const int got_cols = (bn + C - 1) / C;
     int buf = 0, slot = 0;
     uint32_t tph = 0, sph = 0, rph = 0;
     bool ok = true;
     for (int u = first; ok && u < units; u += step) {
-      const LinUnit w = groups.unit(L, u);
-      const LinLane l = LinLane::make<GATED>(a, w.g, w.nt * kTileCols + quarter * (kTileCols / 4));
-      float acc[FP8 ? kMaxBn : 16];
+      const LinUnit w = groups.unit(L, n_tiles, u);
+      const int f0 = w.nt * tile_cols;             // the tile's first output column
+      LinLane l = LinLane::make<GATED>(a, w.g, f0 + quarter * (GATED ? 16 : 32));
+      l.in = l.in && row < R;
+      const int per = (w.n + C - 1) / C;           // columns that each CTA finishes
+      const int mine = min(per, w.n - rank * per);
+      if (a.residual && l.in)
+        for (int c = part; c < mine; c += 2)
+          prefetch_l2(static_cast<const __nv_bfloat16*>(a.residual) +
+                      (long long)(w.m0 + rank * per + c) * a.residual_stride + l.f);
+      float acc[FP8 ? kChunks * 16 : 16];
       if (FP8) {
+        // which of the slot's two products this lane's weight row has
+        const int kind = GATED ? lane >> 4 : ((f0 + row) >> 7) - (f0 >> 7);
 #pragma unroll
-        for (int i = 0; i < kMaxBn; ++i) acc[i] = 0.f;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!wait_fast(sfull0 + 8u * slot, sph, abort_flag, a.status) ||
-              !wait_fast(tfull_bar(buf), tph, abort_flag, a.status)) {
+        for (int i = 0; i < kChunks * 16; ++i) acc[i] = 0.f;
+        for (int kb = kb0; kb < kb1; kb += kps) {
+          if (!wait_fast(sfull_bar(slot), sph, abort_flag, status) ||
+              !wait_fast(tfull_bar(buf), tph, abort_flag, status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const float* sc = scales + slot * bn * (GATED ? 2 : 1);
+          const int nk = min(kps, kb1 - kb);
+          const float* sc = scales + slot * kps * 2 * bn;
+          const uint32_t t0 = lanes + buf * buf_cols;
+          // two products on their way from TMEM at a time: of two K blocks, or (one per stage) of two
+          // runs of columns
+          auto load = [&](int j, int col, uint32_t (&v)[16], float4 (&k)[4]) {
+            tmem_ld16(t0 + j * stride + col, v);
 #pragma unroll
-          for (int c = 0; c < kMaxBn / 16; ++c)
-            if (c * 16 < w.n)
-              lin_promote16<GATED>(acc + (FP8 ? 16 * c : 0), lanes + buf * stride, sc, 16 * c, lane >> 4);
+            for (int q = 0; q < 4; ++q)
+              k[q] = *reinterpret_cast<const float4*>(sc + scale_at(bn, j, col + 4 * q, kind & 1));
+          };
+          auto add = [&](float* y, uint32_t (&v)[16], float4 (&k)[4]) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              fma2(y[4 * q], y[4 * q + 1], k[q].x, k[q].y, __uint_as_float(v[4 * q]),
+                   __uint_as_float(v[4 * q + 1]));
+              fma2(y[4 * q + 2], y[4 * q + 3], k[q].z, k[q].w, __uint_as_float(v[4 * q + 2]),
+                   __uint_as_float(v[4 * q + 3]));
+            }
+          };
+          uint32_t v0[16], v1[16];
+          float4 k0[4], k1[4];
+          if (nk == 1) {
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+              const int col = 16 * (2 * c + part);
+              if (col >= w.n) break;
+              const bool two = col + 32 < w.n;
+              load(0, col, v0, k0);
+              if (two) load(0, col + 32, v1, k1);
+              tmem_wait_ld16(v0);
+              add(acc + (FP8 ? 16 * c : 0), v0, k0);
+              if (two) {
+                tmem_wait_ld16(v1);
+                add(acc + (FP8 ? 16 * c + 16 : 0), v1, k1);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              const int col = 16 * (2 * c + part);
+              if (col >= w.n) break;
+              for (int j = 0; j < nk; j += 2) {
+                load(j, col, v0, k0);
+                if (j + 1 < nk) load(j + 1, col, v1, k1);
+                tmem_wait_ld16(v0);
+                add(acc + (FP8 ? 16 * c : 0), v0, k0);
+                if (j + 1 < nk) {
+                  tmem_wait_ld16(v1);
+                  add(acc + (FP8 ? 16 * c : 0), v1, k1);
+                }
+              }
+            }
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(tempty_bar(buf));
-            mbar_arrive(sempty0 + 8u * slot);
+            mbar_arrive(sempty_bar(slot));
           }
           if (++buf == bufs) {
             buf = 0;
             tph ^= 1u;
           }
-          if (++slot == kLinScaleSlots) {
+          if (++slot == kScaleSlots) {
             slot = 0;
             sph ^= 1u;
           }
         }
-      } else if (!wait_fast(tfull_bar(buf), tph, abort_flag, a.status)) {
+      } else if (!wait_fast(tfull_bar(buf), tph, abort_flag, status)) {
         ok = false;
       }
       if (!ok) break;
       tc_fence_after();
-      // C > 1: this CTA's sums of columns [d * per, (d + 1) * per) go to CTA d
-      const int per = (w.n + C - 1) / C;
-      if (C > 1 && u != first) {
-        if (!wait_bounded_cluster(rempty_bar, rph ^ 1u, abort_flag, a.status)) {
-          ok = false;
-          break;
-        }
+      // what the unit before sent has been added up, here and by the others
+      if (C > 1 && u != first && !wait_bounded_cluster(rempty_bar, rph ^ 1u, abort_flag, status)) {
+        ok = false;
+        break;
       }
 #pragma unroll
-      for (int c = 0; c < kMaxBn / 16; ++c) {
-        if (c * 16 >= w.n) break;
+      for (int c = 0; c < kChunks; ++c) {
+        const int col = 16 * (2 * c + part);
+        if (col >= w.n) break;
         float v[16];
         if (FP8) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = acc[FP8 ? 16 * c + i : 0];
         } else {
           uint32_t t[16];
-          tmem_ld16(lanes + buf * stride + 16 * c, t);
+          tmem_ld16(lanes + buf * buf_cols + col, t);
           tmem_wait_ld16(t);
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(t[i]);
         }
         if (C == 1) {
-          lin_store<GATED, GATED ? 8 : 16>(a, l, w.m0 + 16 * c, w.n - 16 * c, v);
-        } else {
-          int d = 16 * c / per, at = 16 * c - d * per;
+          lin_store<GATED, GATED ? 8 : 16>(a, l, w.m0 + col, w.n - col, v);
+        } else if (row < w_rows) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (16 * c + i < w.n) {
-              st_cluster(mapa_shared(smem_addr(red + (rank * per + at) * kLinWRows + row), d), v[i]);
-              if (++at == per) {
-                at = 0;
-                ++d;
-              }
-            }
-          }
+          for (int i = 0; i < 16; ++i)
+            if (col + i < w.n) sent[(col + i) * w_rows + row] = v[i];
         }
       }
       if (!FP8) {
@@ -281,113 +430,224 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
         }
       }
       if (C > 1) {
-        __syncwarp();
-        if (lane < C) mbar_arrive_cluster(mapa_shared(rfull_bar, lane));
-        if (!wait_bounded_cluster(rfull_bar, rph, abort_flag, a.status)) {
+        fence_async_shared();
+        epilogue_barrier();
+        if (warp == 2 && lane < C) {
+          // the others' sums of this CTA's columns, and this one's of theirs
+          const uint32_t col_bytes = w_rows * 4;
+          if (lane == rank) {
+            mbar_expect_tx(rfull_bar, max(mine, 0) * (C - 1) * col_bytes);
+          } else {
+            const int theirs = min(per, w.n - lane * per);
+            if (theirs > 0)
+              copy_to_cluster(mapa_shared(smem_addr(got + rank * got_cols * w_rows), lane),
+                              smem_addr(sent + lane * per * w_rows), theirs * col_bytes,
+                              mapa_shared(rfull_bar, lane));
+          }
+        }
+        if (!wait_fast(rfull_bar, rph, abort_flag, status)) {
           ok = false;
           break;
         }
-        const int mine = min(per, w.n - rank * per);
-        for (int c0 = 0; c0 < mine; c0 += 16) {
+        for (int c0 = part * 16; c0 < mine; c0 += 32) {
           float v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = 0.f;
-          for (int s = 0; s < C; ++s) {
+          if (row < w_rows) {
+            for (int s = 0; s < C; ++s) {
+              const float* from = s == rank ? sent + rank * per * w_rows : got + s * got_cols * w_rows;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c0 + i < mine) v[i] += red[(s * per + c0 + i) * kLinWRows + row];
+              for (int i = 0; i < 16; ++i)
+                if (c0 + i < mine) v[i] += from[(c0 + i) * w_rows + row];
+            }
           }
           lin_store<GATED, GATED ? 8 : 16>(a, l, w.m0 + rank * per + c0, mine - c0, v);
         }
-        __syncwarp();
-        if (lane < C) mbar_arrive_cluster(mapa_shared(rempty_bar, lane));
+        if (u + step < units) {
+          __syncwarp();
+          if (lane < C) mbar_arrive_cluster(mapa_shared(rempty_bar, lane));
+        }
         rph ^= 1u;
       }
     }
   } else if (FP8) {
     // ------------------------------------------------------------ scales
-    uint32_t it = 0;
-    for (int u = first; u < units; u += step) {
-      const LinUnit w = groups.unit(L, u);
-      if (!LinScales<GATED, kMaxBn>::unit(L, w, w.nt * kTileCols, kb0, kb1, scales,
-                                          bn * (GATED ? 2 : 1), sfull0, sempty0, it, abort_flag))
-        break;
+    const int wblocks = (a.N + 127) >> 7;
+    int slot = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int u = first; ok && u < units; u += step) {
+      const LinUnit w = groups.unit(L, n_tiles, u);
+      const int b0 = (w.nt * tile_cols) >> 7;
+      const int b1 = GATED ? b0 + (a.cols >> 7) : min(b0 + 1, wblocks - 1);
+      const float* w0 = a.w_scale + ((long long)w.g * wblocks + b0) * L.k_blocks;
+      const float* w1 = a.w_scale + ((long long)w.g * wblocks + b1) * L.k_blocks;
+      const float* xs = a.x_scale + w.m0 + lane;
+      for (int kb = kb0; kb < kb1; kb += kps) {
+        if (!wait_fast(sempty_bar(slot), ph, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        float* dst = scales + slot * kps * 2 * bn;
+        for (int j0 = 0; j0 < kps; j0 += 4) {
+          float v[4][kMaxBn / 32], s0[4], s1[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool in = j0 + j < kps && kb + j0 + j < kb1;
+            s0[j] = in ? __ldg(w0 + kb + j0 + j) : 0.f;
+            s1[j] = in ? __ldg(w1 + kb + j0 + j) : 0.f;
+#pragma unroll
+            for (int i = 0; i < kMaxBn / 32; ++i)
+              v[j][i] = in && lane + 32 * i < w.n ? __ldg(xs + (long long)(kb + j0 + j) * a.T + 32 * i)
+                                                  : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j0 + j >= kps) break;
+#pragma unroll
+            for (int i = 0; i < kMaxBn / 32; ++i) {
+              const int c = lane + 32 * i;
+              if (c < bn) {
+                dst[scale_at(bn, j0 + j, c, 0)] = v[j][i] * s0[j];
+                dst[scale_at(bn, j0 + j, c, 1)] = v[j][i] * s1[j];
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull_bar(slot));
+        if (++slot == kScaleSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      }
     }
   }
 
   tc_fence_before();
-  cluster_sync();               // no CTA leaves while another may still write to it
+  if (C > 1) cluster_sync();    // no CTA leaves while another may still write to it or read it
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, kTmemCols);
   }
 }
 
-template <bool FP8, bool GATED>
-cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& L, int C, int units,
-                   size_t smem, cudaStream_t stream) {
-  auto kernel = linear_stream_kernel<FP8, GATED>;
-  // CTAs that the device holds of each cluster size, found once per device
-  static int room[64][kMaxCluster + 1];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || dev < 0 || dev >= 64) return e == cudaSuccess ? cudaErrorInvalidDevice : e;
+cudaLaunchConfig_t config(bool fp8, int C, unsigned grid, size_t smem, cudaStream_t stream,
+                          cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(threads_of(FP8));
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads_of(fp8));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (!room[dev][C]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmemMax);
-    if (e != cudaSuccess) return e;
-    int n = 0;
-    cfg.gridDim = dim3(C);
-    cfg.dynamicSmemBytes = kLinSmemMax;
-    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-    if (e != cudaSuccess) return e;
-    cfg.dynamicSmemBytes = smem;
-    room[dev][C] = n > 0 ? n : 1;
+  if (C > 1) {
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = C;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
   }
-  const int clusters = units < room[dev][C] ? units : room[dev][C];
-  cfg.gridDim = dim3(clusters * C);
-  return cudaLaunchKernelEx(&cfg, kernel, w, x, L, C);
+  return cfg;
+}
+
+// Prepares the kernel on the current device and finds its clusters there, once.
+template <bool FP8, bool GATED>
+int room(int C) {
+  static int cached[64][kMaxCluster + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (!cached[dev][C]) {
+    auto kernel = linear_stream_kernel<FP8, GATED>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmemMax) !=
+        cudaSuccess)
+      return 0;
+    int n = num_sms();
+    if (C > 1) {
+      cudaLaunchAttribute attr;
+      const cudaLaunchConfig_t cfg = config(FP8, C, C, kLinSmemMax, nullptr, &attr);
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    }
+    cached[dev][C] = n > 0 ? n : 1;
+  }
+  return cached[dev][C];
+}
+
+template <bool FP8, bool GATED>
+cudaError_t launch(const Maps& maps, const LinLaunch& L, unsigned grid, size_t smem,
+                   cudaStream_t stream) {
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = config(FP8, L.cluster, grid, smem, stream, &attr);
+  return cudaLaunchKernelEx(&cfg, linear_stream_kernel<FP8, GATED>, maps, L);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_stream(LinLaunch L, int cluster, int max_units, cudaStream_t stream) {
+int linear_stream_room(const LinearArgs& a, int size) {
+  if (size < 1 || size > kMaxCluster) return 0;
+  const bool gated = a.act == GBMOE_EPI_SILU_MUL;
+  if (a.fp8) return gated ? room<true, true>(size) : room<true, false>(size);
+  return gated ? room<false, true>(size) : room<false, false>(size);
+}
+
+cudaError_t launch_linear_stream(LinLaunch L, long long max_units, cudaStream_t stream) {
   const LinearArgs& a = L.a;
   const bool gated = a.act == GBMOE_EPI_SILU_MUL;
-  if (L.bn < 16 || L.bn > kMaxBn || L.bn % 16 || cluster < 1 || cluster > kMaxCluster ||
-      cluster > L.k_blocks)
+  const int C = L.cluster, most_rows = L.rows[0];
+  if (L.bn < 16 || L.bn > kMaxBn || L.bn % 16 || C < 1 || C > kMaxCluster || C > L.k_blocks ||
+      L.choices < 1 || L.choices > kWMaps)
     return cudaErrorInvalidValue;
-  const uint32_t stage = kLinWBytes + L.bn * 128;
-  const uint32_t per = (L.bn + cluster - 1) / cluster;
-  const uint32_t red = cluster > 1 ? cluster * per * kLinWRows * 4 : 0;
-  const uint32_t scale = a.fp8 ? kLinScaleSlots * L.bn * 4 * (gated ? 2 : 1) : 0;
+  for (int i = 0; i < L.choices; ++i) {
+    const int r = L.rows[i];
+    // tiles start on the swizzle's 8 rows; gated ones are whole blocks of 16 features, and have one
+    // scale block of either kind
+    if (r < 8 || r > most_rows || r > kLinWRows || r % 8 || (gated && r % 32) ||
+        (gated && a.fp8 && 128 % (r / 2)))
+      return cudaErrorInvalidValue;
+  }
+  const uint32_t w_rows = most_rows, per_k = (w_rows + L.bn) * 128;
+  const uint32_t red = C > 1 ? (L.bn + C * ((L.bn + C - 1) / C)) * w_rows * 4 : 0;
   const uint32_t tab = (4u * (3 * a.G + 1) + 15) & ~15u, bars = kBars * 8 + 16;
-  const uint32_t rest = red + scale + tab + bars + 1024;
-  int stages = (int)((kLinSmemMax - rest) / stage);
-  if (stages > kMaxStages) stages = kMaxStages;
-  if (stages < 2) return cudaErrorInvalidValue;
-  L.stages = stages;
-  L.red_off = stages * stage;
-  L.scale_off = L.red_off + red;
-  L.bar_off = L.scale_off + scale;
-  L.tab_off = L.bar_off + bars;
-  CUtensorMap w, x;
-  if (!lin_maps(a, L.bn, &w, &x)) return cudaErrorInvalidValue;
-  const size_t smem = stages * stage + rest;
+  // A stage's round trip, barriers, copies and commit, takes one thread or the other near 200 ns, some
+  // 25 KB of HBM's time: large stages, of which three still fit
+  const uint32_t range = (L.k_blocks + C - 1) / C;
+  const uint32_t free_bytes = kLinSmemMax - 1024 - (red + tab + bars > kLinWBytes ? red + tab + bars : kLinWBytes);
+  uint32_t kps = free_bytes / 3 / per_k;
+  if (kps > range) kps = range;
+  if (kps > (uint32_t)kMaxKps) kps = kMaxKps;
+  if (getenv("LIN_KPS")) kps = atoi(getenv("LIN_KPS"));
   if (a.fp8)
-    return gated ? launch<true, true>(w, x, L, cluster, max_units, smem, stream)
-                 : launch<true, false>(w, x, L, cluster, max_units, smem, stream);
-  return gated ? launch<false, true>(w, x, L, cluster, max_units, smem, stream)
-               : launch<false, false>(w, x, L, cluster, max_units, smem, stream);
+    while (kps > 1 && kps * L.bn > 128) --kps;
+  if (kps < 1) kps = 1;
+  const uint32_t stage = kps * per_k;
+  const uint32_t scale = a.fp8 ? kScaleSlots * kps * 2 * L.bn * 4 : 0;
+  // the MMA reads 128 rows from each K block's weights on: behind the last of them too
+  const uint32_t over = kLinWBytes, rest = red + scale + tab + bars;
+  const uint32_t behind = rest > over ? rest : over;
+  if (kLinSmemMax < 1024 + behind + 2 * stage) return cudaErrorInvalidValue;
+  uint32_t stages = (kLinSmemMax - 1024 - behind) / stage;
+  if (stages > (uint32_t)kMaxStages) stages = kMaxStages;
+  L.whole = lin_whole(a);
+  L.kps = (int)kps;
+  L.stages = (int)stages;
+  L.red_off = (int)(stages * stage);
+  L.scale_off = L.red_off + (int)red;
+  L.bar_off = L.scale_off + (int)scale;
+  L.tab_off = L.bar_off + (int)bars;
+  Maps maps;
+  const int boxed = L.whole ? (int)kps : 0;
+  bool ok = lin_map_x(a, L.bn, boxed, &maps.x[0]) &&
+            (!a.offsets || lin_map_x(a, 8, boxed, &maps.x[1]));
+  for (int i = 0; i < L.choices; ++i) ok = ok && lin_map_tiles(a, L.rows[i], boxed, &maps.w[i]);
+  if (!ok) return cudaErrorInvalidValue;
+  const int most = linear_stream_room(a, C);
+  if (most < 1) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)(max_units < most ? max_units : most) * C;
+  const size_t smem = 1024 + stages * stage + behind;
+  if (a.fp8)
+    return gated ? launch<true, true>(maps, L, grid, smem, stream)
+                 : launch<true, false>(maps, L, grid, smem, stream);
+  return gated ? launch<false, true>(maps, L, grid, smem, stream)
+               : launch<false, false>(maps, L, grid, smem, stream);
 }
 
 }  // namespace gbmoe
