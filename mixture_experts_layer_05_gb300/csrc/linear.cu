@@ -47,42 +47,97 @@ bool lin_map_tiles(const LinearArgs& a, int rows, int kps, CUtensorMap* w) {
   return encode(a, w, a.weight, 5, dims, strides, box);
 }
 
+namespace {
+
+int ceil_div(long long x, long long y) { return (int)((x + y - 1) / y); }
+
+// How the stream kernel cuts a call: tiles of `rows` weight rows, `cluster` CTAs to a tile.
+struct StreamCut {
+  int bn, cluster, rows;
+  double ns;
+};
+
+// Groups count as if all of them had rows. Whole rounds are what is looked for; no cut is faster than
+// HBM; a join of partial sums and the cluster's start take about 3.5 us, and some more for the sums'
+// size. cluster 0: the device holds no cluster of some size.
+StreamCut cut_stream(const LinearArgs& a, int groups, int mean, int k_blocks) {
+  const bool gated = a.act == GBMOE_EPI_SILU_MUL;
+  StreamCut best = {0, 0, 0, 1e30};
+  // Dense: the rows, cut evenly. Groups: room for the larger ones, in steps of 16 up to 64 (16 of 2048
+  // to 7168, mean 16: 73.5 us with 64 against 82.6 with 16; mean 2: 65.9 and 66.3).
+  const int bn = a.offsets ? 4 * mean : ceil_div(mean, ceil_div(mean, a.fp8 ? 64 : 128));
+  best.bn = (bn + 15) & ~15;
+  if (a.offsets && best.bn > 64) best.bn = 64;
+  const int n = best.bn, grain = gated ? 32 : 8;             // rows per step of R
+  const long long blocks = ceil_div(a.T, n) + (a.offsets ? groups - 1 : 0);
+  const double hbm = (double)groups * a.N * a.K * (a.fp8 ? 1 : 2) / 6700;
+  for (int C = 1; C <= 8 && C <= k_blocks; ++C) {
+    const int room = linear_stream_room(a, n, C);
+    if (room < 1) return StreamCut{n, 0, 0, 0};
+    const int kb = ceil_div(k_blocks, C);
+    for (int rounds = 1; rounds <= 8; ++rounds) {
+      const long long tiles = (long long)room * rounds / blocks;  // of one group's rows
+      int R = tiles < 1 ? 129 : ceil_div(a.N, tiles);
+      R = ceil_div(R < 8 ? 8 : R, grain) * grain;
+      if (gated && a.fp8 && R == 96) R = 128;      // a tile has one scale block of either kind
+      if (R > 128) {
+        if (rounds < 8) continue;
+        R = 128;
+      }
+      const int turns = ceil_div(blocks * ceil_div(a.N, R), room);
+      const double run = (double)turns * lin_unit_ns(a.fp8, R, n, kb);
+      const double ns = (run > hbm ? run : hbm) + (C > 1 ? turns * (3500 + n * R / 20.0) : 0);
+      if (ns < best.ns * 0.98) {
+        best.ns = ns;
+        best.cluster = C;
+        best.rows = R;
+      }
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   LinLaunch L = {};
   L.a = a;
   L.k_blocks = (a.K * (a.fp8 ? 1 : 2) + 127) / 128;
-  const int cols = a.act == GBMOE_EPI_SILU_MUL ? 64 : 128;   // output columns of 128 weight rows
-  auto ceil_div = [](long long x, long long y) { return (int)((x + y - 1) / y); };
+  const bool gated = a.act == GBMOE_EPI_SILU_MUL;
   const int mean = ceil_div(a.T, a.G);
   const int groups = a.G < a.T ? a.G : a.T;                  // with rows, at most
-  // The kernel. Dense bf16 calls change at 96 rows (K = N = 4096: 64 rows 13.9 us in the stream kernel,
-  // 128 rows 15.4 there and 15.0 in pairs, 256 17.6 and 15.7); e4m3 ones likewise, where more rows cost
-  // the stream kernel's promotion more (K = 7168, N = 4096: 96 rows 18.0 and 30.5, K = N = 4096: 128 rows
-  // 19.0 and 20.8). Groups change earlier, as the largest has a multiple of the mean and is then cut (16
-  // of 2048 to 7168, mean 32: 76.9 and 79.4 evenly, 81.0 and 79.5 unevenly filled, mean 48: 77.8 and 80.3,
-  // 87.0 and 85.1; e4m3, mean 8: 42.6 and 44.1, 43.7 and 43.0, mean 16: 46.8 and 45.5, 60.9 and 46.8).
-  const bool many = mean > (!a.offsets ? 96 : a.fp8 ? 8 : 32);
-  if (many && a.fp8) {
-    L.bn = 128;
-    L.n_tiles = ceil_div(a.cols, 2 * cols);
-    L.gm = 16;
-    const long long units = ((long long)ceil_div(a.T, L.bn) + groups - 1) * L.n_tiles;
-    return launch_linear_fp8(L, units, stream);
+  // 256 weight rows to a unit, in the two kernels for many rows
+  const int wide_tiles = ceil_div(a.cols, gated ? 128 : 256);
+
+  // Few rows or many. Groups change early, as the largest has a multiple of the mean and is then cut (16
+  // of 2048 to 7168, stream and many, evenly and unevenly filled: mean 32 76.9 and 79.4 us, 81.0 and
+  // 79.5, mean 48 77.8 and 80.3, 87.0 and 85.1; e4m3, mean 8: 42.6 and 44.1, 43.7 and 43.0, mean 16:
+  // 46.8 and 45.5, 60.9 and 46.8). Dense bf16 calls change at 96 rows (K = N = 4096: 64 rows 13.4 us in
+  // the stream kernel, 128 rows 17.6 there and 14.8 in pairs). In e4m3 it goes by the outputs too, whose
+  // units of 128 by 256 take the kernel for many rows some 500 ns a K block: 128 rows of K = 4096 15.3
+  // and 21.4 us to 4096 outputs, 160 rows 47.4 and 24.7 to 16384.
+  bool many = mean > (!a.offsets ? 96 : a.fp8 ? 8 : 32);
+  StreamCut cut = {};
+  if (!a.offsets && a.fp8 && mean <= 256) {
+    cut = cut_stream(a, groups, mean, L.k_blocks);
+    many = cut.ns > 500.0 * L.k_blocks * ceil_div((long long)ceil_div(a.T, 128) * wide_tiles, num_sms());
+  } else if (!many) {
+    cut = cut_stream(a, groups, mean, L.k_blocks);
   }
   if (many) {
-    L.n_tiles = ceil_div(a.cols, 2 * cols);
+    L.n_tiles = wide_tiles;
     L.gm = 16;
-    L.bn = 256;
-    if (!a.offsets) {
+    L.bn = a.fp8 ? 128 : 256;
+    if (!a.fp8 && !a.offsets) {
       // the rows are cut evenly, so that the units come out in few rounds; a K block of a unit takes the
       // MMAs' 1.1 ns a row, or what the issue of its copies takes
       long long best = 1ll << 62;
       for (int blocks = ceil_div(a.T, 256); blocks <= 4 * ceil_div(a.T, 256); ++blocks) {
         const int bn = (ceil_div(a.T, blocks) + 31) & ~31;
-        if (bn < 64) break;
-        const long long units = (long long)ceil_div(a.T, bn) * L.n_tiles;
+        if (bn < 64 && blocks > 1) break;
         const int ns = 9 * bn / 8 > 140 + bn / 8 ? 9 * bn / 8 : 140 + bn / 8;
-        const long long cost = ceil_div(units, num_sms() / 2) * (long long)ns;
+        const long long cost =
+            ceil_div((long long)ceil_div(a.T, bn) * L.n_tiles, num_sms() / 2) * (long long)ns;
         if (cost < best) {
           best = cost;
           L.bn = bn;
@@ -90,60 +145,23 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
       }
     }
     const long long units = ((long long)ceil_div(a.T, L.bn) + groups - 1) * L.n_tiles;
-    return launch_linear_pair(L, units, stream);
+    return a.fp8 ? launch_linear_fp8(L, units, stream) : launch_linear_pair(L, units, stream);
   }
-  // Dense: the rows, cut evenly. Groups: room for the larger ones, in steps of 16 up to 64 (mean 16: 73.5
-  // us with 64 against 82.6 with 16; mean 2: 65.9 and 66.3).
-  int bn = a.offsets ? 4 * mean : ceil_div(mean, ceil_div(mean, 128));
-  bn = (bn + 15) & ~15;
-  if (a.offsets && bn > 64) bn = 64;
-  L.bn = bn;
+  if (cut.cluster < 1) return cudaErrorInvalidConfiguration;
+  L.bn = cut.bn;
   L.gm = 1 << 16;
-  // The cut: tiles of R weight rows, C CTAs to a tile, in whole rounds. No cut is faster than HBM; a
-  // join of partial sums and the cluster's start take about 3.5 us, and some more for the sums' size.
-  const bool gated = a.act == GBMOE_EPI_SILU_MUL;
-  const int grain = gated ? 32 : 8;                          // rows per step of R
-  const long long blocks = ceil_div(a.T, L.bn) + (a.offsets ? groups - 1 : 0);
-  const int n = bn;
-  const double hbm = (double)groups * a.N * a.K * (a.fp8 ? 1 : 2) / 6700;
-  double best = 1e30;
-  int best_C = 1, best_R = 128;
-  for (int C = 1; C <= 8 && C <= L.k_blocks; ++C) {
-    const int room = linear_stream_room(a, C);
-    if (room < 1) return cudaErrorInvalidConfiguration;
-    const int kb = ceil_div(L.k_blocks, C);
-    for (int rounds = 1; rounds <= 8; ++rounds) {
-      const long long tiles = (long long)room * rounds / blocks;  // of one group's rows
-      int R = tiles < 1 ? 129 : ceil_div(a.N, tiles);
-      R = ceil_div(R < 8 ? 8 : R, grain) * grain;
-      if (gated && a.fp8 && R == 96) R = 128;      // a tile has one scale block of either kind
-      const bool last = rounds == 8;
-      if (R > 128) {
-        if (!last) continue;
-        R = 128;
-      }
-      const int turns = ceil_div(blocks * ceil_div(a.N, R), room);
-      const double run = (double)turns * lin_unit_ns(a.fp8, R, n, kb);
-      const double cost = (run > hbm ? run : hbm) + (C > 1 ? turns * (3500 + n * R / 20.0) : 0);
-      if (cost < best * 0.98) {
-        best = cost;
-        best_C = C;
-        best_R = R;
-      }
-    }
-  }
-  L.cluster = best_C;
-  if (a.offsets) {                                 // the kernel cuts by the rows that it finds
+  L.cluster = cut.cluster;
+  L.rows[0] = cut.rows;
+  L.choices = 1;
+  if (a.offsets) {                                 // the kernel cuts by the groups that it finds
     L.rows[0] = 128;
     L.rows[1] = 64;
     L.rows[2] = 32;
     L.choices = 3;
-  } else {
-    L.rows[0] = best_R;
-    L.choices = 1;
   }
   const int least = L.rows[L.choices - 1];
   L.n_tiles = ceil_div(a.cols, gated ? least / 2 : least);
+  const long long blocks = ceil_div(a.T, L.bn) + (a.offsets ? groups - 1 : 0);
   return launch_linear_stream(L, blocks * L.n_tiles, stream);
 }
 

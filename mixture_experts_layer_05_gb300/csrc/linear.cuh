@@ -32,7 +32,8 @@ struct LinLaunch {
   int tab_off;     // byte offsets in shared memory, from the aligned base: group table,
   int bar_off;     // barriers,
   int red_off;     // (stream kernel) partial sums of a cluster,
-  int scale_off;   // row scales (e4m3)
+  int scale_off;   // row scales (e4m3),
+  int half_off;    // (stream kernel, e4m3) sums of every other K block
   // stream kernel
   int cluster;     // CTAs that cut a unit's K blocks
   int rows[3];     // weight rows per tile: the choices (the kernel picks, by its groups), largest first,
@@ -103,6 +104,9 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "r"(v),
       "r"(w)
       : "memory");
+}
+__device__ __forceinline__ void lin_prefetch(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 // One thread of a converged warp. Unlike a test of the lane it tells the compiler that there is one, so
 // that the descriptors of the TMA and MMA instructions stay in uniform registers (with a test of the lane
@@ -397,7 +401,7 @@ bool lin_map_rows(const LinearArgs& a, int rows, int kps, CUtensorMap* w);
 // block of 16 features, 0), or (0, 0, 2 group, block, K block).
 bool lin_map_tiles(const LinearArgs& a, int rows, int kps, CUtensorMap* w);
 // Clusters of `size` CTAs of the stream kernel that the device holds (0: an error).
-int linear_stream_room(const LinearArgs& a, int size);
+int linear_stream_room(const LinearArgs& a, int bn, int size);
 cudaError_t launch_linear_stream(LinLaunch L, long long max_units, cudaStream_t stream);
 cudaError_t launch_linear_pair(LinLaunch L, long long max_units, cudaStream_t stream);
 cudaError_t launch_linear_fp8(LinLaunch L, long long max_units, cudaStream_t stream);

@@ -167,6 +167,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const LinUnit w = groups.unit(L, L.n_tiles, u);
       const LinLane l = LinLane::make<GATED>(
           a, w.g, (w.nt * 2 + rank) * kTileCols + quarter * (kTileCols / 4));
+      // the residual's way from HBM lies under the products
+      if (a.residual && l.in)
+        for (int at = part * 32; at < w.n; at += 64)
+          for (int i = 0; i < 32 && at + i < w.n; ++i)
+            lin_prefetch(static_cast<const __nv_bfloat16*>(a.residual) +
+                         (long long)(w.m0 + at + i) * a.residual_stride + l.f);
       if (!wait_fast(tfull_bar(buf), tph, abort_flag, status)) break;
       tc_fence_after();
 #pragma unroll 1

@@ -14,14 +14,12 @@
 // Warps: 0 TMA, 1 TMEM and MMA, 2..9 epilogue (two per TMEM lane quarter, alternating by 16 columns), 10
 // (e4m3) scales. e4m3 products are promoted to fp32 with their scales K block by K block, as the FP8
 // layer's are: each K block of a stage has its own TMEM columns.
-#include <cstdlib>
-
 #include "linear.cuh"
 
 namespace gbmoe {
 namespace {
 
-constexpr int kMaxBn = 128;
+constexpr int kMaxBn = 128, kMaxBnFp8 = 64;      // (e4m3 keeps its sums in registers)
 constexpr int kMaxCluster = 8;
 constexpr int kMaxStages = 16;
 constexpr int kMaxKps = 8;                       // K blocks per stage
@@ -57,9 +55,6 @@ __device__ __forceinline__ void fence_async_shared() {
 __device__ __forceinline__ void epilogue_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
 
 // Scales of a slot: for K block j of the stage and row c, the products with the two weight blocks that
 // a tile can meet (gate and up; or the blocks before and behind a border of 128 rows), four rows of
@@ -68,7 +63,8 @@ __device__ __forceinline__ int scale_at(int bn, int j, int c, int kind) {
   return j * 2 * bn + (c >> 2) * 8 + kind * 4 + (c & 3);
 }
 
-template <bool FP8, bool GATED>
+// CHUNKS: runs of 16 columns that an epilogue warp holds, for bn up to 32 * CHUNKS.
+template <bool FP8, bool GATED, int CHUNKS>
 __global__ void __launch_bounds__(threads_of(FP8), 1)
     linear_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LinLaunch L) {
   extern __shared__ uint8_t smem_raw[];
@@ -140,22 +136,25 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   };
 
   int early = 0;                                   // stages filled before the barrier below
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
+  if (warp == 0) {
+    // a lane for each: one thread's chain of them is a quarter of a microsecond
+    if (lane < stages) {
+      mbar_init(full_bar(lane), 1);
+      mbar_init(empty_bar(lane), 1);
     }
-    for (int b = 0; b < bufs; ++b) {
-      mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), kEpiWarps);
+    if (lane < bufs) {
+      mbar_init(tfull_bar(lane), 1);
+      mbar_init(tempty_bar(lane), kEpiWarps);
     }
-    mbar_init(rfull_bar, 1);
-    mbar_init(rempty_bar, kEpiWarps * C);
-    for (int s = 0; s < kScaleSlots; ++s) {
-      mbar_init(sfull_bar(s), 1);
-      mbar_init(sempty_bar(s), kEpiWarps);
+    if (lane < kScaleSlots) {
+      mbar_init(sfull_bar(lane), 1);
+      mbar_init(sempty_bar(lane), kEpiWarps);
     }
-    *abort_flag = 0;
+    if (lane == 0) {
+      mbar_init(rfull_bar, 1);
+      mbar_init(rempty_bar, kEpiWarps * C);
+      *abort_flag = 0;
+    }
     fence_mbar_init();
   }
   if (!a.offsets && warp == 0) {
@@ -163,7 +162,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     const int blocks = (a.T + bn - 1) / bn;
     if (first < blocks * L.n_tiles) {
       early = min(stages, (kb1 - kb0 + kps - 1) / kps);
-      __syncwarp();
+      __syncwarp();                                // all lanes' barriers are there
       if (lin_elect()) {
         const LinUnit w = LinGroups::place(L, L.n_tiles, first, 0, 0, blocks, 0, a.T);
         for (int i = 0; i < early; ++i) fill(w, w_rows, 0, kb0 + i * kps, i);
@@ -287,7 +286,9 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16);
     const int row = quarter * 32 + lane;
-    constexpr int kChunks = kMaxBn / 32;           // runs of 16 columns of this warp: part, part + 2, ..
+    // e4m3 with one run of columns: the two warps of a quarter take every other K block instead
+    const bool halves = FP8 && bn == 16;
+    float* other = reinterpret_cast<float*>(smem + L.half_off);  // [column][128 rows] of the second one
     float* sent = reinterpret_cast<float*>(smem + L.red_off);   // [column][w_rows]
     float* got = sent + bn * w_rows;                            // [rank][column][w_rows]
     const int got_cols = (bn + C - 1) / C;
@@ -303,14 +304,14 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       const int mine = min(per, w.n - rank * per);
       if (a.residual && l.in)
         for (int c = part; c < mine; c += 2)
-          prefetch_l2(static_cast<const __nv_bfloat16*>(a.residual) +
+          lin_prefetch(static_cast<const __nv_bfloat16*>(a.residual) +
                       (long long)(w.m0 + rank * per + c) * a.residual_stride + l.f);
-      float acc[FP8 ? kChunks * 16 : 16];
+      float acc[FP8 ? CHUNKS * 16 : 16];
       if (FP8) {
         // which of the slot's two products this lane's weight row has
         const int kind = GATED ? lane >> 4 : ((f0 + row) >> 7) - (f0 >> 7);
 #pragma unroll
-        for (int i = 0; i < kChunks * 16; ++i) acc[i] = 0.f;
+        for (int i = 0; i < CHUNKS * 16; ++i) acc[i] = 0.f;
         for (int kb = kb0; kb < kb1; kb += kps) {
           if (!wait_fast(sfull_bar(slot), sph, abort_flag, status) ||
               !wait_fast(tfull_bar(buf), tph, abort_flag, status)) {
@@ -323,51 +324,58 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
           const uint32_t t0 = lanes + buf * buf_cols;
           // two products on their way from TMEM at a time: of two K blocks, or (one per stage) of two
           // runs of columns
-          auto load = [&](int j, int col, uint32_t (&v)[16], float4 (&k)[4]) {
-            tmem_ld16(t0 + j * stride + col, v);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              k[q] = *reinterpret_cast<const float4*>(sc + scale_at(bn, j, col + 4 * q, kind & 1));
-          };
-          auto add = [&](float* y, uint32_t (&v)[16], float4 (&k)[4]) {
+          auto load = [&](int j, int col, uint32_t (&v)[16]) { tmem_ld16(t0 + j * stride + col, v); };
+          auto add = [&](float* y, int j, int col, uint32_t (&v)[16]) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              fma2(y[4 * q], y[4 * q + 1], k[q].x, k[q].y, __uint_as_float(v[4 * q]),
+              const float4 k =
+                  *reinterpret_cast<const float4*>(sc + scale_at(bn, j, col + 4 * q, kind & 1));
+              fma2(y[4 * q], y[4 * q + 1], k.x, k.y, __uint_as_float(v[4 * q]),
                    __uint_as_float(v[4 * q + 1]));
-              fma2(y[4 * q + 2], y[4 * q + 3], k[q].z, k[q].w, __uint_as_float(v[4 * q + 2]),
+              fma2(y[4 * q + 2], y[4 * q + 3], k.z, k.w, __uint_as_float(v[4 * q + 2]),
                    __uint_as_float(v[4 * q + 3]));
             }
           };
           uint32_t v0[16], v1[16];
-          float4 k0[4], k1[4];
-          if (nk == 1) {
+          if (halves) {
+            for (int j = (kb - kb0 + part) & 1; j < nk; j += 4) {
+              load(j, 0, v0);
+              if (j + 2 < nk) load(j + 2, 0, v1);
+              tmem_wait_ld16(v0);
+              add(acc, j, 0, v0);
+              if (j + 2 < nk) {
+                tmem_wait_ld16(v1);
+                add(acc, j + 2, 0, v1);
+              }
+            }
+          } else if (nk == 1) {
 #pragma unroll
-            for (int c = 0; c < kChunks; c += 2) {
+            for (int c = 0; c < CHUNKS; c += 2) {
               const int col = 16 * (2 * c + part);
               if (col >= w.n) break;
-              const bool two = col + 32 < w.n;
-              load(0, col, v0, k0);
-              if (two) load(0, col + 32, v1, k1);
+              const bool two = CHUNKS > 1 && col + 32 < w.n;
+              load(0, col, v0);
+              if (two) load(0, col + 32, v1);
               tmem_wait_ld16(v0);
-              add(acc + (FP8 ? 16 * c : 0), v0, k0);
+              add(acc + (FP8 ? 16 * c : 0), 0, col, v0);
               if (two) {
                 tmem_wait_ld16(v1);
-                add(acc + (FP8 ? 16 * c + 16 : 0), v1, k1);
+                add(acc + (FP8 && CHUNKS > 1 ? 16 * c + 16 : 0), 0, col + 32, v1);
               }
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
+            for (int c = 0; c < CHUNKS; ++c) {
               const int col = 16 * (2 * c + part);
               if (col >= w.n) break;
               for (int j = 0; j < nk; j += 2) {
-                load(j, col, v0, k0);
-                if (j + 1 < nk) load(j + 1, col, v1, k1);
+                load(j, col, v0);
+                if (j + 1 < nk) load(j + 1, col, v1);
                 tmem_wait_ld16(v0);
-                add(acc + (FP8 ? 16 * c : 0), v0, k0);
+                add(acc + (FP8 ? 16 * c : 0), j, col, v0);
                 if (j + 1 < nk) {
                   tmem_wait_ld16(v1);
-                  add(acc + (FP8 ? 16 * c : 0), v1, k1);
+                  add(acc + (FP8 ? 16 * c : 0), j + 1, col, v1);
                 }
               }
             }
@@ -392,13 +400,25 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       }
       if (!ok) break;
       tc_fence_after();
+      if (halves) {
+        if (part == 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) other[i * kLinWRows + row] = acc[i];
+        }
+        epilogue_barrier();
+        if (part == 0) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[i] += other[i * kLinWRows + row];
+        }
+        if (u + step < units) epilogue_barrier();  // before the next unit's are written
+      }
       // what the unit before sent has been added up, here and by the others
       if (C > 1 && u != first && !wait_bounded_cluster(rempty_bar, rph ^ 1u, abort_flag, status)) {
         ok = false;
         break;
       }
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
+      for (int c = 0; c < CHUNKS; ++c) {
         const int col = 16 * (2 * c + part);
         if (col >= w.n) break;
         float v[16];
@@ -490,14 +510,14 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
         }
         float* dst = scales + slot * kps * 2 * bn;
         for (int j0 = 0; j0 < kps; j0 += 4) {
-          float v[4][kMaxBn / 32], s0[4], s1[4];
+          float v[4][CHUNKS], s0[4], s1[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const bool in = j0 + j < kps && kb + j0 + j < kb1;
             s0[j] = in ? __ldg(w0 + kb + j0 + j) : 0.f;
             s1[j] = in ? __ldg(w1 + kb + j0 + j) : 0.f;
 #pragma unroll
-            for (int i = 0; i < kMaxBn / 32; ++i)
+            for (int i = 0; i < CHUNKS; ++i)
               v[j][i] = in && lane + 32 * i < w.n ? __ldg(xs + (long long)(kb + j0 + j) * a.T + 32 * i)
                                                   : 0.f;
           }
@@ -505,7 +525,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
           for (int j = 0; j < 4; ++j) {
             if (j0 + j >= kps) break;
 #pragma unroll
-            for (int i = 0; i < kMaxBn / 32; ++i) {
+            for (int i = 0; i < CHUNKS; ++i) {
               const int c = lane + 32 * i;
               if (c < bn) {
                 dst[scale_at(bn, j0 + j, c, 0)] = v[j][i] * s0[j];
@@ -551,13 +571,13 @@ cudaLaunchConfig_t config(bool fp8, int C, unsigned grid, size_t smem, cudaStrea
 }
 
 // Prepares the kernel on the current device and finds its clusters there, once.
-template <bool FP8, bool GATED>
+template <bool FP8, bool GATED, int CHUNKS>
 int room(int C) {
   static int cached[64][kMaxCluster + 1];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (!cached[dev][C]) {
-    auto kernel = linear_stream_kernel<FP8, GATED>;
+    auto kernel = linear_stream_kernel<FP8, GATED, CHUNKS>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmemMax) !=
         cudaSuccess)
       return 0;
@@ -572,28 +592,29 @@ int room(int C) {
   return cached[dev][C];
 }
 
-template <bool FP8, bool GATED>
+template <bool FP8, bool GATED, int CHUNKS>
 cudaError_t launch(const Maps& maps, const LinLaunch& L, unsigned grid, size_t smem,
                    cudaStream_t stream) {
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = config(FP8, L.cluster, grid, smem, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, linear_stream_kernel<FP8, GATED>, maps, L);
+  return cudaLaunchKernelEx(&cfg, linear_stream_kernel<FP8, GATED, CHUNKS>, maps, L);
 }
 
 }  // namespace
 
-int linear_stream_room(const LinearArgs& a, int size) {
+int linear_stream_room(const LinearArgs& a, int bn, int size) {
   if (size < 1 || size > kMaxCluster) return 0;
   const bool gated = a.act == GBMOE_EPI_SILU_MUL;
-  if (a.fp8) return gated ? room<true, true>(size) : room<true, false>(size);
-  return gated ? room<false, true>(size) : room<false, false>(size);
+  if (a.fp8 && bn <= 32) return gated ? room<true, true, 1>(size) : room<true, false, 1>(size);
+  if (a.fp8) return gated ? room<true, true, 2>(size) : room<true, false, 2>(size);
+  return gated ? room<false, true, 4>(size) : room<false, false, 4>(size);
 }
 
 cudaError_t launch_linear_stream(LinLaunch L, long long max_units, cudaStream_t stream) {
   const LinearArgs& a = L.a;
   const bool gated = a.act == GBMOE_EPI_SILU_MUL;
   const int C = L.cluster, most_rows = L.rows[0];
-  if (L.bn < 16 || L.bn > kMaxBn || L.bn % 16 || C < 1 || C > kMaxCluster || C > L.k_blocks ||
+  if (L.bn < 16 || L.bn > (a.fp8 ? kMaxBnFp8 : kMaxBn) || L.bn % 16 || C < 1 || C > kMaxCluster || C > L.k_blocks ||
       L.choices < 1 || L.choices > kWMaps)
     return cudaErrorInvalidValue;
   for (int i = 0; i < L.choices; ++i) {
@@ -614,14 +635,14 @@ cudaError_t launch_linear_stream(LinLaunch L, long long max_units, cudaStream_t 
   uint32_t kps = free_bytes / 3 / per_k;
   if (kps > range) kps = range;
   if (kps > (uint32_t)kMaxKps) kps = kMaxKps;
-  if (getenv("LIN_KPS")) kps = atoi(getenv("LIN_KPS"));
   if (a.fp8)
     while (kps > 1 && kps * L.bn > 128) --kps;
   if (kps < 1) kps = 1;
   const uint32_t stage = kps * per_k;
   const uint32_t scale = a.fp8 ? kScaleSlots * kps * 2 * L.bn * 4 : 0;
+  const uint32_t half = a.fp8 && L.bn == 16 ? 16 * kLinWRows * 4 : 0;
   // the MMA reads 128 rows from each K block's weights on: behind the last of them too
-  const uint32_t over = kLinWBytes, rest = red + scale + tab + bars;
+  const uint32_t over = kLinWBytes, rest = red + scale + half + tab + bars;
   const uint32_t behind = rest > over ? rest : over;
   if (kLinSmemMax < 1024 + behind + 2 * stage) return cudaErrorInvalidValue;
   uint32_t stages = (kLinSmemMax - 1024 - behind) / stage;
@@ -631,7 +652,8 @@ cudaError_t launch_linear_stream(LinLaunch L, long long max_units, cudaStream_t 
   L.stages = (int)stages;
   L.red_off = (int)(stages * stage);
   L.scale_off = L.red_off + (int)red;
-  L.bar_off = L.scale_off + (int)scale;
+  L.half_off = L.scale_off + (int)scale;
+  L.bar_off = L.half_off + (int)half;
   L.tab_off = L.bar_off + (int)bars;
   Maps maps;
   const int boxed = L.whole ? (int)kps : 0;
@@ -639,15 +661,18 @@ cudaError_t launch_linear_stream(LinLaunch L, long long max_units, cudaStream_t 
             (!a.offsets || lin_map_x(a, 8, boxed, &maps.x[1]));
   for (int i = 0; i < L.choices; ++i) ok = ok && lin_map_tiles(a, L.rows[i], boxed, &maps.w[i]);
   if (!ok) return cudaErrorInvalidValue;
-  const int most = linear_stream_room(a, C);
+  const int most = linear_stream_room(a, L.bn, C);
   if (most < 1) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(max_units < most ? max_units : most) * C;
   const size_t smem = 1024 + stages * stage + behind;
+  if (a.fp8 && L.bn <= 32)
+    return gated ? launch<true, true, 1>(maps, L, grid, smem, stream)
+                 : launch<true, false, 1>(maps, L, grid, smem, stream);
   if (a.fp8)
-    return gated ? launch<true, true>(maps, L, grid, smem, stream)
-                 : launch<true, false>(maps, L, grid, smem, stream);
-  return gated ? launch<false, true>(maps, L, grid, smem, stream)
-               : launch<false, false>(maps, L, grid, smem, stream);
+    return gated ? launch<true, true, 2>(maps, L, grid, smem, stream)
+                 : launch<true, false, 2>(maps, L, grid, smem, stream);
+  return gated ? launch<false, true, 4>(maps, L, grid, smem, stream)
+               : launch<false, false, 4>(maps, L, grid, smem, stream);
 }
 
 }  // namespace gbmoe
