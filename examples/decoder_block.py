@@ -3,8 +3,8 @@ attention, output projection, norm with an 8-bit output, FP8 FusedMoE layer.
 
     python examples/decoder_block.py            # prompts, then decode steps; prints the times
 
-The block's own kernels do everything but the two dense projections (plain torch products).
-Weights are random; pages are handed out by a trivial allocator.
+Every step runs in the package's kernels; the output projection adds the residual stream in its
+epilogue. Weights are random; pages are handed out by a trivial allocator.
 """
 import argparse
 import os
@@ -90,7 +90,7 @@ class DecoderBlock:
         """Attention of the batch's new tokens x [T, hidden]; (attention rows, residual stream)."""
         s = self.s
         y, res, _, _ = binding.moe_rms_norm(x, self.norm1, residual=residual)
-        qkv = (y @ self.wqkv.t()).view(x.shape[0], -1, s.head_dim)
+        qkv = binding.moe_linear(y, self.wqkv).view(x.shape[0], -1, s.head_dim)
         paged = (self.k_cache, self.v_cache, *batch)
         q = self.attn.append(qkv[:, :s.q_heads], qkv[:, s.q_heads:s.q_heads + s.kv_heads],
                              qkv[:, s.q_heads + s.kv_heads:], *paged, cos_sin=self.cos_sin)
@@ -99,8 +99,8 @@ class DecoderBlock:
     def __call__(self, x, residual, batch):
         """(block output, residual stream): their sum is the next block's input."""
         o, res = self.attend(x, residual, batch)
-        h = o.flatten(1) @ self.wo.t()
-        y, res, yq, ys = binding.moe_rms_norm(h, self.norm2, residual=res, out="both")
+        res = binding.moe_linear(o.flatten(1), self.wo, residual=res)
+        y, _, yq, ys = binding.moe_rms_norm(res, self.norm2, out="both")
         return self.moe(y, gate_weight=self.gate, hidden_q=yq, hidden_scale=ys), res
 
     def status(self):

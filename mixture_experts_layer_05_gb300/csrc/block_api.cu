@@ -13,6 +13,8 @@ namespace gbmoe {
 namespace {
 
 constexpr int kMaxRows = 1 << 22;
+constexpr int kMaxLinearK = 1 << 24;
+constexpr int64_t kMaxLinearStride = (1ll << 39) - 16;  // a tensor map's strides have 40 bits of bytes
 constexpr size_t kStatusBytes = 256;
 // attention: the status region, then the counters of cut units
 constexpr size_t kAttnHeadBytes = 1024;
@@ -88,8 +90,8 @@ gbmoe_status_t linear(int T, int G, int K, int N, const int32_t* offsets, bool g
   const bool gated = g->activation == GBMOE_EPI_SILU_MUL;
   if (fp8 != (g->x_scale != nullptr) || fp8 != (g->weight_scale != nullptr))
     return GBMOE_ERR_INVALID_ARG;
-  if (K % (fp8 ? kFp8Block : 8) || (gated && N % (fp8 ? 2 * kFp8Block : 32)) ||
-      G > kLinearMaxGroups || (int64_t)G * N > INT32_MAX)
+  if (K % (fp8 ? kFp8Block : 8) || K > kMaxLinearK || (gated && N % (fp8 ? 2 * kFp8Block : 32)) ||
+      G > kLinearMaxGroups || (int64_t)G * N > INT32_MAX || g->x_stride > kMaxLinearStride)
     return GBMOE_ERR_UNSUPPORTED;
   // tiles of 128 columns by 16 rows are the smallest that any kernel counts
   if (((int64_t)T / 16 + G) * ((N + 127) / 128) > (1 << 30)) return GBMOE_ERR_UNSUPPORTED;

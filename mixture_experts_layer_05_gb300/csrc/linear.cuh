@@ -46,9 +46,9 @@ struct LinLaunch {
 // to measurements at K = N = 4096: a CTA takes 128 bytes a ns from L2 and HBM together; a K block's
 // MMAs, whose time goes by their 128 rows, and the operands of its columns take 90 and 1 a row (e4m3: its
 // promotion 90 and 5); a unit's beginning and end 300.
-__host__ __device__ inline int lin_unit_ns(bool fp8, int R, int n, int k_blocks) {
+__host__ __device__ inline long long lin_unit_ns(bool fp8, int R, int n, int k_blocks) {
   const int math = 90 + (fp8 ? 5 * n : n);
-  return k_blocks * (R + n > math ? R + n : math) + 300;
+  return (long long)k_blocks * (R + n > math ? R + n : math) + 300;
 }
 
 namespace {

@@ -32,8 +32,8 @@ constexpr int kScaleSlots = 4;                   // e4m3: stages of scales in fl
 
 constexpr int threads_of(bool fp8) { return 64 + 32 * kEpiWarps + (fp8 ? 32 : 0); }
 // barriers: full, empty per stage; tfull, tempty per TMEM buffer; partial sums received, sent ones
-// consumed; scales full, empty per slot
-constexpr int kBars = 2 * kMaxStages + 2 * kBufsMax + 2 + 2 * kScaleSlots;
+// consumed; the epilogue's warps; scales full, empty per slot
+constexpr int kBars = 2 * kMaxStages + 2 * kBufsMax + 3 + 2 * kScaleSlots;
 
 struct Maps {
   CUtensorMap w[kWMaps];
@@ -51,9 +51,6 @@ __device__ __forceinline__ void copy_to_cluster(uint32_t dst, uint32_t src, uint
 }
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-__device__ __forceinline__ void epilogue_barrier() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
 }
 
 // Scales of a slot: for K block j of the stage and row c, the products with the two weight blocks that
@@ -85,9 +82,9 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + kBufsMax + b); };
   const uint32_t rfull_bar = bar0 + 8u * (2 * kMaxStages + 2 * kBufsMax);
-  const uint32_t rempty_bar = rfull_bar + 8u;
-  auto sfull_bar = [&](int s) { return rempty_bar + 8u + 8u * s; };
-  auto sempty_bar = [&](int s) { return rempty_bar + 8u + 8u * (kScaleSlots + s); };
+  const uint32_t rempty_bar = rfull_bar + 8u, meet_bar = rempty_bar + 8u;
+  auto sfull_bar = [&](int s) { return meet_bar + 8u + 8u * s; };
+  auto sempty_bar = [&](int s) { return meet_bar + 8u + 8u * (kScaleSlots + s); };
   // TMEM: two accumulators, or a stage's K block products side by side
   uint32_t stride = 16;
   while ((int)stride < bn) stride *= 2;
@@ -153,6 +150,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     if (lane == 0) {
       mbar_init(rfull_bar, 1);
       mbar_init(rempty_bar, kEpiWarps * C);
+      mbar_init(meet_bar, kEpiWarps);
       *abort_flag = 0;
     }
     fence_mbar_init();
@@ -293,8 +291,16 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     float* got = sent + bn * w_rows;                            // [rank][column][w_rows]
     const int got_cols = (bn + C - 1) / C;
     int buf = 0, slot = 0;
-    uint32_t tph = 0, sph = 0, rph = 0;
+    uint32_t tph = 0, sph = 0, rph = 0, mph = 0;
     bool ok = true;
+    // the epilogue's warps meet, in bounded time as all waits
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(meet_bar);
+      const bool met = wait_fast(meet_bar, mph, abort_flag, status);
+      mph ^= 1u;
+      return met;
+    };
     for (int u = first; ok && u < units; u += step) {
       const LinUnit w = groups.unit(L, n_tiles, u);
       const int f0 = w.nt * tile_cols;             // the tile's first output column
@@ -405,12 +411,18 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) other[i * kLinWRows + row] = acc[i];
         }
-        epilogue_barrier();
+        if (!meet()) {
+          ok = false;
+          break;
+        }
         if (part == 0) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[i] += other[i * kLinWRows + row];
         }
-        if (u + step < units) epilogue_barrier();  // before the next unit's are written
+        if (u + step < units && !meet()) {         // before the next unit's are written
+          ok = false;
+          break;
+        }
       }
       // what the unit before sent has been added up, here and by the others
       if (C > 1 && u != first && !wait_bounded_cluster(rempty_bar, rph ^ 1u, abort_flag, status)) {
@@ -451,7 +463,10 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       }
       if (C > 1) {
         fence_async_shared();
-        epilogue_barrier();
+        if (!meet()) {
+          ok = false;
+          break;
+        }
         if (warp == 2 && lane < C) {
           // the others' sums of this CTA's columns, and this one's of theirs
           const uint32_t col_bytes = w_rows * 4;

@@ -47,7 +47,8 @@ def test_refusals(lib, G):
         assert _call(lib, G=G, **kw) == BAD, kw
     for kw in (dict(K=100), dict(K=4), dict(FP8, K=136), dict(FP8, K=64), dict(activation=5, N=528),
                dict(activation=5, N=33), dict(FP8, activation=5, N=128), dict(FP8, activation=5, N=384),
-               dict(weight_quant=2), dict(T=1 << 22, N=1 << 23)):
+               dict(weight_quant=2), dict(T=1 << 22, N=1 << 23), dict(K=(1 << 24) + 8),
+               dict(x_stride=1 << 39)):
         assert _call(lib, G=G, **kw) == UNSUP, kw
 
 
