@@ -262,39 +262,53 @@ struct LinLane {
   }
 };
 
-// 2 COLS (GATED) or COLS values per lane: the sums of the warp's weight rows for rows t0 .. t0 + cnt
-// of x, cnt <= the number of values. With GATED lanes l and l + 16 swap halves: the lower keep the
-// first half of the columns, the upper the second.
+// What the epilogue adds to COLS values of this lane: row weights and residual of rows t0 .. t0 + cnt.
 template <bool GATED, int COLS>
-__device__ __forceinline__ void lin_store(const LinearArgs& a, const LinLane& l, int t0, int cnt,
-                                          float (&v)[GATED ? 2 * COLS : COLS]) {
-  float y[COLS], rw[COLS];
+struct LinExtra {
+  float rw[COLS];
   __nv_bfloat16 res[COLS];
-  const bool upper = GATED && (threadIdx.x & 16) != 0;
-  if (upper) {
-    t0 += COLS;
-    cnt -= COLS;
-  }
-  // all loads first and unconditional (rows past the last repeat it), so that they fly together
-  if (cnt > 0) {
+
+  // Unconditional loads (rows past the last repeat it), so that they fly together; called early, they
+  // fly under the products.
+  __device__ __forceinline__ void fetch(const LinearArgs& a, const LinLane& l, int t0, int cnt) {
+    if (GATED && (threadIdx.x & 16)) {
+      t0 += COLS;
+      cnt -= COLS;
+    }
+    if (!l.in || cnt <= 0) return;
     if (a.row_weight) {
 #pragma unroll
       for (int i = 0; i < COLS; ++i) rw[i] = __ldg(a.row_weight + t0 + min(i, cnt - 1));
     }
-    if (a.residual && l.in) {
+    if (a.residual) {
       const __nv_bfloat16* r =
           static_cast<const __nv_bfloat16*>(a.residual) + (long long)t0 * a.residual_stride + l.f;
 #pragma unroll
       for (int i = 0; i < COLS; ++i) res[i] = r[min(i, cnt - 1) * a.residual_stride];
     }
   }
+};
+
+// 2 COLS (GATED) or COLS values per lane: the sums of the warp's weight rows for rows t0 .. t0 + cnt
+// of x, cnt <= the number of values. With GATED lanes l and l + 16 swap halves: the lower keep the
+// first half of the columns, the upper the second.
+template <bool GATED, int COLS>
+__device__ __forceinline__ void lin_store(const LinearArgs& a, const LinLane& l, int t0, int cnt,
+                                          float (&v)[GATED ? 2 * COLS : COLS],
+                                          const LinExtra<GATED, COLS>& x) {
+  float y[COLS];
   if (GATED) {
+    const bool upper = (threadIdx.x & 16) != 0;
 #pragma unroll
     for (int i = 0; i < COLS; ++i) {
       const float other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + COLS], 16);
       const float gate = (upper ? other : v[i]) + l.bias;
       const float up = (upper ? v[i + COLS] : other) + l.up_bias;
       y[i] = lin_silu(gate) * up;
+    }
+    if (upper) {
+      t0 += COLS;
+      cnt -= COLS;
     }
   } else {
 #pragma unroll
@@ -304,11 +318,11 @@ __device__ __forceinline__ void lin_store(const LinearArgs& a, const LinLane& l,
   if (!l.in || cnt <= 0) return;
   if (a.row_weight) {
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) y[i] *= rw[i];
+    for (int i = 0; i < COLS; ++i) y[i] *= x.rw[i];
   }
   if (a.residual) {
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) y[i] += __bfloat162float(res[i]);
+    for (int i = 0; i < COLS; ++i) y[i] += __bfloat162float(x.res[i]);
   }
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (long long)t0 * a.out_stride + l.f;
 #pragma unroll

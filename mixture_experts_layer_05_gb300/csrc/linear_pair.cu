@@ -167,9 +167,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const LinUnit w = groups.unit(L, L.n_tiles, u);
       const LinLane l = LinLane::make<GATED>(
           a, w.g, (w.nt * 2 + rank) * kTileCols + quarter * (kTileCols / 4));
-      // the residual's way from HBM lies under the products
+      // the first run of columns comes under the products, and the others' residual to L2
+      constexpr int kStore = GATED ? 16 : 32;
+      LinExtra<GATED, kStore> extra;
+      extra.fetch(a, l, w.m0 + part * 32, w.n - part * 32);
       if (a.residual && l.in)
-        for (int at = part * 32; at < w.n; at += 64)
+        for (int at = part * 32 + 64; at < w.n; at += 64)
           for (int i = 0; i < 32 && at + i < w.n; ++i)
             lin_prefetch(static_cast<const __nv_bfloat16*>(a.residual) +
                          (long long)(w.m0 + at + i) * a.residual_stride + l.f);
@@ -183,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld(t);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(t[i]);
-        lin_store<GATED, GATED ? 16 : 32>(a, l, w.m0 + at, w.n - at, v);
+        if (at >= 64) extra.fetch(a, l, w.m0 + at, w.n - at);
+        lin_store<GATED, kStore>(a, l, w.m0 + at, w.n - at, v, extra);
       }
       tc_fence_before();
       __syncwarp();

@@ -308,8 +308,12 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       l.in = l.in && row < R;
       const int per = (w.n + C - 1) / C;           // columns that each CTA finishes
       const int mine = min(per, w.n - rank * per);
-      if (a.residual && l.in)
-        for (int c = part; c < mine; c += 2)
+      // the first run of columns that this warp finishes; further ones are brought to L2
+      constexpr int kStore = GATED ? 8 : 16;
+      LinExtra<GATED, kStore> extra;
+      extra.fetch(a, l, w.m0 + rank * per + 16 * part, mine - 16 * part);
+      if (a.residual && l.in && mine > 32)
+        for (int c = 32 + part; c < mine; c += 2)
           lin_prefetch(static_cast<const __nv_bfloat16*>(a.residual) +
                       (long long)(w.m0 + rank * per + c) * a.residual_stride + l.f);
       float acc[FP8 ? CHUNKS * 16 : 16];
@@ -445,7 +449,8 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
           for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(t[i]);
         }
         if (C == 1) {
-          lin_store<GATED, GATED ? 8 : 16>(a, l, w.m0 + col, w.n - col, v);
+          if (c > 0) extra.fetch(a, l, w.m0 + col, w.n - col);
+          lin_store<GATED, kStore>(a, l, w.m0 + col, w.n - col, v, extra);
         } else if (row < w_rows) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -496,7 +501,8 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
                 if (c0 + i < mine) v[i] += from[(c0 + i) * w_rows + row];
             }
           }
-          lin_store<GATED, GATED ? 8 : 16>(a, l, w.m0 + rank * per + c0, mine - c0, v);
+          if (c0 >= 32) extra.fetch(a, l, w.m0 + rank * per + c0, mine - c0);
+          lin_store<GATED, kStore>(a, l, w.m0 + rank * per + c0, mine - c0, v, extra);
         }
         if (u + step < units) {
           __syncwarp();

@@ -1,7 +1,11 @@
 """moe_linear and moe_grouped_linear on the GPU against 64-bit references whose bounds count the
 operators' roundings (tests/linear_cases.py)."""
 import math
+import os
 import random
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
@@ -64,6 +68,32 @@ def test_linear_fp8(cuda_lib, T, K, N):
                                        (700, 4096, 4096, "silu_mul")])
 def test_linear_fp8_wide(cuda_lib, T, K, N, act):
     c = Linear(T, K, N, act=act, fp8=True, residual=True)
+    c.check(c.call(binding))
+
+
+# sizes that the cut of few rows answers with clusters of 1 to 8 CTAs, tiles of 8 to 128 weight rows and
+# one to three rounds of units
+CUTS = [(1, 512, 256), (1, 512, 24576), (48, 4096, 4096), (1, 4096, 2048), (24, 4096, 2048),
+        (64, 4096, 2048), (64, 2048, 2048), (24, 8192, 1024), (48, 2048, 256), (64, 2048, 1024),
+        (80, 512, 12288), (80, 512, 24576), (80, 4096, 4096), (64, 8192, 24576), (1, 8192, 4096),
+        (80, 2048, 2048), (1, 8192, 2048), (80, 2048, 1024), (80, 4096, 1024), (96, 4160, 1000)]
+
+
+@pytest.mark.parametrize("T,K,N", CUTS)
+@pytest.mark.parametrize("act", ["none", "silu_mul"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_linear_cuts_of_few_rows(cuda_lib, T, K, N, act, fp8):
+    if fp8 and K % 128 or act == "silu_mul" and N % 256:
+        pytest.skip("sizes of the other form")
+    c = Linear(T, K, N, act=act, fp8=fp8, bias=True, residual=True)
+    c.check(c.call(binding))
+
+
+@pytest.mark.parametrize("T", [96, 97, 192, 256, 257])
+@pytest.mark.parametrize("K,N", [(512, 1024), (2048, 9000)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_linear_between_few_and_many_rows(cuda_lib, T, K, N, fp8):
+    c = Linear(T, K, N, act="silu", fp8=fp8, residual=True)
     c.check(c.call(binding))
 
 
@@ -180,6 +210,26 @@ def test_grouped_drawn(cuda_lib, seed):
                residual=rng.random() < 0.5, lead=rng.choice([0, 3]), tail=rng.choice([0, 9]))
     if c.T:
         c.check(c.call(binding))
+
+
+@pytest.mark.parametrize("sizes", [[4], [1, 2], [0, 9, 8, 7], [100, 3, 0, 1]])
+@pytest.mark.parametrize("K,N", [(4096, 512), (8192, 2048), (512, 8192), (2048, 96 * 128)])
+@pytest.mark.parametrize("act", ["none", "silu_mul"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_grouped_few_groups(cuda_lib, sizes, K, N, act, fp8):
+    """Long sums for few rows: several CTAs to a tile, in several rounds where the tiles are small."""
+    c = Linear(0, K, N, sizes=sizes, act=act, fp8=fp8, weighted=True, residual=True)
+    c.check(c.call(binding))
+
+
+@pytest.mark.parametrize("mean", [8, 9, 32, 33])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_grouped_between_few_and_many_rows(cuda_lib, mean, fp8):
+    rng = random.Random(mean)
+    sizes = [rng.randint(0, 2 * mean) for _ in range(11)]
+    sizes.append(max(0, 12 * mean - sum(sizes)))
+    c = Linear(0, 640, 768, sizes=sizes, act="silu_mul", fp8=fp8, bias=True)
+    c.check(c.call(binding))
 
 
 def test_grouped_most_groups(cuda_lib):
@@ -317,6 +367,54 @@ def test_captured_calls_follow_their_offsets(cuda_lib, rows, fp8):
         torch.cuda.synchronize()
         for o in outs:
             c.check(o)
+
+
+FIRST_IN_CAPTURE = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+from mixture_experts_layer_05_gb300 import binding
+from tests.linear_cases import Linear
+cases = [Linear(T, 512, 1024, act=act, fp8=fp8) for T in (3, 600) for act in ("none", "silu_mul")
+         for fp8 in (False, True)] + [Linear(48, 4096, 4096)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = [c.call(binding) for c in cases]
+graph.replay()
+torch.cuda.synchronize()
+for c, o in zip(cases, outs):
+    c.check(o)
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture(cuda_lib):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE.format(root=root)], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_calls_from_several_threads(cuda_lib):
+    cases = [Linear(T, 1024, 768, fp8=T % 2 == 1) for T in (1, 2, 40, 41, 300, 301)]
+    want = [c.call(binding) for c in cases]
+    torch.cuda.synchronize()
+    got = [None] * len(cases)
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i] = cases[i].call(binding)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
 
 
 def test_binding_refuses(cuda_lib):
