@@ -85,7 +85,7 @@ StreamCut cut_stream(const LinearArgs& a, int groups, int mean, int k_blocks) {
         R = 128;
       }
       const int turns = ceil_div(blocks * ceil_div(a.N, R), room);
-      const double run = (double)turns * lin_unit_ns(a.fp8, R, n, kb);
+      const double run = (double)turns * lin_unit_ns(a.fp8, gated, R, n, kb);
       const double ns = (run > hbm ? run : hbm) + (C > 1 ? turns * (3500 + n * R / 20.0) : 0);
       if (ns < best.ns * 0.98) {
         best.ns = ns;

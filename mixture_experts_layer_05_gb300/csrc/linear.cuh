@@ -44,10 +44,10 @@ struct LinLaunch {
 
 // The stream kernel's time for a unit of R weight rows and n rows of x over so many K blocks, in ns, fitted
 // to measurements at K = N = 4096: a CTA takes 128 bytes a ns from L2 and HBM together; a K block's
-// MMAs, whose time goes by their 128 rows, and the operands of its columns take 90 and 1 a row (e4m3: its
-// promotion 90 and 5); a unit's beginning and end 300.
-__host__ __device__ inline long long lin_unit_ns(bool fp8, int R, int n, int k_blocks) {
-  const int math = 90 + (fp8 ? 5 * n : n);
+// MMAs, whose time goes by their 128 (plain tiles of up to 64: 64) weight rows, and the operands of its
+// columns take 90 and 1 (55 and 1.2) a row of x (e4m3: its promotion 90 and 5); a unit's beginning and end 300.
+__host__ __device__ inline long long lin_unit_ns(bool fp8, bool gated, int R, int n, int k_blocks) {
+  const int math = fp8 ? 90 + 5 * n : R <= 64 && !gated ? 55 + 6 * n / 5 : 90 + n;
   return (long long)k_blocks * (R + n > math ? R + n : math) + 300;
 }
 

@@ -4,7 +4,8 @@
 // CTAs), so the 6.8 TB/s need every SM, all of them for the same time. So the tile is cut to the SMs
 // rather than to the MMA: a unit is R <= 128 weight rows by at most bn rows of x, where R is such that
 // the units come out in whole rounds; the MMA (tcgen05.mma, M = 128) runs over R rows and over what lies
-// behind them in shared memory, whose TMEM lanes nobody reads. Where the rows of x are many against R,
+// behind them in shared memory, whose TMEM lanes nobody reads. (Plain tiles of up to 64 rows run with
+// M = 64: with few columns an MMA takes as long as its weight rows' operands, 23 cycles instead of 39.) Where the rows of x are many against R,
 // their reading costs more than that of the weights; there a cluster of C CTAs takes a tile of C times
 // the rows and cuts its K blocks into C ranges. The C partial sums are joined through distributed
 // shared memory: each CTA sends the columns that CTA d finishes to d (one bulk copy each), which adds
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       const int nt = (a.cols + cols - 1) / cols;
       const long long u = (long long)groups.before[a.G] * nt;
       if (i > 0 && u > 1 << 30) break;             // units are counted in 32 bits
-      const long long cost = (u + step - 1) / step * lin_unit_ns(FP8, r, xr, kb1 - kb0);
+      const long long cost = (u + step - 1) / step * lin_unit_ns(FP8, GATED, r, xr, kb1 - kb0);
       if (i == 0 || cost < best) {
         best = cost;
         pick = i;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   }
   const int units = groups.units(n_tiles);
   const int tile_cols = GATED ? R / 2 : R;
+  const bool half_m = !GATED && R <= 64;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       for (int u = first; ok && u < units; u += step) {
         const LinUnit w = groups.unit(L, n_tiles, u);
         const int n = (w.n + 15) & ~15;
-        const uint32_t idesc = FP8 ? idesc_e4m3(128, n) : idesc_bf16(128, n);
+        const uint32_t idesc = FP8 ? idesc_e4m3(half_m ? 64 : 128, n) : idesc_bf16(half_m ? 64 : 128, n);
         const uint32_t step_w = (uint32_t)R * 8;   // a K block's weights and rows, in 16-byte units
         const uint32_t step_x = (uint32_t)(grouped && w.n <= 8 ? 8 : bn) * 8;
         for (int kb = kb0; kb < kb1; kb += kps) {
@@ -283,7 +285,9 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    const int row = quarter * 32 + lane;
+    const int spot = quarter * 32 + lane;
+    // the lane's weight row: with M = 64, D's rows are the first 16 lanes of every quarter
+    const int row = !half_m ? spot : lane < 16 ? quarter * 16 + lane : kLinWRows;
     // e4m3 with one run of columns: the two warps of a quarter take every other K block instead
     const bool halves = FP8 && bn == 16;
     float* other = reinterpret_cast<float*>(smem + L.half_off);  // [column][128 rows] of the second one
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     for (int u = first; ok && u < units; u += step) {
       const LinUnit w = groups.unit(L, n_tiles, u);
       const int f0 = w.nt * tile_cols;             // the tile's first output column
-      LinLane l = LinLane::make<GATED>(a, w.g, f0 + quarter * (GATED ? 16 : 32));
+      LinLane l = LinLane::make<GATED>(a, w.g, f0 + quarter * (GATED || half_m ? 16 : 32));
       l.in = l.in && row < R;
       const int per = (w.n + C - 1) / C;           // columns that each CTA finishes
       const int mine = min(per, w.n - rank * per);
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
       if (halves) {
         if (part == 1) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) other[i * kLinWRows + row] = acc[i];
+          for (int i = 0; i < 16; ++i) other[i * kLinWRows + spot] = acc[i];
         }
         if (!meet()) {
           ok = false;
@@ -421,7 +425,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
         }
         if (part == 0) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[i] += other[i * kLinWRows + row];
+          for (int i = 0; i < 16; ++i) acc[i] += other[i * kLinWRows + spot];
         }
         if (u + step < units && !meet()) {         // before the next unit's are written
           ok = false;
