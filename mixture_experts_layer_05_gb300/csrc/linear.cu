@@ -97,6 +97,35 @@ StreamCut cut_stream(const LinearArgs& a, int groups, int mean, int k_blocks) {
   return best;
 }
 
+// How the kernels for many rows cut it: units of 256 weight rows and `bn` rows of x. A K block of a unit
+// takes the e4m3 kernel some 500 ns (128 rows, one CTA), pairs of CTAs the MMAs' 1.1 ns a row, or
+// what the issue of its copies takes. Half of the groups count as ending in a block of their own.
+struct WideCut {
+  int bn, tiles;
+  double ns;
+};
+
+WideCut cut_wide(const LinearArgs& a, int groups, int k_blocks) {
+  WideCut best = {0, ceil_div(a.cols, a.act == GBMOE_EPI_SILU_MUL ? 128 : 256), 1e30};
+  const double hbm = (double)groups * a.N * a.K * (a.fp8 ? 1 : 2) / 6700;
+  const int most = a.fp8 ? 128 : 256;
+  for (int cut = 1; cut <= (a.fp8 ? 1 : 4); ++cut) {
+    // dense: the rows, cut evenly into up to four times as many blocks as needed
+    const int rows = a.offsets || a.fp8 ? most / cut : ceil_div(a.T, (long long)cut * ceil_div(a.T, most));
+    const int bn = a.fp8 ? most : (rows + 31) & ~31;
+    if (bn < 64 && cut > 1) break;
+    const long long blocks = ceil_div(a.T, bn) + (a.offsets ? groups / 2 : 0);
+    const int one = a.fp8 ? 500 : 9 * bn / 8 > 140 + bn / 8 ? 9 * bn / 8 : 140 + bn / 8;
+    const double run = (double)one * k_blocks * ceil_div(blocks * best.tiles, num_sms() / (a.fp8 ? 1 : 2));
+    const double ns = run > hbm ? run : hbm;
+    if (ns < best.ns) {
+      best.ns = ns;
+      best.bn = bn;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
@@ -106,48 +135,27 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   const bool gated = a.act == GBMOE_EPI_SILU_MUL;
   const int mean = ceil_div(a.T, a.G);
   const int groups = a.G < a.T ? a.G : a.T;                  // with rows, at most
-  // 256 weight rows to a unit, in the two kernels for many rows
-  const int wide_tiles = ceil_div(a.cols, gated ? 128 : 256);
 
-  // Few rows or many. Groups change early, as the largest has a multiple of the mean and is then cut (16
-  // of 2048 to 7168, stream and many, evenly and unevenly filled: mean 32 76.9 and 79.4 us, 81.0 and
-  // 79.5, mean 48 77.8 and 80.3, 87.0 and 85.1; e4m3, mean 8: 42.6 and 44.1, 43.7 and 43.0, mean 16:
-  // 46.8 and 45.5, 60.9 and 46.8). Dense bf16 calls change at 96 rows (K = N = 4096: 64 rows 13.4 us in
-  // the stream kernel, 128 rows 17.6 there and 14.8 in pairs). In e4m3 it goes by the outputs too, whose
-  // units of 128 by 256 take the kernel for many rows some 500 ns a K block: 128 rows of K = 4096 15.3
-  // and 21.4 us to 4096 outputs, 160 rows 47.4 and 24.7 to 16384.
-  bool many = mean > (!a.offsets ? 96 : a.fp8 ? 8 : 32);
+  // Few rows or many: by the modelled times. Measured, stream and many (us): K = N = 4096, bf16, 64 rows
+  // 12.5 and 14.6, 128 rows 17.6 and 14.8; 96 rows of 2048 to 2048 10.8 and 9.3; e4m3, 128 rows of 4096 to
+  // 4096 15.3 and 21.4, 160 to 16384 47.4 and 24.7; 16 groups of 2048 to 7168, mean 32 76.9 and 79.4,
+  // mean 64 88.5 and 81.6; e4m3, mean 8 42.6 and 44.1, mean 16 59.7 and 45.5. Above 96 rows the stream
+  // kernel's ring gets short, and it has to be well ahead.
+  const WideCut wide = cut_wide(a, groups, L.k_blocks);
+  bool many = mean > (a.offsets ? 128 : 512);
   StreamCut cut = {};
-  if (!a.offsets && a.fp8 && mean <= 256) {
+  if (!many) {
     cut = cut_stream(a, groups, mean, L.k_blocks);
-    many = cut.ns > 500.0 * L.k_blocks * ceil_div((long long)ceil_div(a.T, 128) * wide_tiles, num_sms());
-  } else if (!many) {
-    cut = cut_stream(a, groups, mean, L.k_blocks);
+    if (cut.cluster < 1) return cudaErrorInvalidConfiguration;
+    many = cut.ns > (a.offsets || mean <= 96 ? 1.0 : 0.7) * wide.ns;
   }
   if (many) {
-    L.n_tiles = wide_tiles;
+    L.n_tiles = wide.tiles;
     L.gm = 16;
-    L.bn = a.fp8 ? 128 : 256;
-    if (!a.fp8 && !a.offsets) {
-      // the rows are cut evenly, so that the units come out in few rounds; a K block of a unit takes the
-      // MMAs' 1.1 ns a row, or what the issue of its copies takes
-      long long best = 1ll << 62;
-      for (int blocks = ceil_div(a.T, 256); blocks <= 4 * ceil_div(a.T, 256); ++blocks) {
-        const int bn = (ceil_div(a.T, blocks) + 31) & ~31;
-        if (bn < 64 && blocks > 1) break;
-        const int ns = 9 * bn / 8 > 140 + bn / 8 ? 9 * bn / 8 : 140 + bn / 8;
-        const long long cost =
-            ceil_div((long long)ceil_div(a.T, bn) * L.n_tiles, num_sms() / 2) * (long long)ns;
-        if (cost < best) {
-          best = cost;
-          L.bn = bn;
-        }
-      }
-    }
+    L.bn = wide.bn;
     const long long units = ((long long)ceil_div(a.T, L.bn) + groups - 1) * L.n_tiles;
     return a.fp8 ? launch_linear_fp8(L, units, stream) : launch_linear_pair(L, units, stream);
   }
-  if (cut.cluster < 1) return cudaErrorInvalidConfiguration;
   L.bn = cut.bn;
   L.gm = 1 << 16;
   L.cluster = cut.cluster;

@@ -31,7 +31,7 @@ struct LinLaunch {
   int stages;
   int tab_off;     // byte offsets in shared memory, from the aligned base: group table,
   int bar_off;     // barriers,
-  int red_off;     // (stream kernel) partial sums of a cluster,
+  int red_off;     // partial sums of a cluster (stream kernel), values on their way out (e4m3),
   int scale_off;   // row scales (e4m3),
   int half_off;    // (stream kernel, e4m3) sums of every other K block
   // stream kernel
@@ -328,79 +328,6 @@ __device__ __forceinline__ void lin_store(const LinearArgs& a, const LinLane& l,
 #pragma unroll
   for (int i = 0; i < COLS; ++i)
     if (i < cnt) o[i * a.out_stride] = __float2bfloat16_rn(y[i]);
-}
-
-// 8 consecutive bf16 values as fp32, or the first `cnt` of them; wide: 16-byte aligned.
-__device__ __forceinline__ void lin_load8(const __nv_bfloat16* p, bool wide, int cnt, float (&v)[8]) {
-  if (wide && cnt >= 8) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_bf16x2(u[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < cnt ? __bfloat162float(p[i]) : 0.f;
-  }
-}
-
-// The N sums of one row t from output column f0 on (GATED: N / 2 gate sums, then their up sums).
-template <bool GATED, int N>
-__device__ __forceinline__ void lin_store_row(const LinearArgs& a, int g, int t, int f0,
-                                              float (&acc)[N]) {
-  const __nv_bfloat16* bias =
-      a.bias ? static_cast<const __nv_bfloat16*>(a.bias) + (long long)g * a.N : nullptr;
-  const __nv_bfloat16* res =
-      a.residual ? static_cast<const __nv_bfloat16*>(a.residual) + t * a.residual_stride : nullptr;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + t * a.out_stride;
-  const float rw = a.row_weight ? __ldg(a.row_weight + t) : 1.f;
-  auto wide = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-#pragma unroll
-  for (int c = 0; c < (GATED ? N / 2 : N); c += 8) {
-    const int f = f0 + c, cnt = a.cols - f;
-    if (cnt <= 0) break;
-    float y[8], b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = acc[c + i];
-    if (bias) {
-      lin_load8(bias + f, wide(bias + f), cnt, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] += b[i];
-    }
-    if (GATED) {
-      float up[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) up[i] = acc[(c + i + N / 2) % N];
-      if (bias) {
-        lin_load8(bias + a.cols + f, wide(bias + a.cols + f), cnt, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) up[i] += b[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = lin_silu(y[i]) * up[i];
-    } else {
-      lin_activate(y, a.act);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] *= rw;
-    if (res) {
-      lin_load8(res + f, wide(res + f), cnt, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] += b[i];
-    }
-    if (cnt >= 8 && wide(out + f)) {
-      *reinterpret_cast<uint4*>(out + f) =
-          make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                     pack_bf16x2(y[6], y[7]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < cnt) out[f + i] = __float2bfloat16_rn(y[i]);
-    }
-  }
 }
 
 }  // namespace

@@ -5,9 +5,14 @@
 // the rows of x are on the MMA's M side: a TMEM lane is a row, whose scale is one register, and the
 // weights' scale is the same for 128 columns, so that promoting costs one fma a value. (With the
 // weights on M, as the other kernels have them, the rows' scales change from column to column, and
-// reading them takes shared memory's time from the operands.) For the same reason one CTA works
-// by itself: the round trip of a TMEM buffer, MMA to registers to MMA, is on the critical path, and
-// with pairs of CTAs it crosses SMs (measured: 674 us for 8192 rows of 7168 to 4096 columns).
+// reading them takes shared memory's time from the operands.)
+//
+// What bounds it is the round trip of a TMEM buffer: TMEM holds two products of 128 x 256, so that a K
+// block takes half of its products' 270 ns, the commit, the promotion, and the way back to the issuing
+// thread, some 720 ns together. 8192 rows of 7168 to 4096 columns take 226 us (2.1 PFLOP/s); without the
+// promotion's arithmetic 213, without the products 198, without either 181. Pairs of CTAs (M = 256), whose
+// operands are two thirds, take the same 242 as single ones did then, as the way back crosses SMs, and
+// waste more on short groups (257 us for 217, 8192 rows in 16 groups).
 //
 // Unit: 128 rows of one group by 256 weight rows (SILU_MUL: 128 gate rows and their up rows).
 // Warps: 0 TMA, 1 TMEM and MMA, 2..17 epilogue: the four warps of a TMEM lane quarter take 64 columns
@@ -20,20 +25,139 @@ namespace gbmoe {
 namespace {
 
 constexpr int kBM = 128, kBN = 256;
-constexpr int kStages = 4;
 constexpr int kEpiWarps = 16;
 constexpr int kCols = 64;                        // accumulator columns of an epilogue thread
 constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
 constexpr uint32_t kABytes = kBM * 128, kBBytes = kBN * 128, kStageBytes = kABytes + kBBytes;
 constexpr uint32_t kTmemCols = 512, kStride = 256;
 constexpr int kAhead = 4;                        // K blocks that the scales' loads run ahead
+constexpr int kPitch = 33;                       // of the 32 x 32 values that an epilogue warp turns
+// the two ways out (below): by rows leaves the ring a stage more
+constexpr int stages_of(bool by_rows) { return by_rows ? 4 : 3; }
+constexpr uint32_t turn_bytes_of(bool by_rows) { return by_rows ? 0 : kEpiWarps * 32 * kPitch * 4; }
 
+// 8 consecutive bf16 values, 16-byte aligned, as fp32.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 x = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_bf16x2(u[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+// The two ways out of a thread's sums, which are of one row. By rows, 16 bytes at a time, for SILU_MUL where
+// the alignment allows it (4096 rows of 512 to 6144: 44 us against 61 turned, 8192 rows in 16 groups: 214
+// against 241). Else turned in shared memory, so that a lane has a column and the warp's accesses are 64
+// bytes of a row, whatever its alignment (the same plain: 43 us by rows and 35 turned, 8192 rows of 7168
+// to 4096: 242 and 226; by rows of odd width, 2 bytes at a time, 1879 rows of 256 to 6854: 106 and 20).
+
+// SILU_MUL: 32 gate and 32 up sums of row t, output columns f0 .. f0 + 32.
+__device__ __forceinline__ void store_row(const LinearArgs& a, int g, int t, int f0,
+                                          float (&acc)[kCols]) {
+  const __nv_bfloat16* bias =
+      a.bias ? static_cast<const __nv_bfloat16*>(a.bias) + (long long)g * a.N : nullptr;
+  const __nv_bfloat16* res =
+      a.residual ? static_cast<const __nv_bfloat16*>(a.residual) + t * a.residual_stride : nullptr;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + t * a.out_stride;
+  const float rw = a.row_weight ? __ldg(a.row_weight + t) : 1.f;
+#pragma unroll
+  for (int c = 0; c < 32; c += 8) {
+    const int f = f0 + c;
+    if (f >= a.cols) break;
+    float y[8], b[8];
+    if (bias) {
+      load8(bias + f, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[c + i] += b[i];
+      load8(bias + a.cols + f, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[32 + c + i] += b[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = lin_silu(acc[c + i]) * acc[32 + c + i] * rw;
+    if (res) {
+      load8(res + f, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += b[i];
+    }
+    *reinterpret_cast<uint4*>(out + f) =
+        make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                   pack_bf16x2(y[6], y[7]));
+  }
+}
+
+// A warp's 32 rows from row t0 on, `rows` of them real: lane l has the row t0 + l, columns f0 .. f0 + 64
+// (GATED: 32 gate sums, then their 32 up sums).
 template <bool GATED>
+__device__ __forceinline__ void store_turned(const LinearArgs& a, int g, int t0, int rows, int f0,
+                                             float (&acc)[kCols], float* turn) {
+  const int lane = threadIdx.x & 31;
+  const __nv_bfloat16* bias =
+      a.bias ? static_cast<const __nv_bfloat16*>(a.bias) + (long long)g * a.N : nullptr;
+  if (GATED) {
+    if (bias) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const int f = min(f0 + c, a.cols - 1);     // columns past the last are not stored
+        acc[c] += __bfloat162float(bias[f]);
+        acc[32 + c] += __bfloat162float(bias[a.cols + f]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 32; ++c) acc[c] = lin_silu(acc[c]) * acc[32 + c];
+  }
+#pragma unroll
+  for (int half = 0; half < (GATED ? 1 : 2); ++half) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) turn[lane * kPitch + c] = acc[32 * half + c];
+    __syncwarp();
+    const int f = f0 + 32 * half + lane;
+    if (f < a.cols) {
+      const float b = !GATED && bias ? __bfloat162float(bias[f]) : 0.f;
+      const long long rs = a.residual_stride, os = a.out_stride;
+      const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(a.residual) + t0 * rs + f;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + t0 * os + f;
+#pragma unroll 1
+      for (int i0 = 0; i0 < rows; i0 += 8) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = turn[(i0 + i) * kPitch + lane] + b;
+        if (!GATED) lin_activate(y, a.act);
+        if (a.row_weight) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= __ldg(a.row_weight + t0 + min(i0 + i, rows - 1));
+        }
+        if (a.residual) {
+          __nv_bfloat16 res[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (i0 + i < rows) res[i] = *r;
+            r += rs;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] += __bfloat162float(res[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i0 + i < rows) *o = __float2bfloat16_rn(y[i]);
+          o += os;
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
+template <bool GATED, bool BY_ROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_x,
                       const __grid_constant__ LinLaunch L) {
   constexpr int kTileCols = GATED ? 128 : 256;     // output columns per unit
+  constexpr int kStages = stages_of(BY_ROWS);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -146,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // SILU_MUL gate [32 part, + 32) and up [128 + 32 part, + 32), else [64 part, + 64)
     const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16) + (GATED ? 32 : 64) * part;
     const int r = quarter * 32 + lane;
+    float* turn = reinterpret_cast<float*>(smem + L.red_off) + (warp - 2) * 32 * kPitch;
     int buf = 0;
     uint32_t tph = 0;
     bool ok = true;
@@ -181,7 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const LinUnit w = groups.unit(L, L.n_tiles, u);
-      if (r < w.n) lin_store_row<GATED>(a, w.g, w.m0 + r, w.nt * kTileCols + part * (kTileCols / 4), acc);
+      const int f0 = w.nt * kTileCols + part * (kTileCols / 4), rows = min(32, w.n - quarter * 32);
+      if (BY_ROWS) {
+        if (lane < rows) store_row(a, w.g, w.m0 + r, f0, acc);
+      } else if (rows > 0) {
+        store_turned<GATED>(a, w.g, w.m0 + quarter * 32, rows, f0, acc, turn);
+      }
     }
   } else {
     // ------------------------------------------------------------ scales
@@ -233,10 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool GATED>
+template <bool GATED, bool BY_ROWS>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& L, long long units,
                    size_t smem, cudaStream_t stream) {
-  auto kernel = linear_fp8_kernel<GATED>;
+  auto kernel = linear_fp8_kernel<GATED, BY_ROWS>;
   static bool ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -256,16 +386,23 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const LinLaunch& 
 cudaError_t launch_linear_fp8(LinLaunch L, long long max_units, cudaStream_t stream) {
   const LinearArgs& a = L.a;
   if (!a.fp8 || L.bn != kBM) return cudaErrorInvalidValue;
-  L.stages = kStages;
-  L.scale_off = kStages * kStageBytes;
-  L.bar_off = L.scale_off + 2 * kBM * (int)sizeof(float2);
-  const uint32_t bars = (2 * kStages + 4) * 8 + 16;
-  L.tab_off = L.bar_off + bars;
+  auto on16 = [](const void* p, long long stride) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0;
+  };
+  const bool gated = a.act == GBMOE_EPI_SILU_MUL;
+  const bool by_rows = gated && on16(a.out, a.out_stride) && (!a.bias || on16(a.bias, a.cols)) &&
+                       (!a.residual || on16(a.residual, a.residual_stride));
+  L.stages = stages_of(by_rows);
+  L.scale_off = L.stages * (int)kStageBytes;
+  L.red_off = L.scale_off + 2 * kBM * (int)sizeof(float2);
+  L.bar_off = L.red_off + (int)turn_bytes_of(by_rows);
+  L.tab_off = L.bar_off + (2 * L.stages + 4) * 8 + 16;
   CUtensorMap w, x;
   if (!lin_map_rows(a, 128, 0, &w) || !lin_map_x(a, kBM, 0, &x)) return cudaErrorInvalidValue;
   const size_t smem = L.tab_off + 4 * (3 * a.G + 1) + 1024;
-  return a.act == GBMOE_EPI_SILU_MUL ? launch<true>(w, x, L, max_units, smem, stream)
-                                     : launch<false>(w, x, L, max_units, smem, stream);
+  if (by_rows) return launch<true, true>(w, x, L, max_units, smem, stream);
+  return gated ? launch<true, false>(w, x, L, max_units, smem, stream)
+               : launch<false, false>(w, x, L, max_units, smem, stream);
 }
 
 }  // namespace gbmoe
