@@ -57,9 +57,8 @@ struct StreamCut {
   double ns;
 };
 
-// Groups count as if all of them had rows. Whole rounds are what is looked for; no cut is faster than
-// HBM; a join of partial sums and the cluster's start take about 3.5 us, and some more for the sums'
-// size. cluster 0: the device holds no cluster of some size.
+// Groups count as if all of them had rows. A join of partial sums and the cluster's start take about 3.5 us,
+// and some more for the sums' size. cluster 0: the device holds no cluster of some size.
 StreamCut cut_stream(const LinearArgs& a, int groups, int mean, int k_blocks) {
   const bool gated = a.act == GBMOE_EPI_SILU_MUL;
   StreamCut best = {0, 0, 0, 1e30};
@@ -70,7 +69,6 @@ StreamCut cut_stream(const LinearArgs& a, int groups, int mean, int k_blocks) {
   if (a.offsets && best.bn > 64) best.bn = 64;
   const int n = best.bn, grain = gated ? 32 : 8;             // rows per step of R
   const long long blocks = ceil_div(a.T, n) + (a.offsets ? groups - 1 : 0);
-  const double hbm = (double)groups * a.N * a.K * (a.fp8 ? 1 : 2) / 6700;
   for (int C = 1; C <= 8 && C <= k_blocks; ++C) {
     const int room = linear_stream_room(a, n, C);
     if (room < 1) return StreamCut{n, 0, 0, 0};
@@ -84,9 +82,11 @@ StreamCut cut_stream(const LinearArgs& a, int groups, int mean, int k_blocks) {
         if (rounds < 8) continue;
         R = 128;
       }
-      const int turns = ceil_div(blocks * ceil_div(a.N, R), room);
-      const double run = (double)turns * lin_unit_ns(a.fp8, gated, R, n, kb);
-      const double ns = (run > hbm ? run : hbm) + (C > 1 ? turns * (3500 + n * R / 20.0) : 0);
+      const long long units = blocks * ceil_div(a.N, R);
+      // the weights of a group's further row blocks come from L2
+      const long long line = lin_line_ns(units, room, lin_unit_ns(a.fp8, gated, R, n, kb),
+                                         (long long)R * a.K * (a.fp8 ? 1 : 2) * groups / blocks);
+      const double ns = line + (C > 1 ? ceil_div(units, room) * (3500 + n * R / 20.0) : 0);
       if (ns < best.ns * 0.98) {
         best.ns = ns;
         best.cluster = C;
@@ -98,8 +98,9 @@ StreamCut cut_stream(const LinearArgs& a, int groups, int mean, int k_blocks) {
 }
 
 // How the kernels for many rows cut it: units of 256 weight rows and `bn` rows of x. A K block of a unit
-// takes the e4m3 kernel some 500 ns (128 rows, one CTA), pairs of CTAs the MMAs' 1.1 ns a row, or
-// what the issue of its copies takes. Half of the groups count as ending in a block of their own.
+// takes the e4m3 kernel some 500 ns (128 rows, one CTA; a unit's way out 3 us more), pairs of CTAs the
+// MMAs' 1.1 ns a row, or what the issue of its copies takes. Half of the groups count as ending in a block of their own, and
+// all as having one.
 struct WideCut {
   int bn, tiles;
   double ns;
@@ -114,9 +115,11 @@ WideCut cut_wide(const LinearArgs& a, int groups, int k_blocks) {
     const int rows = a.offsets || a.fp8 ? most / cut : ceil_div(a.T, (long long)cut * ceil_div(a.T, most));
     const int bn = a.fp8 ? most : (rows + 31) & ~31;
     if (bn < 64 && cut > 1) break;
-    const long long blocks = ceil_div(a.T, bn) + (a.offsets ? groups / 2 : 0);
-    const int one = a.fp8 ? 500 : 9 * bn / 8 > 140 + bn / 8 ? 9 * bn / 8 : 140 + bn / 8;
-    const double run = (double)one * k_blocks * ceil_div(blocks * best.tiles, num_sms() / (a.fp8 ? 1 : 2));
+    const int some = ceil_div(a.T, bn) + (a.offsets ? groups / 2 : 0);
+    const long long blocks = some > groups ? some : groups;
+    const double block = 9 * bn / 8 > 140 + bn / 8 ? 9 * bn / 8 : 140 + bn / 8;
+    const double one = a.fp8 ? 500.0 * k_blocks + 3000 : block * k_blocks;
+    const double run = one * ceil_div(blocks * best.tiles, num_sms() / (a.fp8 ? 1 : 2));
     const double ns = run > hbm ? run : hbm;
     if (ns < best.ns) {
       best.ns = ns;
@@ -140,14 +143,15 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   // 12.5 and 14.6, 128 rows 17.6 and 14.8; 96 rows of 2048 to 2048 10.8 and 9.3; e4m3, 128 rows of 4096 to
   // 4096 15.3 and 21.4, 160 to 16384 47.4 and 24.7; 16 groups of 2048 to 7168, mean 32 76.9 and 79.4,
   // mean 64 88.5 and 81.6; e4m3, mean 8 42.6 and 44.1, mean 16 59.7 and 45.5. Above 96 rows the stream
-  // kernel's ring gets short, and it has to be well ahead.
+  // kernel's ring gets short, and it has to be well ahead; of small groups fewer may have rows than the
+  // model counts, which suits it.
   const WideCut wide = cut_wide(a, groups, L.k_blocks);
   bool many = mean > (a.offsets ? 128 : 512);
   StreamCut cut = {};
   if (!many) {
     cut = cut_stream(a, groups, mean, L.k_blocks);
     if (cut.cluster < 1) return cudaErrorInvalidConfiguration;
-    many = cut.ns > (a.offsets || mean <= 96 ? 1.0 : 0.7) * wide.ns;
+    many = cut.ns > (a.offsets && mean <= 8 ? 1.15 : mean <= 96 ? 1.0 : 0.7) * wide.ns;
   }
   if (many) {
     L.n_tiles = wide.tiles;
@@ -162,10 +166,10 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   L.rows[0] = cut.rows;
   L.choices = 1;
   if (a.offsets) {                                 // the kernel cuts by the groups that it finds
-    L.rows[0] = 128;
-    L.rows[1] = 64;
-    L.rows[2] = 32;
-    L.choices = 3;
+    const int step = a.fp8 && gated ? 64 : 32;     // (such a tile has one scale block of either kind)
+    L.choices = 0;
+    for (int R = 128; R >= 64; R -= step) L.rows[L.choices++] = R;
+    L.rows[L.choices++] = 32;
   }
   const int least = L.rows[L.choices - 1];
   L.n_tiles = ceil_div(a.cols, gated ? least / 2 : least);

@@ -25,7 +25,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxStages = 16;
 constexpr int kMaxKps = 8;                       // K blocks per stage
 constexpr int kXMaps = 2;                        // x boxes of bn and of 8 rows
-constexpr int kWMaps = 3;                        // weight boxes of L.rows[i] rows
+constexpr int kWMaps = 4;                        // weight boxes of L.rows[i] rows
 constexpr uint32_t kTmemCols = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kBufsMax = 8;                      // TMEM buffers
@@ -181,17 +181,21 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  // The tile: of the choices, the one with the shortest line of rounds.
+  // The tile: of the choices, the one whose line of units takes least (16 groups of which 10 have rows,
+  // 7168 to 4096 gated: 320 tiles of 128 rows took 103 us on 152 SMs, 430 of 96 95).
   int R = L.rows[0], pick = 0, n_tiles = L.n_tiles;
   if (grouped) {
     long long best = 0;
     const int xr = (a.T + a.G - 1) / a.G <= 8 ? 8 : bn;
+    // All CTAs have to come to the same tile, so nothing of a CTA's own goes in here. A smaller tile is not
+    // read faster: the ring holds as many K blocks of it, and fewer bytes.
+    const long long unit_ns = lin_unit_ns(FP8, GATED, L.rows[0], xr, (L.k_blocks + C - 1) / C);
     for (int i = 0; i < L.choices; ++i) {
       const int r = L.rows[i], cols = GATED ? r / 2 : r;
       const int nt = (a.cols + cols - 1) / cols;
       const long long u = (long long)groups.before[a.G] * nt;
       if (i > 0 && u > 1 << 30) break;             // units are counted in 32 bits
-      const long long cost = (u + step - 1) / step * lin_unit_ns(FP8, GATED, r, xr, kb1 - kb0);
+      const long long cost = lin_line_ns(u, step, unit_ns, (long long)r * L.k_blocks * 128);
       if (i == 0 || cost < best) {
         best = cost;
         pick = i;
@@ -518,49 +522,61 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   } else if (FP8) {
     // ------------------------------------------------------------ scales
     const int wblocks = (a.N + 127) >> 7;
+    // A stage's scales, fetched while the stage before is on its way: the loads' latency, paid between a
+    // free slot and the next, would be longer than a stage takes (128 rows in 16 groups, 2048 to 7168:
+    // 38 us).
+    float v[kMaxKps][CHUNKS], s0[kMaxKps], s1[kMaxKps];
+    auto fetch = [&](const LinUnit& w, int kb) {
+      const int b0 = (w.nt * tile_cols) >> 7;
+      const int b1 = GATED ? b0 + (a.cols >> 7) : min(b0 + 1, wblocks - 1);
+      const float* w0 = a.w_scale + ((long long)w.g * wblocks + b0) * L.k_blocks + kb;
+      const float* w1 = a.w_scale + ((long long)w.g * wblocks + b1) * L.k_blocks + kb;
+      const float* xs = a.x_scale + (long long)kb * a.T + w.m0 + lane;
+#pragma unroll
+      for (int j = 0; j < kMaxKps; ++j) {
+        const bool in = j < kps && kb + j < kb1;
+        s0[j] = in ? __ldg(w0 + j) : 0.f;
+        s1[j] = in ? __ldg(w1 + j) : 0.f;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i)
+          v[j][i] = in && lane + 32 * i < w.n ? __ldg(xs + (long long)j * a.T + 32 * i) : 0.f;
+      }
+    };
     int slot = 0;
     uint32_t ph = 1;
     bool ok = true;
+    LinUnit w;
+    if (first < units) {
+      w = groups.unit(L, n_tiles, first);
+      fetch(w, kb0);
+    }
     for (int u = first; ok && u < units; u += step) {
-      const LinUnit w = groups.unit(L, n_tiles, u);
-      const int b0 = (w.nt * tile_cols) >> 7;
-      const int b1 = GATED ? b0 + (a.cols >> 7) : min(b0 + 1, wblocks - 1);
-      const float* w0 = a.w_scale + ((long long)w.g * wblocks + b0) * L.k_blocks;
-      const float* w1 = a.w_scale + ((long long)w.g * wblocks + b1) * L.k_blocks;
-      const float* xs = a.x_scale + w.m0 + lane;
       for (int kb = kb0; kb < kb1; kb += kps) {
         if (!wait_fast(sempty_bar(slot), ph, abort_flag, status)) {
           ok = false;
           break;
         }
         float* dst = scales + slot * kps * 2 * bn;
-        for (int j0 = 0; j0 < kps; j0 += 4) {
-          float v[4][CHUNKS], s0[4], s1[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bool in = j0 + j < kps && kb + j0 + j < kb1;
-            s0[j] = in ? __ldg(w0 + kb + j0 + j) : 0.f;
-            s1[j] = in ? __ldg(w1 + kb + j0 + j) : 0.f;
+        for (int j = 0; j < kMaxKps; ++j) {
+          if (j >= kps) break;
 #pragma unroll
-            for (int i = 0; i < CHUNKS; ++i)
-              v[j][i] = in && lane + 32 * i < w.n ? __ldg(xs + (long long)(kb + j0 + j) * a.T + 32 * i)
-                                                  : 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j0 + j >= kps) break;
-#pragma unroll
-            for (int i = 0; i < CHUNKS; ++i) {
-              const int c = lane + 32 * i;
-              if (c < bn) {
-                dst[scale_at(bn, j0 + j, c, 0)] = v[j][i] * s0[j];
-                dst[scale_at(bn, j0 + j, c, 1)] = v[j][i] * s1[j];
-              }
+          for (int i = 0; i < CHUNKS; ++i) {
+            const int c = lane + 32 * i;
+            if (c < bn) {
+              dst[scale_at(bn, j, c, 0)] = v[j][i] * s0[j];
+              dst[scale_at(bn, j, c, 1)] = v[j][i] * s1[j];
             }
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(sfull_bar(slot));
+        if (kb + kps < kb1) {
+          fetch(w, kb + kps);
+        } else if (u + step < units) {
+          w = groups.unit(L, n_tiles, u + step);
+          fetch(w, kb0);
+        }
         if (++slot == kScaleSlots) {
           slot = 0;
           ph ^= 1u;
