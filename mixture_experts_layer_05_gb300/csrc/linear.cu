@@ -146,7 +146,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   // kernel's ring gets short, and it has to be well ahead; of small groups fewer may have rows than the
   // model counts, which suits it.
   const WideCut wide = cut_wide(a, groups, L.k_blocks);
-  bool many = mean > (a.offsets ? 128 : 512);
+  bool many = mean > (a.offsets ? 128 : 4096);
   StreamCut cut = {};
   if (!many) {
     cut = cut_stream(a, groups, mean, L.k_blocks);
