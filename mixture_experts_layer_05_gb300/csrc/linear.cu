@@ -142,16 +142,17 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream) {
   // Few rows or many: by the modelled times. Measured, stream and many (us): K = N = 4096, bf16, 64 rows
   // 12.5 and 14.6, 128 rows 17.6 and 14.8; 96 rows of 2048 to 2048 10.8 and 9.3; e4m3, 128 rows of 4096 to
   // 4096 15.3 and 21.4, 160 to 16384 47.4 and 24.7; 16 groups of 2048 to 7168, mean 32 76.9 and 79.4,
-  // mean 64 88.5 and 81.6; e4m3, mean 8 42.6 and 44.1, mean 16 59.7 and 45.5. Above 96 rows the stream
-  // kernel's ring gets short, and it has to be well ahead; of small groups fewer may have rows than the
-  // model counts, which suits it.
+  // mean 64 88.5 and 81.6; e4m3, mean 8 42.6 and 44.1, mean 16 59.7 and 45.5. Where HBM bounds both the few
+  // rows' kernel is ahead (4 rows of 4096 to 24576 38.6 and 41.3), and of small groups fewer may have rows
+  // than the model counts, which suits it too; above 96 rows its ring gets short, and it has to be
+  // well ahead.
   const WideCut wide = cut_wide(a, groups, L.k_blocks);
   bool many = mean > (a.offsets ? 128 : 4096);
   StreamCut cut = {};
   if (!many) {
     cut = cut_stream(a, groups, mean, L.k_blocks);
     if (cut.cluster < 1) return cudaErrorInvalidConfiguration;
-    many = cut.ns > (a.offsets && mean <= 8 ? 1.15 : mean <= 96 ? 1.0 : 0.7) * wide.ns;
+    many = cut.ns > (mean <= (a.offsets ? 8 : 64) ? 1.15 : mean <= 96 ? 1.0 : 0.7) * wide.ns;
   }
   if (many) {
     L.n_tiles = wide.tiles;

@@ -6,6 +6,11 @@
 // walks the units, and two TMEM accumulators let the epilogue of one unit run under the products of
 // the next. (e4m3 operands have a kernel of their own, linear_fp8.cu.)
 //
+// 8192 rows of 4096 to 6144 columns: 217 us in a short run (1.9 PFLOP/s, cuBLAS's burst), 249 in long ones
+// under the power cap (1.66, cuBLAS's sustained rate 1.69). Below 128 rows a unit the two copies of a K
+// block, some 140 ns of the issuing thread, are what holds. (Two K blocks a stage: 235 us for 217, and 19.4
+// for 16.6 with 512 rows of 4096 to 4096.)
+//
 // Warps: 0 TMA, 1 TMEM and MMA (leader), 2..9 epilogue, two to a TMEM lane quarter.
 #include "linear.cuh"
 

@@ -1,16 +1,23 @@
 // moe_linear / moe_grouped_linear for few rows per group: bound by reading the weights.
 //
-// One SM draws about 48 GB/s from HBM through TMA, however deep its ring is (measured with 48 to 152
-// CTAs), so the 6.8 TB/s need every SM, all of them for the same time. So the tile is cut to the SMs
-// rather than to the MMA: a unit is R <= 128 weight rows by at most bn rows of x, where R is such that
-// the units come out in whole rounds; the MMA (tcgen05.mma, M = 128) runs over R rows and over what lies
-// behind them in shared memory, whose TMEM lanes nobody reads. (Plain tiles of up to 64 rows run with
-// M = 64: with few columns an MMA takes as long as its weight rows' operands, 23 cycles instead of 39.) Where the rows of x are many against R,
-// their reading costs more than that of the weights; there a cluster of C CTAs takes a tile of C times
-// the rows and cuts its K blocks into C ranges. The C partial sums are joined through distributed
-// shared memory: each CTA sends the columns that CTA d finishes to d (one bulk copy each), which adds
-// them in the order of the ranges, so that the result does not depend on timing and nothing is kept in
-// a workspace between calls.
+// The weights come at HBM's rate when every SM reads for the same time, and one thread can issue the
+// copies fast enough: 48 CTAs drew 6.1 TB/s with stages of 37 KB, but a stage costs the issuing threads
+// near 200 ns whatever its size. So the tile is cut to the SMs rather than to the MMA: a unit is R <= 128
+// weight rows by at most bn rows of x, where R is such that the units come out in whole rounds, and a
+// copy takes several K blocks of them. The MMA (tcgen05.mma, M = 128) runs over R rows and over what
+// lies behind them in shared memory, whose TMEM lanes nobody reads. (Plain tiles of up to 64 rows run with
+// M = 64: with few columns an MMA takes as long as its weight rows' operands, 23 cycles instead of 39.)
+//
+// Where the rows of x are many against R, their reading and the MMAs cost more than the weights; there a
+// cluster of C CTAs takes a tile of C times the rows and cuts its K blocks into C ranges. The C partial
+// sums are joined through distributed shared memory: each CTA sends the columns that CTA d finishes to d
+// (one bulk copy each), which adds them in the order of the ranges, so that the result does not depend
+// on timing and nothing is kept in a workspace between calls.
+//
+// Graph replay: 4 rows of 4096 to 6144 columns 11.8 us (HBM 7.4), to 24576 32.7 (29.7), 96 to 4096 14.9 (5.3),
+// 24 rows in 16 groups, 10 of them with rows, of 7168 to 4096 gated 94 (86.7); e4m3, 16 rows of
+// 7168 to 6144 12.4 (6.5). What is left is the start, 2.5 us to the first weights, and 2.5 us of launch
+// and way out.
 //
 // Warps: 0 TMA, 1 TMEM and MMA, 2..9 epilogue (two per TMEM lane quarter, alternating by 16 columns), 10
 // (e4m3) scales. e4m3 products are promoted to fp32 with their scales K block by K block, as the FP8
