@@ -7,18 +7,17 @@
 // weights on M, as the other kernels have them, the rows' scales change from column to column, and
 // reading them takes shared memory's time from the operands.)
 //
-// What bounds it is the round trip of a TMEM buffer: TMEM holds two products of 128 x 256, so that a K
-// block takes half of its products' 270 ns, the commit, the promotion, and the way back to the issuing
-// thread, some 720 ns together. 8192 rows of 7168 to 4096 columns take 226 us (2.1 PFLOP/s); without the
-// promotion's arithmetic 213, without the products 198, without either 181. Pairs of CTAs (M = 256), whose
-// operands are two thirds, take the same 242 as single ones did then, as the way back crosses SMs, and
-// waste more on short groups (257 us for 217, 8192 rows in 16 groups).
+// 8192 rows of 7168 to 4096 columns take 224 us (2.1 PFLOP/s). Two limits hold it at almost the same height:
+// products and promotion, which take turns at TMEM's two buffers of 128 x 256 (212 us without the copies),
+// and products and copies (216 without the promotion); products alone take 160, copies alone 172. Pairs of
+// CTAs (M = 256), whose operands are two thirds, lift the second only: 242 us as single ones then, and 257
+// for 217 with 8192 rows in 16 groups, as short groups waste more of them.
 //
 // Unit: 128 rows of one group by 256 weight rows (SILU_MUL: 128 gate rows and their up rows).
 // Warps: 0 TMA, 1 TMEM and MMA, 2..17 epilogue: the four warps of a TMEM lane quarter take 64 columns
-// each, of which every thread keeps the running sums of its row (four warps of an SM's quarter hide
-// the latency of TMEM better than two with 128 columns each); 18 scales: it writes the products
-// of the rows' and the weights' scales of a K block beside the TMEM buffer that they belong to.
+// each, of which every thread keeps the running sums of its row (two with 128 columns each: 278 us for 213
+// with 8192 gated rows in 16 groups, the same for the dense call); 18 scales: it writes the products of the
+// rows' and the weights' scales of a K block beside the TMEM buffer that they belong to.
 #include "linear.cuh"
 
 namespace gbmoe {
