@@ -14,6 +14,8 @@ namespace {
 
 constexpr int kMaxRows = 1 << 22;
 constexpr int kMaxLinearK = 1 << 24;
+// a tile may end 255 rows behind the last weight row, and rows and columns are counted in 32 bits
+constexpr int64_t kMaxLinearRows = INT32_MAX - 1024;
 constexpr int64_t kMaxLinearStride = (1ll << 39) - 16;  // a tensor map's strides have 40 bits of bytes
 constexpr size_t kStatusBytes = 256;
 // attention: the status region, then the counters of cut units
@@ -91,7 +93,7 @@ gbmoe_status_t linear(int T, int G, int K, int N, const int32_t* offsets, bool g
   if (fp8 != (g->x_scale != nullptr) || fp8 != (g->weight_scale != nullptr))
     return GBMOE_ERR_INVALID_ARG;
   if (K % (fp8 ? kFp8Block : 8) || K > kMaxLinearK || (gated && N % (fp8 ? 2 * kFp8Block : 32)) ||
-      G > kLinearMaxGroups || (int64_t)G * N > INT32_MAX || g->x_stride > kMaxLinearStride)
+      G > kLinearMaxGroups || (int64_t)G * N > kMaxLinearRows || g->x_stride > kMaxLinearStride)
     return GBMOE_ERR_UNSUPPORTED;
   // tiles of 128 columns by 16 rows are the smallest that any kernel counts
   if (((int64_t)T / 16 + G) * ((N + 127) / 128) > (1 << 30)) return GBMOE_ERR_UNSUPPORTED;

@@ -61,6 +61,13 @@ def test_grouped_refusals(lib):
     assert _call(lib, G=1024, N=1 << 21) == UNSUP
 
 
+def test_refuses_weights_whose_last_tile_passes_32_bits(lib):
+    """A tile ends up to 255 rows behind the last, and rows and columns are counted in 32 bits."""
+    for N in ((1 << 31) - 1, (1 << 31) - 256, (1 << 31) - 1024):
+        assert _call(lib, T=1, K=8, N=N) == UNSUP, N
+    assert _call(lib, T=1, K=8, N=(1 << 28) - 128, G=8) == UNSUP
+
+
 def test_binding_refuses_host_tensors(lib):
     x, w = torch.zeros(2, 256, dtype=torch.bfloat16), torch.zeros(64, 256, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
