@@ -642,7 +642,8 @@ gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int32_t num_t
  * output tiles (of 128 columns by 16 rows). x 16-byte aligned, x_stride a multiple of 16 bytes; weight
  * 16-byte aligned; the others aligned to their elements. A run that is negative or outside [0, T]
  * sets GBMOE_ERR_DEVICE_CHECK and has no rows; runs that overlap have unspecified outputs where they
- * do. A NaN or an infinity in a row of x reaches that row alone, in a row of weight that column alone
+ * do, and where runs go back and come again, so that they add up to more than T rows, later ones may
+ * have none. A NaN or an infinity in a row of x reaches that row alone, in a row of weight that column alone
  * (SILU_MUL: its pair's). Sums are fp32 throughout (e4m3: per block of 128 columns, then scaled and
  * added in fp32). The order of a sum goes by the call's sizes and groups, so that a row may round
  * differently in another batch; the same call gives the same bits.

@@ -176,6 +176,9 @@ struct LinGroups {
     __syncthreads();
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
+      // Ascending runs have fewer blocks. Those that go back and come again could have so many that their
+      // units pass 32 bits; they are wrong, and keep what is below.
+      const int most = (a.T + L.bn - 1) / L.bn + G;
       int carry = 0;
       for (int g0 = 0; g0 < G; g0 += 32) {
         const int g = g0 + lane;
@@ -185,7 +188,7 @@ struct LinGroups {
           const int t = __shfl_up_sync(0xffffffffu, v, o);
           if (lane >= o) v += t;
         }
-        if (g < G) before[g + 1] = carry + v;
+        if (g < G) before[g + 1] = min(carry + v, most);
         carry += __shfl_sync(0xffffffffu, v, 31);
       }
       if (lane == 0) before[0] = 0;

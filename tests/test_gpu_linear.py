@@ -291,6 +291,39 @@ def test_grouped_bad_offsets_are_reported(cuda_lib, rows):
         assert (got[~named] == 7).all(), off
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows", [5, 300, 20000])
+def test_grouped_offsets_that_go_back_and_come_again(cuda_lib, rows, fp8):
+    """All rows belong to the first run, and to every second one behind it: reported, each row has some
+    run's values, and rows behind the runs are left alone."""
+    G = 40
+    w = torch.ones(G, 128, 128, dtype=torch.bfloat16, device=DEV)
+    x = torch.ones(rows + 3, 128, dtype=torch.bfloat16, device=DEV)
+    kw = {}
+    if fp8:
+        w, x = w.to(torch.float8_e4m3fn), x.to(torch.float8_e4m3fn)
+        kw = dict(x_scale=torch.ones(1, rows + 3, device=DEV), weight_scale=torch.ones(G, 1, 1, device=DEV))
+    off = torch.tensor([0, rows] * (G // 2) + [0], dtype=torch.int32, device=DEV)
+    out = torch.full((rows + 3, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = binding.alloc_workspace(256)
+    binding.moe_grouped_linear(x, w, off, out=out, workspace=ws, **kw)
+    assert _status(ws) == binding.ERR_DEVICE_CHECK
+    assert (out[:rows] == 128).all() and (out[rows:] == 7).all()
+
+
+def test_grouped_offsets_whose_units_would_pass_32_bits(cuda_lib):
+    """512 runs of all 4096 rows: 2^17 blocks of 16 rows by 2^14 tiles."""
+    T, G, K, N = 4096, 1024, 8, 2 ** 21 - 2
+    w = torch.ones(G, N, K, dtype=torch.bfloat16, device=DEV)
+    x = torch.ones(T, K, dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, T] * (G // 2) + [0], dtype=torch.int32, device=DEV)
+    out = torch.full((T, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = binding.alloc_workspace(256)
+    binding.moe_grouped_linear(x, w, off, out=out, workspace=ws)
+    assert _status(ws) == binding.ERR_DEVICE_CHECK
+    assert (out[::97] == K).all() and (out[:, -1] == K).all() and (out[:, ::4099] == K).all()
+
+
 def test_past_32_bits(cuda_lib):
     """Weights, outputs and rows whose offsets pass 2^31 elements."""
     N, K, G = 8192, 4160, 64
