@@ -128,6 +128,16 @@ __device__ __forceinline__ bool lin_elect() {
       : "=r"(r));
   return r != 0;
 }
+// wait_fast by a whole warp. Where a wait gives up, some lanes may still see the phase complete; all of them
+// have to go the same way, to loads from TMEM and barriers that take the warp as one.
+__device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                         int* status) {
+  return __all_sync(0xffffffffu, wait_fast(bar, parity, abort_flag, status)) != 0;
+}
+__device__ __forceinline__ bool lin_wait_cluster(uint32_t bar, uint32_t parity,
+                                                 volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, wait_bounded_cluster(bar, parity, abort_flag, status)) != 0;
+}
 // a0 += s0 * v0, a1 += s1 * v1 (two IEEE fmas in one instruction).
 __device__ __forceinline__ void fma2(float& a0, float& a1, float s0, float s1, float v0, float v1) {
   asm("{\n\t.reg .b64 a, v, s;\n\t"

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
       for (int kb = 0; kb < KB; ++kb) {
-        if (!wait_fast(tfull_bar(buf), tph, abort_flag, status)) {
+        if (!lin_wait(tfull_bar(buf), tph, abort_flag, status)) {
           ok = false;
           break;
         }
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           if (kb0 + i >= KB) break;
-          if (!wait_fast(tempty_bar(buf), tph, abort_flag, status)) {
+          if (!lin_wait(tempty_bar(buf), tph, abort_flag, status)) {
             ok = false;
             break;
           }

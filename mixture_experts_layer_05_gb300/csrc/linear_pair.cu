@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32 && at + i < w.n; ++i)
             lin_prefetch(static_cast<const __nv_bfloat16*>(a.residual) +
                          (long long)(w.m0 + at + i) * a.residual_stride + l.f);
-      if (!wait_fast(tfull_bar(buf), tph, abort_flag, status)) break;
+      if (!lin_wait(tfull_bar(buf), tph, abort_flag, status)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int at = part * 32; at < w.n; at += 64) {

@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(meet_bar);
-      const bool met = wait_fast(meet_bar, mph, abort_flag, status);
+      const bool met = lin_wait(meet_bar, mph, abort_flag, status);
       mph ^= 1u;
       return met;
     };
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
 #pragma unroll
         for (int i = 0; i < CHUNKS * 16; ++i) acc[i] = 0.f;
         for (int kb = kb0; kb < kb1; kb += kps) {
-          if (!wait_fast(sfull_bar(slot), sph, abort_flag, status) ||
-              !wait_fast(tfull_bar(buf), tph, abort_flag, status)) {
+          if (!lin_wait(sfull_bar(slot), sph, abort_flag, status) ||
+              !lin_wait(tfull_bar(buf), tph, abort_flag, status)) {
             ok = false;
             break;
           }
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
             sph ^= 1u;
           }
         }
-      } else if (!wait_fast(tfull_bar(buf), tph, abort_flag, status)) {
+      } else if (!lin_wait(tfull_bar(buf), tph, abort_flag, status)) {
         ok = false;
       }
       if (!ok) break;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
         }
       }
       // what the unit before sent has been added up, here and by the others
-      if (C > 1 && u != first && !wait_bounded_cluster(rempty_bar, rph ^ 1u, abort_flag, status)) {
+      if (C > 1 && u != first && !lin_wait_cluster(rempty_bar, rph ^ 1u, abort_flag, status)) {
         ok = false;
         break;
       }
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
                               mapa_shared(rfull_bar, lane));
           }
         }
-        if (!wait_fast(rfull_bar, rph, abort_flag, status)) {
+        if (!lin_wait(rfull_bar, rph, abort_flag, status)) {
           ok = false;
           break;
         }
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
     }
     for (int u = first; ok && u < units; u += step) {
       for (int kb = kb0; kb < kb1; kb += kps) {
-        if (!wait_fast(sempty_bar(slot), ph, abort_flag, status)) {
+        if (!lin_wait(sempty_bar(slot), ph, abort_flag, status)) {
           ok = false;
           break;
         }
