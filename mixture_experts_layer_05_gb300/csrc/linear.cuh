@@ -128,11 +128,24 @@ __device__ __forceinline__ bool lin_elect() {
       : "=r"(r));
   return r != 0;
 }
-// wait_fast by a whole warp. Where a wait gives up, some lanes may still see the phase complete; all of them
-// have to go the same way, to loads from TMEM and barriers that take the warp as one.
+// The waits of a whole warp. Where one gives up, some lanes may still see the phase complete; all of them
+// have to go the same way, to loads from TMEM and barriers that take the warp as one. (Inlined: behind a call the e4m3 kernels' sums leave
+// the registers, 8192 gated rows in 16 groups 236 us for 217.)
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* status) {
-  return __all_sync(0xffffffffu, wait_fast(bar, parity, abort_flag, status)) != 0;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 63u) == 0u) {
+      if (__any_sync(0xffffffffu, *abort_flag)) return false;
+      if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitTimeoutNs)) {
+        *abort_flag = 1;
+        record_status(status, GBMOE_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
 }
 __device__ __forceinline__ bool lin_wait_cluster(uint32_t bar, uint32_t parity,
                                                  volatile int* abort_flag, int* status) {
