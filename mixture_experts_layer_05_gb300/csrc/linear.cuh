@@ -129,8 +129,8 @@ __device__ __forceinline__ bool lin_elect() {
   return r != 0;
 }
 // The waits of a whole warp. Where one gives up, some lanes may still see the phase complete; all of them
-// have to go the same way, to loads from TMEM and barriers that take the warp as one. (Inlined: behind a call the e4m3 kernels' sums leave
-// the registers, 8192 gated rows in 16 groups 236 us for 217.)
+// have to go the same way, to loads from TMEM and barriers that take the warp as one. (Inlined: behind a
+// call the e4m3 kernels' sums leave the registers, 8192 gated rows in 16 groups 236 us for 217.)
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* status) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -150,6 +150,33 @@ __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ bool lin_wait_cluster(uint32_t bar, uint32_t parity,
                                                  volatile int* abort_flag, int* status) {
   return __all_sync(0xffffffffu, wait_bounded_cluster(bar, parity, abort_flag, status)) != 0;
+}
+// The end of a kernel's work, by all threads: a barrier of the block or of the cluster of C CTAs, behind which
+// none uses another's shared memory. Where one of them gave up, all of them stay until what is still in
+// flight to or from their shared memory and TMEM (copies, MMAs, partial sums) has landed. That takes
+// microseconds, and the barriers that would tell may never complete; a millisecond is far behind it.
+constexpr unsigned long long kLinSettleNs = 1000000;
+__device__ __forceinline__ void lin_leave(int C, volatile int* abort_flag) {
+  __syncwarp();
+  if (C > 1) {
+    if (*abort_flag)
+      for (int r = 0; r < C; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                         mapa_shared(smem_addr(const_cast<int*>(abort_flag)), r)),
+                     "r"(1)
+                     : "memory");
+    __syncwarp();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  if (*abort_flag) {                               // the same for all threads
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kLinSettleNs) {}
+    __syncwarp();
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+  }
 }
 // a0 += s0 * v0, a1 += s1 * v1 (two IEEE fmas in one instruction).
 __device__ __forceinline__ void fma2(float& a0, float& a1, float s0, float s1, float v0, float v1) {

@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   tc_fence_before();
-  cluster_sync();               // no CTA leaves while its peer may still signal or read it
+  lin_leave(2, abort_flag);     // no CTA leaves while its peer may still signal or read it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);

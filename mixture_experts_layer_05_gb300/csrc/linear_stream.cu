@@ -593,8 +593,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   }
 
   tc_fence_before();
-  if (C > 1) cluster_sync();    // no CTA leaves while another may still write to it or read it
-  else __syncthreads();
+  lin_leave(C, abort_flag);     // no CTA leaves while another may still write to it or read it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, kTmemCols);

@@ -1,5 +1,6 @@
-"""What the products' kernels do when a bounded wait runs out: warps stay whole. The waits' helpers run
-in a small program of their own; where the kernels use them is read from the sources."""
+"""What the products' kernels do when a bounded wait runs out: warps stay whole, and no CTA leaves before
+what is in flight has landed. The helpers run in small programs of their own; where the kernels use them is
+read from the sources."""
 import os
 import re
 import subprocess
@@ -39,6 +40,14 @@ def test_only_single_threads_wait_lane_by_lane(name):
     assert calls
     for m in calls:
         assert any("lin_elect()" in h for h in _heads(text, m.start())), text[m.start():m.start() + 60]
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_kernels_end_by_lin_leave(name):
+    """The last barrier in front of TMEM's release is the one that stays where a CTA gave up."""
+    text = _source(name)
+    end = re.findall(r"(\w+)\([^()]*\);\s*if \(warp == 1\) \{\s*tc_fence_after\(\);\s*tmem_dealloc", text)
+    assert end == ["lin_leave"]
 
 
 WAITS = r"""
@@ -88,3 +97,60 @@ def _run(tmp_path, source):
 def test_a_warp_waits_as_one(cuda_lib, tmp_path):
     out, = _run(tmp_path, WAITS)
     assert out == "10" * 16 + "0" * 32 + "1" * 32
+
+
+LEAVE = r"""
+#include <cstdio>
+#include "linear.cuh"
+using namespace gbmoe;
+
+// Warp 3 of the last CTA gives up, or none. Per CTA: its flag, and how long it stayed.
+__global__ void leave(int C, int gives_up, unsigned long long* out) {
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+  const int rank = C > 1 ? (int)cluster_ctarank() : 0;
+  const unsigned long long t0 = globaltimer_ns();
+  if (gives_up && rank == C - 1 && threadIdx.x == 100) abort_flag = 1;
+  lin_leave(C, &abort_flag);
+  const unsigned long long t1 = globaltimer_ns();
+  if (threadIdx.x == 0) {
+    out[2 * rank] = (unsigned long long)abort_flag;
+    out[2 * rank + 1] = t1 - t0;
+  }
+}
+
+int main() {
+  unsigned long long* out;
+  if (cudaMallocManaged(&out, 16 * sizeof(*out)) != cudaSuccess) return 2;
+  for (int C : {1, 2, 8}) {
+    for (int gives_up : {0, 0, 1}) {               // the first call loads the kernel
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(C);
+      cfg.blockDim = dim3(160);
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = C;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if (cudaLaunchKernelEx(&cfg, leave, C, gives_up, out) != cudaSuccess) return 3;
+      if (cudaDeviceSynchronize() != cudaSuccess) return 4;
+      printf("%d %d", C, gives_up);
+      for (int i = 0; i < 2 * C; ++i) printf(" %llu", out[i]);
+      printf("\n");
+    }
+  }
+}
+"""
+
+
+@pytest.mark.gpu
+def test_a_cluster_stays_where_one_gave_up(cuda_lib, tmp_path):
+    lines = [[int(x) for x in l.split()] for l in _run(tmp_path, LEAVE)]
+    assert len(lines) == 9
+    for C, gave_up, *per in lines:
+        assert per[::2] == [gave_up] * C
+        # the timer ticks in steps of up to a few microseconds
+        assert all(t > 990000 if gave_up else t < 900000 for t in per[1::2]), (C, gave_up, per)
