@@ -128,15 +128,28 @@ __device__ __forceinline__ bool lin_elect() {
       : "=r"(r));
   return r != 0;
 }
-// The waits of a whole warp. Where one gives up, some lanes may still see the phase complete; all of them
-// have to go the same way, to loads from TMEM and barriers that take the warp as one. (Inlined: behind a
-// call the e4m3 kernels' sums leave the registers, 8192 gated rows in 16 groups 236 us for 217.)
+// The waits. With CLUSTER they acquire at the scope of the cluster, which a phase that another CTA's
+// arrivals, copies or MMAs complete needs; without, at that of the CTA.
+template <bool CLUSTER>
+__device__ __forceinline__ bool lin_try(uint32_t bar, uint32_t parity) {
+  return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+}
+// One thread's, across the cluster (wait_fast is the other).
+__device__ __forceinline__ bool wait_fast_cluster(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort_flag, int* status) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  return wait_bounded_cluster(bar, parity, abort_flag, status);
+}
+// A whole warp's. Where one gives up, some lanes may still see the phase complete; all of them have to go
+// the same way, to loads from TMEM and barriers that take the warp as one. (Inlined: behind a call the e4m3
+// kernels' sums leave the registers, 8192 gated rows in 16 groups 236 us for 217.)
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* status) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xffffffffu, lin_try<CLUSTER>(bar, parity))) return true;
   const unsigned long long t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, lin_try<CLUSTER>(bar, parity))) return true;
     if ((i & 63u) == 0u) {
       if (__any_sync(0xffffffffu, *abort_flag)) return false;
       if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitTimeoutNs)) {
@@ -146,10 +159,6 @@ __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, volatile
       }
     }
   }
-}
-__device__ __forceinline__ bool lin_wait_cluster(uint32_t bar, uint32_t parity,
-                                                 volatile int* abort_flag, int* status) {
-  return __all_sync(0xffffffffu, wait_bounded_cluster(bar, parity, abort_flag, status)) != 0;
 }
 // The end of a kernel's work, by all threads: a barrier of the block or of the cluster of C CTAs, behind which
 // none uses another's shared memory. Where one of them gave up, all of them stay until what is still in

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int xr = few ? kFewRows : half_bn;
         const uint32_t bytes = 2u * (kLinWBytes + (uint32_t)xr * 128);   // both CTAs'
         for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_fast(empty_bar(s), ph, abort_flag, status)) {
+          if (!wait_fast_cluster(empty_bar(s), ph, abort_flag, status)) {
             ok = false;
             break;
           }
@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = (w.n + 15) & ~15;
         const uint32_t idesc = idesc_bf16(256, n);
         for (int kb = 0; kb < KB; ++kb) {
-          if ((kb == 0 && !wait_fast(tempty_bar(buf), tph, abort_flag, status)) ||
-              !wait_fast(full_bar(s), ph, abort_flag, status)) {
+          if ((kb == 0 && !wait_fast_cluster(tempty_bar(buf), tph, abort_flag, status)) ||
+              !wait_fast_cluster(full_bar(s), ph, abort_flag, status)) {
             ok = false;
             break;
           }
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32 && at + i < w.n; ++i)
             lin_prefetch(static_cast<const __nv_bfloat16*>(a.residual) +
                          (long long)(w.m0 + at + i) * a.residual_stride + l.f);
-      if (!lin_wait(tfull_bar(buf), tph, abort_flag, status)) break;
+      if (!lin_wait<true>(tfull_bar(buf), tph, abort_flag, status)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int at = part * 32; at < w.n; at += 64) {

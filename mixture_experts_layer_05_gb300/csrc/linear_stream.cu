@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
         }
       }
       // what the unit before sent has been added up, here and by the others
-      if (C > 1 && u != first && !lin_wait_cluster(rempty_bar, rph ^ 1u, abort_flag, status)) {
+      if (C > 1 && u != first && !lin_wait<true>(rempty_bar, rph ^ 1u, abort_flag, status)) {
         ok = false;
         break;
       }
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
                               mapa_shared(rfull_bar, lane));
           }
         }
-        if (!lin_wait(rfull_bar, rph, abort_flag, status)) {
+        if (!lin_wait<true>(rfull_bar, rph, abort_flag, status)) {
           ok = false;
           break;
         }

@@ -1,5 +1,5 @@
-"""What the products' kernels do when a bounded wait runs out: warps stay whole, and no CTA leaves before
-what is in flight has landed. The helpers run in small programs of their own; where the kernels use them is
+"""The products' waits: those for other CTAs acquire at the cluster's scope; and where a bounded wait runs
+out, warps stay whole, and no CTA leaves before what is in flight has landed. The helpers run in small programs of their own; where the kernels use them is
 read from the sources."""
 import os
 import re
@@ -40,6 +40,18 @@ def test_only_single_threads_wait_lane_by_lane(name):
     assert calls
     for m in calls:
         assert any("lin_elect()" in h for h in _heads(text, m.start())), text[m.start():m.start() + 60]
+
+
+def test_waits_for_other_ctas_acquire_at_their_scope():
+    """Phases that another CTA of the cluster completes: all of the pairs', whose stages and accumulators are
+    both CTAs', and the few-row kernel's partial sums (received; taken, so that the next may be sent)."""
+    pair = _source("linear_pair.cu")
+    assert re.findall(r"\b(wait_\w+|lin_wait)(<true>)?\(", pair) == [
+        ("wait_fast_cluster", "")] * 3 + [("lin_wait", "<true>")]
+    stream = _source("linear_stream.cu")
+    waits = re.findall(r"\b(wait_\w+|lin_wait)(<true>)?\((\w+)", stream)
+    assert {bar for _, across, bar in waits if across} == {"rfull_bar", "rempty_bar"}
+    assert not {bar for _, across, bar in waits if not across} & {"rfull_bar", "rempty_bar"}
 
 
 @pytest.mark.parametrize("name", KERNELS)
