@@ -67,6 +67,7 @@ class DecoderBlock:
         heads = s.q_heads + 2 * s.kv_heads
         self.wqkv = weight(heads * s.head_dim, s.hidden)
         self.wo = weight(s.hidden, s.q_heads * s.head_dim)
+        self.status_word = binding.alloc_workspace(256, device)    # of the projections
         self.norm1, self.norm2 = 1 + weight(s.hidden), 1 + weight(s.hidden)
         self.gate = weight(s.experts, s.hidden, std=0.05)
         scale = dict(k_scale=0.05, v_scale=0.05) if s.cache == "fp8" else {}
@@ -90,7 +91,8 @@ class DecoderBlock:
         """Attention of the batch's new tokens x [T, hidden]; (attention rows, residual stream)."""
         s = self.s
         y, res, _, _ = binding.moe_rms_norm(x, self.norm1, residual=residual)
-        qkv = binding.moe_linear(y, self.wqkv).view(x.shape[0], -1, s.head_dim)
+        qkv = binding.moe_linear(y, self.wqkv, workspace=self.status_word)
+        qkv = qkv.view(x.shape[0], -1, s.head_dim)
         paged = (self.k_cache, self.v_cache, *batch)
         q = self.attn.append(qkv[:, :s.q_heads], qkv[:, s.q_heads:s.q_heads + s.kv_heads],
                              qkv[:, s.q_heads + s.kv_heads:], *paged, cos_sin=self.cos_sin)
@@ -99,12 +101,14 @@ class DecoderBlock:
     def __call__(self, x, residual, batch):
         """(block output, residual stream): their sum is the next block's input."""
         o, res = self.attend(x, residual, batch)
-        res = binding.moe_linear(o.flatten(1), self.wo, residual=res)
+        res = binding.moe_linear(o.flatten(1), self.wo, residual=res, workspace=self.status_word)
         y, _, yq, ys = binding.moe_rms_norm(res, self.norm2, out="both")
         return self.moe(y, gate_weight=self.gate, hidden_q=yq, hidden_scale=ys), res
 
     def status(self):
-        return self.attn.device_status(), self.moe.device_status()
+        """Of the attention with the projections around it, and of the experts."""
+        attn, projections = self.attn.device_status(), binding.moe_get_device_status(self.status_word)
+        return attn or projections, self.moe.device_status()
 
 
 def main(argv=None):

@@ -635,7 +635,8 @@ gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int32_t num_t
  *   offsets       [num_groups + 1] int32, ascending, device memory that the kernel reads: a captured
  *                 graph replays with its current contents. Empty runs are allowed; rows before
  *                 offsets[0] and from offsets[num_groups] on are left as they are.
- *   workspace     256 bytes, 256-byte aligned: the status word; or NULL (unreported)
+ *   workspace     256 bytes, 256-byte aligned: the status word; or NULL: then a failed device check or a
+ *                 bounded wait that ran out, which may leave rows unwritten, is reported nowhere
  * in_features: a multiple of 8 (FP8_BLOCK128: of 128), at most 2^24. out_features: any; with SILU_MUL
  * a multiple of 32 (FP8_BLOCK128: of 256). Else UNSUPPORTED, as are NVFP4, more than 1024 groups,
  * 2^31 - 1024 or more rows of all weights together, x_stride from 2^39 on, and calls of more than 2^30

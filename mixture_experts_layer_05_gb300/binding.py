@@ -546,8 +546,9 @@ def moe_linear(x, weight, bias=None, activation="none", residual=None, row_weigh
     weight_scale [ceil(N / 128), K / 128]. activation: "none", "relu", "silu", "gelu",
     "gelu_tanh", or "silu_mul" (weight rows gate | up, N / 2 output columns). bias [N] and
     residual [T, columns] bf16, row_weight [T] fp32. Rows of x, residual and out may be strided;
-    out may be the residual. workspace: see alloc_workspace, for device checks that
-    moe_get_device_status reports. stream: a torch.cuda.Stream (None: the current one); the inputs
+    out may be the residual. workspace: see alloc_workspace; moe_get_device_status reports from it
+    that a device check failed or that a bounded wait ran out, after either of which rows may be left
+    unwritten. Without one nothing does. stream: a torch.cuda.Stream (None: the current one); the inputs
     must be ready on it, and a new output belongs to it. All tensors are on one device."""
     return _block().linear(x, weight, None, bias, _epilogue(activation), residual, row_weight,
                            x_scale, weight_scale, out, workspace, stream)

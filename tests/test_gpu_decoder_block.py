@@ -55,3 +55,22 @@ def test_served_tokens_match_the_whole_prompt(cuda_lib, cache):
 def test_example_runs(cuda_lib, capsys):
     db.main(["--prompts", "70", "3", "--steps", "2", "--cache", "fp8"])
     assert "one token each" in capsys.readouterr().out
+
+
+def test_status_covers_the_projections(cuda_lib, monkeypatch):
+    """What a projection reports (a wait that ran out, say) is what the block reports, once."""
+    s = db.Sizes(hidden=512, q_heads=8, kv_heads=2, head_dim=64, page=16, pages=16, experts=8, top_k=2,
+                 intermediate=256, max_position=64)
+    block = db.DecoderBlock(s, max_tokens=8)
+    batch = db.Sequences(s, 1).extend([3])
+    x = torch.randn(3, s.hidden, device="cuda").to(torch.bfloat16)
+    run, given = binding.moe_linear, []
+    monkeypatch.setattr(binding, "moe_linear", lambda *a, workspace=None, **kw: (
+        given.append(workspace), run(*a, workspace=workspace, **kw))[1])
+    block(x, None, batch)
+    assert block.status() == (binding.OK, binding.OK)
+    assert len(given) == 2
+    for workspace in given:
+        workspace[:4].view(torch.int32).fill_(binding.ERR_DEVICE_CHECK)
+        assert block.status() == (binding.ERR_DEVICE_CHECK, binding.OK)
+        assert block.status() == (binding.OK, binding.OK)
