@@ -13,6 +13,7 @@
 #pragma once
 
 #include "linear.h"
+#include "linear_plan.h"
 #include "tc.cuh"
 
 namespace gbmoe {
@@ -36,30 +37,11 @@ struct LinLaunch {
   int half_off;    // (stream kernel, e4m3) sums of every other K block
   // stream kernel
   int cluster;     // CTAs that cut a unit's K blocks
-  int rows[4];     // weight rows per tile: the choices (the kernel picks, by its groups), largest first,
+  int rows[kLinChoices];  // weight rows per tile: the choices (the kernel picks, by its groups), largest first,
   int choices;     // and how many
   int kps;         // K blocks per stage
   int whole;       // K is whole K blocks: a box takes kps of them
 };
-
-// The stream kernel's time for a unit of R weight rows and n rows of x over so many K blocks, in ns, fitted
-// to measurements at K = N = 4096: a CTA takes 128 bytes a ns from L2 and HBM together; a K block's
-// MMAs, whose time goes by their 128 (plain tiles of up to 64: 64) weight rows, and the operands of its
-// columns take 90 and 1 (55 and 1.2) a row of x (e4m3: its promotion 50 and 5); a unit's beginning and end
-// 300, with e4m3, whose sums leave the registers between two units, 2000.
-__host__ __device__ inline long long lin_unit_ns(bool fp8, bool gated, int R, int n, int k_blocks) {
-  const int math = fp8 ? 50 + 5 * n : R <= 64 && !gated ? 55 + 6 * n / 5 : 90 + n;
-  return (long long)k_blocks * (R + n > math ? R + n : math) + (fp8 ? 2000 : 300);
-}
-
-// The time for `units` of them, `bytes` of weights each, by `step` CTAs or clusters at once: full rounds, in
-// which HBM's 6.7 TB/s may be what holds, and a last one, in which each unit takes its own time at least.
-__host__ __device__ inline long long lin_line_ns(long long units, int step, long long unit_ns,
-                                                 long long bytes) {
-  const long long all = step * bytes / 6700, full = units / step, rest = units % step;
-  const long long last = rest * bytes / 6700;
-  return full * (all > unit_ns ? all : unit_ns) + (rest == 0 ? 0 : last > unit_ns ? last : unit_ns);
-}
 
 namespace {
 

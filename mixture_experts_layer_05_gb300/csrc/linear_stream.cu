@@ -28,11 +28,11 @@ namespace gbmoe {
 namespace {
 
 constexpr int kMaxBn = 128, kMaxBnFp8 = 64;      // (e4m3 keeps its sums in registers)
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = kLinMaxCluster;
 constexpr int kMaxStages = 16;
 constexpr int kMaxKps = 8;                       // K blocks per stage
 constexpr int kXMaps = 2;                        // x boxes of bn and of 8 rows
-constexpr int kWMaps = 4;                        // weight boxes of L.rows[i] rows
+constexpr int kWMaps = kLinChoices;              // weight boxes of L.rows[i] rows
 constexpr uint32_t kTmemCols = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kBufsMax = 8;                      // TMEM buffers
@@ -188,28 +188,12 @@ __global__ void __launch_bounds__(threads_of(FP8), 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  // The tile: of the choices, the one whose line of units takes least (16 groups of which 10 have rows,
-  // 7168 to 4096 gated: 320 tiles of 128 rows took 103 us on 152 SMs, 430 of 96 95).
   int R = L.rows[0], pick = 0, n_tiles = L.n_tiles;
   if (grouped) {
-    long long best = 0;
+    // all CTAs have to come to the same tile, so nothing of a CTA's own goes in here
     const int xr = (a.T + a.G - 1) / a.G <= 8 ? 8 : bn;
-    // All CTAs have to come to the same tile, so nothing of a CTA's own goes in here. A smaller tile is not
-    // read faster: the ring holds as many K blocks of it, and fewer bytes.
-    const long long unit_ns = lin_unit_ns(FP8, GATED, L.rows[0], xr, (L.k_blocks + C - 1) / C);
-    for (int i = 0; i < L.choices; ++i) {
-      const int r = L.rows[i], cols = GATED ? r / 2 : r;
-      const int nt = (a.cols + cols - 1) / cols;
-      const long long u = (long long)groups.before[a.G] * nt;
-      if (i > 0 && u > 1 << 30) break;             // units are counted in 32 bits
-      const long long cost = lin_line_ns(u, step, unit_ns, (long long)r * L.k_blocks * 128);
-      if (i == 0 || cost < best) {
-        best = cost;
-        pick = i;
-        R = r;
-        n_tiles = nt;
-      }
-    }
+    pick = lin_pick(L.rows, L.choices, FP8, GATED, a.cols, L.k_blocks, C, xr, groups.before[a.G], step, &n_tiles);
+    R = L.rows[pick];
   }
   const int units = groups.units(n_tiles);
   const int tile_cols = GATED ? R / 2 : R;

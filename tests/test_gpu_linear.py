@@ -71,8 +71,9 @@ def test_linear_fp8_wide(cuda_lib, T, K, N, act):
     c.check(c.call(binding))
 
 
-# sizes that the cut of few rows answers with clusters of 1 to 8 CTAs, tiles of 8 to 128 weight rows and
-# one to three rounds of units
+# sizes that the cut of few rows answers with clusters of up to 8 CTAs, tiles of 8 to 128 weight rows and
+# one or two rounds of units (a few go to the kernels for many rows); clusters of the other numbers of CTAs,
+# and those that walk several rounds, are tests/linear_cuts.py's
 CUTS = [(1, 512, 256), (1, 512, 24576), (48, 4096, 4096), (1, 4096, 2048), (24, 4096, 2048),
         (64, 4096, 2048), (64, 2048, 2048), (24, 8192, 1024), (48, 2048, 256), (64, 2048, 1024),
         (80, 512, 12288), (80, 512, 24576), (80, 4096, 4096), (64, 8192, 24576), (1, 8192, 4096),
@@ -212,6 +213,7 @@ def test_grouped_drawn(cuda_lib, seed):
         c.check(c.call(binding))
 
 
+# (either several CTAs to a tile or several rounds; both at once: tests/linear_cuts.py)
 @pytest.mark.parametrize("sizes", [[4], [1, 2], [0, 9, 8, 7], [100, 3, 0, 1]])
 @pytest.mark.parametrize("K,N", [(4096, 512), (8192, 2048), (512, 8192), (2048, 96 * 128)])
 @pytest.mark.parametrize("act", ["none", "silu_mul"])
