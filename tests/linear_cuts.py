@@ -29,3 +29,6 @@ ROUNDS = [
     ((11, 1, 1), 15616, 7936, "silu_mul", True, 2, 5),
     ((1,), 25216, 19712, "silu_mul", True, 3, 7),
 ]
+
+# gated e4m3 calls of many rows: (rows, or rows of each group; K, N)
+GATED_FP8 = [(300, 384, 4096), (777, 1024, 2048), ((400, 0, 257, 131), 384, 512)]

@@ -6,7 +6,7 @@ import subprocess
 import pytest
 
 from mixture_experts_layer_05_gb300 import build as build_mod
-from tests.linear_cuts import CLUSTERS, ROOM, ROUNDS
+from tests.linear_cuts import CLUSTERS, GATED_FP8, ROOM, ROUNDS
 from tests.test_gpu_linear import CUTS
 
 PROGRAM = r"""
@@ -70,6 +70,7 @@ def test_cluster_cases_reach_their_cuts(plan):
     got = plan([(rows, K, N, act == "silu_mul", fp8) for rows, K, N, act, fp8, _, _ in cases])
     for case, (many, ctas, bn, _, rounds, _) in zip(cases, got):
         assert (many, ctas, rounds) == (0, *case[5:]), (case, ctas, rounds)
+    assert all(a[0] for a in plan([(rows, K, N, True, True) for rows, K, N in GATED_FP8]))
     # the e4m3 kernel's halves of a run of columns are among them
     assert any(bn == 16 and c[4] and c[6] > 1 for c, (_, _, bn, _, _, _) in zip(cases, got))
 
