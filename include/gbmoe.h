@@ -637,7 +637,7 @@ gbmoe_status_t moe_paged_attention(const gbmoe_attn_config_t* cfg, int32_t num_t
  *                 offsets[0] and from offsets[num_groups] on are left as they are.
  *   workspace     256 bytes, 256-byte aligned: the status word; or NULL: then a failed device check or a
  *                 bounded wait that ran out, which may leave rows unwritten, is reported nowhere
- * in_features: a multiple of 8 (FP8_BLOCK128: of 128), at most 2^24. out_features: any; with SILU_MUL
+ * T: at most 2^22. in_features: a multiple of 8 (FP8_BLOCK128: of 128), at most 2^24. out_features: any; with SILU_MUL
  * a multiple of 32 (FP8_BLOCK128: of 256). Else UNSUPPORTED, as are NVFP4, more than 1024 groups,
  * 2^31 - 1024 or more rows of all weights together, x_stride from 2^39 on, and calls of more than 2^30
  * output tiles (of 128 columns by 16 rows). x 16-byte aligned, x_stride a multiple of 16 bytes; weight

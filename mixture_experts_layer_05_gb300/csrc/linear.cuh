@@ -1,10 +1,11 @@
-// Shared by the kernels of the dense and grouped products (linear_stream.cu, linear_pair.cu): the
-// line of work units, the weight and scale layout in shared memory, and the epilogue.
+// Shared by the kernels of the dense and grouped products (linear_stream.cu, linear_pair.cu, linear_fp8.cu):
+// the line of work units, waits and copies, the activations, and the epilogue of weights on M.
 //
-// Both kernels put the weights on the MMA's M side (a TMEM lane is an output feature) and a block
-// of at most `bn` rows of one group on N, so a ragged run costs no more than its rows rounded up to
-// 16. A unit is (group, row block, tile of features); a group's units follow one another, row blocks
-// fastest within sections of `gm` blocks, so that a weight tile is read from HBM once.
+// A unit is (group, row block, tile of features); a group's units follow one another, row blocks fastest
+// within sections of `gm` blocks, so that a weight tile is read from HBM once. linear_stream.cu and
+// linear_pair.cu put the weights on the MMA's M side (a TMEM lane is an output feature) and a block of at
+// most `bn` rows of one group on N, so a ragged run costs no more than its rows rounded up to 16;
+// linear_fp8.cu has 128 rows of one group on M.
 //
 // Both types have K blocks of 128 bytes (64 bf16, 128 e4m3: one swizzle row, one scale block).
 // With SILU_MUL a tile of weight rows holds 16 gate rows, the 16 up rows of the same features, and

@@ -7,7 +7,7 @@
 // weights on M, as the other kernels have them, the rows' scales change from column to column, and
 // reading them takes shared memory's time from the operands.)
 //
-// 8192 rows of 7168 to 4096 columns take 224 us (2.1 PFLOP/s). Two limits hold it at almost the same height:
+// 8192 rows of 7168 to 4096 columns take 224 to 230 us (2.1 PFLOP/s). Two limits hold it at almost the same height:
 // products and promotion, which take turns at TMEM's two buffers of 128 x 256 (212 us without the copies),
 // and products and copies (216 without the promotion); products alone take 160, copies alone 172. Pairs of
 // CTAs (M = 256), whose operands are two thirds, lift the second only: 242 us as single ones then, and 257

@@ -136,13 +136,15 @@ LinPlan lin_plan(const LinSize& a, int sms, Room room_of) {
   const int mean = lin_ceil_div(a.T, a.G);
   const int groups = a.G < a.T ? a.G : a.T;                  // with rows, at most
 
-  // Few rows or many: by the modelled times. Measured, stream and many (us): K = N = 4096, bf16, 64 rows
-  // 12.5 and 14.6, 128 rows 17.6 and 14.8; 96 rows of 2048 to 2048 10.8 and 9.3; e4m3, 128 rows of 4096 to
-  // 4096 15.3 and 21.4, 160 to 16384 47.4 and 24.7; 16 groups of 2048 to 7168, mean 32 76.9 and 79.4,
-  // mean 64 88.5 and 81.6; e4m3, mean 8 42.6 and 44.1, mean 16 59.7 and 45.5. Where HBM bounds both the few
-  // rows' kernel is ahead (4 rows of 4096 to 24576 38.6 and 41.3), and of small groups fewer may have rows
-  // than the model counts, which suits it too; above 96 rows its ring gets short, and it has to be
-  // well ahead.
+  // Few rows or many: by the modelled times. Measured in one run, graph replay, few and many (us): bf16, 4 rows
+  // of 4096 to 24576 32.3 and 36.9; K = N = 4096, 64 rows 12.7 and 14.8, 96 with residual 14.9 and 15.3, 128
+  // 17.9 and 15.2; 96 rows of 2048 to 2048 10.7 and 9.6, 64 of 4096 to 16384 24.5 and 25.3; 16 groups of 2048
+  // to 7168, mean 4 68.9 and 68.5, 16 73.5 and 73.1, 32 76.7 and 74.3, 64 99.1 and 76.4. e4m3, K = N = 4096,
+  // 128 rows 14.7 and 20.1, 160 to 256 17.5 and 20.2 (the rule takes the slower one there); 160 to 16384
+  // 44.6 and 24.5; the groups' mean 4 39.6 and 40.3, 8 41.0 and 42.1, 16 42.6 and 43.9 (again), 32 48.6 and 46.4.
+  // Where HBM bounds both by the model the few rows' kernel is ahead by up to 14 %, and of small groups fewer
+  // may have rows than the model counts, which suits it too: the first factor. Above 96 rows its ring gets
+  // short, and it has to be well ahead: the last.
   const WideCut wide = cut_wide(a, groups, k_blocks, sms);
   p.many = mean > (a.grouped ? 128 : 4096);
   StreamCut cut = {};
